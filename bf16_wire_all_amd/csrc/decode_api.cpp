@@ -1,0 +1,175 @@
+// Exported entry points of the decode-step calls: argument checks in the order
+// the header documents, then the kernel launches.  Every check runs on the
+// host before anything is enqueued.
+#include <algorithm>
+#include <cmath>
+
+#include "decode.h"
+
+namespace {
+
+constexpr uint64_t kMaxExtent = 1ull << 47;
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+bool overlaps(uintptr_t a, uint64_t na, uintptr_t b, uint64_t nb) {
+  if (na == 0 || nb == 0) return false;
+  return a < b + nb && b < a + na;
+}
+
+uint32_t element_bytes(int kind) { return kind == XFER_KV_BF16 ? 2 : 1; }
+
+// The checks that every call makes of a cache; on XFER_OK *extent holds the
+// bytes from k (and from v) to the end of the last slot.
+int cache_checks(const xfer_kv_cache *c, uint64_t *extent) {
+  if (!c) return XFER_E_INVAL;
+  if (c->kind != XFER_KV_BF16 && c->kind != XFER_KV_E4M3) return XFER_E_INVAL;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return XFER_E_INVAL;
+  if (c->page_stride % 16 || c->token_stride % 16 || c->head_stride % 16) return XFER_E_INVAL;
+  if (c->n_pages == 0 || c->page_tokens == 0 || c->kv_heads == 0) return XFER_E_INVAL;
+  if (c->page_tokens & (c->page_tokens - 1)) return XFER_E_INVAL;
+  if (c->kind == XFER_KV_BF16 && (c->k_scale || c->v_scale)) return XFER_E_INVAL;
+  if (c->reserved) return XFER_E_INVAL;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return XFER_E_UNSUPPORTED;
+  if (c->page_tokens > 65536) return XFER_E_UNSUPPORTED;
+  uint64_t n = (uint64_t)c->head_dim * element_bytes(c->kind);
+  const uint64_t step[3][2] = {{c->page_stride, c->n_pages}, {c->token_stride, c->page_tokens},
+                               {c->head_stride, c->kv_heads}};
+  for (const auto &s : step) {
+    uint64_t reach;
+    if (__builtin_mul_overflow(s[0], s[1] - 1, &reach) || reach > kMaxExtent) return XFER_E_INVAL;
+    n += reach;
+  }
+  if (n > kMaxExtent) return XFER_E_INVAL;
+  *extent = n;
+  return XFER_OK;
+}
+
+// Whether every element of the cache has bytes of its own: from the smallest
+// stride up, each stride must pass the extent of what lies inside it.
+bool slots_disjoint(const xfer_kv_cache *c) {
+  struct Step {
+    uint64_t stride, count;
+  } s[3] = {{c->page_stride, c->n_pages}, {c->token_stride, c->page_tokens}, {c->head_stride, c->kv_heads}};
+  std::sort(s, s + 3, [](const Step &a, const Step &b) { return a.stride < b.stride; });
+  uint64_t extent = (uint64_t)c->head_dim * element_bytes(c->kind);
+  for (const Step &t : s) {
+    if (t.count == 1) continue;
+    if (t.stride < extent) return false;
+    extent += t.stride * (t.count - 1);
+  }
+  return true;
+}
+
+// Rows of `len` bytes, `pitch` apart.
+struct Rows {
+  uintptr_t at;
+  uint64_t pitch, len, n;
+  uint64_t extent() const { return n ? (n - 1) * pitch + len : 0; }
+};
+
+// Whether a row of a shares a byte with a row of b.  Slices of one buffer
+// (equal pitches) interleave without touching; with other pitches the whole
+// extents must be apart.
+bool rows_touch(const Rows &a, const Rows &b) {
+  if (!a.n || !b.n || !a.len || !b.len || !overlaps(a.at, a.extent(), b.at, b.extent())) return false;
+  if (a.pitch != b.pitch || a.n == 1 || b.n == 1) return true;
+  const uint64_t d = b.at >= a.at ? (b.at - a.at) % a.pitch : (a.pitch - (a.at - b.at) % a.pitch) % a.pitch;
+  return d < a.len || a.pitch - d < b.len;
+}
+
+// An ld (elements) of `rows` rows of `row` BF16 elements: a multiple of 8, and
+// not so small that rows overlap or so large that they pass the extent limit.
+bool ld_ok(uint64_t ld, uint64_t rows, uint64_t row) {
+  if (ld % 8) return false;
+  if (rows <= 1) return true;
+  return ld >= row && ld <= kMaxExtent / 2 && (rows - 1) <= kMaxExtent / 2 / ld;
+}
+
+uint32_t log2_of(uint32_t x) { return (uint32_t)__builtin_ctz(x); }
+
+xfer::CacheView view_of(const xfer_kv_cache *c) {
+  xfer::CacheView v{};
+  v.k = static_cast<uint8_t *>(c->k);
+  v.v = static_cast<uint8_t *>(c->v);
+  v.k_scale = c->k_scale;
+  v.v_scale = c->v_scale;
+  v.page_stride = c->page_stride;
+  v.token_stride = c->token_stride;
+  v.head_stride = c->head_stride;
+  v.n_pages = c->n_pages;
+  v.page_log2 = log2_of(c->page_tokens);
+  v.kv_heads = c->kv_heads;
+  v.head_dim = c->head_dim;
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xfer_rope *rope, const int64_t *slots,
+                        uint16_t *q_out, uint64_t q_out_ld, hipStream_t stream) {
+  uint64_t extent = 0;
+  const int st = cache_checks(cache, &extent);
+  if (st != XFER_OK) return st;
+  if (!slots_disjoint(cache) || cache->v == cache->k) return XFER_E_OVERLAP;
+  if (!in || !rope || in->reserved || rope->reserved) return XFER_E_INVAL;
+  if (rope->style != XFER_ROPE_HALVES && rope->style != XFER_ROPE_PAIRS) return XFER_E_INVAL;
+  if (!(in->eps >= 0.0f) || !std::isfinite(in->eps)) return XFER_E_INVAL;
+  if (rope->rot_dim % 8 || rope->rot_dim > cache->head_dim) return XFER_E_INVAL;
+  if (in->tokens == 0) return XFER_OK;
+  const uint64_t T = in->tokens, q_row = (uint64_t)in->q_heads * cache->head_dim;
+  const uint64_t kv_row = (uint64_t)cache->kv_heads * cache->head_dim;
+  if (rope->rot_dim && (!rope->cos_sin || !aligned16(rope->cos_sin) || !rope->positions || !rope->max_pos))
+    return XFER_E_INVAL;
+  if (!slots || !in->k || !in->v || !aligned16(in->k) || !aligned16(in->v)) return XFER_E_INVAL;
+  if (in->q_heads && (!in->q || !q_out || !aligned16(in->q) || !aligned16(q_out))) return XFER_E_INVAL;
+  if (!aligned16(in->q_weight) || !aligned16(in->k_weight)) return XFER_E_INVAL;
+  if (!ld_ok(in->k_ld, T, kv_row) || !ld_ok(in->v_ld, T, kv_row)) return XFER_E_INVAL;
+  if (in->q_heads && (!ld_ok(in->q_ld, T, q_row) || !ld_ok(q_out_ld, T, q_row))) return XFER_E_INVAL;
+
+  const uint64_t nq = in->q_heads ? T : 0;
+  const Rows out{(uintptr_t)q_out, q_out_ld * 2, q_row * 2, nq};
+  const Rows ins[3] = {{(uintptr_t)in->q, in->q_ld * 2, q_row * 2, nq},
+                       {(uintptr_t)in->k, in->k_ld * 2, kv_row * 2, T},
+                       {(uintptr_t)in->v, in->v_ld * 2, kv_row * 2, T}};
+  const bool in_place = nq && q_out == in->q && (q_out_ld == in->q_ld || T == 1);
+  for (int i = 0; i < 3; ++i)
+    if (!(i == 0 && in_place) && rows_touch(out, ins[i])) return XFER_E_INVAL;
+  const uintptr_t caches[2] = {(uintptr_t)cache->k, (uintptr_t)cache->v};
+  for (uintptr_t c : caches) {
+    if (overlaps(c, extent, out.at, out.extent())) return XFER_E_INVAL;
+    for (const Rows &r : ins)
+      if (overlaps(c, extent, r.at, r.extent())) return XFER_E_INVAL;
+  }
+  const uint64_t heads = (uint64_t)in->q_heads + 2ull * cache->kv_heads;
+  if (heads > UINT32_MAX ||
+      xfer::rope_store_workgroups(in->tokens, (uint32_t)heads, cache->head_dim) > xfer::kMaxGridBlocks)
+    return XFER_E_UNSUPPORTED;
+
+  xfer::RopeStoreArgs a{};
+  a.cache = view_of(cache);
+  a.q = in->q;
+  a.k = in->k;
+  a.v = in->v;
+  a.q_weight = in->q_weight;
+  a.k_weight = in->k_weight;
+  a.q_ld = in->q_ld;
+  a.k_ld = in->k_ld;
+  a.v_ld = in->v_ld;
+  a.q_out_ld = q_out_ld;
+  a.cos_sin = rope->cos_sin;
+  a.positions = rope->positions;
+  a.slots = slots;
+  a.q_out = q_out;
+  a.tokens = in->tokens;
+  a.q_heads = in->q_heads;
+  a.max_pos = rope->max_pos;
+  a.rot_dim = rope->rot_dim;
+  a.eps = in->eps;
+  if (xfer::launch_rope_store(a, cache->kind, rope->style, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,149 @@
+"""Python binding of the decode-step calls (include/xfer_decode.h): argument
+marshalling only, as the package's other calls.
+
+Device buffers are torch CUDA tensors on the current device; heads may be
+slices of a fused buffer (the last two dimensions dense, any row stride).
+Every call takes the current torch stream unless `stream` is given, and
+raises XferError on a non-OK status."""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _stream, lib as _base_lib
+
+KV_BF16, KV_E4M3 = 0, 1
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+
+EXPORTED = ["xfer_qkv_rope_store"]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_uint64), ("token_stride", ctypes.c_uint64),
+                ("head_stride", ctypes.c_uint64), ("n_pages", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32),
+                ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("kind", ctypes.c_int32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class RopeC(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("max_pos", ctypes.c_uint32),
+                ("rot_dim", ctypes.c_uint32), ("style", ctypes.c_int32), ("reserved", ctypes.c_uint32)]
+
+
+class QKVC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_ld", ctypes.c_uint64),
+                ("k_ld", ctypes.c_uint64), ("v_ld", ctypes.c_uint64), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("tokens", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)]
+
+
+_lib = None
+
+
+def lib():
+    """The loaded libxfer.so with the decode-step signatures."""
+    global _lib
+    if _lib is None:
+        L = _base_lib()
+        P, U64, I = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int
+        L.xfer_qkv_rope_store.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(QKVC), ctypes.POINTER(RopeC), P, P,
+                                          U64, P]
+        L.xfer_qkv_rope_store.restype = I
+        _lib = L
+    return _lib
+
+
+def _flat(t, itemsize: int, device, what: str) -> int:
+    """Pointer of a contiguous tensor of the call's device (None: NULL)."""
+    if t is None:
+        return 0
+    if t.device != device or t.element_size() != itemsize or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {itemsize}-byte tensor on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, heads, head_dim: int, itemsize: int, device, what: str):
+    """(pointer, rows, heads, ld in elements) of a [rows, heads, head_dim] tensor whose rows are dense."""
+    rows, h, d = t.shape
+    s = t.stride()
+    if t.device != device or t.element_size() != itemsize or d != head_dim or (heads is not None and h != heads):
+        raise ValueError(f"{what}: expected [rows, {heads or 'heads'}, {head_dim}] of {itemsize} bytes on {device}")
+    if s[2] != 1 or (h > 1 and s[1] != d):
+        raise ValueError(f"{what}: a row's heads must lie one after the other")
+    return t.data_ptr(), rows, h, s[0] if rows > 1 else h * d
+
+
+def _on(device) -> None:
+    """Pointers belong to the device that is current when a call is made."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, which is not the current device")
+
+
+class KVCache:
+    """A paged cache of keys and values; keeps its tensors alive."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or v.element_size() != k.element_size():
+            raise ValueError("k and v must be alike: [pages, page_tokens, heads, head_dim] with the same strides")
+        if k.element_size() not in (1, 2) or v.device != k.device or k.device.type != "cuda":
+            raise ValueError("k and v must be BF16 or E4M3 CUDA tensors of one device")
+        n, p, h, d = k.shape
+        s, e = k.stride(), k.element_size()
+        if s[3] != 1:
+            raise ValueError("a head's elements must lie one after the other")
+        for scale in (k_scale, v_scale):
+            if scale is not None and scale.numel() != h:
+                raise ValueError("one scale for each head")
+        self.device, self.kv_heads, self.head_dim, self.page_tokens, self.n_pages = k.device, h, d, p, n
+        self.tensors = (k, v, k_scale, v_scale)
+        # the stride of a dimension of one element is never walked: any multiple of 16 will do
+        stride = [s[i] * e if k.shape[i] > 1 else 0 for i in range(3)]
+        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, 4, k.device, "k_scale") or None,
+                          _flat(v_scale, 4, k.device, "v_scale") or None, stride[0], stride[1], stride[2], n, p, h, d,
+                          KV_BF16 if e == 2 else KV_E4M3, 0)
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> KVCache:
+    """k, v: [pages, page_tokens, heads, head_dim] CUDA tensors or views (BF16 or
+    2-byte patterns, or E4M3 bytes), any strides but a dense last dimension;
+    k_scale, v_scale: F32[heads] of an E4M3 cache."""
+    return KVCache(k, v, k_scale, v_scale)
+
+
+def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """q: [tokens, q_heads, head_dim], k, v: [tokens, kv_heads, head_dim] (2-byte
+    elements; slices of a fused projection will do); positions: int32[tokens]
+    and cos_sin: F32[max_pos, rot_dim] (both None: no rotation); slots:
+    int64[tokens]; q_out like q (q itself is computed in place);
+    interleaved: dims 2i and 2i + 1 form a pair, not i and i + rot_dim / 2."""
+    dev, d = cache.device, cache.head_dim
+    _on(dev)
+    kp, tokens, _, k_ld = _rows(k, cache.kv_heads, d, 2, dev, "k")
+    vp, vt, _, v_ld = _rows(v, cache.kv_heads, d, 2, dev, "v")
+    qp, qt, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
+    op, ot, _, o_ld = _rows(q_out, q_heads, d, 2, dev, "q_out")
+    if not (vt == qt == ot == tokens == slots.numel()):
+        raise ValueError("q, k, v, q_out and slots must have one row for each token")
+    for w in (q_weight, k_weight):
+        if w is not None and w.numel() != d:
+            raise ValueError("one weight for each element of a head")
+    rope = RopeC(0, 0, 0, 0, ROPE_PAIRS if interleaved else ROPE_HALVES, 0)
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions.numel() != tokens:
+            raise ValueError("cos_sin must be [max_pos, rot_dim], with a position for each token")
+        rope.cos_sin = _flat(cos_sin, 4, dev, "cos_sin")
+        rope.positions = _flat(positions, 4, dev, "positions")
+        rope.max_pos, rope.rot_dim = cos_sin.shape
+    qkv = QKVC(qp, kp, vp, q_ld, k_ld, v_ld, _flat(q_weight, 2, dev, "q_weight"), _flat(k_weight, 2, dev, "k_weight"),
+               tokens, q_heads, eps, 0)
+    _check(lib().xfer_qkv_rope_store(ctypes.byref(cache.c), ctypes.byref(qkv), ctypes.byref(rope),
+                                     _flat(slots, 8, dev, "slots"), op, o_ld, _stream(stream)), "xfer_qkv_rope_store")
+
+
+def qkv_rope_store_raw(cache: KVCacheC, qkv: QKVC, rope: RopeC, slots_ptr: int, q_out_ptr: int, q_out_ld: int,
+                       stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_qkv_rope_store(ctypes.byref(cache), ctypes.byref(qkv), ctypes.byref(rope), slots_ptr, q_out_ptr,
+                                     q_out_ld, _stream(stream))

@@ -1,0 +1,140 @@
+/*
+ * xfer_decode.h - the decode-step calls of libxfer, for AMD Instinct MI355X
+ * (gfx950): what a decode worker computes around the transfers of xfer.h.
+ *
+ *   xfer_qkv_rope_store  norms of queries and keys for each head, the
+ *                        position rotation, and the new keys and values
+ *                        written into a paged cache
+ *
+ * The caches are the ones that xfer_gather_runs, xfer_scatter_runs and
+ * xfer_paged_copy move.  All conventions of xfer.h hold (host checks first,
+ * hot calls only enqueue on `stream`, the caller owns every buffer, results
+ * are deterministic, pointers belong to the device current on the calling
+ * thread, empty work is XFER_OK with nothing enqueued) with one difference:
+ * these calls compute in binary32 (or wider where stated), so their results
+ * are rounded values of the formulas below, the same bits on every call with
+ * the same arguments and inputs.
+ */
+#ifndef XFER_DECODE_H
+#define XFER_DECODE_H
+
+#include "xfer.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* -------------------------------------------------------- the paged cache */
+
+/* How a cache holds its elements. */
+enum {
+  XFER_KV_BF16 = 0, /* BF16 bit patterns                                   */
+  XFER_KV_E4M3 = 1  /* 8-bit floats (4 exponent bits, 3 mantissa bits, no
+                       infinities, 448 the largest), each standing for its
+                       value times the head's scale                        */
+};
+
+/*
+ * A paged cache of keys and values.  Element d of head h of slot s of page p
+ * of the keys is at byte
+ *   k + p * page_stride + s * token_stride + h * head_stride + d * (element bytes)
+ * and the same of the values at v.  So pages may hold whole tokens
+ * ([slot][head][dim]) or one block per head ([head][slot][dim]), and keys
+ * and values may alternate in one buffer.
+ */
+typedef struct {
+  void *k, *v;             /* (device) 16-byte aligned                       */
+  const float *k_scale;    /* (device) F32[kv_heads]; NULL: all 1; XFER_KV_E4M3 only */
+  const float *v_scale;    /* the same for the values                        */
+  uint64_t page_stride;    /* bytes, multiples of 16                         */
+  uint64_t token_stride;
+  uint64_t head_stride;
+  uint32_t n_pages;
+  uint32_t page_tokens;    /* slots in a page: a power of two up to 65,536   */
+  uint32_t kv_heads;
+  uint32_t head_dim;       /* 64, 128 or 256                                 */
+  int32_t kind;            /* XFER_KV_*                                      */
+  uint32_t reserved;       /* 0                                              */
+} xfer_kv_cache;
+
+/*
+ * The checks that every call makes of a cache: XFER_E_INVAL for a NULL cache,
+ * NULL or misaligned k or v, a stride that is not a multiple of 16,
+ * n_pages, page_tokens or kv_heads 0, page_tokens not a power of two, an
+ * unknown kind, scales with XFER_KV_BF16, reserved not 0, or an extent that
+ * passes 2^47 bytes; XFER_E_UNSUPPORTED for another head_dim or page_tokens
+ * above 65,536.
+ */
+
+/* ------------------------------------ norms, rotation and the cache's rows */
+
+enum { XFER_ROPE_HALVES = 0, XFER_ROPE_PAIRS = 1 };
+
+/* The position rotation. */
+typedef struct {
+  const float *cos_sin;     /* (device) F32[max_pos][rot_dim]: row p holds the
+                               rot_dim / 2 cosines, then the sines, of position
+                               p; 16-byte aligned; may be NULL if rot_dim is 0 */
+  const int32_t *positions; /* (device) one per token; may be NULL if rot_dim is 0 */
+  uint32_t max_pos;
+  uint32_t rot_dim;         /* dims of a head that are rotated: a multiple of 8
+                               up to head_dim, 0 for none                    */
+  int32_t style;            /* XFER_ROPE_HALVES: dims i and i + rot_dim / 2
+                               form a pair; XFER_ROPE_PAIRS: 2i and 2i + 1   */
+  uint32_t reserved;        /* 0                                             */
+} xfer_rope;
+
+/* The projections of a batch of tokens: row t of q holds q_heads heads of
+ * head_dim BF16 elements one after the other, rows of k and v kv_heads.  The
+ * three may be slices of one buffer. */
+typedef struct {
+  const uint16_t *q, *k, *v;        /* (device) 16-byte aligned               */
+  uint64_t q_ld, k_ld, v_ld;        /* elements between rows, multiples of 8  */
+  const uint16_t *q_weight;         /* (device) BF16[head_dim], 16-byte aligned;
+                                       NULL: queries are not normalised       */
+  const uint16_t *k_weight;         /* the same for the keys                  */
+  uint32_t tokens;
+  uint32_t q_heads;                 /* any count, 0 for keys and values alone */
+  float eps;                        /* finite, >= 0                           */
+  uint32_t reserved;                /* 0                                      */
+} xfer_qkv;
+
+/*
+ * xfer_qkv_rope_store - for every token t and every head of q and k:
+ *   y_d  = x_d * 1 / sqrt(mean_d(x_d^2) + eps) * weight_d   (x_d if no weight)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)  for each pair (a, b)
+ * with the cosines and sines of the token's position.  The queries go to
+ * q_out (BF16, row t at q_out + t * q_out_ld, heads one after the other), the
+ * keys to slot slots[t] of the cache, and the values, unchanged, to the same
+ * slot.  Everything is computed in binary32 and rounded once, to nearest
+ * even: to BF16, or to E4M3 of (value / the head's scale) limited to +-448.
+ * NaN stays NaN.
+ *
+ *   slots  (device) int64[tokens]: page * page_tokens + slot.  A token whose
+ *          slot is negative, or not below n_pages * page_tokens, is not
+ *          stored (its queries are written all the same).  The slots that are
+ *          stored to must be distinct: which token's bytes remain in a slot
+ *          named twice is unspecified.
+ *   q_out  may be q itself with the same ld (computed in place); NULL is
+ *          allowed if q_heads is 0.
+ *
+ * A token whose position is not in [0, max_pos) gets NaN queries and is not
+ * stored.  No byte of the cache outside the named slots is written.
+ *
+ * Errors: those of the cache; XFER_E_OVERLAP if two slots of the cache share
+ * bytes or v == k; XFER_E_INVAL for NULL or misaligned pointers (k, v, q and
+ * q_out where there are heads; slots), lds that are not multiples of 8 or
+ * smaller than a row, a q_out row that overlaps a row of q, k or v (except in
+ * place) or the cache, an input overlapping the cache, eps negative or not
+ * finite, rot_dim not a multiple of 8 or above head_dim, a rotation with NULL
+ * or misaligned table, NULL positions or max_pos 0, an unknown style, or a
+ * reserved field that is not 0; XFER_E_UNSUPPORTED if the call needs more
+ * than 2^24 - 1 workgroups (about one for 16 heads of a token).
+ */
+XFER_API int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xfer_rope *rope,
+                                 const int64_t *slots, uint16_t *q_out, uint64_t q_out_ld, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* XFER_DECODE_H */

@@ -1,0 +1,40 @@
+"""The decode-step operators' formulas in 64 bits (numpy), one element or row
+at a time where that keeps them plain, and how far a binary32 computation
+with one rounding at its end may be from them."""
+import numpy as np
+
+# Half a step, relative to the value, of a rounding to nearest.
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24, "e4m3": 2.0 ** -4}
+E4M3_MAX = 448.0
+E4M3_TINY = 2.0 ** -10  # half the step below the smallest normal number
+
+
+def rope_heads(x, weight, eps, cos_sin, positions, rot_dim, interleaved):
+    """x: [tokens, heads, D] -> (y, mag): the normalised and rotated heads, and
+    for each element the sum of the two magnitudes its rotation adds up (of
+    an element that is not rotated, its own magnitude)."""
+    x = np.asarray(x, np.float64)
+    if weight is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    y, mag = x.copy(), np.abs(x)
+    half = rot_dim // 2
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        c = cos_sin[positions, i].astype(np.float64)[:, None]
+        s = cos_sin[positions, half + i].astype(np.float64)[:, None]
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., b] * c + x[..., a] * s
+        m = np.abs(x[..., a]) + np.abs(x[..., b])
+        mag[..., a] = mag[..., b] = m
+    return y, mag
+
+
+def rope_tolerance(y, mag, kind):
+    """The norm's sum takes at most 8 + 5 additions, each off by 2^-24, halved
+    by the square root; the reciprocal root 2^-23, two products 2^-23, the
+    rotation's two products and sum 3 * 2^-24 of each side: below 2^-20 of the
+    magnitudes together.  Then the one rounding of the result."""
+    err = 2.0 ** -20 * mag
+    if kind == "e4m3":
+        return err * (1 + HALF["e4m3"]) + np.maximum(HALF["e4m3"] * np.abs(y), E4M3_TINY)
+    return err * (1 + HALF[kind]) + HALF[kind] * np.abs(y)

@@ -1,0 +1,161 @@
+"""The decode-step calls on the CPU: the header's declarations against the
+library and the binding, struct layouts as a C compiler sees them, and every
+documented refusal.  No call here reaches a launch: each either fails a host
+check or is empty work."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+import bf16_wire_all_amd as x
+from bf16_wire_all_amd import decode
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+S0 = 0  # NULL stream: nothing here is enqueued
+K, V, Q, KN, VN, QO = (0x10_0000_0000 * (i + 1) for i in range(6))
+
+STRUCTS = {"xfer_kv_cache": decode.KVCacheC, "xfer_rope": decode.RopeC, "xfer_qkv": decode.QKVC}
+C_TYPES = {"int": ctypes.c_int, "uint32_t": ctypes.c_uint32, "uint64_t": ctypes.c_uint64, "size_t": ctypes.c_size_t,
+           "float": ctypes.c_float}
+
+
+def _declared():
+    src = open(os.path.join(ROOT, "include", "xfer_decode.h")).read()
+    return re.findall(r"XFER_API\s+(\w+)\s+(xfer_\w+)\s*\(([^)]*)\)\s*;", src, re.S)
+
+
+def test_every_declared_call_is_exported_with_the_binding_s_signature():
+    L = decode.lib()
+    decls = _declared()
+    assert sorted(d[1] for d in decls) == sorted(decode.EXPORTED)
+    pointers = {"xfer_shard": x.Shard, **STRUCTS}
+    for ret, name, params in decls:
+        fn = getattr(L, name)
+        assert fn.restype is C_TYPES[ret], name
+        params = [re.sub(r"\bconst\b", "", p).split() for p in " ".join(params.split()).split(",")]
+        assert len(fn.argtypes) == len(params), name
+        for p, py in zip(params, fn.argtypes):
+            if "*" in "".join(p):
+                base = p[0].rstrip("*")
+                assert py is ctypes.c_void_p or py is ctypes.POINTER(pointers[base]), (name, p, py)
+            elif p[0] == "hipStream_t":
+                assert py is ctypes.c_void_p
+            else:
+                assert py is C_TYPES[p[0]], (name, p, py)
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_struct_layouts_match_c(tmp_path):
+    lines = [f'printf("{n} . %zu\\n", sizeof({n}));' for n in STRUCTS]
+    lines += [f'printf("{n} {f[0]} %zu\\n", offsetof({n}, {f[0]}));' for n, s in STRUCTS.items() for f in s._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"xfer_decode.h\"\nint main(void) {\n"
+                   + "\n".join(lines) + "\nreturn 0;\n}\n")
+    exe = str(tmp_path / "layout")
+    inc = os.environ.get("ROCM_PATH", "/opt/rocm") + "/include"
+    r = subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I", inc, "-I",
+                        os.path.join(ROOT, "include"), str(src), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    for line in subprocess.run([exe], capture_output=True, text=True, timeout=60).stdout.splitlines():
+        name, field, value = line.split()
+        s = STRUCTS[name]
+        assert (ctypes.sizeof(s) if field == "." else getattr(s, field).offset) == int(value), line
+
+
+# ------------------------------------------------------------------ caches
+
+def cache(**kw):
+    c = decode.KVCacheC(K, V, None, None, 16 * 2 * 256, 2 * 256, 256, 100, 16, 2, 128, decode.KV_BF16, 0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+BAD_CACHES = [
+    (dict(k=0), x.E_INVAL), (dict(v=0), x.E_INVAL), (dict(k=K + 8), x.E_INVAL), (dict(v=V + 4), x.E_INVAL),
+    (dict(kind=2), x.E_INVAL), (dict(kind=-1), x.E_INVAL), (dict(page_stride=8200), x.E_INVAL),
+    (dict(token_stride=520), x.E_INVAL), (dict(head_stride=8), x.E_INVAL), (dict(n_pages=0), x.E_INVAL),
+    (dict(page_tokens=0), x.E_INVAL), (dict(page_tokens=12), x.E_INVAL), (dict(kv_heads=0), x.E_INVAL),
+    (dict(k_scale=64), x.E_INVAL), (dict(v_scale=64), x.E_INVAL), (dict(reserved=1), x.E_INVAL),
+    (dict(head_dim=96), x.E_UNSUPPORTED), (dict(head_dim=0), x.E_UNSUPPORTED),
+    (dict(page_tokens=1 << 17), x.E_UNSUPPORTED), (dict(page_stride=1 << 46), x.E_INVAL),
+    (dict(page_stride=(1 << 64) - 16), x.E_INVAL),
+]
+
+
+# -------------------------------------------------------------- rope store
+
+def qkv(**kw):
+    q = decode.QKVC(Q, KN, VN, 1024, 256, 256, 64, 64, 10, 8, 1e-6, 0)
+    for k, v in kw.items():
+        setattr(q, k, v)
+    return q
+
+
+def rope(**kw):
+    r = decode.RopeC(128, 64, 1000, 128, decode.ROPE_HALVES, 0)
+    for k, v in kw.items():
+        setattr(r, k, v)
+    return r
+
+
+def store(c=None, q=None, r=None, slots=64, out=QO, out_ld=1024):
+    return decode.qkv_rope_store_raw(c or cache(), q or qkv(), r or rope(), slots, out, out_ld, stream=S0)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_store_refuses_bad_caches(kw, status):
+    assert store(cache(**kw)) == status
+
+
+def test_store_refuses_overlapping_slots():
+    assert store(cache(head_stride=128)) == x.E_OVERLAP          # heads of 256 bytes, 128 apart
+    assert store(cache(token_stride=256)) == x.E_OVERLAP         # a token's second head is the next token's first
+    assert store(cache(page_stride=4096)) == x.E_OVERLAP
+    assert store(cache(page_stride=0)) == x.E_OVERLAP
+    assert store(cache(v=K)) == x.E_OVERLAP
+    # heads first, and keys and values in turn, are fine (empty work: nothing is enqueued)
+    empty = qkv(tokens=0)
+    assert store(cache(head_stride=4096, token_stride=256), empty) == x.OK
+    assert store(cache(page_stride=2 * 8192, v=K + 8192), empty) == x.OK
+    assert store(cache(n_pages=1, page_stride=0), empty) == x.OK  # one page: its stride is never walked
+
+
+@pytest.mark.parametrize("q,r,more,status", [
+    (dict(reserved=1), {}, {}, x.E_INVAL), ({}, dict(reserved=1), {}, x.E_INVAL), ({}, dict(style=2), {}, x.E_INVAL),
+    (dict(eps=-1e-6), {}, {}, x.E_INVAL), (dict(eps=float("nan")), {}, {}, x.E_INVAL),
+    (dict(eps=float("inf")), {}, {}, x.E_INVAL), ({}, dict(rot_dim=12), {}, x.E_INVAL),
+    ({}, dict(rot_dim=136), {}, x.E_INVAL), ({}, dict(cos_sin=0), {}, x.E_INVAL), ({}, dict(cos_sin=72), {}, x.E_INVAL),
+    ({}, dict(positions=0), {}, x.E_INVAL), ({}, dict(max_pos=0), {}, x.E_INVAL), ({}, {}, dict(slots=0), x.E_INVAL),
+    (dict(k=0), {}, {}, x.E_INVAL), (dict(v=0), {}, {}, x.E_INVAL), (dict(q=0), {}, {}, x.E_INVAL),
+    ({}, {}, dict(out=0), x.E_INVAL), (dict(k=KN + 2), {}, {}, x.E_INVAL), (dict(q=Q + 8), {}, {}, x.E_INVAL),
+    ({}, {}, dict(out=QO + 8), x.E_INVAL), (dict(q_weight=8), {}, {}, x.E_INVAL), (dict(k_weight=24), {}, {}, x.E_INVAL),
+    (dict(q_ld=1028), {}, {}, x.E_INVAL), (dict(k_ld=248), {}, {}, x.E_INVAL), (dict(v_ld=0), {}, {}, x.E_INVAL),
+    ({}, {}, dict(out_ld=1016), x.E_INVAL), (dict(q_ld=(1 << 64) - 8), {}, {}, x.E_INVAL),
+    ({}, {}, dict(out=KN), x.E_INVAL),                              # q_out over k
+    ({}, {}, dict(out=Q + 16), x.E_INVAL),                          # over q, not exactly in place
+    ({}, {}, dict(out=Q, out_ld=1032), x.E_INVAL),                  # in place needs the same ld
+    ({}, {}, dict(out=K + 4096), x.E_INVAL), ({}, {}, dict(out=V), x.E_INVAL),
+    (dict(k=K + 16), {}, {}, x.E_INVAL), (dict(q=V + 16), {}, {}, x.E_INVAL),
+    (dict(tokens=1 << 31, q=Q, q_ld=1024), {}, {}, x.E_INVAL),      # so many rows reach the next buffer
+    (dict(tokens=(1 << 24), q_heads=0, q=0), {}, dict(out=0), x.E_UNSUPPORTED),
+])
+def test_store_refusals(q, r, more, status):
+    assert store(q=qkv(**q), r=rope(**r), **more) == status
+
+
+def test_store_in_a_fused_buffer():
+    """q, k and v as slices of rows of 1536 elements; q_out may not touch k's slice."""
+    f = qkv(q=Q, k=Q + 2 * 1024, v=Q + 2 * 1280, q_ld=1536, k_ld=1536, v_ld=1536)
+    assert store(q=f, out=Q + 2 * 512, out_ld=1536) == x.E_INVAL
+    f.tokens = 0
+    assert store(q=f, out=Q, out_ld=1536) == x.OK
+
+
+def test_store_empty_work_needs_no_buffers():
+    e = decode.QKVC(0, 0, 0, 0, 0, 0, 0, 0, 0, 8, 1e-6, 0)
+    assert store(q=e, slots=0, out=0, out_ld=0) == x.OK
+    assert decode.lib().xfer_qkv_rope_store(None, None, None, None, None, 0, None) == x.E_INVAL
