@@ -28,4 +28,28 @@ struct RopeStoreArgs {
 uint64_t rope_store_workgroups(uint32_t tokens, uint32_t heads, uint32_t head_dim);
 hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStream_t stream);
 
+// ---- attention of one new token over a paged cache (attn_paged.hip)
+// How a call's work is cut up: rows of at most vis_max visible tokens in
+// n_splits pieces of chunk tokens, query heads of a kv head in m_groups tiles.
+struct AttnShape {
+  uint32_t chunk, n_splits, m_tiles, m_groups;
+  uint64_t workgroups;
+};
+AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint64_t vis_max);
+uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t q_heads, uint32_t head_dim);
+struct AttnArgs {
+  CacheView cache;
+  const uint32_t *page_table, *lens;
+  uint64_t table_ld;
+  uint32_t rows, max_len, window, sinks;
+  const uint16_t *q;
+  uint64_t q_ld, out_ld;
+  uint32_t q_heads, group;  // group = q_heads / kv_heads
+  float scale;
+  void *out;
+  int out_mode;
+  float *part_o, *part_ml;  // [rows][kv_heads][n_splits][group][head_dim], and (max, sum) of each
+};
+hipError_t launch_attn(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream);
+
 }  // namespace xfer

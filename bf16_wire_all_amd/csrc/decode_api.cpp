@@ -104,6 +104,18 @@ xfer::CacheView view_of(const xfer_kv_cache *c) {
   return v;
 }
 
+// The sizes of an attention call that the workspace follows from; on XFER_OK
+// fills *s and *vis_max.
+int attn_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, uint32_t q_heads, xfer::AttnShape *s) {
+  if (q_heads == 0 || q_heads % c->kv_heads) return XFER_E_INVAL;
+  if (b->sinks && !b->window) return XFER_E_INVAL;
+  if (b->max_len == 0 || b->max_len > 0x7FFFFFFFu) return XFER_E_INVAL;
+  uint64_t vis = b->max_len;
+  if (b->window) vis = std::min<uint64_t>(vis, (uint64_t)b->window + b->sinks);
+  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, vis);
+  return XFER_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -169,6 +181,70 @@ int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xf
   a.rot_dim = rope->rot_dim;
   a.eps = in->eps;
   if (xfer::launch_rope_store(a, cache->kind, rope->style, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
+size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch, uint32_t q_heads) {
+  uint64_t extent = 0;
+  xfer::AttnShape s{};
+  if (!batch || cache_checks(cache, &extent) != XFER_OK || attn_sizes(cache, batch, q_heads, &s) != XFER_OK) return 0;
+  return (size_t)xfer::attn_workspace_bytes(s, batch->rows, q_heads, cache->head_dim);
+}
+
+int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q, uint64_t q_ld,
+                    uint32_t q_heads, float scale, void *out, uint64_t out_ld, int out_mode, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  uint64_t extent = 0;
+  int st = cache_checks(cache, &extent);
+  if (st != XFER_OK) return st;
+  if (!batch || (out_mode != XFER_OUT_F32 && out_mode != XFER_OUT_BF16)) return XFER_E_INVAL;
+  if (!std::isfinite(scale)) return XFER_E_INVAL;
+  xfer::AttnShape s{};
+  if ((st = attn_sizes(cache, batch, q_heads, &s)) != XFER_OK) return st;
+  if (batch->rows == 0) return XFER_OK;
+  const uint64_t R = batch->rows, row = (uint64_t)q_heads * cache->head_dim;
+  const uint64_t pages = ((uint64_t)batch->max_len + cache->page_tokens - 1) / cache->page_tokens;
+  if (!batch->page_table || !batch->lens || (uintptr_t)batch->page_table % 4 || (uintptr_t)batch->lens % 4)
+    return XFER_E_INVAL;
+  if (R > 1 && (batch->table_ld < pages || batch->table_ld > kMaxExtent / 4 || R - 1 > kMaxExtent / 4 / batch->table_ld))
+    return XFER_E_INVAL;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !ld_ok(q_ld, R, row) || !ld_ok(out_ld, R, row))
+    return XFER_E_INVAL;
+  const uint64_t need = xfer::attn_workspace_bytes(s, batch->rows, q_heads, cache->head_dim);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return XFER_E_INVAL;
+
+  const uint64_t ob = out_mode == XFER_OUT_F32 ? 4 : 2;
+  const Rows o{(uintptr_t)out, out_ld * ob, row * ob, R};
+  const Rows ins[3] = {{(uintptr_t)q, q_ld * 2, row * 2, R},
+                       {(uintptr_t)batch->page_table, batch->table_ld * 4, pages * 4, R},
+                       {(uintptr_t)batch->lens, 4, 4, R}};
+  const uintptr_t w = (uintptr_t)workspace, caches[2] = {(uintptr_t)cache->k, (uintptr_t)cache->v};
+  for (const Rows &r : ins)
+    if (rows_touch(o, r) || overlaps(w, need, r.at, r.extent())) return XFER_E_INVAL;
+  for (uintptr_t c : caches)
+    if (overlaps(c, extent, o.at, o.extent()) || overlaps(c, extent, w, need)) return XFER_E_INVAL;
+  if (overlaps(w, need, o.at, o.extent())) return XFER_E_INVAL;
+  if (s.workgroups > xfer::kMaxGridBlocks || R * q_heads > xfer::kMaxGridBlocks) return XFER_E_UNSUPPORTED;
+
+  xfer::AttnArgs a{};
+  a.cache = view_of(cache);
+  a.page_table = batch->page_table;
+  a.lens = batch->lens;
+  a.table_ld = batch->table_ld;
+  a.rows = batch->rows;
+  a.max_len = batch->max_len;
+  a.window = batch->window;
+  a.sinks = batch->sinks;
+  a.q = q;
+  a.q_ld = q_ld;
+  a.out_ld = out_ld;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->kv_heads;
+  a.scale = scale;
+  a.out = out;
+  a.out_mode = out_mode;
+  a.part_ml = static_cast<float *>(workspace);
+  if (xfer::launch_attn(a, cache->kind, s, stream) != hipSuccess) return XFER_E_DEVICE;
   return XFER_OK;
 }
 

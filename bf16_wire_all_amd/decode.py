@@ -9,12 +9,12 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _stream, lib as _base_lib
+from . import OUT_BF16, OUT_F32, _check, _stream, lib as _base_lib
 
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
-EXPORTED = ["xfer_qkv_rope_store"]
+EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged"]
 
 
 class KVCacheC(ctypes.Structure):
@@ -37,6 +37,12 @@ class QKVC(ctypes.Structure):
                 ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)]
 
 
+class PagedBatchC(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table_ld", ctypes.c_uint64),
+                ("rows", ctypes.c_uint32), ("max_len", ctypes.c_uint32), ("window", ctypes.c_uint32),
+                ("sinks", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -45,10 +51,16 @@ def lib():
     global _lib
     if _lib is None:
         L = _base_lib()
-        P, U64, I = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int
+        P, S, U32, U64, I, F = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int,
+                                ctypes.c_float)
         L.xfer_qkv_rope_store.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(QKVC), ctypes.POINTER(RopeC), P, P,
                                           U64, P]
         L.xfer_qkv_rope_store.restype = I
+        L.xfer_attn_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), U32]
+        L.xfer_attn_workspace_bytes.restype = S
+        L.xfer_attn_paged.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, U64, U32, F, P, U64, I,
+                                      P, S, P]
+        L.xfer_attn_paged.restype = I
         _lib = L
     return _lib
 
@@ -147,3 +159,49 @@ def qkv_rope_store_raw(cache: KVCacheC, qkv: QKVC, rope: RopeC, slots_ptr: int, 
     """Raw-pointer form; returns the status without raising."""
     return lib().xfer_qkv_rope_store(ctypes.byref(cache), ctypes.byref(qkv), ctypes.byref(rope), slots_ptr, q_out_ptr,
                                      q_out_ld, _stream(stream))
+
+
+# ------------------------------------------------- attention of one new token
+
+def attn_workspace_bytes(cache: KVCache, rows: int, q_heads: int, max_len: int, window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace that attn_paged needs for these sizes."""
+    batch = PagedBatchC(0, 0, 0, rows, max_len, window, sinks)
+    return int(lib().xfer_attn_workspace_bytes(ctypes.byref(cache.c), ctypes.byref(batch), q_heads))
+
+
+def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
+               sinks: int = 0, stream=None) -> None:
+    """q: [rows, q_heads, head_dim] (2-byte elements); page_table: int32 or uint32
+    [rows, at least ceil(max_len / page_tokens)], dense within a row; lens:
+    int32 or uint32 [rows]; out: like q, BF16 (2-byte) or F32; workspace: a
+    CUDA tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
+    dev, d = cache.device, cache.head_dim
+    _on(dev)
+    qp, rows, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
+    size = out.element_size()
+    if size not in (2, 4):
+        raise ValueError("out must have 2-byte (BF16) or 4-byte (F32) elements")
+    op, o_rows, _, o_ld = _rows(out, q_heads, d, size, dev, "out")
+    if o_rows != rows or lens.numel() != rows or page_table.dim() != 2 or page_table.shape[0] != rows:
+        raise ValueError("q, page_table, lens and out must have the same rows")
+    width, ts = page_table.shape[1], page_table.stride()
+    if page_table.device != dev or page_table.element_size() != 4 or (width > 1 and ts[1] != 1):
+        raise ValueError("page_table: expected 4-byte page numbers, dense within a row")
+    if width * cache.page_tokens < max_len:
+        raise ValueError("page_table is too narrow for max_len")
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _flat(workspace, workspace.element_size(), dev, "workspace")
+    batch = PagedBatchC(page_table.data_ptr(), _flat(lens, 4, dev, "lens"), ts[0] if rows > 1 else width, rows,
+                        max_len, window, sinks)
+    _check(lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
+                                 OUT_F32 if size == 4 else OUT_BF16, ws, ws_bytes, _stream(stream)),
+           "xfer_attn_paged")
+
+
+def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q_heads: int, scale: float,
+                   out_ptr: int, out_ld: int, out_mode: int, ws_ptr: int, ws_bytes: int, stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_attn_paged(ctypes.byref(cache), ctypes.byref(batch), q_ptr, q_ld, q_heads, scale, out_ptr,
+                                 out_ld, out_mode, ws_ptr, ws_bytes, _stream(stream))

@@ -5,6 +5,9 @@
  *   xfer_qkv_rope_store  norms of queries and keys for each head, the
  *                        position rotation, and the new keys and values
  *                        written into a paged cache
+ *   xfer_attn_paged      attention of one new token of every request over
+ *                        such a cache, the whole of it or a window and the
+ *                        first tokens
  *
  * The caches are the ones that xfer_gather_runs, xfer_scatter_runs and
  * xfer_paged_copy move.  All conventions of xfer.h hold (host checks first,
@@ -133,6 +136,75 @@ typedef struct {
  */
 XFER_API int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xfer_rope *rope,
                                  const int64_t *slots, uint16_t *q_out, uint64_t q_out_ld, hipStream_t stream);
+
+/* ------------------------------------------- attention of one new token */
+
+/*
+ * The requests of a batch: row r's token j (its position in the request,
+ * from 0) lies in slot j mod page_tokens of page
+ * page_table[r * table_ld + j / page_tokens].
+ */
+typedef struct {
+  const uint32_t *page_table; /* (device) rows of at least
+                                 ceil(max_len / page_tokens) page numbers     */
+  const uint32_t *lens;       /* (device) tokens in the cache of each row, the
+                                 new one among them; above max_len: max_len   */
+  uint64_t table_ld;          /* page numbers between rows                    */
+  uint32_t rows;
+  uint32_t max_len;           /* the longest row (an upper bound will do, but
+                                 the work is cut up for rows of this length)  */
+  uint32_t window;            /* 0: every token is visible; else the last
+                                 `window` tokens and the first `sinks`        */
+  uint32_t sinks;             /* 0 if window is 0                             */
+} xfer_paged_batch;
+
+/*
+ * xfer_attn_paged - for every row r and query head h, with kv head
+ * g = h / (q_heads / kv_heads) and the row's visible tokens j:
+ *   s_j = scale * q[r][h] . k_j        (k_j times k_scale[g] if there is one)
+ *   out[r][h] = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s)
+ *                                      (v_j times v_scale[g])
+ * A row with no visible token (length 0, or holes alone) gets zeros.  A page
+ * number that is not below n_pages is a hole: its tokens are not visible and
+ * nothing is read for them.  What pages hold past a row's length, and tokens
+ * outside the window, has no influence, NaN and infinities included.
+ *
+ * Several new tokens of one request are rows of their own, with the same
+ * page numbers and increasing lengths.
+ *
+ * Scores, maxima, sums and the weighted sum are held in binary32; a weight
+ * is split into two BF16 numbers for the product with v, which keeps it to
+ * 2^-18 of itself.  The result is rounded once, to nearest even, for
+ * XFER_OUT_BF16.
+ *
+ *   q         (device) BF16 bit patterns, row r at q + r * q_ld, q_heads
+ *             heads of head_dim one after the other; 16-byte aligned, q_ld a
+ *             multiple of 8.
+ *   out       (device) the same of BF16 or F32 (out_mode XFER_OUT_*), rows
+ *             out_ld elements apart (a multiple of 8).
+ *   workspace (device) at least xfer_attn_workspace_bytes() bytes, 16-byte
+ *             aligned, any contents: the partial results of rows that are cut
+ *             up.  May be NULL if that is 0.  Calls that may run concurrently
+ *             must use different workspaces.
+ *
+ * Errors: those of the cache; XFER_E_INVAL for NULL or misaligned pointers
+ * (page_table and lens 4 bytes), q_heads not a positive multiple of kv_heads,
+ * a scale that is not finite, sinks without a window, max_len 0 or above
+ * 2^31 - 1, a table_ld below ceil(max_len / page_tokens) (rows > 1), lds that
+ * are not multiples of 8 or smaller than a row, an unknown out_mode, a small
+ * workspace, or an output or workspace that overlaps q, the cache, the table,
+ * the lengths or one another; XFER_E_UNSUPPORTED for more than 2^24 - 1
+ * workgroups.
+ *
+ * xfer_attn_workspace_bytes - the bytes that such a call needs (0 also for a
+ * batch or cache that xfer_attn_paged refuses).  They depend on the sizes
+ * alone, not on pointers.
+ */
+XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch,
+                                          uint32_t q_heads);
+XFER_API int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q,
+                             uint64_t q_ld, uint32_t q_heads, float scale, void *out, uint64_t out_ld, int out_mode,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -38,3 +38,38 @@ def rope_tolerance(y, mag, kind):
     if kind == "e4m3":
         return err * (1 + HALF["e4m3"]) + np.maximum(HALF["e4m3"] * np.abs(y), E4M3_TINY)
     return err * (1 + HALF[kind]) + HALF[kind] * np.abs(y)
+
+
+def visible(n, window, sinks):
+    """Positions of the tokens that a row of n tokens sees."""
+    j = np.arange(n)
+    return j if window == 0 else j[(j >= n - window) | (j < sinks)]
+
+
+def attention(q, k, v, scale):
+    """One row: q [heads, D], k, v [tokens, kv heads, D] in the values they
+    stand for -> (out, tolerance before the last rounding).
+
+    The products of BF16 (or E4M3) numbers are exact in binary32; their sum of
+    D terms is off by at most 2 * D * 2^-24 of the magnitudes (twice what plain
+    additions may lose, for the matrix cores' own order), the scale and the
+    logarithm's base by 2^-22 of the score.  A weight is off by that, by
+    2^-18 of its split and 2^-21 of the power; numerator and denominator each
+    carry it; every addition of the sums adds 2^-24."""
+    heads, d = q.shape
+    n, kv, _ = k.shape
+    out, tol = np.zeros((heads, d)), np.zeros((heads, d))
+    if n == 0:
+        return out, tol
+    group = heads // kv
+    for h in range(heads):
+        kh, vh = k[:, h // group], v[:, h // group]
+        s = kh @ q[h] * scale
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        out[h] = w @ vh
+        delta = 2 * d * 2.0 ** -24 * (np.abs(kh) @ np.abs(q[h])) * scale + 2.0 ** -22 * np.abs(s)
+        # an error of the largest score moves every weight alike
+        weight = delta + delta[s.argmax()] + 2.0 ** -18 + 2.0 ** -21 + (n + 64) * 2.0 ** -24
+        tol[h] = 2 * ((w * weight) @ np.abs(vh)) + (w @ weight) * np.abs(out[h])
+    return out, tol

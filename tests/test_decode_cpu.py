@@ -17,7 +17,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 S0 = 0  # NULL stream: nothing here is enqueued
 K, V, Q, KN, VN, QO = (0x10_0000_0000 * (i + 1) for i in range(6))
 
-STRUCTS = {"xfer_kv_cache": decode.KVCacheC, "xfer_rope": decode.RopeC, "xfer_qkv": decode.QKVC}
+STRUCTS = {"xfer_kv_cache": decode.KVCacheC, "xfer_rope": decode.RopeC, "xfer_qkv": decode.QKVC,
+           "xfer_paged_batch": decode.PagedBatchC}
 C_TYPES = {"int": ctypes.c_int, "uint32_t": ctypes.c_uint32, "uint64_t": ctypes.c_uint64, "size_t": ctypes.c_size_t,
            "float": ctypes.c_float}
 
@@ -159,3 +160,67 @@ def test_store_empty_work_needs_no_buffers():
     e = decode.QKVC(0, 0, 0, 0, 0, 0, 0, 0, 0, 8, 1e-6, 0)
     assert store(q=e, slots=0, out=0, out_ld=0) == x.OK
     assert decode.lib().xfer_qkv_rope_store(None, None, None, None, None, 0, None) == x.E_INVAL
+
+
+# --------------------------------------------------------------- attention
+
+TABLE, LENS, WS = 0x40_0000, 0x80_0000, 0xC0_0000
+
+
+def batch(**kw):
+    b = decode.PagedBatchC(TABLE, LENS, 64, 3, 1000, 0, 0)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return b
+
+
+def attn(c=None, b=None, q=Q, q_ld=1024, heads=8, scale=0.1, out=QO, out_ld=1024, mode=x.OUT_BF16, ws=WS, ws_bytes=1 << 20):
+    return decode.attn_paged_raw(c or cache(), b or batch(), q, q_ld, heads, scale, out, out_ld, mode, ws, ws_bytes,
+                                 stream=S0)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_attn_refuses_bad_caches(kw, status):
+    assert attn(cache(**kw)) == status
+
+
+def _need(c, b, heads):
+    return decode.lib().xfer_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(b), heads)
+
+
+@pytest.mark.parametrize("b,more", [
+    (dict(page_table=0), {}), (dict(page_table=TABLE + 2), {}), (dict(lens=0), {}), (dict(lens=LENS + 1), {}),
+    (dict(max_len=0), {}), (dict(max_len=1 << 31), {}), (dict(sinks=4), {}), (dict(table_ld=62), {}),
+    (dict(table_ld=1 << 62), {}), ({}, dict(q=0)), ({}, dict(q=Q + 8)), ({}, dict(out=0)), ({}, dict(out=QO + 4)),
+    ({}, dict(q_ld=1016)), ({}, dict(q_ld=1025)), ({}, dict(out_ld=1020)), ({}, dict(out_ld=1 << 63)),
+    ({}, dict(heads=0)), ({}, dict(heads=7)), ({}, dict(mode=2)), ({}, dict(scale=float("nan"))),
+    ({}, dict(scale=float("inf"))), ({}, dict(ws=0)), ({}, dict(ws=WS + 4)), ({}, dict(ws_bytes=100)),
+    ({}, dict(out=Q)), ({}, dict(out=Q + 2048)), ({}, dict(out=K + 64)), ({}, dict(out=V)), ({}, dict(out=TABLE + 64)),
+    ({}, dict(out=LENS)), ({}, dict(out=WS)), ({}, dict(ws=Q)), ({}, dict(ws=K)), ({}, dict(ws=TABLE)),
+    ({}, dict(ws=LENS)), ({}, dict(ws=QO, mode=x.OUT_F32)),
+])
+def test_attn_refusals(b, more):
+    assert attn(b=batch(**b), **more) == x.E_INVAL
+
+
+def test_attn_launch_size_limit():
+    b = batch(rows=1 << 24, max_len=16, table_ld=1)
+    far = 1 << 44
+    b.page_table, b.lens = 3 * far, 4 * far
+    assert attn(b=b, q=far, out=2 * far, ws=0, ws_bytes=0, heads=2, q_ld=256, out_ld=256) == x.E_UNSUPPORTED
+
+
+def test_attn_empty_work_and_workspace_sizes():
+    assert attn(b=batch(rows=0, page_table=0, lens=0), q=0, out=0, ws=0, ws_bytes=0) == x.OK
+    c = cache()
+    assert _need(c, batch(rows=0), 8) == 0
+    assert _need(c, batch(max_len=128), 8) == 0                    # one piece: nothing to join
+    assert _need(c, batch(max_len=100000, window=100, sinks=4), 8) == 0
+    assert _need(c, batch(max_len=100000), 8) > 0
+    assert _need(c, batch(max_len=100000), 7) == 0                 # refused sizes
+    assert _need(cache(head_dim=80), batch(max_len=100000), 8) == 0
+    # a piece's partial results are far smaller than the keys and values it reads
+    for rows in (1, 7, 64, 500):
+        for n in (300, 5000, 131071, 1 << 20):
+            need = _need(c, batch(rows=rows, max_len=n, table_ld=1 << 17), 8)
+            assert need <= max(1 << 20, rows * n * 2 * 2 * 128 * 2 // 16), (rows, n, need)
