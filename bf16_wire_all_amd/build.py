@@ -11,7 +11,7 @@ LIB = os.path.join(HERE, "libxfer.so")
 
 SOURCES = ["api.cpp", "stream_pipeline.cpp", "groups.cpp", "pack_combine.hip", "argmax.hip", "runs_copy.hip",
            "descs_copy.hip", "pages.cpp", "pages_copy.hip", "decode_api.cpp", "rope_store.hip",
-           "attn_paged.hip"]
+           "attn_paged.hip", "sample.hip"]
 
 # -packed-fp32-ops: never emit packed F32 instructions (the host pass warns
 # that it does not know the feature; harmless).  No fast-math and no denormal

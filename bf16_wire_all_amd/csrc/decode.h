@@ -52,4 +52,18 @@ struct AttnArgs {
 };
 hipError_t launch_attn(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream);
 
+// ---- sampling (sample.hip)
+// Workgroups of the widest launch for each row, and the workspace.
+uint32_t sample_slices(uint32_t ncols0, uint32_t ncols1);
+uint64_t sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1);
+struct SampleArgs {
+  ArgmaxShard s[2];
+  uint32_t rows;
+  const xfer_sample_params *params;
+  const float *u;
+  xfer_sampled *out;
+  void *workspace;
+};
+hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
+
 }  // namespace xfer

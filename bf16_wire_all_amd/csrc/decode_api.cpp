@@ -248,4 +248,48 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   return XFER_OK;
 }
 
+size_t xfer_sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
+  if (!ncols0 || !ncols1 || ncols0 > xfer::kArgmaxMaxShardCols || ncols1 > xfer::kArgmaxMaxShardCols) return 0;
+  return (size_t)xfer::sample_workspace_bytes(rows, ncols0, ncols1);
+}
+
+int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sample_params *params, const float *u,
+                      void *out, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!s0 || !s1 || s0->rows != s1->rows) return XFER_E_INVAL;
+  const uint64_t R = s0->rows;
+  if (R == 0) return XFER_OK;
+  const xfer_shard *s[2] = {s0, s1};
+  for (const xfer_shard *x : s)
+    if (x->ncols == 0 || (uint64_t)x->col_offset + x->ncols > (1ull << 31)) return XFER_E_INVAL;
+  if (s0->col_offset < s1->col_offset + (uint64_t)s1->ncols && s1->col_offset < s0->col_offset + (uint64_t)s0->ncols)
+    return XFER_E_INVAL;
+  for (const xfer_shard *x : s)
+    if (x->ncols > xfer::kArgmaxMaxShardCols) return XFER_E_UNSUPPORTED;
+  if (R * xfer::sample_slices(s0->ncols, s1->ncols) > xfer::kMaxGridBlocks) return XFER_E_UNSUPPORTED;
+  for (const xfer_shard *x : s)
+    if (!x->ptr || !aligned16(x->ptr) || !ld_ok(x->ld, R, x->ncols)) return XFER_E_INVAL;
+  if (!params || !aligned16(params) || !u || (uintptr_t)u % 4 || !out || !aligned16(out)) return XFER_E_INVAL;
+  const uint64_t need = xfer::sample_workspace_bytes((uint32_t)R, s0->ncols, s1->ncols);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return XFER_E_INVAL;
+  const uintptr_t o = (uintptr_t)out, w = (uintptr_t)workspace;
+  const uint64_t out_bytes = R * sizeof(xfer_sampled);
+  const Rows ins[4] = {{(uintptr_t)s0->ptr, s0->ld * 2, (uint64_t)s0->ncols * 2, R},
+                       {(uintptr_t)s1->ptr, s1->ld * 2, (uint64_t)s1->ncols * 2, R},
+                       {(uintptr_t)params, sizeof(xfer_sample_params), sizeof(xfer_sample_params), R},
+                       {(uintptr_t)u, 4, 4, R}};
+  for (const Rows &r : ins)
+    if (overlaps(o, out_bytes, r.at, r.extent()) || overlaps(w, need, r.at, r.extent())) return XFER_E_INVAL;
+  if (overlaps(o, out_bytes, w, need)) return XFER_E_INVAL;
+
+  xfer::SampleArgs a{};
+  for (int i = 0; i < 2; ++i) a.s[i] = xfer::ArgmaxShard{s[i]->ptr, s[i]->ld, s[i]->ncols, s[i]->col_offset};
+  a.rows = (uint32_t)R;
+  a.params = params;
+  a.u = u;
+  a.out = static_cast<xfer_sampled *>(out);
+  a.workspace = workspace;
+  if (xfer::launch_sample(a, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
 }  // extern "C"

@@ -9,12 +9,18 @@ from __future__ import annotations
 
 import ctypes
 
-from . import OUT_BF16, OUT_F32, _check, _stream, lib as _base_lib
+import numpy as np
+
+from . import OUT_BF16, OUT_F32, Shard, _check, _stream, lib as _base_lib
 
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
-EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged"]
+EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged", "xfer_sample_workspace_bytes",
+            "xfer_sample_merge"]
+
+SAMPLE_PARAMS = np.dtype([("temperature", "<f4"), ("top_k", "<u4"), ("top_p", "<f4"), ("min_p", "<f4")])
+SAMPLED = np.dtype([("prob", "<f4"), ("idx", "<i4")])
 
 
 class KVCacheC(ctypes.Structure):
@@ -61,6 +67,10 @@ def lib():
         L.xfer_attn_paged.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, U64, U32, F, P, U64, I,
                                       P, S, P]
         L.xfer_attn_paged.restype = I
+        L.xfer_sample_workspace_bytes.argtypes = [U32, U32, U32]
+        L.xfer_sample_workspace_bytes.restype = S
+        L.xfer_sample_merge.argtypes = [ctypes.POINTER(Shard), ctypes.POINTER(Shard), P, P, P, P, S, P]
+        L.xfer_sample_merge.restype = I
         _lib = L
     return _lib
 
@@ -205,3 +215,46 @@ def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q
     """Raw-pointer form; returns the status without raising."""
     return lib().xfer_attn_paged(ctypes.byref(cache), ctypes.byref(batch), q_ptr, q_ld, q_heads, scale, out_ptr,
                                  out_ld, out_mode, ws_ptr, ws_bytes, _stream(stream))
+
+
+# ------------------------------------------------------------------ sampling
+
+def shard(logits, ncols: int, col_offset: int) -> Shard:
+    """A column shard of BF16 logits: a CUDA tensor [rows, at least ncols] whose
+    rows are dense; the shard keeps it alive."""
+    rows, width = logits.shape
+    ts = logits.stride()
+    if not logits.is_cuda or logits.element_size() != 2 or width < ncols or (width > 1 and ts[1] != 1):
+        raise ValueError("expected a CUDA tensor of 2-byte elements, dense within a row and ncols wide")
+    s = Shard(logits.data_ptr(), ts[0] if rows > 1 else width, rows, ncols, col_offset)
+    s.tensor = logits
+    return s
+
+
+def sample_workspace_bytes(rows: int, ncols0: int, ncols1: int) -> int:
+    return int(lib().xfer_sample_workspace_bytes(rows, ncols0, ncols1))
+
+
+def sample_merge(s0: Shard, s1: Shard, params, u, out, workspace, stream=None) -> None:
+    """params: CUDA tensor of rows * 16 bytes (SAMPLE_PARAMS records); u: F32[rows]
+    in [0, 1); out: CUDA tensor of rows * 8 bytes (SAMPLED records); workspace:
+    at least sample_workspace_bytes() bytes, any contents."""
+    dev, rows = u.device, s0.rows
+    _on(dev)
+    if params.numel() * params.element_size() != rows * SAMPLE_PARAMS.itemsize or u.numel() != rows:
+        raise ValueError("params and u must have one record for each row")
+    if out.numel() * out.element_size() != rows * SAMPLED.itemsize:
+        raise ValueError("out must have 8 bytes for each row")
+    _check(lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1),
+                                   _flat(params, params.element_size(), dev, "params"), _flat(u, 4, dev, "u"),
+                                   _flat(out, out.element_size(), dev, "out"),
+                                   _flat(workspace, workspace.element_size(), dev, "workspace"),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+           "xfer_sample_merge")
+
+
+def sample_merge_raw(s0: Shard, s1: Shard, params_ptr: int, u_ptr: int, out_ptr: int, ws_ptr: int, ws_bytes: int,
+                     stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1), params_ptr, u_ptr, out_ptr, ws_ptr, ws_bytes,
+                                   _stream(stream))

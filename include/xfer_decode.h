@@ -8,6 +8,9 @@
  *   xfer_attn_paged      attention of one new token of every request over
  *                        such a cache, the whole of it or a window and the
  *                        first tokens
+ *   xfer_sample_merge    sampling with temperature, top-k, top-p and min-p
+ *                        from logits in two column shards, beside
+ *                        xfer_argmax_merge
  *
  * The caches are the ones that xfer_gather_runs, xfer_scatter_runs and
  * xfer_paged_copy move.  All conventions of xfer.h hold (host checks first,
@@ -205,6 +208,63 @@ XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer
 XFER_API int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q,
                              uint64_t q_ld, uint32_t q_heads, float scale, void *out, uint64_t out_ld, int out_mode,
                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* --------------------------------------------------------------- sampling */
+
+/* One row's settings. */
+typedef struct {
+  float temperature; /* logits are divided by it; not above 0, or NaN: the
+                        first element of the row's order is taken (greedy)    */
+  uint32_t top_k;    /* keep the first top_k elements; 0: all                 */
+  float top_p;       /* keep the shortest prefix of those whose weights sum to
+                        top_p of theirs, one element at least; 1 or more, or
+                        NaN: all                                              */
+  float min_p;       /* of those, keep elements whose weight is at least min_p
+                        times the largest; above 1 counts as 1; NaN: all      */
+} xfer_sample_params; /* 16 bytes */
+
+typedef struct {
+  float prob;  /* the taken element's probability among the kept ones */
+  int32_t idx; /* its global id, -1 if the row has nothing to take    */
+} xfer_sampled; /* 8 bytes */
+
+/*
+ * xfer_sample_merge - one element of every row of a block of logit rows split
+ * by columns between two ranks (the shards of xfer_argmax_merge), drawn by a
+ * given number u in [0, 1).
+ *
+ * Row order: as xfer_argmax_merge, larger value first (numeric, -0 == +0),
+ * then the lower global id.  With l_i in that order and T the temperature,
+ * w_i = exp((l_i - l_0) / T) (an element equal to l_0 has weight 1, infinite
+ * ones included).  Elements that are -inf (masked) or NaN are never taken and
+ * count nowhere.  top_k, then top_p, then min_p each keep a prefix of the
+ * order.  With Z the kept weights' sum, the taken element is the first whose
+ * running sum of weights exceeds u * Z (the last kept one if rounding leaves
+ * none; u below 0 or NaN counts as 0), and prob = w / Z.  Greedy rows keep
+ * one element, so prob is 1.
+ *
+ * Weights and their sums are computed in binary64.  A BF16 logit has at most
+ * 65,536 values, so a row is counted by value and equal logits share one
+ * exponential.
+ *
+ *   params     (device) xfer_sample_params[rows], 16-byte aligned.
+ *   u          (device) F32[rows].
+ *   out        (device) xfer_sampled[rows], 16-byte aligned.
+ *   workspace  (device) at least xfer_sample_workspace_bytes(rows, s0->ncols,
+ *              s1->ncols) bytes, 16-byte aligned, any contents.  Calls that
+ *              may run concurrently must use different workspaces.
+ *
+ * Errors: XFER_E_INVAL for NULL or misaligned pointers (ptr and ld * 2 must
+ * be multiples of 16, u of 4), different row counts, ncols == 0, shards whose
+ * id ranges overlap, col_offset + ncols > 2^31, a small workspace, or an
+ * output or workspace overlapping an input or one another;
+ * XFER_E_UNSUPPORTED for a shard wider than 2,097,152 columns or more than
+ * 2^24 - 1 workgroups (one for a row and 32,768 columns).
+ */
+XFER_API size_t xfer_sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1);
+XFER_API int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sample_params *params,
+                               const float *u, void *out, void *workspace, size_t workspace_bytes,
+                               hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -73,3 +73,31 @@ def attention(q, k, v, scale):
         weight = delta + delta[s.argmax()] + 2.0 ** -18 + 2.0 ** -21 + (n + 64) * 2.0 ** -24
         tol[h] = 2 * ((w * weight) @ np.abs(vh)) + (w @ weight) * np.abs(out[h])
     return out, tol
+
+
+def sample(values, ids, temperature, top_k, top_p, min_p, u):
+    """One row: values (float64, in any order) with their ids -> (id, probability, margin), margin
+    being how near u * Z comes to a border of the drawn element, relative to Z."""
+    order = np.lexsort((ids, -values))
+    order = order[values[order] > -np.inf]                 # NaN compares false
+    if order.size == 0:
+        return -1, 0.0, 1.0
+    x = values[order]
+    greedy = not temperature > 0
+    with np.errstate(invalid="ignore", over="ignore"):
+        w = np.exp((x - x[0]) / (1.0 if greedy else temperature))
+    w[x == x[0]] = 1.0
+    if np.isinf(x[0]):
+        w[x != x[0]] = 0.0
+    n = 1 if greedy else x.size if top_k == 0 else min(top_k, x.size)
+    w = w[:n]
+    if top_p < 1:
+        sums = np.cumsum(w)
+        w = w[:max(1, int(np.searchsorted(sums, top_p * sums[-1], side="left")) + 1)]
+    if min_p == min_p:
+        w = w[w >= min(min_p, 1.0)]
+    sums = np.cumsum(w)
+    target = (u if u > 0 else 0.0) * sums[-1]
+    at = min(int(np.searchsorted(sums, target, side="right")), w.size - 1)
+    margin = np.min(np.abs(sums - target)) / sums[-1]
+    return int(ids[order[at]]), float(w[at] / sums[-1]), float(margin)

@@ -19,6 +19,7 @@ K, V, Q, KN, VN, QO = (0x10_0000_0000 * (i + 1) for i in range(6))
 
 STRUCTS = {"xfer_kv_cache": decode.KVCacheC, "xfer_rope": decode.RopeC, "xfer_qkv": decode.QKVC,
            "xfer_paged_batch": decode.PagedBatchC}
+RECORDS = {"xfer_sample_params": decode.SAMPLE_PARAMS, "xfer_sampled": decode.SAMPLED}
 C_TYPES = {"int": ctypes.c_int, "uint32_t": ctypes.c_uint32, "uint64_t": ctypes.c_uint64, "size_t": ctypes.c_size_t,
            "float": ctypes.c_float}
 
@@ -41,7 +42,7 @@ def test_every_declared_call_is_exported_with_the_binding_s_signature():
         for p, py in zip(params, fn.argtypes):
             if "*" in "".join(p):
                 base = p[0].rstrip("*")
-                assert py is ctypes.c_void_p or py is ctypes.POINTER(pointers[base]), (name, p, py)
+                assert py is ctypes.c_void_p or py is ctypes.POINTER(pointers.get(base)), (name, p, py)
             elif p[0] == "hipStream_t":
                 assert py is ctypes.c_void_p
             else:
@@ -52,6 +53,8 @@ def test_every_declared_call_is_exported_with_the_binding_s_signature():
 def test_struct_layouts_match_c(tmp_path):
     lines = [f'printf("{n} . %zu\\n", sizeof({n}));' for n in STRUCTS]
     lines += [f'printf("{n} {f[0]} %zu\\n", offsetof({n}, {f[0]}));' for n, s in STRUCTS.items() for f in s._fields_]
+    lines += [f'printf("{n} . %zu\\n", sizeof({n}));' for n in RECORDS]
+    lines += [f'printf("{n} {f} %zu\\n", offsetof({n}, {f}));' for n, r in RECORDS.items() for f in r.names]
     src = tmp_path / "layout.c"
     src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"xfer_decode.h\"\nint main(void) {\n"
                    + "\n".join(lines) + "\nreturn 0;\n}\n")
@@ -62,6 +65,10 @@ def test_struct_layouts_match_c(tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     for line in subprocess.run([exe], capture_output=True, text=True, timeout=60).stdout.splitlines():
         name, field, value = line.split()
+        if name in RECORDS:
+            r = RECORDS[name]
+            assert (r.itemsize if field == "." else r.fields[field][1]) == int(value), line
+            continue
         s = STRUCTS[name]
         assert (ctypes.sizeof(s) if field == "." else getattr(s, field).offset) == int(value), line
 
@@ -224,3 +231,46 @@ def test_attn_empty_work_and_workspace_sizes():
         for n in (300, 5000, 131071, 1 << 20):
             need = _need(c, batch(rows=rows, max_len=n, table_ld=1 << 17), 8)
             assert need <= max(1 << 20, rows * n * 2 * 2 * 128 * 2 // 16), (rows, n, need)
+
+
+# ---------------------------------------------------------------- sampling
+
+def shards(n0=1000, n1=900, ld0=1000, ld1=904, rows=3, off0=0, off1=1000, p0=K, p1=V):
+    return x.Shard(p0, ld0, rows, n0, off0), x.Shard(p1, ld1, rows, n1, off1)
+
+
+def samp(s=None, params=Q, u=KN, out=QO, ws=VN, ws_bytes=1 << 24):
+    s0, s1 = s or shards()
+    return decode.sample_merge_raw(s0, s1, params, u, out, ws, ws_bytes, stream=S0)
+
+
+@pytest.mark.parametrize("s,more,status", [
+    (dict(n0=0), {}, x.E_INVAL), (dict(n1=0), {}, x.E_INVAL), (dict(off1=999), {}, x.E_INVAL),
+    (dict(off0=500, off1=0), {}, x.E_INVAL), (dict(off1=(1 << 31) - 899), {}, x.E_INVAL),
+    (dict(p0=0), {}, x.E_INVAL), (dict(p1=V + 8), {}, x.E_INVAL), (dict(ld0=1004), {}, x.E_INVAL),
+    (dict(ld1=896), {}, x.E_INVAL), (dict(ld0=1 << 62), {}, x.E_INVAL),
+    (dict(n0=2097153, ld0=2097160, off1=3000000), {}, x.E_UNSUPPORTED),
+    (dict(rows=1 << 24), {}, x.E_UNSUPPORTED),
+    (dict(rows=1 << 22, n0=100000, ld0=100000, off1=100000), {}, x.E_UNSUPPORTED),
+    ({}, dict(params=0), x.E_INVAL), ({}, dict(params=Q + 8), x.E_INVAL), ({}, dict(u=0), x.E_INVAL),
+    ({}, dict(u=KN + 2), x.E_INVAL), ({}, dict(out=0), x.E_INVAL), ({}, dict(out=QO + 8), x.E_INVAL),
+    ({}, dict(ws=0), x.E_INVAL), ({}, dict(ws=VN + 4), x.E_INVAL), ({}, dict(ws_bytes=1000), x.E_INVAL),
+    ({}, dict(out=K + 16), x.E_INVAL), ({}, dict(out=V), x.E_INVAL), ({}, dict(out=Q + 32), x.E_INVAL),
+    ({}, dict(out=KN), x.E_INVAL), ({}, dict(out=VN + 64), x.E_INVAL), ({}, dict(ws=K), x.E_INVAL),
+    ({}, dict(ws=V + 32), x.E_INVAL), ({}, dict(ws=Q), x.E_INVAL), ({}, dict(ws=KN), x.E_INVAL),
+])
+def test_sample_refusals(s, more, status):
+    assert samp(shards(**s), **more) == status
+
+
+def test_sample_empty_work_and_workspace_sizes():
+    assert samp(shards(rows=0, p0=0, p1=0, n0=0), params=0, u=0, out=0, ws=0, ws_bytes=0) == x.OK
+    s0, s1 = shards()
+    s1.rows = 4
+    assert samp((s0, s1)) == x.E_INVAL
+    assert decode.lib().xfer_sample_merge(None, None, None, None, None, None, 0, None) == x.E_INVAL
+    need = decode.sample_workspace_bytes
+    assert need(0, 10, 10) == 0 and need(5, 0, 10) == 0 and need(5, 10, 2097153) == 0
+    for n0, n1 in ((1, 1), (16384, 16384), (16384, 16392), (64768, 64512), (2097152, 2097152)):
+        assert 0 < need(1, n0, n1) <= 8 * 65280 + 4 * (n0 + n1 + 128 * 8) + 1024
+        assert need(7, n0, n1) >= 7 * (need(1, n0, n1) - 1024)
