@@ -4,12 +4,19 @@
 // Every visible key and value is read once and little is done with it: 4 *
 // group operations for each element, so HBM bandwidth bounds the call, and
 // the layout serves the loads:
-//   - a workgroup takes (row, kv head, piece of the row's visible tokens) and
-//     all query heads of that kv head (16 or 32 at a time), so a key is read
-//     once for all of them.  Its four waves take tiles of 32 tokens in turn,
-//     each with a running maximum and sum of its own, and meet once at the
-//     end, in LDS.  Rows that are cut into pieces leave (max, sum, weighted
-//     sum) in the workspace, and a second launch joins them;
+//   - the work is one line of units, 128 visible tokens of a (row, kv head)
+//     each, row after row; every workgroup adds up the rows' lengths for itself
+//     and takes an equal run of it.  So rows of any mixture of lengths keep all
+//     compute units busy for the same time, and no more workgroups start than
+//     stay resident.  A (row, kv head) that falls to several workgroups leaves
+//     (max, sum, weighted sum) of each part in the workspace, at most two for a
+//     workgroup, and a second launch joins them;
+//   - a workgroup takes all query heads of a kv head, so a key is read from
+//     memory once for all of them.  Four waves take tiles of 32 tokens in turn,
+//     each with a running maximum and sum of its own, and meet once for each
+//     (row, kv head), in LDS.  Heads beyond 16 have four more waves, which take
+//     the same tiles at the same time (up to 32 heads; the next 32 are a kv
+//     head of their own);
 //   - scores are products K Q^T on matrix cores (16x16x32): K's operand is 16
 //     bytes of a token's row for each lane, straight from global memory, and
 //     a lane ends with four tokens' scores of one query head in each of two
@@ -33,13 +40,14 @@
 namespace xfer {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kWaves = 4;                        // that share the tokens
+constexpr int kThreads = 64 * kWaves;            // for 16 query heads
 constexpr uint32_t kTile = 32;                   // tokens of a wave's tile
 constexpr uint32_t kStep = kTile * kWaves;       // tokens of a workgroup's round
-constexpr uint32_t kMinChunkSteps = 2;
-constexpr uint32_t kTargetWorkgroups = 2048;
-constexpr uint32_t kMaxSplits = 256;             // one thread of the join for each
+constexpr uint32_t kMinUnits = 2;                // of a workgroup
+constexpr uint32_t kWholeUnits = 16;              // of a row that need not be cut up
+constexpr uint32_t kComputeUnits = 256;
+constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
 constexpr uint32_t kXcds = 8;
 
@@ -96,6 +104,15 @@ struct Layout {
   static constexpr int kMfmaV = D / 16;
 };
 
+// Waves that stay resident on a SIMD, by what their registers allow: with
+// heads of 256 the queries lie in LDS for it.
+template <int D, int KIND>
+struct Residence {
+  static constexpr bool kQInLds = D == 256;
+  static constexpr bool kValuesAhead = Layout<D, KIND>::kDwordsV <= 2;
+  static constexpr int kPerSimd = D == 64 ? 4 : D == 128 ? 3 : 2;
+};
+
 // Dims that product j of V^T P^T gives for row n of its result (n < 16).
 template <int D, int KIND>
 __device__ __forceinline__ uint32_t dim_of(uint32_t j, uint32_t n) {
@@ -127,43 +144,135 @@ struct Weights {
   v4u hi, lo;
 };
 
-template <int D, int KIND, int MT>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(AttnArgs a, uint32_t chunk, uint32_t n_splits,
-                                                           uint32_t m_groups) {
-  using L = Layout<D, KIND>;
-  constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
-  __shared__ float lds_o[kWaves][16][D + kPad];
-  __shared__ float lds_m[kWaves][MT * 16], lds_l[kWaves][MT * 16];
+// What a (row, kv head) that fell to several workgroups leaves: its first
+// part's slot (kWhole: one workgroup did it all), and how many parts.
+struct Parts {
+  uint32_t slot, n;
+};
+constexpr uint32_t kWhole = 0xFFFFFFFFu;
 
-  // Workgroups of one (piece, row) follow one another on one XCD, whose L2
-  // then serves the lines that two heads share; (piece, row) go round the XCDs.
+__device__ __forceinline__ uint32_t units_of(const Visible &v) { return v.n ? (v.n + kStep - 1) / kStep : 1; }
+
+// A workgroup's run of units: where it starts, and how long it is.
+struct Run {
+  uint64_t per, length;  // of any workgroup, and of this one (0: nothing to do)
+  uint32_t row;
+  uint64_t at;           // the first unit within the row
+};
+
+// Adds up the rows' units (a row has units_of() for each of `inner_n` heads)
+// and cuts them into equal runs; by all threads.
+template <int THREADS>
+__device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint32_t wg, uint32_t n_wg) {
+  __shared__ uint64_t totals[THREADS / 64];
+  __shared__ uint64_t start[2];
+  const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const uint32_t each = (a.rows + THREADS - 1) / THREADS;
+  const uint32_t r0 = min(tid * each, a.rows), r1 = min(r0 + each, a.rows);
+  uint64_t mine = 0;
+  for (uint32_t r = r0; r < r1; ++r) mine += (uint64_t)units_of(visible_of(a, r)) * inner_n;
+  uint64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint64_t x = __shfl_up(incl, d);
+    if ((int)lane >= d) incl += x;
+  }
+  if (lane == 63) totals[wave] = incl;
+  __syncthreads();
+  uint64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < (int)wave) incl += totals[w];
+    all += totals[w];
+  }
+  Run run;
+  run.per = max((uint64_t)kMinUnits, (all + n_wg - 1) / n_wg);
+  const uint64_t from = wg * run.per;
+  run.length = from < all ? min(run.per, all - from) : 0;
+  if (incl - mine <= from && from < incl) {
+    uint64_t before = incl - mine;
+    uint32_t r = r0;
+    for (; r + 1 < r1; ++r) {
+      const uint64_t u = (uint64_t)units_of(visible_of(a, r)) * inner_n;
+      if (from < before + u) break;
+      before += u;
+    }
+    start[0] = r;
+    start[1] = from - before;
+  }
+  __syncthreads();
+  run.row = __builtin_amdgcn_readfirstlane((uint32_t)start[0]);
+  run.at = start[1];
+  return run;
+}
+
+template <int D, int KIND, int MT>
+__global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void attn_kernel(AttnArgs a,
+                                                                                           uint32_t m_groups) {
+  using L = Layout<D, KIND>;
+  constexpr bool kQInLds = Residence<D, KIND>::kQInLds, kValuesAhead = Residence<D, KIND>::kValuesAhead;
+  constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
+  __shared__ float lds_all_o[MT][kWaves][16][D + kPad];
+  __shared__ float lds_all_m[MT][kWaves][16], lds_all_l[MT][kWaves][16];
+
   const uint32_t inner_n = a.cache.kv_heads * m_groups;
   const uint32_t xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
-  const uint32_t inner = rest % inner_n, pair = rest / inner_n * kXcds + xcd;
-  const uint32_t split = pair / a.rows, row = pair % a.rows;
-  if (split >= n_splits) return;
-  const uint32_t kvh = inner / m_groups, mg = inner % m_groups;
+  uint32_t wg = 0;
+  Run run;
+  if (a.parts) {
+    // Neighbouring runs on one XCD: its L2 then serves the lines that two
+    // heads share.
+    wg = xcd * (gridDim.x / kXcds) + rest;
+    run = run_of<kThreads * MT>(a, inner_n, wg, gridDim.x);
+    if (run.length == 0) return;
+  } else {
+    // A workgroup for each (row, kv head): rows go round the XCDs, and the
+    // heads of a row follow one another on one.
+    run.row = rest / inner_n * kXcds + xcd;
+    if (run.row >= a.rows) return;
+  }
 
-  const Visible vis = visible_of(a, row);
-  const uint32_t v0 = split * chunk;
-  if (v0 >= vis.n && !(n_splits == 1)) return;  // the join does not ask for this piece
-  const uint32_t v1 = min(v0 + chunk, vis.n);
+  // Four waves' tokens and 16 query heads: tile m.
+  const uint32_t m = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), tid = threadIdx.x % kThreads;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16, g = lane / 16;
+  auto &lds_o = lds_all_o[m];
+  auto &lds_m = lds_all_m[m];
+  auto &lds_l = lds_all_l[m];
+  // The queries, in the lanes' order, where the exchange lies later.
+  v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
+  static_assert(!kQInLds || L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
+  uint32_t row = run.row;
+  Visible vis = visible_of(a, row);
+  uint32_t units = units_of(vis);
+  uint32_t inner = rest % inner_n, unit = 0;
+  uint64_t left = units;
+  if (a.parts) {
+    inner = __builtin_amdgcn_readfirstlane((uint32_t)(run.at / units));
+    unit = __builtin_amdgcn_readfirstlane((uint32_t)(run.at % units));
+    left = run.length;
+  }
+  bool first_segment = true;
 
-  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64, n = lane % 16, g = lane / 16;
-  const uint32_t h0 = mg * (MT * 16);  // first query head of this tile within the group
+#pragma unroll 1
+  while (left) {
+  const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
+  const uint32_t kvh = inner / m_groups, h0 = inner % m_groups * (MT * 16) + 16 * m;  // first query head within the group
+  const uint32_t v0 = unit * kStep, v1 = min((unit + take) * kStep, vis.n);
 
-  // Q: query head h0 + 16 * m + n, the dims that this lane's K loads hold.
-  v4u q[MT][L::kMfmaK];
+  // Q: query head h0 + n, the dims that this lane's K loads hold.
+  v4u q[L::kMfmaK];
+  auto load_q = [&](int k) {
+    const uint32_t h = h0 + n;
+    const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
+    return h < a.group ? *reinterpret_cast<const v4u *>(a.q + row * a.q_ld + (uint64_t)(kvh * a.group + h) * D + d)
+                       : v4u{0, 0, 0, 0};
+  };
+  if constexpr (kQInLds) {
+    for (int k = wave; k < L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k);
+    __syncthreads();
+  } else {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const uint32_t h = h0 + 16 * m + n;
-#pragma unroll
-    for (int k = 0; k < L::kMfmaK; ++k) {
-      const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
-      q[m][k] = v4u{0, 0, 0, 0};
-      if (h < a.group)
-        q[m][k] = *reinterpret_cast<const v4u *>(a.q + row * a.q_ld + (uint64_t)(kvh * a.group + h) * D + d);
-    }
+    for (int k = 0; k < L::kMfmaK; ++k) q[k] = load_q(k);
   }
   float scale2 = a.scale * 1.4426950408889634f;
   if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
@@ -209,45 +318,46 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(AttnAr
     }
   };
 
-  v4f o[MT][L::kMfmaV];
-  float mx[MT], sum[MT];
+  v4f o[L::kMfmaV];
+  float mx = -INFINITY, sum = 0;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mx[m] = -INFINITY;
-    sum[m] = 0;
-#pragma unroll
-    for (int j = 0; j < L::kMfmaV; ++j) o[m][j] = v4f{0, 0, 0, 0};
+  for (int j = 0; j < L::kMfmaV; ++j) o[j] = v4f{0, 0, 0, 0};
+
+  // The value rows of this lane group's eight tokens; bit e of the result:
+  // token e is not there (then the cache's first slot is read).
+  auto load_values = [&](uint32_t (&vr)[8][L::kDwordsV], int64_t off) -> uint32_t {
+    const uint32_t lo = (uint32_t)off, hi = (uint32_t)((uint64_t)off >> 32);
+    uint32_t gone = 0;
+#define XFER_ROW(E)                                                                        \
+  {                                                                                        \
+    const uint32_t h = row_lane<E>(hi);                                                    \
+    const bool no = (int32_t)h < 0;                                                        \
+    gone |= no ? 1u << E : 0;                                                              \
+    load_v<D, KIND>(vr[E], vbase + (no ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo)), n);   \
   }
+    XFER_ROW(0) XFER_ROW(1) XFER_ROW(2) XFER_ROW(3) XFER_ROW(4) XFER_ROW(5) XFER_ROW(6) XFER_ROW(7)
+#undef XFER_ROW
+    return gone;
+  };
 
   uint32_t t = v0 + wave * kTile;
   int64_t off = -1;
   Place next{};
+  uint32_t vr[8][L::kDwordsV], absent = 0;
   if (t < v1) {
     off = offset_of(look_up(t));
     load_k(off);
+    if constexpr (kValuesAhead) absent = load_values(vr, off);
     next = look_up(t + kStep);
   }
   for (; t < v1; t += kStep) {
-    // Value rows of this lane group's eight tokens.
-    uint32_t vr[8][L::kDwordsV];
-    const uint32_t lo = (uint32_t)off, hi = (uint32_t)((uint64_t)off >> 32);
-    uint32_t absent = 0;  // bit e: token e of this group is not there
+    // keep the queries where they are: read anew from LDS for each tile
+    if constexpr (kQInLds) asm volatile("" ::: "memory");
+    if constexpr (!kValuesAhead) absent = load_values(vr, off);
     const bool full = __all(off >= 0);
-#define XFER_ROW(E)                                                            \
-  {                                                                            \
-    const uint32_t h = row_lane<E>(hi);                                        \
-    const bool gone = (int32_t)h < 0;                                          \
-    const uint64_t at = gone ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo);      \
-    absent |= gone ? 1u << E : 0;                                              \
-    load_v<D, KIND>(vr[E], vbase + at, n);                                     \
-  }
-    XFER_ROW(0) XFER_ROW(1) XFER_ROW(2) XFER_ROW(3) XFER_ROW(4) XFER_ROW(5) XFER_ROW(6) XFER_ROW(7)
-#undef XFER_ROW
 
     // Scores: lane (n, g) gets query head n's of tokens 4g + i and 16 + 4g + i.
-    v4f s[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) s[m][0] = s[m][1] = v4f{0, 0, 0, 0};
+    v4f s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -261,53 +371,56 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(AttnAr
           op = v4u{e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1),
                    e4m3x2_to_bf16<true>(w1)};
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][half] = mfma(op, q[m][kk], s[m][half]);
+        if constexpr (kQInLds)
+          s[half] = mfma(op, lds_q[kk * 64 + lane], s[half]);
+        else
+          s[half] = mfma(op, q[kk], s[half]);
       }
     }
 
-    // The next tile's keys, while this one's weights are computed.
+    // The next tile's keys (and values, where registers allow), while this
+    // one's weights are computed.
     const int64_t off_next = offset_of(next);
+    uint32_t vr_next[kValuesAhead ? 8 : 1][L::kDwordsV], absent_next = 0;
     if (t + kStep < v1) {
       load_k(off_next);
+      if constexpr (kValuesAhead) absent_next = load_values(vr_next, off_next);
       next = look_up(t + 2 * kStep);
     }
 
-    Weights w[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    Weights w;
+    {
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = s[m][e / 4][e % 4] * scale2;
+      for (int e = 0; e < 8; ++e) x[e] = s[e / 4][e % 4] * scale2;
       if (!full) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (absent >> e) & 1 ? -INFINITY : x[e];
       }
       float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (__any(top > mx[m] + kRaise)) {
+      if (__any(top > mx + kRaise)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float raised = fmaxf(mx[m], top);
+        const float raised = fmaxf(mx, top);
         // a head that has seen nothing yet has nothing to rescale
-        const float f = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - raised);
-        mx[m] = raised;
-        sum[m] *= f;
+        const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - raised);
+        mx = raised;
+        sum *= f;
 #pragma unroll
-        for (int j = 0; j < L::kMfmaV; ++j) o[m][j] *= f;
+        for (int j = 0; j < L::kMfmaV; ++j) o[j] *= f;
       }
-      const float base = mx[m] == -INFINITY ? 0.0f : mx[m];
-      float p[8], low[8];
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         p[e] = __builtin_amdgcn_exp2f(x[e] - base);
-        sum[m] += p[e];
+        sum += p[e];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[m].hi[i] = bf16x2(p[2 * i], p[2 * i + 1]);
-        low[2 * i] = p[2 * i] - __uint_as_float(w[m].hi[i] << 16);
-        low[2 * i + 1] = p[2 * i + 1] - __uint_as_float(w[m].hi[i] & 0xFFFF0000u);
-        w[m].lo[i] = bf16x2(low[2 * i], low[2 * i + 1]);
+        w.hi[i] = bf16x2(p[2 * i], p[2 * i + 1]);
+        w.lo[i] = bf16x2(p[2 * i] - __uint_as_float(w.hi[i] << 16),
+                         p[2 * i + 1] - __uint_as_float(w.hi[i] & 0xFFFF0000u));
       }
     }
 
@@ -337,118 +450,151 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attn_kernel(AttnAr
         even[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x05040100);
         odd[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x07060302);
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        o[m][2 * i] = mfma(even, w[m].hi, o[m][2 * i]);
-        o[m][2 * i] = mfma(even, w[m].lo, o[m][2 * i]);
-        o[m][2 * i + 1] = mfma(odd, w[m].hi, o[m][2 * i + 1]);
-        o[m][2 * i + 1] = mfma(odd, w[m].lo, o[m][2 * i + 1]);
-      }
+      o[2 * i] = mfma(even, w.hi, o[2 * i]);
+      o[2 * i] = mfma(even, w.lo, o[2 * i]);
+      o[2 * i + 1] = mfma(odd, w.hi, o[2 * i + 1]);
+      o[2 * i + 1] = mfma(odd, w.lo, o[2 * i + 1]);
     }
     off = off_next;
+    if constexpr (kValuesAhead) {
+      absent = absent_next;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int i = 0; i < L::kDwordsV; ++i) vr[e][i] = vr_next[e][i];
+    }
   }
 
   // The four waves' results, joined in LDS.
+  const bool whole = take == units;
+  const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
+  if (unit == 0 && threadIdx.x == 0 && a.parts)
+    reinterpret_cast<Parts *>(a.parts)[(uint64_t)row * inner_n + inner] =
+        whole ? Parts{kWhole, 1} : Parts{slot, 1 + (uint32_t)((units - take + run.per - 1) / run.per)};
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (g == 0) {
+    lds_m[wave][n] = mx;
+    lds_l[wave][n] = sum;
+  }
+  __syncthreads();
+  {
+    float top = -INFINITY;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    sum[m] += __shfl_xor(sum[m], 16);
-    sum[m] += __shfl_xor(sum[m], 32);
-    if (g == 0) {
-      lds_m[wave][16 * m + n] = mx[m];
-      lds_l[wave][16 * m + n] = sum[m];
-    }
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
+    const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - top);
+#pragma unroll
+    for (int j = 0; j < L::kMfmaV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[j][i] * f;
   }
   __syncthreads();
   const float v_scale = KIND == XFER_KV_E4M3 && a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
-    float top = -INFINITY;
+  for (int it = 0; it < D / 64; ++it) {
+    const uint32_t at = it * kThreads + tid, hq = at / (D / 4), d = at % (D / 4) * 4;
+    const uint32_t h = h0 + hq;
+    if (h >= a.group) continue;
+    float top = -INFINITY, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][16 * m + n]);
-    const float f = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
+    v4f r = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < L::kMfmaV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[m][j][i] * f;
-    __syncthreads();
-#pragma unroll
-    for (int it = 0; it < D / 64; ++it) {
-      const uint32_t at = it * kThreads + tid, hq = at / (D / 4), d = at % (D / 4) * 4;
-      const uint32_t h = h0 + 16 * m + hq;
-      if (h >= a.group) continue;
-      float all = -INFINITY, total = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) all = fmaxf(all, lds_m[w][16 * m + hq]);
-      v4f r = {0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float mw = lds_m[w][16 * m + hq];
-        total += mw == -INFINITY ? lds_l[w][16 * m + hq] : lds_l[w][16 * m + hq] * __builtin_amdgcn_exp2f(mw - all);
-        r += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
-      }
-      if (n_splits == 1) {
-        const float inv = total == 0.0f ? 0.0f : v_scale / total;
-        r *= inv;
-        const uint64_t at_out = row * a.out_ld + (uint64_t)(kvh * a.group + h) * D + d;
-        if (a.out_mode == XFER_OUT_F32)
-          *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at_out) = r;
-        else
-          *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at_out) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
-      } else {
-        const uint64_t part = (((uint64_t)row * a.cache.kv_heads + kvh) * n_splits + split) * a.group + h;
-        *reinterpret_cast<v4f *>(a.part_o + part * D + d) = r;
-        if (d == 0) {
-          a.part_ml[2 * part] = all;
-          a.part_ml[2 * part + 1] = total;
-        }
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = lds_m[w][hq];
+      total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
+      r += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
+    }
+    if (whole) {
+      const float inv = total == 0.0f ? 0.0f : v_scale / total;
+      r *= inv;
+      const uint64_t at_out = row * a.out_ld + (uint64_t)(kvh * a.group + h) * D + d;
+      if (a.out_mode == XFER_OUT_F32)
+        *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at_out) = r;
+      else
+        *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at_out) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
+    } else {
+      const uint64_t part = (uint64_t)slot * min(a.group, (uint32_t)MT * 16) + 16 * m + hq;
+      *reinterpret_cast<v4f *>(a.part_o + part * D + d) = r;
+      if (d == 0) {
+        a.part_ml[2 * part] = top;
+        a.part_ml[2 * part + 1] = total;
       }
     }
   }
+
+  // The next (row, kv head).
+  left -= take;
+  first_segment = false;
+  unit = 0;
+  if (++inner == inner_n) {
+    inner = 0;
+    if (++row == a.rows) break;
+    vis = visible_of(a, row);
+    units = units_of(vis);
+  }
+  if (left) __syncthreads();  // LDS is written again
+  }
 }
 
-// One workgroup for each (row, query head): the pieces' weighted sums, each
-// scaled to the largest maximum, in the pieces' order.
+// One workgroup for each (row, query head): the weighted sums of its parts, each
+// scaled to the largest maximum, in the parts' order.
 template <int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t chunk, uint32_t n_splits) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t m_tile, uint32_t m_groups) {
   constexpr uint32_t kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  __shared__ float lds_w[kMaxSplits];
-  __shared__ float lds_red[kWaves];
+  constexpr int kEach = kMaxWorkgroups / kThreads;  // parts of a thread
+  __shared__ float lds_w[kMaxWorkgroups];
+  __shared__ float lds_red[2][kWaves];
   __shared__ v4f lds_o[kAtOnce][kLanes];
   const uint32_t row = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads;
   const uint32_t kvh = head / a.group, h = head % a.group, tid = threadIdx.x;
-  const Visible vis = visible_of(a, row);
-  const uint32_t pieces = (vis.n + chunk - 1) / chunk;
-  const uint64_t part0 = ((uint64_t)row * a.cache.kv_heads + kvh) * n_splits;
+  const Parts parts = reinterpret_cast<const Parts *>(a.parts)[((uint64_t)row * a.cache.kv_heads + kvh) * m_groups + h / m_tile];
+  if (parts.slot == kWhole) return;
+  // Part p > 0 is the first thing that the workgroup p further on did.
+  auto place = [&](uint32_t p) {
+    return (uint64_t)(p ? (parts.slot / 2 + p) * 2 : parts.slot) * min(a.group, m_tile) + h % m_tile;
+  };
 
-  float m = -INFINITY, l = 0;
-  if (tid < pieces) {
-    m = a.part_ml[2 * ((part0 + tid) * a.group + h)];
-    l = a.part_ml[2 * ((part0 + tid) * a.group + h) + 1];
+  float m[kEach], l[kEach], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t p = i * kThreads + tid;
+    m[i] = -INFINITY;
+    l[i] = 0;
+    if (p < parts.n) {
+      m[i] = a.part_ml[2 * place(p)];
+      l[i] = a.part_ml[2 * place(p) + 1];
+    }
+    top = fmaxf(top, m[i]);
   }
-  float top = m;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if (tid % 64 == 0) lds_red[tid / 64] = top;
+  if (tid % 64 == 0) lds_red[0][tid / 64] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(lds_red[0], lds_red[1]), fmaxf(lds_red[2], lds_red[3]));
-  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-  if (tid < pieces) lds_w[tid] = f;
-  float total = m == -INFINITY ? l : l * f;
+  top = fmaxf(fmaxf(lds_red[0][0], lds_red[0][1]), fmaxf(lds_red[0][2], lds_red[0][3]));
+  float total = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t p = i * kThreads + tid;
+    const float f = m[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
+    if (p < parts.n) lds_w[p] = f;
+    total += m[i] == -INFINITY ? l[i] : l[i] * f;
+  }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+  if (tid % 64 == 0) lds_red[1][tid / 64] = total;
   __syncthreads();
-  if (tid % 64 == 0) lds_red[tid / 64] = total;
-  const uint32_t d4 = tid % kLanes, s0 = tid / kLanes;
+  const uint32_t d4 = tid % kLanes, p0 = tid / kLanes;
   v4f r = {0, 0, 0, 0};
-  for (uint32_t s = s0; s < pieces; s += kAtOnce)
-    r += lds_w[s] * *reinterpret_cast<const v4f *>(a.part_o + ((part0 + s) * a.group + h) * D + 4 * d4);
-  lds_o[s0][d4] = r;
+#pragma unroll 4
+  for (uint32_t p = p0; p < parts.n; p += kAtOnce)
+    r += lds_w[p] * *reinterpret_cast<const v4f *>(a.part_o + place(p) * D + 4 * d4);
+  lds_o[p0][d4] = r;
   __syncthreads();
-  if (s0 != 0) return;
+  if (p0 != 0) return;
 #pragma unroll
   for (uint32_t s = 1; s < kAtOnce; ++s) r += lds_o[s][d4];
-  total = (lds_red[0] + lds_red[1]) + (lds_red[2] + lds_red[3]);
+  total = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
   const float v_scale = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
   r *= total == 0.0f ? 0.0f : v_scale / total;
   const uint64_t at = row * a.out_ld + (uint64_t)head * D + 4 * d4;
@@ -458,51 +604,75 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
     *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
 }
 
+// Workgroups that stay resident: waves of a SIMD, for one or two tiles.
+uint32_t resident(uint32_t head_dim, uint32_t m_tiles) {
+  const int waves = head_dim == 64    ? Residence<64, XFER_KV_BF16>::kPerSimd
+                    : head_dim == 128 ? Residence<128, XFER_KV_BF16>::kPerSimd
+                                      : Residence<256, XFER_KV_BF16>::kPerSimd;
+  return kComputeUnits * (waves / m_tiles);
+}
+
 template <int D, int KIND>
 hipError_t launch_tiles(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
   const dim3 grid((uint32_t)s.workgroups);
-  if (s.m_tiles == 1)
-    return launch(attn_kernel<D, KIND, 1>, grid, dim3(kThreads), 0, stream, a, s.chunk, s.n_splits, s.m_groups);
-  return launch(attn_kernel<D, KIND, 2>, grid, dim3(kThreads), 0, stream, a, s.chunk, s.n_splits, s.m_groups);
+  if (s.m_tiles == 1) return launch(attn_kernel<D, KIND, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  return launch(attn_kernel<D, KIND, 2>, grid, dim3(2 * kThreads), 0, stream, a, s.m_groups);
 }
 
 template <int D>
 hipError_t launch_dim(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream) {
   const hipError_t e =
       kind == XFER_KV_BF16 ? launch_tiles<D, XFER_KV_BF16>(a, s, stream) : launch_tiles<D, XFER_KV_E4M3>(a, s, stream);
-  if (e != hipSuccess || s.n_splits == 1) return e;
-  return launch(attn_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a, s.chunk, s.n_splits);
+  if (e != hipSuccess || !s.joined) return e;
+  return launch(attn_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a, 16 * s.m_tiles,
+                s.m_groups);
 }
+
+uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
+// Query heads of all the workgroups' parts: two parts for each.
+uint64_t parts_of(const AttnShape &s) { return 2ull * s.workgroups * s.part_heads; }
 
 }  // namespace
 
-AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint64_t vis_max) {
+AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint64_t vis_max) {
   AttnShape s{};
+  if (rows == 0) return s;
   s.m_tiles = group <= 16 ? 1 : 2;
   const uint32_t tile = 16 * s.m_tiles;
   s.m_groups = group / tile + (group % tile != 0);
-  const uint64_t inner = (uint64_t)kv_heads * s.m_groups, pairs = rows * inner;
-  const uint64_t steps = (vis_max + kStep - 1) / kStep;
-  uint64_t chunk = kMinChunkSteps;
-  chunk = chunk * kTargetWorkgroups < pairs * steps ? (pairs * steps + kTargetWorkgroups - 1) / kTargetWorkgroups : chunk;
-  if (chunk * kMaxSplits < steps) chunk = (steps + kMaxSplits - 1) / kMaxSplits;
-  if (chunk > steps) chunk = steps;
-  s.chunk = (uint32_t)(chunk * kStep);
-  s.n_splits = (uint32_t)((steps + chunk - 1) / chunk);
-  s.workgroups = ((uint64_t)rows * s.n_splits + kXcds - 1) / kXcds * kXcds * inner;
+  s.part_heads = group < tile ? group : tile;
+  const uint64_t inner = (uint64_t)kv_heads * s.m_groups, steps = (vis_max + kStep - 1) / kStep;
+  // Whole (row, kv head)s where none is long and there are enough of them, or
+  // where there is nothing to cut; else equal runs.
+  const uint64_t most = resident(head_dim, s.m_tiles);
+  s.joined = steps > kMinUnits && (steps > kWholeUnits || rows * inner < most / 2);
+  if (!s.joined) {
+    s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
+    return s;
+  }
+  uint64_t n;
+  if (__builtin_mul_overflow(rows * inner, steps, &n)) n = UINT64_MAX;
+  n = (n - 1) / kMinUnits + 1;
+  s.workgroups = n < most ? (n + kXcds - 1) / kXcds * kXcds : most;
   return s;
 }
 
-uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t q_heads, uint32_t head_dim) {
-  if (s.n_splits == 1) return 0;
-  const uint64_t parts = (uint64_t)rows * q_heads * s.n_splits;
-  return (parts * 8 + 15) / 16 * 16 + parts * head_dim * 4;
+// Layout: (max, sum) of each part, the weighted sums, the parts of each (row, kv head).
+uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t kv_heads, uint32_t head_dim) {
+  if (!s.joined) return 0;
+  const uint64_t parts = parts_of(s);
+  return parts * 8 + parts * head_dim * 4 + up16((uint64_t)rows * kv_heads * s.m_groups * sizeof(Parts));
 }
 
 hipError_t launch_attn(const AttnArgs &in, int kind, const AttnShape &s, hipStream_t stream) {
   AttnArgs a = in;
-  const uint64_t parts = (uint64_t)a.rows * a.q_heads * s.n_splits;
-  if (s.n_splits > 1) a.part_o = a.part_ml + (parts * 8 + 15) / 16 * 4;
+  if (s.joined) {
+    const uint64_t parts = parts_of(s);
+    a.part_o = a.part_ml + 2 * parts;
+    a.parts = a.part_o + parts * a.cache.head_dim;
+  } else {
+    a.part_ml = nullptr;  // the workgroups take whole (row, kv head)s
+  }
   if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s, stream);
   if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s, stream);
   return launch_dim<256>(a, kind, s, stream);

@@ -29,14 +29,16 @@ uint64_t rope_store_workgroups(uint32_t tokens, uint32_t heads, uint32_t head_di
 hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStream_t stream);
 
 // ---- attention of one new token over a paged cache (attn_paged.hip)
-// How a call's work is cut up: rows of at most vis_max visible tokens in
-// n_splits pieces of chunk tokens, query heads of a kv head in m_groups tiles.
+// How a call's work is cut up: query heads of a kv head in m_groups of 16 *
+// m_tiles, workgroups that share the visible tokens (of vis_max a row, at
+// most) evenly, and whether a (row, kv head) may fall to several of them.
 struct AttnShape {
-  uint32_t chunk, n_splits, m_tiles, m_groups;
+  uint32_t m_tiles, m_groups, part_heads;
   uint64_t workgroups;
+  bool joined;
 };
-AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint64_t vis_max);
-uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t q_heads, uint32_t head_dim);
+AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint64_t vis_max);
+uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t kv_heads, uint32_t head_dim);
 struct AttnArgs {
   CacheView cache;
   const uint32_t *page_table, *lens;
@@ -48,7 +50,8 @@ struct AttnArgs {
   float scale;
   void *out;
   int out_mode;
-  float *part_o, *part_ml;  // [rows][kv_heads][n_splits][group][head_dim], and (max, sum) of each
+  float *part_ml, *part_o;  // (max, sum) of each query head of each part, and its weighted sum
+  void *parts;              // where each (row, kv head)'s parts are (NULL: none has two)
 };
 hipError_t launch_attn(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream);
 

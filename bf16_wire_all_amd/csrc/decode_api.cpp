@@ -105,14 +105,14 @@ xfer::CacheView view_of(const xfer_kv_cache *c) {
 }
 
 // The sizes of an attention call that the workspace follows from; on XFER_OK
-// fills *s and *vis_max.
+// fills *s.
 int attn_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, uint32_t q_heads, xfer::AttnShape *s) {
   if (q_heads == 0 || q_heads % c->kv_heads) return XFER_E_INVAL;
   if (b->sinks && !b->window) return XFER_E_INVAL;
   if (b->max_len == 0 || b->max_len > 0x7FFFFFFFu) return XFER_E_INVAL;
   uint64_t vis = b->max_len;
   if (b->window) vis = std::min<uint64_t>(vis, (uint64_t)b->window + b->sinks);
-  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, vis);
+  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, c->head_dim, vis);
   return XFER_OK;
 }
 
@@ -188,7 +188,7 @@ size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_ba
   uint64_t extent = 0;
   xfer::AttnShape s{};
   if (!batch || cache_checks(cache, &extent) != XFER_OK || attn_sizes(cache, batch, q_heads, &s) != XFER_OK) return 0;
-  return (size_t)xfer::attn_workspace_bytes(s, batch->rows, q_heads, cache->head_dim);
+  return (size_t)xfer::attn_workspace_bytes(s, batch->rows, cache->kv_heads, cache->head_dim);
 }
 
 int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q, uint64_t q_ld,
@@ -210,7 +210,7 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
     return XFER_E_INVAL;
   if (!q || !out || !aligned16(q) || !aligned16(out) || !ld_ok(q_ld, R, row) || !ld_ok(out_ld, R, row))
     return XFER_E_INVAL;
-  const uint64_t need = xfer::attn_workspace_bytes(s, batch->rows, q_heads, cache->head_dim);
+  const uint64_t need = xfer::attn_workspace_bytes(s, batch->rows, cache->kv_heads, cache->head_dim);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return XFER_E_INVAL;
 
   const uint64_t ob = out_mode == XFER_OUT_F32 ? 4 : 2;

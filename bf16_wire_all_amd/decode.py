@@ -10,8 +10,9 @@ from __future__ import annotations
 import ctypes
 
 import numpy as np
+import torch
 
-from . import OUT_BF16, OUT_F32, Shard, _check, _stream, lib as _base_lib
+from . import OK, OUT_BF16, OUT_F32, Shard, _check, _stream, lib as _base_lib
 
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
@@ -75,31 +76,35 @@ def lib():
     return _lib
 
 
-def _flat(t, itemsize: int, device, what: str) -> int:
+# The checks below run at every call, in front of kernels of a few
+# microseconds: each asks a tensor as few things as it can.
+
+def _flat(t, itemsize: int, device: int, what: str) -> int:
     """Pointer of a contiguous tensor of the call's device (None: NULL)."""
     if t is None:
         return 0
-    if t.device != device or t.element_size() != itemsize or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {itemsize}-byte tensor on {device}")
+    if t.get_device() != device or t.element_size() != itemsize or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {itemsize}-byte tensor on cuda:{device}")
     return t.data_ptr()
 
 
-def _rows(t, heads, head_dim: int, itemsize: int, device, what: str):
+def _rows(t, heads, head_dim: int, itemsize: int, device: int, what: str):
     """(pointer, rows, heads, ld in elements) of a [rows, heads, head_dim] tensor whose rows are dense."""
     rows, h, d = t.shape
-    s = t.stride()
-    if t.device != device or t.element_size() != itemsize or d != head_dim or (heads is not None and h != heads):
-        raise ValueError(f"{what}: expected [rows, {heads or 'heads'}, {head_dim}] of {itemsize} bytes on {device}")
-    if s[2] != 1 or (h > 1 and s[1] != d):
+    s0, s1, s2 = t.stride()
+    if t.get_device() != device or t.element_size() != itemsize or d != head_dim or (heads is not None and h != heads):
+        raise ValueError(f"{what}: expected [rows, {heads or 'heads'}, {head_dim}] of {itemsize} bytes on cuda:{device}")
+    if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{what}: a row's heads must lie one after the other")
-    return t.data_ptr(), rows, h, s[0] if rows > 1 else h * d
+    return t.data_ptr(), rows, h, s0 if rows > 1 else h * d
 
 
-def _on(device) -> None:
-    """Pointers belong to the device that is current when a call is made."""
-    import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, which is not the current device")
+def _stream_on(device: int, stream) -> int:
+    """The stream of a call whose tensors are on `device`, which has to be the
+    current one: pointers belong to the device that is current at the call."""
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on device {device}, which is not the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 class KVCache:
@@ -117,12 +122,12 @@ class KVCache:
         for scale in (k_scale, v_scale):
             if scale is not None and scale.numel() != h:
                 raise ValueError("one scale for each head")
-        self.device, self.kv_heads, self.head_dim, self.page_tokens, self.n_pages = k.device, h, d, p, n
+        self.device, self.kv_heads, self.head_dim, self.page_tokens, self.n_pages = k.get_device(), h, d, p, n
         self.tensors = (k, v, k_scale, v_scale)
         # the stride of a dimension of one element is never walked: any multiple of 16 will do
         stride = [s[i] * e if k.shape[i] > 1 else 0 for i in range(3)]
-        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, 4, k.device, "k_scale") or None,
-                          _flat(v_scale, 4, k.device, "v_scale") or None, stride[0], stride[1], stride[2], n, p, h, d,
+        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, 4, self.device, "k_scale") or None,
+                          _flat(v_scale, 4, self.device, "v_scale") or None, stride[0], stride[1], stride[2], n, p, h, d,
                           KV_BF16 if e == 2 else KV_E4M3, 0)
 
 
@@ -141,7 +146,7 @@ def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_
     int64[tokens]; q_out like q (q itself is computed in place);
     interleaved: dims 2i and 2i + 1 form a pair, not i and i + rot_dim / 2."""
     dev, d = cache.device, cache.head_dim
-    _on(dev)
+    stream = _stream_on(dev, stream)
     kp, tokens, _, k_ld = _rows(k, cache.kv_heads, d, 2, dev, "k")
     vp, vt, _, v_ld = _rows(v, cache.kv_heads, d, 2, dev, "v")
     qp, qt, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
@@ -160,8 +165,10 @@ def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_
         rope.max_pos, rope.rot_dim = cos_sin.shape
     qkv = QKVC(qp, kp, vp, q_ld, k_ld, v_ld, _flat(q_weight, 2, dev, "q_weight"), _flat(k_weight, 2, dev, "k_weight"),
                tokens, q_heads, eps, 0)
-    _check(lib().xfer_qkv_rope_store(ctypes.byref(cache.c), ctypes.byref(qkv), ctypes.byref(rope),
-                                     _flat(slots, 8, dev, "slots"), op, o_ld, _stream(stream)), "xfer_qkv_rope_store")
+    status = lib().xfer_qkv_rope_store(ctypes.byref(cache.c), ctypes.byref(qkv), ctypes.byref(rope),
+                                       _flat(slots, 8, dev, "slots"), op, o_ld, stream)
+    if status != OK:
+        _check(status, "xfer_qkv_rope_store")
 
 
 def qkv_rope_store_raw(cache: KVCacheC, qkv: QKVC, rope: RopeC, slots_ptr: int, q_out_ptr: int, q_out_ld: int,
@@ -186,7 +193,7 @@ def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, 
     int32 or uint32 [rows]; out: like q, BF16 (2-byte) or F32; workspace: a
     CUDA tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
     dev, d = cache.device, cache.head_dim
-    _on(dev)
+    stream = _stream_on(dev, stream)
     qp, rows, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
     size = out.element_size()
     if size not in (2, 4):
@@ -195,19 +202,20 @@ def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, 
     if o_rows != rows or lens.numel() != rows or page_table.dim() != 2 or page_table.shape[0] != rows:
         raise ValueError("q, page_table, lens and out must have the same rows")
     width, ts = page_table.shape[1], page_table.stride()
-    if page_table.device != dev or page_table.element_size() != 4 or (width > 1 and ts[1] != 1):
+    if page_table.get_device() != dev or page_table.element_size() != 4 or (width > 1 and ts[1] != 1):
         raise ValueError("page_table: expected 4-byte page numbers, dense within a row")
     if width * cache.page_tokens < max_len:
         raise ValueError("page_table is too narrow for max_len")
     ws, ws_bytes = 0, 0
     if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-        ws = _flat(workspace, workspace.element_size(), dev, "workspace")
+        size_w = workspace.element_size()
+        ws_bytes, ws = workspace.numel() * size_w, _flat(workspace, size_w, dev, "workspace")
     batch = PagedBatchC(page_table.data_ptr(), _flat(lens, 4, dev, "lens"), ts[0] if rows > 1 else width, rows,
                         max_len, window, sinks)
-    _check(lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
-                                 OUT_F32 if size == 4 else OUT_BF16, ws, ws_bytes, _stream(stream)),
-           "xfer_attn_paged")
+    status = lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
+                                   OUT_F32 if size == 4 else OUT_BF16, ws, ws_bytes, stream)
+    if status != OK:
+        _check(status, "xfer_attn_paged")
 
 
 def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q_heads: int, scale: float,
@@ -239,18 +247,18 @@ def sample_merge(s0: Shard, s1: Shard, params, u, out, workspace, stream=None) -
     """params: CUDA tensor of rows * 16 bytes (SAMPLE_PARAMS records); u: F32[rows]
     in [0, 1); out: CUDA tensor of rows * 8 bytes (SAMPLED records); workspace:
     at least sample_workspace_bytes() bytes, any contents."""
-    dev, rows = u.device, s0.rows
-    _on(dev)
-    if params.numel() * params.element_size() != rows * SAMPLE_PARAMS.itemsize or u.numel() != rows:
+    dev, rows = u.get_device(), s0.rows
+    stream = _stream_on(dev, stream)
+    ps, os_, ws = params.element_size(), out.element_size(), workspace.element_size()
+    if params.numel() * ps != rows * 16 or u.numel() != rows:
         raise ValueError("params and u must have one record for each row")
-    if out.numel() * out.element_size() != rows * SAMPLED.itemsize:
+    if out.numel() * os_ != rows * 8:
         raise ValueError("out must have 8 bytes for each row")
-    _check(lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1),
-                                   _flat(params, params.element_size(), dev, "params"), _flat(u, 4, dev, "u"),
-                                   _flat(out, out.element_size(), dev, "out"),
-                                   _flat(workspace, workspace.element_size(), dev, "workspace"),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)),
-           "xfer_sample_merge")
+    status = lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1), _flat(params, ps, dev, "params"),
+                                     _flat(u, 4, dev, "u"), _flat(out, os_, dev, "out"),
+                                     _flat(workspace, ws, dev, "workspace"), workspace.numel() * ws, stream)
+    if status != OK:
+        _check(status, "xfer_sample_merge")
 
 
 def sample_merge_raw(s0: Shard, s1: Shard, params_ptr: int, u_ptr: int, out_ptr: int, ws_ptr: int, ws_bytes: int,
