@@ -14,9 +14,8 @@
 //   - a workgroup takes all query heads of a kv head, so a key is read from
 //     memory once for all of them.  Four waves take tiles of 32 tokens in turn,
 //     each with a running maximum and sum of its own, and meet once for each
-//     (row, kv head), in LDS.  Heads beyond 16 have four more waves, which take
-//     the same tiles at the same time (up to 32 heads; the next 32 are a kv
-//     head of their own);
+//     (row, kv head), in LDS.  Heads beyond 16 take more registers of these
+//     waves (up to 32 heads; the next 32 are a kv head of their own);
 //   - scores are products K Q^T on matrix cores (16x16x32): K's operand is 16
 //     bytes of a token's row for each lane, straight from global memory, and
 //     a lane ends with four tokens' scores of one query head in each of two
@@ -44,8 +43,8 @@ constexpr int kWaves = 4;                        // that share the tokens
 constexpr int kThreads = 64 * kWaves;            // for 16 query heads
 constexpr uint32_t kTile = 32;                   // tokens of a wave's tile
 constexpr uint32_t kStep = kTile * kWaves;       // tokens of a workgroup's round
-constexpr uint32_t kMinUnits = 2;                // of a workgroup
-constexpr uint32_t kWholeUnits = 16;              // of a row that need not be cut up
+constexpr uint32_t kWholeUnits = 16;             // of a row that need not be cut up
+constexpr uint32_t kJoinUnits = 4;               // that the join is worth
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
@@ -84,14 +83,12 @@ struct Visible {
   uint32_t n, first, gap;
 };
 __device__ __forceinline__ Visible visible_of(const AttnArgs &a, uint32_t row) {
+  const uint32_t n = min(a.lens[row], a.max_len);
+  const uint32_t before = n - min(n, a.window);  // tokens in front of the window
   Visible v;
-  v.n = min(a.lens[row], a.max_len);
-  v.first = v.gap = 0;
-  if (a.window && v.n > a.window) {
-    v.first = min(a.sinks, v.n - a.window);
-    v.gap = v.n - a.window - v.first;
-    v.n = a.window + v.first;
-  }
+  v.first = min(a.sinks, before);
+  v.gap = before - v.first;
+  v.n = n - v.gap;
   return v;
 }
 
@@ -104,13 +101,13 @@ struct Layout {
   static constexpr int kMfmaV = D / 16;
 };
 
-// Waves that stay resident on a SIMD, by what their registers allow: with
-// heads of 256 the queries lie in LDS for it.
-template <int D, int KIND>
+// Waves that stay resident on a SIMD.  Two, where registers allow: more wait
+// on more places of the memory at once, and two rows of 131071 tokens (heads of
+// 128, BF16) take 187 us on three of a SIMD and 169 on two.
+template <int D, int KIND, int TILES>
 struct Residence {
-  static constexpr bool kQInLds = D == 256;
-  static constexpr bool kValuesAhead = Layout<D, KIND>::kDwordsV <= 2;
-  static constexpr int kPerSimd = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr bool kQInLds = D == 256 && TILES == 1;
+  static constexpr int kPerSimd = D == 256 && (KIND == XFER_KV_BF16 || TILES == 2) ? 1 : 2;
 };
 
 // Dims that product j of V^T P^T gives for row n of its result (n < 16).
@@ -121,18 +118,25 @@ __device__ __forceinline__ uint32_t dim_of(uint32_t j, uint32_t n) {
   return n * (D / 16) + j;
 }
 
-template <int D, int KIND>
+// STREAM: each line is read once and by one workgroup.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load(const uint8_t *p) {
+  if (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
+  return *reinterpret_cast<const T *>(p);
+}
+
+template <int D, int KIND, bool STREAM>
 __device__ __forceinline__ void load_v(uint32_t *dst, const uint8_t *row, uint32_t n) {
   constexpr int W = Layout<D, KIND>::kDwordsV;
   if constexpr (W == 1) {
-    dst[0] = *reinterpret_cast<const uint32_t *>(row + 4 * n);
+    dst[0] = load<STREAM, uint32_t>(row + 4 * n);
   } else if constexpr (W == 2) {
-    const v2u w = *reinterpret_cast<const v2u *>(row + 8 * n);
+    const v2u w = load<STREAM, v2u>(row + 8 * n);
     dst[0] = w.x, dst[1] = w.y;
   } else {
 #pragma unroll
     for (int c = 0; c < W / 4; ++c) {
-      const v4u w = *reinterpret_cast<const v4u *>(row + 256 * c + 16 * n);
+      const v4u w = load<STREAM, v4u>(row + 256 * c + 16 * n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) dst[4 * c + i] = w[i];
     }
@@ -162,12 +166,11 @@ struct Run {
 
 // Adds up the rows' units (a row has units_of() for each of `inner_n` heads)
 // and cuts them into equal runs; by all threads.
-template <int THREADS>
 __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint32_t wg, uint32_t n_wg) {
-  __shared__ uint64_t totals[THREADS / 64];
+  __shared__ uint64_t totals[kWaves];
   __shared__ uint64_t start[2];
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const uint32_t each = (a.rows + THREADS - 1) / THREADS;
+  const uint32_t each = (a.rows + kThreads - 1) / kThreads;
   const uint32_t r0 = min(tid * each, a.rows), r1 = min(r0 + each, a.rows);
   uint64_t mine = 0;
   for (uint32_t r = r0; r < r1; ++r) mine += (uint64_t)units_of(visible_of(a, r)) * inner_n;
@@ -181,14 +184,16 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   __syncthreads();
   uint64_t all = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < (int)wave) incl += totals[w];
     all += totals[w];
   }
   Run run;
-  run.per = max((uint64_t)kMinUnits, (all + n_wg - 1) / n_wg);
+  run.per = (all + n_wg - 1) / n_wg;
   const uint64_t from = wg * run.per;
-  run.length = from < all ? min(run.per, all - from) : 0;
+  // No guarded subtraction here: the compiler has taken such a guard away
+  // (from < all ? min(per, all - from) : 0 became min(per, all - from)).
+  run.length = min(run.per, all - min(from, all));
   if (incl - mine <= from && from < incl) {
     uint64_t before = incl - mine;
     uint32_t r = r0;
@@ -206,14 +211,17 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   return run;
 }
 
-template <int D, int KIND, int MT>
-__global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void attn_kernel(AttnArgs a,
-                                                                                           uint32_t m_groups) {
+template <int D, int KIND, int TILES>
+__global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
+                                                                                             uint32_t m_groups) {
   using L = Layout<D, KIND>;
-  constexpr bool kQInLds = Residence<D, KIND>::kQInLds, kValuesAhead = Residence<D, KIND>::kValuesAhead;
+  using R = Residence<D, KIND, TILES>;
+  constexpr int MR = TILES;
+  // A line holds the rows of two heads where they are shorter than it.
+  constexpr bool kStream = D * L::kBytes >= 128;
   constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
-  __shared__ float lds_all_o[MT][kWaves][16][D + kPad];
-  __shared__ float lds_all_m[MT][kWaves][16], lds_all_l[MT][kWaves][16];
+  __shared__ float lds_o[kWaves][16][D + kPad];
+  __shared__ float lds_all_m[MR][kWaves][16], lds_all_l[MR][kWaves][16];
 
   const uint32_t inner_n = a.cache.kv_heads * m_groups;
   const uint32_t xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
@@ -223,7 +231,7 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
     // Neighbouring runs on one XCD: its L2 then serves the lines that two
     // heads share.
     wg = xcd * (gridDim.x / kXcds) + rest;
-    run = run_of<kThreads * MT>(a, inner_n, wg, gridDim.x);
+    run = run_of(a, inner_n, wg, gridDim.x);
     if (run.length == 0) return;
   } else {
     // A workgroup for each (row, kv head): rows go round the XCDs, and the
@@ -232,15 +240,11 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
     if (run.row >= a.rows) return;
   }
 
-  // Four waves' tokens and 16 query heads: tile m.
-  const uint32_t m = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), tid = threadIdx.x % kThreads;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16, g = lane / 16;
-  auto &lds_o = lds_all_o[m];
-  auto &lds_m = lds_all_m[m];
-  auto &lds_l = lds_all_l[m];
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16,
+                 g = lane / 16;
   // The queries, in the lanes' order, where the exchange lies later.
   v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
-  static_assert(!kQInLds || L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
+  static_assert(!R::kQInLds || L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
   uint32_t row = run.row;
   Visible vis = visible_of(a, row);
   uint32_t units = units_of(vis);
@@ -256,23 +260,25 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
 #pragma unroll 1
   while (left) {
   const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
-  const uint32_t kvh = inner / m_groups, h0 = inner % m_groups * (MT * 16) + 16 * m;  // first query head within the group
+  const uint32_t kvh = inner / m_groups, h0 = inner % m_groups * (16 * MR);  // first query head within the group
   const uint32_t v0 = unit * kStep, v1 = min((unit + take) * kStep, vis.n);
 
-  // Q: query head h0 + n, the dims that this lane's K loads hold.
-  v4u q[L::kMfmaK];
-  auto load_q = [&](int k) {
-    const uint32_t h = h0 + n;
+  // Q: query head h0 + 16 * r + n, the dims that this lane's K loads hold.
+  v4u q[R::kQInLds ? 1 : MR][L::kMfmaK];
+  auto load_q = [&](int r, int k) {
+    const uint32_t h = h0 + 16 * r + n;
     const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
     return h < a.group ? *reinterpret_cast<const v4u *>(a.q + row * a.q_ld + (uint64_t)(kvh * a.group + h) * D + d)
                        : v4u{0, 0, 0, 0};
   };
-  if constexpr (kQInLds) {
-    for (int k = wave; k < L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k);
+  if constexpr (R::kQInLds) {
+    for (int k = wave; k < L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(0, k);
     __syncthreads();
   } else {
 #pragma unroll
-    for (int k = 0; k < L::kMfmaK; ++k) q[k] = load_q(k);
+    for (int r = 0; r < MR; ++r)
+#pragma unroll
+      for (int k = 0; k < L::kMfmaK; ++k) q[r][k] = load_q(r, k);
   }
   float scale2 = a.scale * 1.4426950408889634f;
   if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
@@ -314,14 +320,19 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
       const uint64_t o = ((uint64_t)(uint32_t)__shfl((int)hi, from) << 32) | (uint32_t)__shfl((int)lo, from);
       const uint8_t *p = kbase + ((int64_t)o < 0 ? 0 : o);  // a hole's scores are replaced: any row will do
 #pragma unroll
-      for (int i = 0; i < L::kLoadsK; ++i) k[s][i] = *reinterpret_cast<const v4u *>(p + 64 * i);
+      for (int i = 0; i < L::kLoadsK; ++i) k[s][i] = load<kStream, v4u>(p + 64 * i);
     }
   };
 
-  v4f o[L::kMfmaV];
-  float mx = -INFINITY, sum = 0;
+  v4f o[MR][L::kMfmaV];
+  float mx[MR], sum[MR];
 #pragma unroll
-  for (int j = 0; j < L::kMfmaV; ++j) o[j] = v4f{0, 0, 0, 0};
+  for (int r = 0; r < MR; ++r) {
+    mx[r] = -INFINITY;
+    sum[r] = 0;
+#pragma unroll
+    for (int j = 0; j < L::kMfmaV; ++j) o[r][j] = v4f{0, 0, 0, 0};
+  }
 
   // The value rows of this lane group's eight tokens; bit e of the result:
   // token e is not there (then the cache's first slot is read).
@@ -333,7 +344,7 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
     const uint32_t h = row_lane<E>(hi);                                                    \
     const bool no = (int32_t)h < 0;                                                        \
     gone |= no ? 1u << E : 0;                                                              \
-    load_v<D, KIND>(vr[E], vbase + (no ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo)), n);   \
+    load_v<D, KIND, kStream>(vr[E], vbase + (no ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo)), n);   \
   }
     XFER_ROW(0) XFER_ROW(1) XFER_ROW(2) XFER_ROW(3) XFER_ROW(4) XFER_ROW(5) XFER_ROW(6) XFER_ROW(7)
 #undef XFER_ROW
@@ -343,21 +354,22 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
   uint32_t t = v0 + wave * kTile;
   int64_t off = -1;
   Place next{};
-  uint32_t vr[8][L::kDwordsV], absent = 0;
   if (t < v1) {
     off = offset_of(look_up(t));
     load_k(off);
-    if constexpr (kValuesAhead) absent = load_values(vr, off);
     next = look_up(t + kStep);
   }
   for (; t < v1; t += kStep) {
     // keep the queries where they are: read anew from LDS for each tile
-    if constexpr (kQInLds) asm volatile("" ::: "memory");
-    if constexpr (!kValuesAhead) absent = load_values(vr, off);
+    if constexpr (R::kQInLds) asm volatile("" ::: "memory");
+    uint32_t vr[8][L::kDwordsV];
+    const uint32_t absent = load_values(vr, off);
     const bool full = __all(off >= 0);
 
     // Scores: lane (n, g) gets query head n's of tokens 4g + i and 16 + 4g + i.
-    v4f s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    v4f s[MR][2];
+#pragma unroll
+    for (int r = 0; r < MR; ++r) s[r][0] = s[r][1] = v4f{0, 0, 0, 0};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -371,56 +383,56 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
           op = v4u{e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1),
                    e4m3x2_to_bf16<true>(w1)};
         }
-        if constexpr (kQInLds)
-          s[half] = mfma(op, lds_q[kk * 64 + lane], s[half]);
-        else
-          s[half] = mfma(op, q[kk], s[half]);
+        if constexpr (R::kQInLds) {
+          s[0][half] = mfma(op, lds_q[kk * 64 + lane], s[0][half]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < MR; ++r) s[r][half] = mfma(op, q[r][kk], s[r][half]);
+        }
       }
     }
 
-    // The next tile's keys (and values, where registers allow), while this
-    // one's weights are computed.
+    // The next tile's keys, while this one's weights are computed.
     const int64_t off_next = offset_of(next);
-    uint32_t vr_next[kValuesAhead ? 8 : 1][L::kDwordsV], absent_next = 0;
     if (t + kStep < v1) {
       load_k(off_next);
-      if constexpr (kValuesAhead) absent_next = load_values(vr_next, off_next);
       next = look_up(t + 2 * kStep);
     }
 
-    Weights w;
-    {
+    Weights w[MR];
+#pragma unroll
+    for (int r = 0; r < MR; ++r) {
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = s[e / 4][e % 4] * scale2;
+      for (int e = 0; e < 8; ++e) x[e] = s[r][e / 4][e % 4] * scale2;
       if (!full) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (absent >> e) & 1 ? -INFINITY : x[e];
       }
       float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (__any(top > mx + kRaise)) {
+      if (__any(top > mx[r] + kRaise)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float raised = fmaxf(mx, top);
+        const float raised = fmaxf(mx[r], top);
         // a head that has seen nothing yet has nothing to rescale
-        const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - raised);
-        mx = raised;
-        sum *= f;
+        const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - raised);
+        mx[r] = raised;
+        sum[r] *= f;
 #pragma unroll
-        for (int j = 0; j < L::kMfmaV; ++j) o[j] *= f;
+        for (int j = 0; j < L::kMfmaV; ++j) o[r][j] *= f;
       }
-      const float base = mx == -INFINITY ? 0.0f : mx;
+      const float base = mx[r] == -INFINITY ? 0.0f : mx[r];
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         p[e] = __builtin_amdgcn_exp2f(x[e] - base);
-        sum += p[e];
+        sum[r] += p[e];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w.hi[i] = bf16x2(p[2 * i], p[2 * i + 1]);
-        w.lo[i] = bf16x2(p[2 * i] - __uint_as_float(w.hi[i] << 16),
-                         p[2 * i + 1] - __uint_as_float(w.hi[i] & 0xFFFF0000u));
+        w[r].hi[i] = bf16x2(p[2 * i], p[2 * i + 1]);
+        w[r].lo[i] = bf16x2(p[2 * i] - __uint_as_float(w[r].hi[i] << 16),
+                            p[2 * i + 1] - __uint_as_float(w[r].hi[i] & 0xFFFF0000u));
       }
     }
 
@@ -450,19 +462,15 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
         even[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x05040100);
         odd[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x07060302);
       }
-      o[2 * i] = mfma(even, w.hi, o[2 * i]);
-      o[2 * i] = mfma(even, w.lo, o[2 * i]);
-      o[2 * i + 1] = mfma(odd, w.hi, o[2 * i + 1]);
-      o[2 * i + 1] = mfma(odd, w.lo, o[2 * i + 1]);
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+        o[r][2 * i] = mfma(even, w[r].hi, o[r][2 * i]);
+        o[r][2 * i] = mfma(even, w[r].lo, o[r][2 * i]);
+        o[r][2 * i + 1] = mfma(odd, w[r].hi, o[r][2 * i + 1]);
+        o[r][2 * i + 1] = mfma(odd, w[r].lo, o[r][2 * i + 1]);
+      }
     }
     off = off_next;
-    if constexpr (kValuesAhead) {
-      absent = absent_next;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int i = 0; i < L::kDwordsV; ++i) vr[e][i] = vr_next[e][i];
-    }
   }
 
   // The four waves' results, joined in LDS.
@@ -471,54 +479,62 @@ __global__ __launch_bounds__(kThreads *MT, (Residence<D, KIND>::kPerSimd)) void 
   if (unit == 0 && threadIdx.x == 0 && a.parts)
     reinterpret_cast<Parts *>(a.parts)[(uint64_t)row * inner_n + inner] =
         whole ? Parts{kWhole, 1} : Parts{slot, 1 + (uint32_t)((units - take + run.per - 1) / run.per)};
-  sum += __shfl_xor(sum, 16);
-  sum += __shfl_xor(sum, 32);
-  if (g == 0) {
-    lds_m[wave][n] = mx;
-    lds_l[wave][n] = sum;
-  }
-  __syncthreads();
-  {
-    float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
-    const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - top);
-#pragma unroll
-    for (int j = 0; j < L::kMfmaV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[j][i] * f;
+  for (int r = 0; r < MR; ++r) {
+    sum[r] += __shfl_xor(sum[r], 16);
+    sum[r] += __shfl_xor(sum[r], 32);
+    if (g == 0) {
+      lds_all_m[r][wave][n] = mx[r];
+      lds_all_l[r][wave][n] = sum[r];
+    }
   }
   __syncthreads();
   const float v_scale = KIND == XFER_KV_E4M3 && a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
 #pragma unroll
-  for (int it = 0; it < D / 64; ++it) {
-    const uint32_t at = it * kThreads + tid, hq = at / (D / 4), d = at % (D / 4) * 4;
-    const uint32_t h = h0 + hq;
-    if (h >= a.group) continue;
-    float top = -INFINITY, total = 0;
+  for (int r = 0; r < MR; ++r) {
+    auto &lds_m = lds_all_m[r];
+    auto &lds_l = lds_all_l[r];
+    if (r) __syncthreads();
+    {
+      float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
-    v4f r = {0, 0, 0, 0};
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
+      const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - top);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float mw = lds_m[w][hq];
-      total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
-      r += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
+      for (int j = 0; j < L::kMfmaV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[r][j][i] * f;
     }
-    if (whole) {
-      const float inv = total == 0.0f ? 0.0f : v_scale / total;
-      r *= inv;
-      const uint64_t at_out = row * a.out_ld + (uint64_t)(kvh * a.group + h) * D + d;
-      if (a.out_mode == XFER_OUT_F32)
-        *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at_out) = r;
-      else
-        *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at_out) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
-    } else {
-      const uint64_t part = (uint64_t)slot * min(a.group, (uint32_t)MT * 16) + 16 * m + hq;
-      *reinterpret_cast<v4f *>(a.part_o + part * D + d) = r;
-      if (d == 0) {
-        a.part_ml[2 * part] = top;
-        a.part_ml[2 * part + 1] = total;
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < D / 64; ++it) {
+      const uint32_t at = it * kThreads + tid, hq = at / (D / 4), d = at % (D / 4) * 4;
+      const uint32_t h = h0 + 16 * r + hq;
+      if (h >= a.group) continue;
+      float top = -INFINITY, total = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
+      v4f v = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float mw = lds_m[w][hq];
+        total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
+        v += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
+      }
+      if (whole) {
+        v *= total == 0.0f ? 0.0f : v_scale / total;
+        const uint64_t at_out = row * a.out_ld + (uint64_t)(kvh * a.group + h) * D + d;
+        if (a.out_mode == XFER_OUT_F32)
+          *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at_out) = v;
+        else
+          *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at_out) = v2u{bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
+      } else {
+        const uint64_t part = (uint64_t)slot * min(a.group, (uint32_t)TILES * 16) + 16 * r + hq;
+        *reinterpret_cast<v4f *>(a.part_o + part * D + d) = v;
+        if (d == 0) {
+          a.part_ml[2 * part] = top;
+          a.part_ml[2 * part + 1] = total;
+        }
       }
     }
   }
@@ -604,19 +620,23 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
     *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
 }
 
-// Workgroups that stay resident: waves of a SIMD, for one or two tiles.
-uint32_t resident(uint32_t head_dim, uint32_t m_tiles) {
-  const int waves = head_dim == 64    ? Residence<64, XFER_KV_BF16>::kPerSimd
-                    : head_dim == 128 ? Residence<128, XFER_KV_BF16>::kPerSimd
-                                      : Residence<256, XFER_KV_BF16>::kPerSimd;
-  return kComputeUnits * (waves / m_tiles);
+// Workgroups that stay resident.
+template <int D, int KIND>
+uint32_t resident(uint32_t tiles) {
+  return kComputeUnits * (tiles == 1 ? Residence<D, KIND, 1>::kPerSimd : Residence<D, KIND, 2>::kPerSimd);
+}
+template <int KIND>
+uint32_t resident(uint32_t head_dim, uint32_t tiles) {
+  return head_dim == 64    ? resident<64, KIND>(tiles)
+         : head_dim == 128 ? resident<128, KIND>(tiles)
+                           : resident<256, KIND>(tiles);
 }
 
 template <int D, int KIND>
 hipError_t launch_tiles(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
   const dim3 grid((uint32_t)s.workgroups);
   if (s.m_tiles == 1) return launch(attn_kernel<D, KIND, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
-  return launch(attn_kernel<D, KIND, 2>, grid, dim3(2 * kThreads), 0, stream, a, s.m_groups);
+  return launch(attn_kernel<D, KIND, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
 }
 
 template <int D>
@@ -634,7 +654,8 @@ uint64_t parts_of(const AttnShape &s) { return 2ull * s.workgroups * s.part_head
 
 }  // namespace
 
-AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint64_t vis_max) {
+AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind,
+                     uint64_t vis_max) {
   AttnShape s{};
   if (rows == 0) return s;
   s.m_tiles = group <= 16 ? 1 : 2;
@@ -642,17 +663,17 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   s.m_groups = group / tile + (group % tile != 0);
   s.part_heads = group < tile ? group : tile;
   const uint64_t inner = (uint64_t)kv_heads * s.m_groups, steps = (vis_max + kStep - 1) / kStep;
-  // Whole (row, kv head)s where none is long and there are enough of them, or
-  // where there is nothing to cut; else equal runs.
-  const uint64_t most = resident(head_dim, s.m_tiles);
-  s.joined = steps > kMinUnits && (steps > kWholeUnits || rows * inner < most / 2);
+  // Whole (row, kv head)s where none is long, and cutting them up would spare a
+  // workgroup no more units than the second launch costs; else equal runs.
+  const uint64_t most =
+      kind == XFER_KV_BF16 ? resident<XFER_KV_BF16>(head_dim, s.m_tiles) : resident<XFER_KV_E4M3>(head_dim, s.m_tiles);
+  s.joined = steps > kWholeUnits || steps > rows * inner * steps / most + kJoinUnits;
   if (!s.joined) {
     s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
     return s;
   }
   uint64_t n;
   if (__builtin_mul_overflow(rows * inner, steps, &n)) n = UINT64_MAX;
-  n = (n - 1) / kMinUnits + 1;
   s.workgroups = n < most ? (n + kXcds - 1) / kXcds * kXcds : most;
   return s;
 }

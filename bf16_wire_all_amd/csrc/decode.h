@@ -37,13 +37,14 @@ struct AttnShape {
   uint64_t workgroups;
   bool joined;
 };
-AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, uint64_t vis_max);
+AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind,
+                     uint64_t vis_max);
 uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t kv_heads, uint32_t head_dim);
 struct AttnArgs {
   CacheView cache;
   const uint32_t *page_table, *lens;
   uint64_t table_ld;
-  uint32_t rows, max_len, window, sinks;
+  uint32_t rows, max_len, window, sinks;  // window: UINT32_MAX for every token
   const uint16_t *q;
   uint64_t q_ld, out_ld;
   uint32_t q_heads, group;  // group = q_heads / kv_heads

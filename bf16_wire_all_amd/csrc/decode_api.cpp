@@ -112,7 +112,7 @@ int attn_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, uint32_t q_hea
   if (b->max_len == 0 || b->max_len > 0x7FFFFFFFu) return XFER_E_INVAL;
   uint64_t vis = b->max_len;
   if (b->window) vis = std::min<uint64_t>(vis, (uint64_t)b->window + b->sinks);
-  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, c->head_dim, vis);
+  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, c->head_dim, c->kind, vis);
   return XFER_OK;
 }
 
@@ -233,7 +233,7 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   a.table_ld = batch->table_ld;
   a.rows = batch->rows;
   a.max_len = batch->max_len;
-  a.window = batch->window;
+  a.window = batch->window ? batch->window : UINT32_MAX;
   a.sinks = batch->sinks;
   a.q = q;
   a.q_ld = q_ld;

@@ -154,6 +154,14 @@ def test_long_rows_in_pieces(kind, out):
     run(w, calls=2)
 
 
+@pytest.mark.parametrize("d,kind", [(64, "bf16"), (128, "e4m3"), (256, "bf16")])
+def test_fewer_units_than_workgroups(d, kind):
+    """The grid is laid out for rows of max_len: shorter rows leave workgroups that must find nothing to do."""
+    run(World([0, 3, 700, 1, 0], 4, 2, d, 16, kind, max_len=16000, seed=15))
+    run(World([1], 4, 1, d, 16, kind, max_len=130000, seed=16))
+    run(World(EDGE, 4, 2, d, 16, kind, "heads", max_len=5000, seed=d))
+
+
 def test_many_short_rows_and_one_long():
     run(World([1 + 7 * i % 60 for i in range(200)] + [3000], 4, 1, 64, 16, seed=4))
 
