@@ -44,7 +44,7 @@ constexpr int kThreads = 64 * kWaves;            // for 16 query heads
 constexpr uint32_t kTile = 32;                   // tokens of a wave's tile
 constexpr uint32_t kStep = kTile * kWaves;       // tokens of a workgroup's round
 constexpr uint32_t kWholeUnits = 16;             // of a row that need not be cut up
-constexpr uint32_t kJoinUnits = 4;               // that the join is worth
+constexpr uint32_t kJoinUnits = 3;               // that the join is worth
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two

@@ -10,7 +10,7 @@
 //
 // Two launches:
 //   1. count: a workgroup counts a slice of one shard in LDS (16 bits for each
-//      pattern, so a slice has fewer than 65,536 columns) and writes the values
+//      value, so a slice has fewer than 65,536 columns) and writes the values
 //      that occur, in order, with their counts;
 //   2. draw: a workgroup for each row adds up its slices' lists in LDS the
 //      same way, finds the cuts and the drawn element (its value and how many
@@ -20,41 +20,53 @@
 // shards in one workgroup.
 // The kernel boundary orders the two steps, as in the argmax.
 //
-// The bins fill a compute unit's LDS, so 16 waves share it and instructions
-// bound the work (a wave's instruction holds its SIMD for four clocks, and
-// four waves share one): a pattern's bin is its magnitude, with the counts of
-// the two signs in one word, which takes four operations for each logit, and
-// the order is made once, when the bins are read; empty runs of 256 bins are
-// passed over; one wave does the searches, 64 probes at a time, without
-// barriers between them.
+// A slice's range of magnitudes is found before it is counted, and 8,192 bins
+// (64 powers of two, both signs' counts in one word) hold it in 32 KiB of LDS:
+// several workgroups share a compute unit, and clearing and reading the bins
+// costs little.  What bounds the rest is instructions: those that issue (a
+// wave's instruction holds its SIMD for four clocks), so a logit takes two
+// packed operations for each pair and about five more to be counted, the order
+// is made once, when the bins are read, and one wave does the searches, 64
+// probes at a time, without barriers between them; and those that have to be
+// fetched, for a workgroup runs through most of the code once: loops are left
+// as loops (rows of 129,280: 20 us of kernels became __ONE__).  Ranges that are
+// wider, and sums of counts past 16 bits, take a path of eight passes.
 #include "decode.h"
 
 namespace xfer {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr uint32_t kPieceCols = 32768;           // columns that a workgroup holds at a time
-// Columns of a slice: a piece where that leaves compute units without a slice,
-// else as many as 16 bits count, since a list costs as much as a piece.
-constexpr uint32_t kSliceCols = kPieceCols, kWideSliceCols = 65528;
 constexpr uint32_t kInf = 0x7F80u;               // the pattern of +inf; -inf has the sign bit too
 // Values in the row's order, +inf first: positive patterns count down, zero
 // (of either sign) is bin kInf, negative ones count up.
 constexpr uint32_t kBins = 2 * kInf;
-constexpr uint32_t kWords = 32768;               // one for each magnitude: +count in the low half, -count in the high
+constexpr uint32_t kWords = 8192;                // bins in LDS: +count in the low half, -count in the high
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr uint32_t kLdsEntries = 7168;           // lists up to this long stay in LDS, beside the bins
+// Columns of a slice: as few as a piece where that gives compute units work
+// that would have none, else up to as many as 16 bits count.
+constexpr uint32_t kPieceCols = 16384, kWideSliceCols = 65528;
+constexpr uint32_t kOneCols = 32768;             // of a row that one launch counts
+constexpr uint32_t kLdsEntries = 5888;           // lists up to this long stay in LDS
 constexpr uint32_t kMaxSlices = 128;
-constexpr uint32_t kCountWorkgroups = 256;       // one on each compute unit: the bins fill its LDS
+constexpr uint32_t kCountWorkgroups = 512;       // two on each compute unit
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
 
 // The BF16 pattern of a bin (+0 for zero).
 __device__ __forceinline__ uint32_t pattern_of(uint32_t bin) {
   return bin <= kInf ? kInf - bin : 0x8000u | (bin - kInf);
 }
 __device__ __forceinline__ double value_of(uint32_t bin) { return (double)__uint_as_float(pattern_of(bin) << 16); }
+// The bin of a pattern that counts.
+__device__ __forceinline__ uint32_t bin_of(uint32_t v) {
+  const uint32_t mag = v & 0x7FFFu;
+  return v & 0x8000u ? kInf + mag : kInf - mag;
+}
+// Whether a pattern counts: neither NaN nor -inf.
+__device__ __forceinline__ bool counts(uint32_t v) { return (v & 0x7FFFu) <= kInf && v != 0xFF80u; }
 
 // A barrier that orders LDS alone: loads from global memory stay in flight
 // across it, and stores need not have arrived.
@@ -83,69 +95,10 @@ __device__ __forceinline__ Slice slice_of(const Shards &sh, uint32_t row, uint32
   return {sh.ptr[s] + row * sh.ld[s] + c0, min(sh.width[s], sh.ncols[s] - c0), sh.off[s] + c0};
 }
 
-// Piece i of a slice.
-__device__ __forceinline__ Slice piece_of(const Slice &s, uint32_t i) {
-  const uint32_t c0 = min(i * kPieceCols, s.cols);
-  return {s.ptr + c0, min(kPieceCols, s.cols - c0), s.gid + c0};
-}
-
-// This thread's elements of a piece, all loads in flight at once.
-constexpr int kRounds = kPieceCols / 8 / kThreads;
-constexpr uint32_t kMasked = 0xFF80FF80u;        // two of -inf
-struct Held {
-  v4u w[kRounds];
-  uint32_t last;  // one element of an incomplete last vector, above another of -inf
-};
-__device__ __forceinline__ Held load_piece(const Slice &s) {
-  Held h;
-  const v4u *vp = reinterpret_cast<const v4u *>(s.ptr);
-  const uint32_t n_vec = s.cols / 8;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const uint32_t v = r * kThreads + threadIdx.x;
-    h.w[r] = v4u{kMasked, kMasked, kMasked, kMasked};
-    if (v < n_vec) h.w[r] = vp[v];
-  }
-  h.last = kMasked;
-  if (threadIdx.x < s.cols % 8) h.last = (uint32_t)s.ptr[n_vec * 8 + threadIdx.x] << 16 | 0xFF80u;
-  return h;
-}
-
-__device__ __forceinline__ void count_low(uint32_t *hist, uint32_t x) {
-  atomicAdd(&hist[x & 0x7FFFu], (x >> 15 & 1u) * 0xFFFFu + 1u);
-}
-__device__ __forceinline__ void count_high(uint32_t *hist, uint32_t x) {
-  atomicAdd(&hist[x >> 16 & 0x7FFFu], (x >> 31) * 0xFFFFu + 1u);
-}
-// The same for elements that may be masked: a wave's atomics on one address
-// take their turns, and a mask would send most of them to that of -inf.
-__device__ __forceinline__ void count_two_unmasked(uint32_t *hist, uint32_t x) {
-  if ((x & 0xFFFFu) != 0xFF80u) count_low(hist, x);
-  if (x >> 16 != 0xFF80u) count_high(hist, x);
-}
-
-// Counts of a piece added to hist.  Whether the elements are looked at one by
-// one for masked ones goes by the first of each vector.
-__device__ __forceinline__ void count_piece(uint32_t *hist, const Held &h) {
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    if (__any((h.w[r].x & 0xFFFFu) == 0xFF80u)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) count_two_unmasked(hist, h.w[r][i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        count_low(hist, h.w[r][i]);
-        count_high(hist, h.w[r][i]);
-      }
-    }
-  }
-  count_two_unmasked(hist, h.last);
-}
-
 __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
+__device__ __forceinline__ uint32_t wave_number() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
 // Running sums over the lanes of a wave, by DPP moves (lanes that a move does
 // not reach add 0).
@@ -188,9 +141,151 @@ __device__ __forceinline__ uint32_t read_lane(uint32_t x, uint32_t lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, (int)lane);
 }
 
-// The values that occur in hist, in order.  The words go in groups of 256, a
-// lane four in a row, group after group round the waves; the constructor
-// returns once every group's numbers are known.
+
+// ------------------------------------------------------ pieces in registers
+
+// Elements of a piece, all loads in flight at once.  Lanes past its end hold
+// -inf, which counts nowhere.
+constexpr uint32_t kMasked = 0xFF80FF80u;
+constexpr int kRounds = kPieceCols / 8 / kThreads;
+struct Held {
+  v4u w[kRounds];
+  uint32_t last;   // one element of an incomplete last vector, above another of -inf
+  uint32_t n_vec;  // vectors of the piece
+
+  __device__ __forceinline__ void load(const Slice &s) {
+    const v4u *vp = reinterpret_cast<const v4u *>(s.ptr);
+    n_vec = s.cols / 8;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t v = r * kThreads + threadIdx.x;
+      w[r] = v4u{kMasked, kMasked, kMasked, kMasked};
+      if (v < n_vec) w[r] = vp[v];
+    }
+    last = kMasked;
+    if (threadIdx.x < s.cols % 8) last = (uint32_t)s.ptr[n_vec * 8 + threadIdx.x] << 16 | 0xFF80u;
+  }
+  // visit(round, vector) of every vector; rounds that hold nothing for this
+  // wave are left out.  A loop, whose vectors move up, and not its rounds one
+  // after the other in code.
+  template <typename Visit>
+  __device__ __forceinline__ void each(const Visit &visit) const {
+    v4u x[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) x[r] = w[r];
+#pragma unroll 1
+    for (uint32_t r = 0; r < kRounds && r * kThreads + wave_number() * 64 < n_vec; ++r) {
+      visit(r, x[0]);
+#pragma unroll
+      for (int i = 1; i < kRounds; ++i) x[i - 1] = x[i];
+    }
+  }
+  // one(element) of every element.
+  template <typename One>
+  __device__ __forceinline__ void each_one(const One &one) const {
+    each([&](uint32_t, const v4u &x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        one(x[i] & 0xFFFFu);
+        one(x[i] >> 16);
+      }
+    });
+    one(last >> 16);
+  }
+};
+
+// Up to eight pieces, one after the other: of a slice, or of two.
+struct Pieces {
+  Slice s[2];
+  uint32_t n0, n;
+  __device__ __forceinline__ Slice operator[](uint32_t i) const {
+    const bool second = i >= n0;
+    const uint32_t c0 = min((second ? i - n0 : i) * kPieceCols, second ? s[1].cols : s[0].cols);
+    const uint16_t *ptr = (second ? s[1].ptr : s[0].ptr) + c0;
+    return {ptr, min(kPieceCols, (second ? s[1].cols : s[0].cols) - c0), (second ? s[1].gid : s[0].gid) + c0};
+  }
+};
+__device__ __forceinline__ Pieces pieces_of(const Slice &a) {
+  const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
+  return {{a, a}, n, n};
+}
+__device__ __forceinline__ Pieces pieces_of(const Slice &a, const Slice &b) {
+  const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
+  return {{a, b}, n, n + max(1u, (b.cols + kPieceCols - 1) / kPieceCols)};
+}
+
+// Magnitudes from lo to hi (hi 0: none).
+struct Span {
+  uint32_t lo, hi;
+};
+// Widens this lane's span by its elements of a piece, zero and what does not
+// count left out; whether the wave's piece holds any of those.
+__device__ __forceinline__ bool widen(Span *s, const Held &h) {
+  v2us top = {0, 0}, low = {0xFFFF, 0xFFFF};
+  h.each([&](uint32_t, const v4u &x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const v2us m = __builtin_bit_cast(v2us, x[i] & 0x7FFF7FFFu);
+      top = __builtin_elementwise_max(top, m);
+      low = __builtin_elementwise_min(low, m);
+    }
+  });
+  const uint32_t t = max((uint32_t)top.x, (uint32_t)top.y), l = min((uint32_t)low.x, (uint32_t)low.y);
+  if (!__any(t >= kInf || l == 0 || h.last != kMasked)) {
+    s->lo = min(s->lo, l);
+    s->hi = max(s->hi, t);
+    return false;
+  }
+  h.each_one([&](uint32_t v) {
+    const uint32_t m = v & 0x7FFFu;
+    if (counts(v) && m) {
+      s->lo = min(s->lo, m);
+      s->hi = max(s->hi, m);
+    }
+  });
+  return true;
+}
+
+// ------------------------------------------------------------------ counting
+
+struct Bins {
+  uint32_t word[kWords];
+};
+
+__device__ __forceinline__ void clear(Bins *bins) {
+  v4u *p = reinterpret_cast<v4u *>(bins->word);
+#pragma unroll
+  for (uint32_t i = 0; i < kWords / 4 / kThreads; ++i) p[i * kThreads + threadIdx.x] = v4u{0, 0, 0, 0};
+}
+
+// Counts a wave's elements of a piece in the bins of magnitudes base .. base +
+// kWords - 1, which have to hold all of them but zero; *zeros takes the zeros.
+__device__ __forceinline__ void count_held(Bins *bins, const Held &h, bool odd, uint32_t base, uint32_t *zeros) {
+  uint32_t *word = bins->word;
+  if (!odd) {
+    h.each([&](uint32_t, const v4u &x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        atomicAdd(&word[(x[i] & 0x7FFFu) - base], (x[i] >> 15 & 1u) * 0xFFFFu + 1u);
+        atomicAdd(&word[(x[i] >> 16 & 0x7FFFu) - base], (x[i] >> 31) * 0xFFFFu + 1u);
+      }
+    });
+    return;
+  }
+  uint32_t n = 0;
+  h.each_one([&](uint32_t v) {
+    const uint32_t m = v & 0x7FFFu;
+    n += m == 0;
+    // a mask's elements would all wait for one address
+    if (counts(v) && m) atomicAdd(&word[m - base], (v >> 15) * 0xFFFFu + 1u);
+  });
+  n = read_lane(scan(n), 63);
+  if (n && threadIdx.x % 64 == 0) atomicAdd(zeros, n);
+}
+
+// The entries of the bins, in order.  The words go in groups of 256, a lane
+// four in a row, group after group round the waves; the constructor returns
+// once every group's numbers are known.
 constexpr int kGroups = kWords / 256;
 struct GroupCounts {
   uint32_t pos[kGroups], neg[kGroups];
@@ -198,169 +293,242 @@ struct GroupCounts {
 struct Compact {
   static constexpr int kOwn = kGroups / kWaves;  // groups of a wave
   v4u x[kOwn];
-  uint32_t pos_total, total;   // entries above zero, and in all
-  uint32_t pos_incl[2], neg_incl[2];  // of lane l: running numbers up to groups 2l and 2l + 1
+  uint32_t zeros, pos_total, total;  // elements that are zero; entries above zero, and in all
+  uint32_t pos_incl, neg_incl;       // of lane l: running numbers up to group l
 
-  __device__ __forceinline__ Compact(const uint32_t *hist, GroupCounts *counts) {
-    const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const v4u *words = reinterpret_cast<const v4u *>(hist);
+  // visit(group, words) of this wave's groups that are not empty.
+  template <typename Visit>
+  __device__ __forceinline__ void each(const Visit &visit) const {
+    v4u y[kOwn];
 #pragma unroll
-    for (int r = 0; r < kOwn; ++r) x[r] = words[(r * kWaves + wave) * 64 + lane];
-    if (wave == 0 && lane == 0) {
-      // zero of either sign: the first of the values not above it
-      const uint32_t z = x[0].x;
-      x[0].x = ((z & 0xFFFFu) + (z >> 16)) << 16;
+    for (int r = 0; r < kOwn; ++r) y[r] = x[r];
+#pragma unroll 1
+    for (uint32_t r = 0; r < kOwn; ++r) {
+      if (__any((y[0].x | y[0].y | y[0].z | y[0].w) != 0)) visit(r * kWaves + wave_number(), y[0]);
+#pragma unroll
+      for (int i = 1; i < kOwn; ++i) y[i - 1] = y[i];
     }
-    if (wave == kWaves - 1) {
-      // -inf and NaN count nowhere
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t mag = (kGroups - 1) * 256 + lane * 4 + i;
-        const uint32_t w = x[kOwn - 1][i];
-        x[kOwn - 1][i] = mag > kInf ? 0 : mag == kInf ? w & 0xFFFFu : w;
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kOwn; ++r) {
-      uint32_t p = 0, n = 0;
-      if (__any((x[r].x | x[r].y | x[r].z | x[r].w) != 0)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p += __popcll(__ballot((x[r][i] & 0xFFFFu) != 0));
-          n += __popcll(__ballot(x[r][i] >> 16 != 0));
-        }
-      }
-      if (lane == 0) {
-        counts->pos[r * kWaves + wave] = p;
-        counts->neg[r * kWaves + wave] = n;
-      }
-    }
-    lds_barrier();
-    const uint32_t p0 = counts->pos[2 * lane], n0 = counts->neg[2 * lane];
-    pos_incl[1] = scan(p0 + counts->pos[2 * lane + 1]);
-    neg_incl[1] = scan(n0 + counts->neg[2 * lane + 1]);
-    pos_incl[0] = pos_incl[1] - counts->pos[2 * lane + 1];
-    neg_incl[0] = neg_incl[1] - counts->neg[2 * lane + 1];
-    pos_total = read_lane(pos_incl[1], 63);
-    total = pos_total + read_lane(neg_incl[1], 63);
   }
 
-  // out(index, bin, count) for each.
-  template <typename Emit>
-  __device__ __forceinline__ void emit(const Emit &out) {
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  __device__ __forceinline__ Compact(const Bins *bins, uint32_t n_zeros, GroupCounts *groups) {
+    const uint32_t lane = threadIdx.x % 64;
+    const v4u *words = reinterpret_cast<const v4u *>(bins->word);
 #pragma unroll
-    for (int r = 0; r < kOwn; ++r) {
-      if (!__any((x[r].x | x[r].y | x[r].z | x[r].w) != 0)) continue;
-      const uint32_t g = r * kWaves + wave, mag0 = g * 256 + lane * 4;
+    for (int r = 0; r < kOwn; ++r) x[r] = words[(r * kWaves + wave_number()) * 64 + lane];
+    if (lane < kOwn) groups->pos[lane * kWaves + wave_number()] = groups->neg[lane * kWaves + wave_number()] = 0;
+    each([&](uint32_t g, const v4u &y) {
+      uint32_t p = 0, n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p += __popcll(__ballot((y[i] & 0xFFFFu) != 0));
+        n += __popcll(__ballot(y[i] >> 16 != 0));
+      }
+      if (lane == 0) {
+        groups->pos[g] = p;
+        groups->neg[g] = n;
+      }
+    });
+    lds_barrier();
+    static_assert(kGroups <= 64, "a lane for each group");
+    pos_incl = scan(lane < kGroups ? groups->pos[lane % kGroups] : 0);
+    neg_incl = scan(lane < kGroups ? groups->neg[lane % kGroups] : 0);
+    zeros = n_zeros;
+    pos_total = read_lane(pos_incl, 63);
+    total = pos_total + (zeros != 0) + read_lane(neg_incl, 63);
+  }
+
+  // out(index, bin, count) for each; word 0 stands for magnitude `base`.
+  template <typename Emit>
+  __device__ __forceinline__ void emit(uint32_t base, const Emit &out) const {
+    const uint32_t lane = threadIdx.x % 64;
+    if (zeros && threadIdx.x == 0) out(pos_total, kInf, zeros);
+    each([&](uint32_t g, const v4u &y) {
+      const uint32_t mag0 = base + g * 256 + lane * 4;
       uint32_t p_below = 0, p_own = 0, p_all = 0, n_below = 0, n_all = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool own = (x[r][i] & 0xFFFFu) != 0;
+        const bool own = (y[i] & 0xFFFFu) != 0;
         const uint64_t a = __ballot(own);
         p_below += lanes_below(a);
         p_own += own;
         p_all += __popcll(a);
-        const uint64_t b = __ballot(x[r][i] >> 16 != 0);
+        const uint64_t b = __ballot(y[i] >> 16 != 0);
         n_below += lanes_below(b);
         n_all += __popcll(b);
       }
-      const uint32_t p_incl = read_lane(g % 2 ? pos_incl[1] : pos_incl[0], g / 2);
-      const uint32_t n_incl = read_lane(g % 2 ? neg_incl[1] : neg_incl[0], g / 2);
       // above zero the order goes down the magnitudes: later groups, later
       // lanes and a lane's later words come first
-      uint32_t at = pos_total - p_incl + (p_all - p_below - p_own);
+      uint32_t at = pos_total - read_lane(pos_incl, g) + (p_all - p_below - p_own);
 #pragma unroll
       for (int i = 3; i >= 0; --i)
-        if (const uint32_t c = x[r][i] & 0xFFFFu) out(at++, kInf - (mag0 + i), c);
-      at = pos_total + n_incl - n_all + n_below;
+        if (const uint32_t c = y[i] & 0xFFFFu) out(at++, kInf - (mag0 + i), c);
+      at = pos_total + (zeros != 0) + read_lane(neg_incl, g) - n_all + n_below;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (const uint32_t c = x[r][i] >> 16) out(at++, kInf + mag0 + i, c);
-    }
+        if (const uint32_t c = y[i] >> 16) out(at++, kInf + mag0 + i, c);
+    });
   }
 };
 
-// The same of kInf words that hold one 32-bit count each: the values of counts
-// that 16 bits may not hold.  A wave takes a run of words; returns the number
-// of entries, after a barrier.
-template <typename Emit>
-__device__ __forceinline__ uint32_t compact_wide(const uint32_t *words, uint32_t *scratch, const Emit &out) {
+// The list of any elements, kWords bins at a time with 32 bits for each:
+// count(first bin) adds up those from that one on in bins->word, and
+// out(index, bin, count) gets the entries.  Returns their number, after a barrier.
+template <typename Count, typename Emit>
+__device__ __forceinline__ uint32_t list_in_passes(Bins *bins, uint32_t *scratch, const Count &count, const Emit &out) {
   constexpr uint32_t kRun = kWords / kWaves;
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  uint32_t mine = 0;
-  for (uint32_t w = wave * kRun + lane; w < (wave + 1) * kRun; w += 64) mine += __popcll(__ballot(w < kInf && words[w]));
-  if (lane == 0) scratch[wave] = mine;
-  __syncthreads();
-  uint32_t next = 0, total = 0;
-  for (uint32_t i = 0; i < kWaves; ++i) {
-    if (i < wave) next += scratch[i];
-    total += scratch[i];
+  uint32_t n = 0;
+#pragma unroll 1
+  for (uint32_t bin0 = 0; bin0 < kBins; bin0 += kWords) {
+    clear(bins);
+    lds_barrier();
+    count(bin0);
+    lds_barrier();
+    uint32_t mine = 0;
+    for (uint32_t w = wave * kRun + lane; w < (wave + 1) * kRun; w += 64) mine += __popcll(__ballot(bins->word[w] != 0));
+    if (lane == 0) scratch[wave] = mine;
+    lds_barrier();
+    uint32_t next = n;
+    for (uint32_t i = 0; i < kWaves; ++i) {
+      if (i < wave) next += scratch[i];
+      n += scratch[i];
+    }
+    for (uint32_t w = wave * kRun + lane; w < (wave + 1) * kRun; w += 64) {
+      const uint32_t c = bins->word[w];
+      const uint64_t b = __ballot(c != 0);
+      if (c) out(next + lanes_below(b), bin0 + w, c);
+      next += __popcll(b);
+    }
+    __syncthreads();
   }
-  for (uint32_t w = wave * kRun + lane; w < (wave + 1) * kRun; w += 64) {
-    const uint32_t c = w < kInf ? words[w] : 0;
-    const uint64_t b = __ballot(c != 0);
-    if (c) out(next + lanes_below(b), w, c);
-    next += __popcll(b);
+  return n;
+}
+__device__ __forceinline__ void count_pass(Bins *bins, const Pieces &pieces, uint32_t bin0) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < pieces.n; ++i) {
+    Held h;
+    h.load(pieces[i]);
+    h.each_one([&](uint32_t v) {
+      const uint32_t b = bin_of(v) - bin0;
+      if (counts(v) && b < kWords) atomicAdd(&bins->word[b], 1u);
+    });
   }
-  __syncthreads();
-  return total;
 }
 
-__device__ __forceinline__ void clear(uint32_t *hist) {
-  v4u *p = reinterpret_cast<v4u *>(hist);
+// The waves' spans, and the elements that are zero.
+struct Spans {
+  uint32_t lo[kWaves], hi[kWaves], zeros;
+};
+// This wave's span for the others, before a barrier; from all lanes' spans.
+__device__ __forceinline__ void share_span(Spans *s, const Span &mine) {
+  const uint32_t hi = wave_max(mine.hi), lo = ~wave_max(~mine.lo);
+  if (threadIdx.x % 64 == 0) {
+    s->lo[wave_number()] = lo;
+    s->hi[wave_number()] = hi;
+  }
+  if (threadIdx.x == 0) s->zeros = 0;
+}
+__device__ __forceinline__ Span join_spans(const Spans &s) {
+  Span r{kNone, 0};
 #pragma unroll
-  for (uint32_t i = 0; i < kWords / 4 / kThreads; ++i) p[i * kThreads + threadIdx.x] = v4u{0, 0, 0, 0};
+  for (int w = 0; w < kWaves; ++w) {
+    r.lo = min(r.lo, s.lo[w]);
+    r.hi = max(r.hi, s.hi[w]);
+  }
+  return r;
+}
+// The lowest magnitude of kWords bins that end at hi.
+__device__ __forceinline__ uint32_t base_of(uint32_t hi) { return hi - min(hi, kWords - 1); }
+__device__ __forceinline__ bool fits(const Span &s) { return s.hi - min(s.lo, s.hi) < kWords; }
+
+// The span of all pieces, of which `held` is the first, and then the counts:
+// pieces that are not held any more are read again, last first.  True if the
+// bins hold the counts, after a barrier; false if their span is too wide.
+__device__ __forceinline__ bool count_pieces(Bins *bins, Spans *spans, const Pieces &pieces, Held *held, Span *all) {
+  clear(bins);
+  uint32_t odd = 0;  // bit i: piece i
+  Span mine{kNone, 0};
+  Held &h = *held;
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    Held next = h;
+    if (i + 1 < pieces.n) next.load(pieces[i + 1]);
+    odd |= widen(&mine, h) ? 1u << i : 0;
+    if (i + 1 == pieces.n) break;
+    h = next;
+  }
+  share_span(spans, mine);
+  lds_barrier();
+  *all = join_spans(*spans);
+  if (!fits(*all)) return false;
+  const uint32_t base = base_of(all->hi);
+#pragma unroll 1
+  for (uint32_t i = pieces.n; i-- > 0;) {
+    Held next = h;
+    if (i > 0) next.load(pieces[i - 1]);
+    count_held(bins, h, odd >> i & 1, base, &spans->zeros);
+    h = next;
+  }
+  lds_barrier();
+  return true;
 }
 
-// What the count leaves of a slice besides its list (bin << 16 | count).
+// What the count leaves of a slice besides its list (bin << 16 | count):
+// entries, the largest count, and the span of magnitudes.
 struct SliceInfo {
-  uint32_t length, most;  // entries, and the largest count
+  uint32_t length, most, lo, hi;
 };
 
-// A workgroup goes from slice to slice, and loads the next piece's elements
+// A workgroup goes from slice to slice, and loads the next one's first piece
 // before it sorts out the counts of the one at hand.
-__global__ __launch_bounds__(kThreads) void sample_count_kernel(Shards sh, uint32_t n_slices, uint32_t jobs,
-                                                                uint64_t row_cap, uint32_t *lists, SliceInfo *infos) {
-  __shared__ __attribute__((aligned(16))) uint32_t hist[kWords];
-  __shared__ GroupCounts counts;
+__global__ __launch_bounds__(kThreads, 4) void sample_count_kernel(Shards sh, uint32_t n_slices, uint32_t jobs,
+                                                                   uint64_t row_cap, uint32_t *lists, SliceInfo *infos) {
+  __shared__ __attribute__((aligned(16))) Bins bins;
+  __shared__ GroupCounts groups;
+  __shared__ Spans spans;
   __shared__ uint32_t most[kWaves];
+  const uint32_t lane = threadIdx.x % 64;
+  Held held;
   uint32_t job = blockIdx.x;
-  Slice slice = slice_of(sh, job / n_slices, job % n_slices);
-  Held held = load_piece(piece_of(slice, 0));
+  held.load(pieces_of(slice_of(sh, job / n_slices, job % n_slices))[0]);
+#pragma unroll 1
   for (; job < jobs; job += gridDim.x) {
-    clear(hist);
-    lds_barrier();
-    count_piece(hist, held);
-    if (slice.cols > kPieceCols) count_piece(hist, load_piece(piece_of(slice, 1)));
-    const uint32_t next = job + gridDim.x;
-    if (next < jobs) {
-      slice = slice_of(sh, next / n_slices, next % n_slices);
-      held = load_piece(piece_of(slice, 0));
-    }
-    lds_barrier();
-    Compact c(hist, &counts);
-    const uint32_t row = job / n_slices, k = job % n_slices, s = k >= sh.slices[0];
+    const uint32_t row = job / n_slices, k = job % n_slices, s = k >= sh.slices[0], next = job + gridDim.x;
+    const Pieces pieces = pieces_of(slice_of(sh, row, k));
+    Span all;
+    const bool fit = count_pieces(&bins, &spans, pieces, &held, &all);
+    if (next < jobs) held.load(pieces_of(slice_of(sh, next / n_slices, next % n_slices))[0]);
     uint32_t *list = lists + row * row_cap + (s ? (uint64_t)sh.slices[0] * sh.width[0] : 0) +
                      (uint64_t)(s ? k - sh.slices[0] : k) * sh.width[s];
-    uint32_t largest = 0;
-    c.emit([&](uint32_t i, uint32_t bin, uint32_t count) {
+    uint32_t largest = 0, n;
+    auto put = [&](uint32_t i, uint32_t bin, uint32_t count) {
       list[i] = bin << 16 | count;
       largest = max(largest, count);
-    });
+    };
+    if (fit) {
+      Compact c(&bins, spans.zeros, &groups);
+      c.emit(base_of(all.hi), put);
+      n = c.total;
+    } else {
+      lds_barrier();  // the bins are cleared again
+      n = list_in_passes(&bins, groups.pos, [&](uint32_t bin0) { count_pass(&bins, pieces, bin0); }, put);
+    }
     largest = wave_max(largest);
-    if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = largest;
-    lds_barrier();  // hist and counts are written again
+    if (lane == 0) most[wave_number()] = largest;
+    lds_barrier();  // bins, groups and spans are written again
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) largest = max(largest, most[w]);
-      infos[job] = SliceInfo{c.total, largest};
+      infos[job] = SliceInfo{n, largest, all.lo, all.hi};
     }
   }
 }
 
+// ----------------------------------------------------------------- searching
+
 struct Scratch {
-  uint32_t slice_length[kMaxSlices], slice_count[kMaxSlices];
+  SliceInfo info[kMaxSlices];
+  uint32_t slice_count[kMaxSlices];
   double mass[kWaves];
   uint32_t count[kWaves];
   uint32_t below;          // the first entry whose weight is below min_p's limit
@@ -369,32 +537,19 @@ struct Scratch {
   float prob;
 };
 
-// Smallest r in [1, most] with before + r * w >= target (OVER: > target).
-template <bool OVER>
-__device__ __forceinline__ uint32_t rank_of(double before, double w, uint32_t most, double target) {
+// Smallest r in [1, most] with before + r * w >= target (over: > target).
+__device__ __forceinline__ uint32_t rank_of(double before, double w, uint32_t most, double target, bool over) {
   const double q = (target - before) / w;
   uint32_t r = q > 1.0 ? (q < (double)most ? (uint32_t)q : most) : 1;
   auto reached = [&](uint32_t k) {
     const double c = before + k * w;
-    return OVER ? c > target : c >= target;
+    return over ? c > target : c >= target;
   };
   // the quotient is off by one step at most
   if (r > 1 && reached(r - 1)) --r;
   if (!reached(r) && r < most) ++r;
   if (!reached(r) && r < most) ++r;
   return r;
-}
-
-// First of n (at most 64 * 16) values for which reached(value index) holds, by
-// one wave; n if none does.  reached is monotone.
-template <typename Reached>
-__device__ __forceinline__ uint32_t first_of_1024(const Reached &reached) {
-  const uint32_t lane = threadIdx.x % 64;
-  const uint64_t coarse = __ballot(reached(lane * 16 + 15));
-  if (!coarse) return kThreads;
-  const uint32_t base = (uint32_t)__builtin_ctzll(coarse) * 16;
-  const uint64_t fine = __ballot(lane < 16 && reached(base + lane % 16));
-  return base + (fine ? (uint32_t)__builtin_ctzll(fine) : 15);
 }
 
 // The cuts and the draw on a list of n > 0 entries: first(i, &count, &weight)
@@ -404,8 +559,8 @@ __device__ __forceinline__ uint32_t first_of_1024(const Reached &reached) {
 // last.  One wave then finds each border: the thread first, then the entry
 // among its own.
 template <typename First, typename Entry>
-__device__ void search(const First &first, const Entry &entry, uint32_t n, const xfer_sample_params &p, float u, double *masses,
-                       uint32_t *counts, Scratch *sc) {
+__device__ __forceinline__ void search(const First &first, const Entry &entry, uint32_t n, const xfer_sample_params &p,
+                                       float u, double *masses, uint32_t *counts, Scratch *sc) {
   const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const uint32_t per = (n + kThreads - 1) / kThreads;
   const uint32_t i0 = min(tid * per, n), i1 = min(i0 + per, n);
@@ -413,6 +568,7 @@ __device__ void search(const First &first, const Entry &entry, uint32_t n, const
   if (tid == 0) sc->below = kNone;
   uint32_t count = 0, below = kNone;
   double mass = 0;
+#pragma unroll 1
   for (uint32_t i = i0; i < i1; ++i) {
     uint32_t c;
     double w;
@@ -435,83 +591,105 @@ __device__ void search(const First &first, const Entry &entry, uint32_t n, const
     const uint32_t wc = scan(lane < kWaves ? sc->count[lane % kWaves] : 0);
     const double wm = scan(lane < kWaves ? sc->mass[lane % kWaves] : 0.0);
     if (wave) {
-      count += read_lane(wc, __builtin_amdgcn_readfirstlane(wave - 1));
-      mass += read_lane(wm, __builtin_amdgcn_readfirstlane(wave - 1));
+      count += read_lane(wc, wave_number() - 1);
+      mass += read_lane(wm, wave_number() - 1);
     }
   }
   counts[tid] = count;
   masses[tid] = mass;
-  __syncthreads();
+  lds_barrier();
   if (wave != 0) return;
 
-  struct Border {
-    uint32_t at, count;  // an entry and its elements
-    uint32_t rank;       // how many of them come up to the border: at first, all
-    uint32_t n_before;   // elements before the entry
-    double before, w;    // the weights before the entry, and of each of its elements
-  };
-  // Among the entries of thread t up to entry `last`, of which `last_count`
-  // elements count at most, the first that reached(running count, running
-  // mass) holds for; the last of them if it holds for none (*none).
-  bool none;
-  auto among = [&](uint32_t t, uint32_t last, uint32_t last_count, const auto &reached) {
-    const uint32_t i = t * per + lane;
-    const bool there = lane < per && i < n && i <= last;
-    uint32_t c = 0;
-    double w = 0;
-    if (there) {
-      entry(i, &c, &w);
-      if (i == last) c = min(c, last_count);
-    }
-    const uint32_t n_run = scan(c) + (t ? counts[t - 1] : 0);
-    const double m_run = scan(c * w) + (t ? masses[t - 1] : 0.0);
-    const uint64_t hit = __ballot(there && reached(n_run, m_run)), all = __ballot(there);
-    none = !hit;
-    const uint32_t l = hit ? (uint32_t)__builtin_ctzll(hit) : 63 - (uint32_t)__builtin_clzll(all);
-    Border b;
-    b.at = t * per + l;
-    b.count = b.rank = read_lane(c, l);
-    b.w = read_lane(w, l);
-    b.n_before = read_lane(n_run, l) - b.count;
-    b.before = l ? read_lane(m_run, l - 1) : t ? masses[t - 1] : 0.0;
-    return b;
-  };
-
-  // top_k
+  // Four borders, one after the other: the last element that top_k keeps, the
+  // first that reaches top_p, the last before min_p's limit, and the drawn one.
+  // f is the last entry kept so far, with `rank` of its elements.
   const uint32_t total = counts[kThreads - 1];
   const bool greedy = !(p.temperature > 0.0f);
   const uint32_t keep = greedy ? 1 : p.top_k == 0 ? total : min(p.top_k, total);
-  uint32_t t = keep == total ? (n - 1) / per : first_of_1024([&](uint32_t s) { return counts[s] >= keep; });
-  Border f = among(t, n - 1, kNone, [&](uint32_t running, double) { return running >= keep; });
-  f.rank = keep - f.n_before;
-  double z = f.before + f.rank * f.w;
-
-  // top_p
-  if (p.top_p < 1.0f) {
-    const double target = (double)p.top_p * z;
-    t = first_of_1024([&](uint32_t s) { return masses[s] >= target; });
-    if (t < kThreads && t * per <= f.at) {
-      const Border b = among(t, f.at, f.rank, [&](uint32_t, double running) { return running >= target; });
-      if (!none || b.at < f.at) {
-        f = b;
-        f.rank = rank_of<false>(b.before, b.w, b.count, target);
-      }
+  struct {
+    uint32_t at, rank;
+    double z;  // weights up to there
+  } f = {n - 1, kNone, 0.0};
+#pragma unroll 1
+  for (int border = 0; border < 4; ++border) {
+    double target = 0;
+    uint32_t t, last = f.at, last_count = f.rank;
+    if (border == 1) {
+      if (!(p.top_p < 1.0f)) continue;
+      target = (double)p.top_p * f.z;
+    } else if (border == 2) {
+      // the first entry's weight is 1, so an entry below the limit has one before it
+      if (sc->below > f.at) continue;
+      last = sc->below - 1;
+      last_count = kNone;
+    } else if (border == 3) {
+      target = u > 0.0f ? (double)u * f.z : 0.0;
     }
-  }
-  // min_p: the first entry's weight is 1, so an entry below it has one before it
-  const uint32_t m_at = sc->below;
-  if (m_at <= f.at) f = among((m_at - 1) / per, m_at - 1, kNone, [](uint32_t, double) { return false; });
-  z = f.before + f.rank * f.w;
-
-  // The draw.
-  const double target = u > 0.0f ? (double)u * z : 0.0;
-  t = first_of_1024([&](uint32_t s) { return masses[s] > target; });
-  if (t * per > f.at) t = f.at / per;
-  const Border d = among(t, f.at, f.rank, [&](uint32_t, double running) { return running > target; });
-  if (lane == 0) {
-    sc->at = d.at;
-    sc->rank = (none ? d.count : rank_of<true>(d.before, d.w, d.count, target)) - 1;
-    sc->prob = (float)(d.w / z);
+    // The thread: its running sums reach the border.
+    auto reached = [&](uint32_t c, double m) {
+      return border == 0 ? c >= keep : border == 1 ? m >= target : border == 3 && m > target;
+    };
+    constexpr uint32_t kStep = kThreads / 64;
+    const uint32_t probe = lane * kStep + kStep - 1;
+    const uint64_t coarse = __ballot(reached(counts[probe], masses[probe]));
+    t = kThreads;
+    if (coarse) {
+      const uint32_t base = (uint32_t)__builtin_ctzll(coarse) * kStep, fine_probe = base + lane % kStep;
+      const uint64_t fine = __ballot(lane < kStep && reached(counts[fine_probe], masses[fine_probe]));
+      t = base + (fine ? (uint32_t)__builtin_ctzll(fine) : kStep - 1);
+    }
+    if (t * per > last) {
+      if (border == 1) continue;  // all of them are kept
+      t = last / per;
+    }
+    // The entry: the first of the thread's, up to `last` with at most
+    // last_count elements, that reaches it, or the last of them.
+    uint32_t n_base = t ? counts[t - 1] : 0, at = 0, c_at = 0, n_before = 0;
+    double m_base = t ? masses[t - 1] : 0.0, before = 0, w_at = 0;
+    bool none = true;
+#pragma unroll 1
+    for (uint32_t c0 = 0; c0 < per && none; c0 += 64) {
+      const uint32_t i = t * per + c0 + lane;
+      const bool there = c0 + lane < per && i < n && i <= last;
+      const uint64_t all = __ballot(there);
+      if (!all) break;
+      uint32_t c = 0;
+      double w = 0;
+      if (there) {
+        entry(i, &c, &w);
+        if (i == last) c = min(c, last_count);
+      }
+      const uint32_t n_run = scan(c) + n_base;
+      const double m_run = scan(c * w) + m_base;
+      const uint64_t hit = __ballot(there && reached(n_run, m_run));
+      none = !hit;
+      const uint32_t l = hit ? (uint32_t)__builtin_ctzll(hit) : 63 - (uint32_t)__builtin_clzll(all);
+      at = t * per + c0 + l;
+      c_at = read_lane(c, l);
+      w_at = read_lane(w, l);
+      n_before = read_lane(n_run, l) - c_at;
+      before = l ? read_lane(m_run, l - 1) : m_base;
+      n_base = read_lane(n_run, 63);
+      m_base = read_lane(m_run, 63);
+    }
+    uint32_t rank = c_at;
+    if (border == 0)
+      rank = keep - n_before;
+    else if (border == 1 && none && at == f.at)
+      continue;  // no cut
+    else if (border != 2 && !none)
+      rank = rank_of(before, w_at, c_at, target, border == 3);
+    if (border == 3) {
+      if (lane == 0) {
+        sc->at = at;
+        sc->rank = rank - 1;
+        sc->prob = (float)(w_at / f.z);
+      }
+    } else {
+      f.at = at;
+      f.rank = rank;
+      f.z = before + rank * w_at;
+    }
   }
 }
 
@@ -519,71 +697,78 @@ __device__ void search(const First &first, const Entry &entry, uint32_t n, const
 // one of 0).
 __device__ __forceinline__ uint32_t zero_half(uint32_t x) { return (x - 0x00010001u) & ~x & 0x80008000u; }
 
-// Column of the rank-th element (from 0) of `bin` in a slice, kNone (to every
-// thread) if it holds no more than rank; *held becomes how many it holds.
-__device__ uint32_t locate(const Slice &s, uint32_t bin, uint32_t rank, uint32_t *held, uint32_t *totals,
-                           uint32_t *place) {
-  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-  const Held h = load_piece(s);
+// The global id of the rank-th element (from 0) of `bin` in the pieces, which
+// hold one.  `totals` (LDS): a number for each round of a wave.
+__device__ __forceinline__ uint32_t locate(const Pieces &pieces, uint32_t bin, uint32_t rank, uint32_t *totals,
+                                           uint32_t *place) {
+  const uint32_t tid = threadIdx.x, wave = wave_number(), lane = tid % 64;
   // zero has two patterns: without its sign it has one
   const uint32_t keep = bin == kInf ? 0x7FFF7FFFu : 0xFFFFFFFFu, two = pattern_of(bin) * 0x10001u;
-  uint32_t match[kRounds];  // bit e: element e of this thread's vector is of the bin
-  if (tid == 0) place[0] = kNone;
+  Held h;
+  h.load(pieces[0]);
+#pragma unroll 1
+  for (uint32_t i = 0;; ++i) {
+    const Slice s = pieces[i];
+    Held next = h;
+    if (i + 1 < pieces.n) next.load(pieces[i + 1]);
+    auto matches = [&](const v4u &x) {
+      uint32_t m = 0;  // bit e: element e of this thread's vector is of the bin
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    match[r] = 0;
-    uint32_t x[4], some = 0;
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t d = (x[j] & keep) ^ two;
+        m |= ((d & 0xFFFFu) == 0) << (2 * j) | (d >> 16 == 0) << (2 * j + 1);
+      }
+      return m;
+    };
+    static_assert(kRounds * kWaves <= 64, "one lane for each round of a wave");
+    if (lane < kRounds) totals[lane * kWaves + wave] = 0;
+    if (tid == 0) place[0] = kNone;
+    h.each([&](uint32_t r, const v4u &x) {
+      uint32_t some = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = (h.w[r][i] & keep) ^ two;
-      some |= zero_half(x[i]);
+      for (int j = 0; j < 4; ++j) some |= zero_half((x[j] & keep) ^ two);
+      if (!__any(some != 0)) return;
+      const uint32_t c = scan((uint32_t)__popc(matches(x)));
+      if (lane == 63) totals[r * kWaves + wave] = c;
+    });
+    // the elements of an incomplete last vector, held by the first threads, come last
+    const bool last = ((h.last & keep) ^ two) >> 16 == 0;
+    const uint64_t lasts = __ballot(last);
+    lds_barrier();
+    if (wave == 0) {
+      const uint32_t c = lane < kRounds * kWaves ? totals[lane % (kRounds * kWaves)] : 0, incl = scan(c);
+      if (incl - c <= rank && rank < incl) {
+        place[0] = lane;
+        place[1] = rank - (incl - c);
+      }
+      const uint32_t vectors = read_lane(incl, 63);
+      if (last && vectors + lanes_below(lasts) == rank) {
+        place[0] = 64;
+        place[3] = s.cols / 8 * 8 + lane;
+      }
+      if (lane == 0) place[2] = vectors + __popcll(lasts);
     }
-    uint32_t c = 0;
-    if (__any(some != 0)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) match[r] |= ((x[i] & 0xFFFFu) == 0) << (2 * i) | (x[i] >> 16 == 0) << (2 * i + 1);
-      c = read_lane(scan((uint32_t)__popc(match[r])), 63);
+    lds_barrier();
+    const uint32_t at = place[0];
+    if (at != kNone) {
+      h.each([&](uint32_t r, const v4u &x) {
+        if (at != r * kWaves + wave) return;
+        uint32_t m = matches(x), left = place[1];
+        const uint32_t c = __popc(m), incl = scan(c);
+        if (incl - c <= left && left < incl) {
+          left -= incl - c;
+          for (; left; --left) m &= m - 1;
+          place[3] = (r * kThreads + tid) * 8 + (uint32_t)__builtin_ctz(m);
+        }
+      });
+      lds_barrier();
+      return s.gid + place[3];
     }
-    if (lane == 0) totals[r * kWaves + wave] = c;
+    rank -= place[2];
+    if (i + 1 == pieces.n) return s.gid;  // does not happen
+    h = next;
+    lds_barrier();  // totals and place are written again
   }
-  // the elements of an incomplete last vector, held by the first threads, come last
-  const bool last = ((h.last & keep) ^ two) >> 16 == 0;
-  const uint64_t lasts = __ballot(last);
-  __syncthreads();
-  if (wave == 0) {
-    static_assert(kRounds * kWaves == 64, "one lane for each round of a wave");
-    const uint32_t c = totals[lane];
-    const uint32_t incl = scan(c);
-    if (incl - c <= rank && rank < incl) {
-      place[0] = lane;
-      place[1] = rank - (incl - c);
-    }
-    const uint32_t vectors = read_lane(incl, 63);
-    if (last && vectors + lanes_below(lasts) == rank) {
-      place[0] = 64;
-      place[3] = s.cols / 8 * 8 + lane;
-    }
-    if (lane == 0) place[2] = vectors + __popcll(lasts);
-  }
-  __syncthreads();
-  *held = place[2];
-  const uint32_t at = place[0];
-  if (at == kNone) return kNone;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    if (at != r * kWaves + wave) continue;
-    const uint32_t c = __popc(match[r]);
-    const uint32_t incl = scan(c);
-    uint32_t left = place[1];
-    if (incl - c <= left && left < incl) {
-      left -= incl - c;
-      uint32_t m = match[r];
-      for (; left; --left) m &= m - 1;
-      place[3] = (r * kThreads + tid) * 8 + (uint32_t)__builtin_ctz(m);
-    }
-  }
-  __syncthreads();
-  return place[3];
 }
 
 struct DrawArgs {
@@ -650,11 +835,11 @@ __device__ __forceinline__ Ahead load_ahead(const DrawArgs &a, uint32_t row, con
 
 // visit(entry) of every entry of a row's lists.
 template <typename Visit>
-__device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const uint32_t *lengths, const Share &h,
+__device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const SliceInfo *info, const Share &h,
                                           const Ahead &ahead, const Visit &visit) {
   for (uint32_t k = h.k0; k < a.n_slices; k += h.groups) {
     const uint32_t *list = list_of(a, row, k);
-    const uint32_t n = lengths[k];
+    const uint32_t n = info[k].length;
     for (uint32_t i = h.i0; i < n; i += kAtOnce * h.step) {
       Ahead r = ahead;
       if (k != h.k0 || i != h.i0) {
@@ -669,144 +854,140 @@ __device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const
   }
 }
 
-// ONE: the row is counted here (both shards hold at most kPieceCols columns
+// ONE: the row is counted here (both shards hold at most kOneCols columns
 // together); else its slices' lists are added up.
 template <bool ONE>
-__global__ __launch_bounds__(kThreads) void sample_draw_kernel(DrawArgs a) {
-  __shared__ __attribute__((aligned(16))) uint32_t lds[kWords];
+__global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(DrawArgs a) {
+  // Weights take the place of the bins.
+  __shared__ __attribute__((aligned(16))) union {
+    Bins bins;
+    double weights[kLdsEntries];
+  } lds;
   __shared__ uint32_t list[kLdsEntries];  // bin << 16 | count
-  __shared__ GroupCounts counts;
-  __shared__ uint32_t totals[64];
+  __shared__ double masses[kThreads];
+  __shared__ uint32_t sums[kThreads];
+  __shared__ GroupCounts groups;
+  __shared__ Spans spans;
+  __shared__ uint32_t totals[kRounds * kWaves];
   __shared__ Scratch sc;
-  const uint32_t row = blockIdx.x, tid = threadIdx.x;
+  const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid % 64;
   uint2 *merged = a.merged + row * a.merged_cap;
   const xfer_sample_params p = a.params[row];
   const float u = a.u[row];
 
-  // The row's list: in LDS if counts fit 16 bits and it is no longer than
-  // kLdsEntries, else in the workspace.
-  uint32_t n = 0;
-  bool packed = true;
+  // The row's counts: in the bins if they fit 16 bits and the bins hold their
+  // span (`packed`).
   const Share share = share_of(ONE ? 1 : a.n_slices);
   Ahead ahead{};
+  Pieces pieces = ONE ? pieces_of(slice_of(a.sh, row, 0), slice_of(a.sh, row, 1)) : Pieces{};
+  Span all;
+  bool packed;
   if (ONE) {
-    const Held h0 = load_piece(slice_of(a.sh, row, 0)), h1 = load_piece(slice_of(a.sh, row, 1));
-    clear(lds);
-    lds_barrier();
-    count_piece(lds, h0);
-    count_piece(lds, h1);
-    lds_barrier();
+    Held held;
+    held.load(pieces[0]);
+    packed = count_pieces(&lds.bins, &spans, pieces, &held, &all);
   } else {
-    SliceInfo info{0, 0};
+    SliceInfo info{0, 0, kNone, 0};
     if (tid < a.n_slices) info = a.infos[row * a.n_slices + tid];
     ahead = load_ahead(a, row, share);
-    clear(lds);
-    if (tid < kMaxSlices) {  // the first two waves
-      sc.slice_length[tid] = info.length;
-      const uint32_t most = scan(info.most);
-      if (tid % 64 == 63) sc.count[tid / 64] = most;
-    }
+    clear(&lds.bins);
+    if (tid < kMaxSlices) sc.info[tid] = info;
+    const uint32_t most = scan(info.most);
+    if (lane == 63) sc.count[wave_number()] = most;
+    share_span(&spans, Span{info.lo, info.hi});
     lds_barrier();
-    packed = sc.count[0] + sc.count[1] <= 0xFFFFu;  // no value can occur more often than that
+    all = join_spans(spans);
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += sc.count[w];
+    packed = sum <= 0xFFFFu && fits(all);  // no value can occur more often than that
     if (packed) {
-      for_lists(a, row, sc.slice_length, share, ahead, [&](uint32_t e) {
+      const uint32_t base = base_of(all.hi);
+      for_lists(a, row, sc.info, share, ahead, [&](uint32_t e) {
         const uint32_t b = e >> 16, c = e & 0xFFFFu;
-        if (b < kInf)
-          atomicAdd(&lds[kInf - b], c);
-        else
-          atomicAdd(&lds[b - kInf], c << 16);
+        uint32_t *to = b == kInf ? &spans.zeros : &lds.bins.word[(b < kInf ? kInf - b : b - kInf) - base];
+        atomicAdd(to, b > kInf ? c << 16 : c);
       });
       lds_barrier();
     }
   }
-  if (packed) {
-    Compact c(lds, &counts);
-    n = c.total;
-    if (n <= kLdsEntries)
-      c.emit([&](uint32_t i, uint32_t bin, uint32_t count) { list[i] = bin << 16 | count; });
+
+  // The row's list: in LDS if it is no longer than kLdsEntries, else in the
+  // workspace.
+  uint32_t n;
+  bool near = false;
+  auto put = [&](uint32_t i, uint32_t bin, uint32_t count) {
+    if (near)
+      list[i] = bin << 16 | count;
     else
-      c.emit([&](uint32_t i, uint32_t bin, uint32_t count) { merged[i] = make_uint2(bin, count); });
-    __syncthreads();
+      merged[i] = make_uint2(bin, count);
+  };
+  if (packed) {
+    Compact c(&lds.bins, spans.zeros, &groups);
+    n = c.total;
+    near = n <= kLdsEntries;
+    c.emit(base_of(all.hi), put);
   } else {
-    // One half of the values at a time, 32 bits for each (lds is clear for the first).
-#pragma unroll 1
-    for (uint32_t half = 0; half < 2; ++half) {
-      for_lists(a, row, sc.slice_length, share, ahead, [&](uint32_t e) {
-        const uint32_t b = (e >> 16) - half * kInf;
-        if (b < kInf) atomicAdd(&lds[b], e & 0xFFFFu);
-      });
-      __syncthreads();
-      n += compact_wide(lds, totals, [&](uint32_t i, uint32_t bin, uint32_t count) {
-        merged[n + i] = make_uint2(half * kInf + bin, count);
-      });
-      clear(lds);
-      __syncthreads();
-    }
+    lds_barrier();  // the bins are cleared again
+    n = list_in_passes(&lds.bins, groups.pos, [&](uint32_t bin0) {
+      if (ONE) {
+        count_pass(&lds.bins, pieces, bin0);
+      } else {
+        for_lists(a, row, sc.info, share, ahead, [&](uint32_t e) {
+          const uint32_t b = (e >> 16) - bin0;
+          if (b < kWords) atomicAdd(&lds.bins.word[b], e & 0xFFFFu);
+        });
+      }
+    }, put);
   }
+  __syncthreads();
   if (n == 0) {
     if (tid == 0) a.out[row] = xfer_sampled{0.0f, -1};
     return;
   }
 
-  const bool in_lds = packed && n <= kLdsEntries;
   const double per_t = p.temperature > 0.0f ? 1.0 / (double)p.temperature : 1.0;
-  const double top = value_of(in_lds ? list[0] >> 16 : merged[0].x);
+  auto bin_at = [&](uint32_t i) { return near ? list[i] >> 16 : merged[i].x; };
+  const double top = value_of(bin_at(0));
   const bool top_inf = isinf(top);
-  auto weight = [&](uint32_t i, uint32_t bin) -> double {
-    if (i == 0) return 1.0;
-    return top_inf ? 0.0 : exp((value_of(bin) - top) * per_t);
+  auto weight = [&](uint32_t i) { return i == 0 ? 1.0 : top_inf ? 0.0 : exp((value_of(bin_at(i)) - top) * per_t); };
+  auto first = [&](uint32_t i, uint32_t *c, double *w) {
+    *c = near ? list[i] & 0xFFFFu : merged[i].y;
+    *w = weight(i);
+    if (near) lds.weights[i] = *w;
   };
-  // The bins are done with: weights and running sums take their place.
-  double *weights = reinterpret_cast<double *>(lds), *masses = weights + kLdsEntries;
-  uint32_t *sums = reinterpret_cast<uint32_t *>(masses + kThreads);
-  static_assert(kLdsEntries * 8 + kThreads * 12 <= kWords * 4, "they fit");
-  if (in_lds) {
-    auto entry = [&](uint32_t i, uint32_t *c, double *w) { *c = list[i] & 0xFFFFu, *w = weights[i]; };
-    auto first = [&](uint32_t i, uint32_t *c, double *w) {
-      const uint32_t e = list[i];
-      *c = e & 0xFFFFu;
-      weights[i] = *w = weight(i, e >> 16);
-    };
-    search(first, entry, n, p, u, masses, sums, &sc);
-  } else {
-    auto entry = [&](uint32_t i, uint32_t *c, double *w) {
-      const uint2 e = merged[i];
-      *c = e.y, *w = weight(i, e.x);
-    };
-    search(entry, entry, n, p, u, masses, sums, &sc);
-  }
+  auto entry = [&](uint32_t i, uint32_t *c, double *w) {
+    *c = near ? list[i] & 0xFFFFu : merged[i].y;
+    *w = near ? lds.weights[i] : weight(i);
+  };
+  search(first, entry, n, p, u, masses, sums, &sc);
   __syncthreads();
-  const uint32_t bin = in_lds ? list[sc.at] >> 16 : merged[sc.at].x;
-  uint32_t rank = sc.rank, k = 0;
+  const uint32_t bin = bin_at(sc.at);
+  uint32_t rank = sc.rank;
   if (!ONE) {
     // How many of the value each slice holds: its list is in order.
-    for (uint32_t s = tid / 64; s < a.n_slices; s += kWaves) {
-      const uint32_t c = count_in_list(list_of(a, row, s), sc.slice_length[s], bin);
-      if (tid % 64 == 0) sc.slice_count[s] = c;
+    uint32_t k = 0;
+    for (uint32_t j = wave_number(); j < a.n_slices; j += kWaves) {
+      const uint32_t c = count_in_list(list_of(a, row, j), sc.info[j].length, bin);
+      if (lane == 0) sc.slice_count[j] = c;
     }
-    __syncthreads();
+    lds_barrier();
     while (k + 1 < a.n_slices && rank >= sc.slice_count[k]) rank -= sc.slice_count[k++];
+    pieces = pieces_of(slice_of(a.sh, row, k));
   }
-  // In one of two pieces: the slice's, or the row's two shards.
-  uint32_t held;
-  Slice s = ONE ? slice_of(a.sh, row, 0) : piece_of(slice_of(a.sh, row, k), 0);
-  uint32_t col = locate(s, bin, rank, &held, totals, sc.place);
-  if (col == kNone) {
-    lds_barrier();  // place is written again
-    s = ONE ? slice_of(a.sh, row, 1) : piece_of(slice_of(a.sh, row, k), 1);
-    col = locate(s, bin, rank - held, &held, totals, sc.place);
-  }
-  if (tid == 0) a.out[row] = xfer_sampled{sc.prob, (int32_t)(s.gid + col)};
+  const uint32_t id = locate(pieces, bin, rank, totals, sc.place);
+  if (tid == 0) a.out[row] = xfer_sampled{sc.prob, (int32_t)id};
 }
 
 uint32_t round_up8(uint32_t x) { return (x + 7u) & ~7u; }
+uint32_t cut(uint32_t cols, uint32_t most) { return cols / most + (cols % most != 0); }
 
 }  // namespace
 
 // Slices of the narrower kind that a row is cut into, at most.
 uint32_t sample_slices(uint32_t ncols0, uint32_t ncols1) {
-  if ((uint64_t)ncols0 + ncols1 <= kPieceCols) return 1;
-  return (ncols0 + kSliceCols - 1) / kSliceCols + (ncols1 + kSliceCols - 1) / kSliceCols;
+  if ((uint64_t)ncols0 + ncols1 <= kOneCols) return 1;
+  return cut(ncols0, kPieceCols) + cut(ncols1, kPieceCols);
 }
 
 namespace {
@@ -818,12 +999,15 @@ struct Sizes {
 };
 Sizes sizes_of(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
   Sizes z{};
-  z.one = (uint64_t)ncols0 + ncols1 <= kPieceCols;
+  z.one = (uint64_t)ncols0 + ncols1 <= kOneCols;
   const uint32_t n[2] = {ncols0, ncols1};
-  const uint32_t most = (uint64_t)rows * sample_slices(n[0], n[1]) <= kCountWorkgroups ? kSliceCols : kWideSliceCols;
+  uint32_t most = z.one ? kOneCols : kPieceCols;
+  auto slices = [&] { return cut(n[0], most) + cut(n[1], most); };
+  while (!z.one && most < kWideSliceCols && (slices() > kMaxSlices || (uint64_t)rows * slices() > kCountWorkgroups))
+    most = most * 2 < kWideSliceCols ? most * 2 : kWideSliceCols;
   for (int i = 0; i < 2; ++i) {
-    z.slices[i] = (n[i] + most - 1) / most;
-    z.width[i] = round_up8((n[i] + z.slices[i] - 1) / z.slices[i]);
+    z.slices[i] = cut(n[i], most);
+    z.width[i] = round_up8(cut(n[i], z.slices[i]));
     z.row_cap += (uint64_t)z.slices[i] * z.width[i];
   }
   z.merged_cap = z.row_cap < kBins ? z.row_cap : kBins;
@@ -834,7 +1018,8 @@ uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
 
 }  // namespace
 
-// Layout: the rows' merged lists, the slices' lengths, the slices' lists.
+// Layout: the rows' lists that LDS does not hold, what the count leaves of each
+// slice, the slices' lists.
 uint64_t sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
   const Sizes z = sizes_of(rows, ncols0, ncols1);
   uint64_t n = rows * z.merged_cap * 8;
