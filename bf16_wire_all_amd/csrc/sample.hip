@@ -36,8 +36,6 @@
 namespace xfer {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr uint32_t kInf = 0x7F80u;               // the pattern of +inf; -inf has the sign bit too
 // Values in the row's order, +inf first: positive patterns count down, zero
 // (of either sign) is bin kInf, negative ones count up.
@@ -48,9 +46,9 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 // that would have none, else up to as many as 16 bits count.
 constexpr uint32_t kPieceCols = 16384, kWideSliceCols = 65528;
 constexpr uint32_t kOneCols = 32768;             // of a row that one launch counts
-constexpr uint32_t kLdsEntries = 5888;           // lists up to this long stay in LDS
 constexpr uint32_t kMaxSlices = 128;
-constexpr uint32_t kCountWorkgroups = 512;       // two on each compute unit
+constexpr uint32_t kComputeUnits = 256;
+constexpr uint32_t kCountWorkgroups = 2 * kComputeUnits;
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned short v2us __attribute__((ext_vector_type(2)));
@@ -142,12 +140,37 @@ __device__ __forceinline__ uint32_t read_lane(uint32_t x, uint32_t lane) {
 }
 
 
+// What the count leaves of a slice besides its list (bin << 16 | count):
+// entries, the largest count, and the span of magnitudes.
+struct SliceInfo {
+  uint32_t length, most, lo, hi;
+};
+
+struct DrawArgs {
+  Shards sh;
+  const xfer_sample_params *params;
+  const float *u;
+  xfer_sampled *out;
+  const uint32_t *lists;    // per slice (two launches)
+  const SliceInfo *infos;
+  uint2 *merged;            // a row's list where LDS does not hold it: (bin, count)
+  uint64_t row_cap, merged_cap;
+  uint32_t n_slices;
+};
+
+// A workgroup of kThreads: 16 waves where a compute unit has one workgroup to
+// run, 8 where it has more and two share it.
+template <int kThreads>
+struct Team {
+static constexpr int kWaves = kThreads / 64;
+static constexpr uint32_t kLdsEntries = kThreads == 512 ? 5888 : 8192;  // lists up to this long stay in LDS
+
 // ------------------------------------------------------ pieces in registers
 
 // Elements of a piece, all loads in flight at once.  Lanes past its end hold
 // -inf, which counts nowhere.
-constexpr uint32_t kMasked = 0xFF80FF80u;
-constexpr int kRounds = kPieceCols / 8 / kThreads;
+static constexpr uint32_t kMasked = 0xFF80FF80u;
+static constexpr int kRounds = kPieceCols / 8 / kThreads;
 struct Held {
   v4u w[kRounds];
   uint32_t last;   // one element of an incomplete last vector, above another of -inf
@@ -180,6 +203,13 @@ struct Held {
       for (int i = 1; i < kRounds; ++i) x[i - 1] = x[i];
     }
   }
+  // The same with the rounds one after the other in code, for a short visit.
+  template <typename Visit>
+  __device__ __forceinline__ void each_short(const Visit &visit) const {
+#pragma unroll
+    for (uint32_t r = 0; r < kRounds; ++r)
+      if (r * kThreads + wave_number() * 64 < n_vec) visit(r, w[r]);
+  }
   // one(element) of every element.
   template <typename One>
   __device__ __forceinline__ void each_one(const One &one) const {
@@ -205,11 +235,11 @@ struct Pieces {
     return {ptr, min(kPieceCols, (second ? s[1].cols : s[0].cols) - c0), (second ? s[1].gid : s[0].gid) + c0};
   }
 };
-__device__ __forceinline__ Pieces pieces_of(const Slice &a) {
+__device__ __forceinline__ static Pieces pieces_of(const Slice &a) {
   const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
   return {{a, a}, n, n};
 }
-__device__ __forceinline__ Pieces pieces_of(const Slice &a, const Slice &b) {
+__device__ __forceinline__ static Pieces pieces_of(const Slice &a, const Slice &b) {
   const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
   return {{a, b}, n, n + max(1u, (b.cols + kPieceCols - 1) / kPieceCols)};
 }
@@ -220,9 +250,9 @@ struct Span {
 };
 // Widens this lane's span by its elements of a piece, zero and what does not
 // count left out; whether the wave's piece holds any of those.
-__device__ __forceinline__ bool widen(Span *s, const Held &h) {
+__device__ __forceinline__ static bool widen(Span *s, const Held &h) {
   v2us top = {0, 0}, low = {0xFFFF, 0xFFFF};
-  h.each([&](uint32_t, const v4u &x) {
+  h.each_short([&](uint32_t, const v4u &x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const v2us m = __builtin_bit_cast(v2us, x[i] & 0x7FFF7FFFu);
@@ -252,7 +282,7 @@ struct Bins {
   uint32_t word[kWords];
 };
 
-__device__ __forceinline__ void clear(Bins *bins) {
+__device__ __forceinline__ static void clear(Bins *bins) {
   v4u *p = reinterpret_cast<v4u *>(bins->word);
 #pragma unroll
   for (uint32_t i = 0; i < kWords / 4 / kThreads; ++i) p[i * kThreads + threadIdx.x] = v4u{0, 0, 0, 0};
@@ -260,10 +290,10 @@ __device__ __forceinline__ void clear(Bins *bins) {
 
 // Counts a wave's elements of a piece in the bins of magnitudes base .. base +
 // kWords - 1, which have to hold all of them but zero; *zeros takes the zeros.
-__device__ __forceinline__ void count_held(Bins *bins, const Held &h, bool odd, uint32_t base, uint32_t *zeros) {
+__device__ __forceinline__ static void count_held(Bins *bins, const Held &h, bool odd, uint32_t base, uint32_t *zeros) {
   uint32_t *word = bins->word;
   if (!odd) {
-    h.each([&](uint32_t, const v4u &x) {
+    h.each_short([&](uint32_t, const v4u &x) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         atomicAdd(&word[(x[i] & 0x7FFFu) - base], (x[i] >> 15 & 1u) * 0xFFFFu + 1u);
@@ -286,7 +316,7 @@ __device__ __forceinline__ void count_held(Bins *bins, const Held &h, bool odd, 
 // The entries of the bins, in order.  The words go in groups of 256, a lane
 // four in a row, group after group round the waves; the constructor returns
 // once every group's numbers are known.
-constexpr int kGroups = kWords / 256;
+static constexpr int kGroups = kWords / 256;
 struct GroupCounts {
   uint32_t pos[kGroups], neg[kGroups];
 };
@@ -374,7 +404,7 @@ struct Compact {
 // count(first bin) adds up those from that one on in bins->word, and
 // out(index, bin, count) gets the entries.  Returns their number, after a barrier.
 template <typename Count, typename Emit>
-__device__ __forceinline__ uint32_t list_in_passes(Bins *bins, uint32_t *scratch, const Count &count, const Emit &out) {
+__device__ __forceinline__ static uint32_t list_in_passes(Bins *bins, uint32_t *scratch, const Count &count, const Emit &out) {
   constexpr uint32_t kRun = kWords / kWaves;
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
   uint32_t n = 0;
@@ -403,7 +433,7 @@ __device__ __forceinline__ uint32_t list_in_passes(Bins *bins, uint32_t *scratch
   }
   return n;
 }
-__device__ __forceinline__ void count_pass(Bins *bins, const Pieces &pieces, uint32_t bin0) {
+__device__ __forceinline__ static void count_pass(Bins *bins, const Pieces &pieces, uint32_t bin0) {
 #pragma unroll 1
   for (uint32_t i = 0; i < pieces.n; ++i) {
     Held h;
@@ -420,7 +450,7 @@ struct Spans {
   uint32_t lo[kWaves], hi[kWaves], zeros;
 };
 // This wave's span for the others, before a barrier; from all lanes' spans.
-__device__ __forceinline__ void share_span(Spans *s, const Span &mine) {
+__device__ __forceinline__ static void share_span(Spans *s, const Span &mine) {
   const uint32_t hi = wave_max(mine.hi), lo = ~wave_max(~mine.lo);
   if (threadIdx.x % 64 == 0) {
     s->lo[wave_number()] = lo;
@@ -428,7 +458,7 @@ __device__ __forceinline__ void share_span(Spans *s, const Span &mine) {
   }
   if (threadIdx.x == 0) s->zeros = 0;
 }
-__device__ __forceinline__ Span join_spans(const Spans &s) {
+__device__ __forceinline__ static Span join_spans(const Spans &s) {
   Span r{kNone, 0};
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -438,13 +468,13 @@ __device__ __forceinline__ Span join_spans(const Spans &s) {
   return r;
 }
 // The lowest magnitude of kWords bins that end at hi.
-__device__ __forceinline__ uint32_t base_of(uint32_t hi) { return hi - min(hi, kWords - 1); }
-__device__ __forceinline__ bool fits(const Span &s) { return s.hi - min(s.lo, s.hi) < kWords; }
+__device__ __forceinline__ static uint32_t base_of(uint32_t hi) { return hi - min(hi, kWords - 1); }
+__device__ __forceinline__ static bool fits(const Span &s) { return s.hi - min(s.lo, s.hi) < kWords; }
 
 // The span of all pieces, of which `held` is the first, and then the counts:
 // pieces that are not held any more are read again, last first.  True if the
 // bins hold the counts, after a barrier; false if their span is too wide.
-__device__ __forceinline__ bool count_pieces(Bins *bins, Spans *spans, const Pieces &pieces, Held *held, Span *all) {
+__device__ __forceinline__ static bool count_pieces(Bins *bins, Spans *spans, const Pieces &pieces, Held *held, Span *all) {
   clear(bins);
   uint32_t odd = 0;  // bit i: piece i
   Span mine{kNone, 0};
@@ -473,16 +503,10 @@ __device__ __forceinline__ bool count_pieces(Bins *bins, Spans *spans, const Pie
   return true;
 }
 
-// What the count leaves of a slice besides its list (bin << 16 | count):
-// entries, the largest count, and the span of magnitudes.
-struct SliceInfo {
-  uint32_t length, most, lo, hi;
-};
-
 // A workgroup goes from slice to slice, and loads the next one's first piece
 // before it sorts out the counts of the one at hand.
-__global__ __launch_bounds__(kThreads, 4) void sample_count_kernel(Shards sh, uint32_t n_slices, uint32_t jobs,
-                                                                   uint64_t row_cap, uint32_t *lists, SliceInfo *infos) {
+__device__ __forceinline__ static void count(const Shards &sh, uint32_t n_slices, uint32_t jobs, uint64_t row_cap,
+                                      uint32_t *lists, SliceInfo *infos) {
   __shared__ __attribute__((aligned(16))) Bins bins;
   __shared__ GroupCounts groups;
   __shared__ Spans spans;
@@ -531,14 +555,14 @@ struct Scratch {
   uint32_t slice_count[kMaxSlices];
   double mass[kWaves];
   uint32_t count[kWaves];
-  uint32_t below;          // the first entry whose weight is below min_p's limit
+  uint32_t below[kWaves];  // a wave's first entry whose weight is below min_p's limit
   uint32_t place[4];
   uint32_t at, rank;       // the drawn entry, and the drawn element's place among its equals
   float prob;
 };
 
 // Smallest r in [1, most] with before + r * w >= target (over: > target).
-__device__ __forceinline__ uint32_t rank_of(double before, double w, uint32_t most, double target, bool over) {
+__device__ __forceinline__ static uint32_t rank_of(double before, double w, uint32_t most, double target, bool over) {
   const double q = (target - before) / w;
   uint32_t r = q > 1.0 ? (q < (double)most ? (uint32_t)q : most) : 1;
   auto reached = [&](uint32_t k) {
@@ -553,19 +577,20 @@ __device__ __forceinline__ uint32_t rank_of(double before, double w, uint32_t mo
 }
 
 // The cuts and the draw on a list of n > 0 entries: first(i, &count, &weight)
-// once for each entry, then entry(i, &count, &weight).
-// Thread t sums up entries [t * per, (t + 1) * per); `masses` and `counts`
-// (LDS, one for each thread) become the running sums up to each thread's
-// last.  One wave then finds each border: the thread first, then the entry
-// among its own.
+// once for each entry, then entry(i, &count, &weight); `keep` elements are left
+// by top_k.  Thread t sums up entries [t * per, (t + 1) * per); `masses` and
+// `counts` (LDS, one for each thread) become the running sums of each wave.
+// One wave then finds each border: the wave first, then the thread, then the
+// entry among its own.
 template <typename First, typename Entry>
-__device__ __forceinline__ void search(const First &first, const Entry &entry, uint32_t n, const xfer_sample_params &p,
-                                       float u, double *masses, uint32_t *counts, Scratch *sc) {
-  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+__device__ __forceinline__ static void search(const First &first, const Entry &entry, uint32_t n, uint32_t keep,
+                                       const xfer_sample_params &p, float u, double *masses, uint32_t *counts,
+                                       Scratch *sc) {
+  const uint32_t tid = threadIdx.x, wave = wave_number(), lane = tid % 64;
+  if (n <= 64 && wave) return;  // the first wave holds all entries
   const uint32_t per = (n + kThreads - 1) / kThreads;
   const uint32_t i0 = min(tid * per, n), i1 = min(i0 + per, n);
   const double least = p.min_p > 1.0f ? 1.0 : (double)p.min_p;
-  if (tid == 0) sc->below = kNone;
   uint32_t count = 0, below = kNone;
   double mass = 0;
 #pragma unroll 1
@@ -579,33 +604,29 @@ __device__ __forceinline__ void search(const First &first, const Entry &entry, u
   }
   count = scan(count);
   mass = scan(mass);
+  counts[tid] = count;
+  masses[tid] = mass;
+  const uint64_t any_below = __ballot(below != kNone);
+  if (any_below) below = read_lane(below, (uint32_t)__builtin_ctzll(any_below));
   if (lane == 63) {
     sc->count[wave] = count;
     sc->mass[wave] = mass;
+    sc->below[wave] = below;
   }
-  __syncthreads();
-  const uint64_t any_below = __ballot(below != kNone);
-  if (any_below && lane == (uint32_t)__builtin_ctzll(any_below)) atomicMin(&sc->below, below);
-  {
-    // the waves before this one, in order
-    const uint32_t wc = scan(lane < kWaves ? sc->count[lane % kWaves] : 0);
-    const double wm = scan(lane < kWaves ? sc->mass[lane % kWaves] : 0.0);
-    if (wave) {
-      count += read_lane(wc, wave_number() - 1);
-      mass += read_lane(wm, wave_number() - 1);
-    }
-  }
-  counts[tid] = count;
-  masses[tid] = mass;
-  lds_barrier();
+  if (n > 64) __syncthreads();
   if (wave != 0) return;
+
+  // Of lane w: the running sums up to wave w's end, and the first entry whose
+  // weight is below min_p's limit.
+  const bool is_wave = lane < kWaves && (n > 64 || lane == 0);
+  const uint32_t wave_counts = scan(is_wave ? sc->count[lane % kWaves] : 0);
+  const double wave_masses = scan(is_wave ? sc->mass[lane % kWaves] : 0.0);
+  const uint32_t m_at = ~wave_max(~(is_wave ? sc->below[lane % kWaves] : kNone));
 
   // Four borders, one after the other: the last element that top_k keeps, the
   // first that reaches top_p, the last before min_p's limit, and the drawn one.
   // f is the last entry kept so far, with `rank` of its elements.
-  const uint32_t total = counts[kThreads - 1];
-  const bool greedy = !(p.temperature > 0.0f);
-  const uint32_t keep = greedy ? 1 : p.top_k == 0 ? total : min(p.top_k, total);
+  keep = min(keep, read_lane(wave_counts, 63));
   struct {
     uint32_t at, rank;
     double z;  // weights up to there
@@ -619,33 +640,43 @@ __device__ __forceinline__ void search(const First &first, const Entry &entry, u
       target = (double)p.top_p * f.z;
     } else if (border == 2) {
       // the first entry's weight is 1, so an entry below the limit has one before it
-      if (sc->below > f.at) continue;
-      last = sc->below - 1;
+      if (m_at > f.at) continue;
+      last = m_at - 1;
       last_count = kNone;
     } else if (border == 3) {
       target = u > 0.0f ? (double)u * f.z : 0.0;
     }
-    // The thread: its running sums reach the border.
+    // The wave and the thread whose running sums reach the border.
     auto reached = [&](uint32_t c, double m) {
       return border == 0 ? c >= keep : border == 1 ? m >= target : border == 3 && m > target;
     };
-    constexpr uint32_t kStep = kThreads / 64;
-    const uint32_t probe = lane * kStep + kStep - 1;
-    const uint64_t coarse = __ballot(reached(counts[probe], masses[probe]));
+    const uint64_t waves = __ballot(is_wave && reached(wave_counts, wave_masses));
+    uint32_t n_base = 0;
+    double m_base = 0;
     t = kThreads;
-    if (coarse) {
-      const uint32_t base = (uint32_t)__builtin_ctzll(coarse) * kStep, fine_probe = base + lane % kStep;
-      const uint64_t fine = __ballot(lane < kStep && reached(counts[fine_probe], masses[fine_probe]));
-      t = base + (fine ? (uint32_t)__builtin_ctzll(fine) : kStep - 1);
+    if (waves) {
+      const uint32_t w = (uint32_t)__builtin_ctzll(waves);
+      const uint32_t n_wave = w ? read_lane(wave_counts, w - 1) : 0;
+      const double m_wave = w ? read_lane(wave_masses, w - 1) : 0.0;
+      const uint32_t n_run = counts[w * 64 + lane] + n_wave;
+      const double m_run = masses[w * 64 + lane] + m_wave;
+      const uint64_t threads = __ballot(reached(n_run, m_run));
+      const uint32_t l = threads ? (uint32_t)__builtin_ctzll(threads) : 63;
+      t = w * 64 + l;
+      n_base = l ? read_lane(n_run, l - 1) : n_wave;
+      m_base = l ? read_lane(m_run, l - 1) : m_wave;
     }
     if (t * per > last) {
       if (border == 1) continue;  // all of them are kept
       t = last / per;
+      const uint32_t w = t / 64, l = t % 64;
+      n_base = (w ? read_lane(wave_counts, w - 1) : 0) + (l ? counts[t - 1] : 0);
+      m_base = (w ? read_lane(wave_masses, w - 1) : 0.0) + (l ? masses[t - 1] : 0.0);
     }
     // The entry: the first of the thread's, up to `last` with at most
     // last_count elements, that reaches it, or the last of them.
-    uint32_t n_base = t ? counts[t - 1] : 0, at = 0, c_at = 0, n_before = 0;
-    double m_base = t ? masses[t - 1] : 0.0, before = 0, w_at = 0;
+    uint32_t at = 0, c_at = 0, n_before = 0;
+    double before = 0, w_at = 0;
     bool none = true;
 #pragma unroll 1
     for (uint32_t c0 = 0; c0 < per && none; c0 += 64) {
@@ -695,11 +726,11 @@ __device__ __forceinline__ void search(const First &first, const Entry &entry, u
 
 // Whether one of two patterns is 0 (it may also say so of a pattern of 1 above
 // one of 0).
-__device__ __forceinline__ uint32_t zero_half(uint32_t x) { return (x - 0x00010001u) & ~x & 0x80008000u; }
+__device__ __forceinline__ static uint32_t zero_half(uint32_t x) { return (x - 0x00010001u) & ~x & 0x80008000u; }
 
 // The global id of the rank-th element (from 0) of `bin` in the pieces, which
 // hold one.  `totals` (LDS): a number for each round of a wave.
-__device__ __forceinline__ uint32_t locate(const Pieces &pieces, uint32_t bin, uint32_t rank, uint32_t *totals,
+__device__ __forceinline__ static uint32_t locate(const Pieces &pieces, uint32_t bin, uint32_t rank, uint32_t *totals,
                                            uint32_t *place) {
   const uint32_t tid = threadIdx.x, wave = wave_number(), lane = tid % 64;
   // zero has two patterns: without its sign it has one
@@ -723,7 +754,7 @@ __device__ __forceinline__ uint32_t locate(const Pieces &pieces, uint32_t bin, u
     static_assert(kRounds * kWaves <= 64, "one lane for each round of a wave");
     if (lane < kRounds) totals[lane * kWaves + wave] = 0;
     if (tid == 0) place[0] = kNone;
-    h.each([&](uint32_t r, const v4u &x) {
+    h.each_short([&](uint32_t r, const v4u &x) {
       uint32_t some = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) some |= zero_half((x[j] & keep) ^ two);
@@ -771,19 +802,7 @@ __device__ __forceinline__ uint32_t locate(const Pieces &pieces, uint32_t bin, u
   }
 }
 
-struct DrawArgs {
-  Shards sh;
-  const xfer_sample_params *params;
-  const float *u;
-  xfer_sampled *out;
-  const uint32_t *lists;    // per slice (two launches)
-  const SliceInfo *infos;
-  uint2 *merged;            // a row's list where LDS does not hold it: (bin, count)
-  uint64_t row_cap, merged_cap;
-  uint32_t n_slices;
-};
-
-__device__ __forceinline__ const uint32_t *list_of(const DrawArgs &a, uint32_t row, uint32_t k) {
+__device__ __forceinline__ static const uint32_t *list_of(const DrawArgs &a, uint32_t row, uint32_t k) {
   const uint32_t s = k >= a.sh.slices[0];
   return a.lists + row * a.row_cap + (s ? (uint64_t)a.sh.slices[0] * a.sh.width[0] : 0) +
          (uint64_t)(s ? k - a.sh.slices[0] : k) * a.sh.width[s];
@@ -791,7 +810,7 @@ __device__ __forceinline__ const uint32_t *list_of(const DrawArgs &a, uint32_t r
 
 // The count of `bin` in a list of n entries in the bins' order (0 if it has
 // none), by one wave: 64 probes at a time.
-__device__ __forceinline__ uint32_t count_in_list(const uint32_t *list, uint32_t n, uint32_t bin) {
+__device__ __forceinline__ static uint32_t count_in_list(const uint32_t *list, uint32_t n, uint32_t bin) {
   const uint32_t lane = threadIdx.x % 64;
   uint32_t lo = 0, hi = n;  // the entry lies in [lo, hi) if there is one
   while (hi - lo > 64) {
@@ -809,12 +828,12 @@ __device__ __forceinline__ uint32_t count_in_list(const uint32_t *list, uint32_t
 
 // How the waves share a row's lists: a slice to each, or several waves to a
 // slice, with kAtOnce loads of each lane in flight.
-constexpr int kAtOnce = 8;
+static constexpr int kAtOnce = 10;
 struct Share {
   uint32_t k0, groups;  // the wave's first slice, and the step to its next
   uint32_t i0, step;    // the lane's first entry, and the step to its next
 };
-__device__ __forceinline__ Share share_of(uint32_t n_slices) {
+__device__ __forceinline__ static Share share_of(uint32_t n_slices) {
   const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
   const uint32_t ways = n_slices < kWaves ? kWaves / n_slices : 1, groups = kWaves / ways;
   return {wave / ways, groups, wave % ways * 64 + lane, ways * 64};
@@ -824,7 +843,7 @@ __device__ __forceinline__ Share share_of(uint32_t n_slices) {
 struct Ahead {
   uint32_t e[kAtOnce];
 };
-__device__ __forceinline__ Ahead load_ahead(const DrawArgs &a, uint32_t row, const Share &h) {
+__device__ __forceinline__ static Ahead load_ahead(const DrawArgs &a, uint32_t row, const Share &h) {
   Ahead r;
   const uint32_t k = min(h.k0, a.n_slices - 1), width = a.sh.width[k >= a.sh.slices[0]];
   const uint32_t *list = list_of(a, row, k);
@@ -835,8 +854,9 @@ __device__ __forceinline__ Ahead load_ahead(const DrawArgs &a, uint32_t row, con
 
 // visit(entry) of every entry of a row's lists.
 template <typename Visit>
-__device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const SliceInfo *info, const Share &h,
+__device__ __forceinline__ static void for_lists(const DrawArgs &a, uint32_t row, const SliceInfo *info, const Share &h,
                                           const Ahead &ahead, const Visit &visit) {
+  const uint32_t lane = threadIdx.x % 64;
   for (uint32_t k = h.k0; k < a.n_slices; k += h.groups) {
     const uint32_t *list = list_of(a, row, k);
     const uint32_t n = info[k].length;
@@ -848,8 +868,10 @@ __device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const
           if (i + j * h.step < n) r.e[j] = list[i + j * h.step];
       }
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (i - lane + j * h.step >= n) break;  // the whole wave
         if (i + j * h.step < n) visit(r.e[j]);
+      }
     }
   }
 }
@@ -857,7 +879,7 @@ __device__ __forceinline__ void for_lists(const DrawArgs &a, uint32_t row, const
 // ONE: the row is counted here (both shards hold at most kOneCols columns
 // together); else its slices' lists are added up.
 template <bool ONE>
-__global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(DrawArgs a) {
+__device__ __forceinline__ static void draw(const DrawArgs &a) {
   // Weights take the place of the bins.
   __shared__ __attribute__((aligned(16))) union {
     Bins bins;
@@ -960,13 +982,16 @@ __global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(DrawArgs a) {
     *c = near ? list[i] & 0xFFFFu : merged[i].y;
     *w = near ? lds.weights[i] : weight(i);
   };
-  search(first, entry, n, p, u, masses, sums, &sc);
+  // As many entries as elements that top_k keeps are enough.
+  const uint32_t keep = !(p.temperature > 0.0f) ? 1 : p.top_k == 0 ? kNone : p.top_k;
+  search(first, entry, min(n, keep), keep, p, u, masses, sums, &sc);
   __syncthreads();
   const uint32_t bin = bin_at(sc.at);
   uint32_t rank = sc.rank;
   if (!ONE) {
     // How many of the value each slice holds: its list is in order.
     uint32_t k = 0;
+#pragma unroll 1
     for (uint32_t j = wave_number(); j < a.n_slices; j += kWaves) {
       const uint32_t c = count_in_list(list_of(a, row, j), sc.info[j].length, bin);
       if (lane == 0) sc.slice_count[j] = c;
@@ -977,6 +1002,26 @@ __global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(DrawArgs a) {
   }
   const uint32_t id = locate(pieces, bin, rank, totals, sc.place);
   if (tid == 0) a.out[row] = xfer_sampled{sc.prob, (int32_t)id};
+}
+
+};  // struct Team
+
+template <int THREADS>
+__global__ __launch_bounds__(THREADS, 4) void sample_count_kernel(Shards sh, uint32_t n_slices, uint32_t jobs,
+                                                                  uint64_t row_cap, uint32_t *lists, SliceInfo *infos) {
+  Team<THREADS>::count(sh, n_slices, jobs, row_cap, lists, infos);
+}
+template <int THREADS, bool ONE>
+__global__ __launch_bounds__(THREADS, 4) void sample_draw_kernel(DrawArgs a) {
+  Team<THREADS>::template draw<ONE>(a);
+}
+// Whether workgroups are the only ones on their compute units.
+bool alone(uint32_t workgroups) { return workgroups <= kComputeUnits; }
+
+template <bool ONE>
+hipError_t launch_draw(const DrawArgs &a, uint32_t rows, hipStream_t stream) {
+  if (alone(rows)) return launch(sample_draw_kernel<1024, ONE>, dim3(rows), dim3(1024), 0, stream, a);
+  return launch(sample_draw_kernel<512, ONE>, dim3(rows), dim3(512), 0, stream, a);
 }
 
 uint32_t round_up8(uint32_t x) { return (x + 7u) & ~7u; }
@@ -1047,7 +1092,7 @@ hipError_t launch_sample(const SampleArgs &in, hipStream_t stream) {
   a.out = in.out;
   a.merged = reinterpret_cast<uint2 *>(ws);
   a.merged_cap = z.merged_cap;
-  if (z.one) return launch(sample_draw_kernel<true>, dim3(in.rows), dim3(kThreads), 0, stream, a);
+  if (z.one) return launch_draw<true>(a, in.rows, stream);
   a.n_slices = z.slices[0] + z.slices[1];
   a.row_cap = z.row_cap;
   const uint32_t jobs = in.rows * a.n_slices;
@@ -1055,10 +1100,13 @@ hipError_t launch_sample(const SampleArgs &in, hipStream_t stream) {
   uint32_t *lists = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(infos) + up16((uint64_t)jobs * sizeof(SliceInfo)));
   a.infos = infos;
   a.lists = lists;
-  const hipError_t e = launch(sample_count_kernel, dim3(jobs < kCountWorkgroups ? jobs : kCountWorkgroups),
-                              dim3(kThreads), 0, stream, a.sh, a.n_slices, jobs, a.row_cap, lists, infos);
+  const dim3 grid(jobs < kCountWorkgroups ? jobs : kCountWorkgroups);
+  const hipError_t e = alone(jobs) ? launch(sample_count_kernel<1024>, grid, dim3(1024), 0, stream, a.sh, a.n_slices,
+                                            jobs, a.row_cap, lists, infos)
+                                   : launch(sample_count_kernel<512>, grid, dim3(512), 0, stream, a.sh, a.n_slices,
+                                            jobs, a.row_cap, lists, infos);
   if (e != hipSuccess) return e;
-  return launch(sample_draw_kernel<false>, dim3(in.rows), dim3(kThreads), 0, stream, a);
+  return launch_draw<false>(a, in.rows, stream);
 }
 
 }  // namespace xfer
