@@ -22,10 +22,16 @@ namespace {
 
 constexpr int kThreads = 256;
 // Heads that a lane takes one after the other: with many tokens four, whose
-// loads are in flight together; with few tokens one, so that the heads of a
-// token spread over more compute units.
+// loads are in flight together (16384 tokens of 56 heads of 128: one 126 us,
+// two 88, four 78, eight 78, all with streaming stores); with few tokens one,
+// so that the heads of a token spread over more compute units.
 constexpr int kHeadsPerLane = 4;
 constexpr uint64_t kManyWorkgroups = 1024;
+// The queries are stored past the caches (88 us became 71; cache rows the same
+// way: 78).  Projections are read past them where the call moves more than they
+// hold (80 us became 71); smaller ones have just been written and are still
+// there (2000 tokens: 10.5 us, 12.5 past the caches).
+constexpr uint64_t kCachedBytes = 128ull << 20;
 
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -67,7 +73,20 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
-template <int D, int KIND, int STYLE, int HEADS>
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load(const uint16_t *p) {
+  if (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
+  return *reinterpret_cast<const T *>(p);
+}
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store(uint16_t *p, T v) {
+  if (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<T *>(p));
+  else
+    *reinterpret_cast<T *>(p) = v;
+}
+
+template <int D, int KIND, int STYLE, int HEADS, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rope_store_kernel(RopeStoreArgs a, uint32_t wg_per_token) {
   constexpr uint32_t kLanes = D / 8;
   constexpr uint32_t kSlots = kThreads / kLanes;  // heads side by side in a workgroup
@@ -99,8 +118,8 @@ __global__ __launch_bounds__(kThreads) void rope_store_kernel(RopeStoreArgs a, u
       const uint16_t *row = h < hq         ? a.q + token * a.q_ld + (uint64_t)h * D
                             : h < hq + hkv ? a.k + token * a.k_ld + (uint64_t)(h - hq) * D
                                            : a.v + token * a.v_ld + (uint64_t)(h - hq - hkv) * D;
-      x0[i] = __builtin_nontemporal_load(reinterpret_cast<const v2u *>(row + d0));
-      x1[i] = __builtin_nontemporal_load(reinterpret_cast<const v2u *>(row + d1));
+      x0[i] = load<STREAM, v2u>(row + d0);
+      x1[i] = load<STREAM, v2u>(row + d1);
     }
   }
   const int64_t slot = a.slots[token];
@@ -162,8 +181,8 @@ __global__ __launch_bounds__(kThreads) void rope_store_kernel(RopeStoreArgs a, u
       uint16_t *row = a.q_out + token * a.q_out_ld + (uint64_t)h * D;
       v2u o0 = {bf16x2(y[0], y[1]), bf16x2(y[2], y[3])}, o1 = {bf16x2(y[4], y[5]), bf16x2(y[6], y[7])};
       if (!pos_ok) o0 = o1 = v2u{0x7FC07FC0u, 0x7FC07FC0u};
-      *reinterpret_cast<v2u *>(row + d0) = o0;
-      *reinterpret_cast<v2u *>(row + d1) = o1;
+      store<(HEADS > 1)>(row + d0, o0);
+      store<(HEADS > 1)>(row + d1, o1);
     } else if (stored) {
       const uint32_t hk = is_v ? h - hq - hkv : h - hq;
       uint8_t *row = (is_v ? a.cache.v : a.cache.k) + slot_bytes + hk * a.cache.head_stride;
@@ -199,8 +218,13 @@ template <int D, int KIND, int STYLE>
 hipError_t launch_shape(const RopeStoreArgs &a, const Shape &s, hipStream_t stream) {
   const dim3 grid(a.tokens * s.wg_per_token);
   if (s.heads_per_lane == 1)
-    return launch(rope_store_kernel<D, KIND, STYLE, 1>, grid, dim3(kThreads), 0, stream, a, s.wg_per_token);
-  return launch(rope_store_kernel<D, KIND, STYLE, kHeadsPerLane>, grid, dim3(kThreads), 0, stream, a, s.wg_per_token);
+    return launch(rope_store_kernel<D, KIND, STYLE, 1, false>, grid, dim3(kThreads), 0, stream, a, s.wg_per_token);
+  const uint64_t heads = a.q_heads + a.cache.kv_heads * 2ull;
+  if (a.tokens * heads * D * 4 <= kCachedBytes)
+    return launch(rope_store_kernel<D, KIND, STYLE, kHeadsPerLane, false>, grid, dim3(kThreads), 0, stream, a,
+                  s.wg_per_token);
+  return launch(rope_store_kernel<D, KIND, STYLE, kHeadsPerLane, true>, grid, dim3(kThreads), 0, stream, a,
+                s.wg_per_token);
 }
 
 template <int D, int KIND>

@@ -149,6 +149,29 @@ def test_in_place_gives_the_same_bits():
     assert torch.equal(w.q.cpu().view(torch.int16), want.view(torch.int16))
 
 
+def test_a_large_batch_gives_the_bits_of_its_halves():
+    """Past 128 MiB the projections are read another way: the same bits as two smaller calls."""
+    say("rope_store, 4800 tokens and its halves")
+    t, hq, hkv, d = 4800, 40, 8, 128
+    assert 4 * t * (hq + 2 * hkv) * d > 128 << 20 > 4 * (t // 2) * (hq + 2 * hkv) * d
+    w = World(t, hq, hkv, d, 16, "bf16", "heads", True, 128, False, seed=11)
+    whole = torch.empty(w.q.shape, dtype=torch.bfloat16, device=DEV)
+    w.call(whole)
+    pool, cs, pos, slots = w.pool.clone(), torch.from_numpy(w.cs).to(DEV), w.pos.to(DEV), w.slots.to(DEV)
+    halves = torch.empty_like(whole)
+    w.pool.zero_()
+    for r in (slice(0, t // 2), slice(t // 2, t)):
+        decode.qkv_rope_store(w.cache, w.q[r], w.nk[r], w.nv[r], pos[r], cs, slots[r], halves[r], w.wq, w.wk)
+    torch.cuda.synchronize()
+    assert torch.equal(whole.view(torch.int16), halves.view(torch.int16))
+    stored = w.k.reshape(-1, hkv, d)[slots[(slots >= 0) & (slots < w.k.shape[0] * 16)]]
+    now, was = w.views(w.pool), w.views(pool)
+    s = slots[(slots >= 0) & (slots < w.k.shape[0] * 16)]
+    assert stored.shape[0] == t - 2
+    for a, b in zip(now, was):
+        assert torch.equal(a[s // 16, s % 16], b[s // 16, s % 16])
+
+
 def test_a_position_outside_the_table_gives_nan_queries_and_stores_nothing():
     w = World(6, 2, 1, 64, 4, "bf16", "tokens", True, 64, False, seed=6)
     w.slots = torch.arange(6)
