@@ -448,19 +448,17 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
     // Weighted sums: product j takes its dim's eight tokens.
 #pragma unroll
     for (int i = 0; i < L::kMfmaV / 2; ++i) {
-      uint32_t two[8];  // dims 2i and 2i + 1 of each token
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (KIND == XFER_KV_BF16)
-          two[e] = vr[e][i];
-        else
-          two[e] = i % 2 ? e4m3x2_to_bf16<true>(vr[e][i / 2]) : e4m3x2_to_bf16<false>(vr[e][i / 2]);
-      }
-      v4u even, odd;
+      v4u even, odd;  // dims 2i and 2i + 1, two tokens in a register
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        even[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x05040100);
-        odd[e] = __builtin_amdgcn_perm(two[2 * e + 1], two[2 * e], 0x07060302);
+        if constexpr (KIND == XFER_KV_BF16) {
+          even[e] = __builtin_amdgcn_perm(vr[2 * e + 1][i], vr[2 * e][i], 0x05040100);
+          odd[e] = __builtin_amdgcn_perm(vr[2 * e + 1][i], vr[2 * e][i], 0x07060302);
+        } else {
+          const uint32_t pairs = __builtin_amdgcn_perm(vr[2 * e + 1][i / 2], vr[2 * e][i / 2], i % 2 ? 0x07030602 : 0x05010400);
+          even[e] = e4m3x2_to_bf16<false>(pairs);
+          odd[e] = e4m3x2_to_bf16<true>(pairs);
+        }
       }
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
