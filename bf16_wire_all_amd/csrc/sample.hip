@@ -42,9 +42,9 @@ constexpr uint32_t kInf = 0x7F80u;               // the pattern of +inf; -inf ha
 constexpr uint32_t kBins = 2 * kInf;
 constexpr uint32_t kWords = 8192;                // bins in LDS: +count in the low half, -count in the high
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-// Columns of a slice: as few as a piece where that gives compute units work
-// that would have none, else up to as many as 16 bits count.
-constexpr uint32_t kPieceCols = 16384, kWideSliceCols = 65528;
+// Columns of a slice, which a workgroup holds in registers: as few as the first
+// where that gives compute units work that would have none, up to the second.
+constexpr uint32_t kSliceCols = 16384, kWideSliceCols = 40960;
 constexpr uint32_t kOneCols = 32768;             // of a row that one launch counts
 constexpr uint32_t kMaxSlices = 128;
 constexpr uint32_t kComputeUnits = 256;
@@ -52,6 +52,7 @@ constexpr uint32_t kCountWorkgroups = 2 * kComputeUnits;
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+typedef short v2s __attribute__((ext_vector_type(2)));
 
 // The BF16 pattern of a bin (+0 for zero).
 __device__ __forceinline__ uint32_t pattern_of(uint32_t bin) {
@@ -165,105 +166,113 @@ struct Team {
 static constexpr int kWaves = kThreads / 64;
 static constexpr uint32_t kLdsEntries = kThreads == 512 ? 5888 : 8192;  // lists up to this long stay in LDS
 
-// ------------------------------------------------------ pieces in registers
+// ------------------------------------------------------ a slice in registers
 
-// Elements of a piece, all loads in flight at once.  Lanes past its end hold
-// -inf, which counts nowhere.
+// Elements of N parts, each from a round of vectors of its own on; all loads in
+// flight at once.  What lies past a part's end is -inf, which counts nowhere.
 static constexpr uint32_t kMasked = 0xFF80FF80u;
-static constexpr int kRounds = kPieceCols / 8 / kThreads;
+static constexpr uint32_t kRounds = kWideSliceCols / 8 / kThreads;
+// The first round of the second part (kOneCols in two parts never take more
+// than kRounds).
+__device__ __forceinline__ static uint32_t second_round(const Slice &first) {
+  return (first.cols + 8 * kThreads - 1) / (8 * kThreads);
+}
 struct Held {
   v4u w[kRounds];
-  uint32_t last;   // one element of an incomplete last vector, above another of -inf
-  uint32_t n_vec;  // vectors of the piece
+  uint32_t own;   // bit r: this wave has vectors of round r
+  uint32_t busy;  // waves that have any
 
-  __device__ __forceinline__ void load(const Slice &s) {
-    const v4u *vp = reinterpret_cast<const v4u *>(s.ptr);
-    n_vec = s.cols / 8;
+  template <int N>
+  __device__ __forceinline__ void load(const Slice (&part)[N]) {
+    const uint32_t tid = threadIdx.x, wave = wave_number(), r1 = N == 2 ? second_round(part[0]) : kRounds;
+    own = 0;
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const uint32_t v = r * kThreads + threadIdx.x;
+    for (uint32_t r = 0; r < kRounds; ++r) {
+      const bool second = N == 2 && r >= r1;
+      const Slice &s = part[second ? N - 1 : 0];
+      const uint32_t v0 = (second ? r - r1 : r) * kThreads;
       w[r] = v4u{kMasked, kMasked, kMasked, kMasked};
-      if (v < n_vec) w[r] = vp[v];
+      if (v0 + tid < s.cols / 8) w[r] = reinterpret_cast<const v4u *>(s.ptr)[v0 + tid];
+      own |= (v0 + wave * 64 < (s.cols + 7) / 8 ? 1u : 0u) << r;
     }
-    last = kMasked;
-    if (threadIdx.x < s.cols % 8) last = (uint32_t)s.ptr[n_vec * 8 + threadIdx.x] << 16 | 0xFF80u;
+    busy = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Slice &s = part[i];
+      busy = max(busy, min((uint32_t)kWaves, (s.cols + 511) / 512));
+      // an incomplete last vector, element by element
+      const uint32_t last = s.cols / 8, rest = s.cols % 8;
+      if (rest && tid == last % kThreads) {
+        v4u x{kMasked, kMasked, kMasked, kMasked};
+#pragma unroll
+        for (uint32_t e = 0; e < 7; ++e)
+          if (e < rest) {
+            const uint32_t v = s.ptr[last * 8 + e];
+            x[e / 2] = e % 2 ? (x[e / 2] & 0xFFFFu) | v << 16 : (x[e / 2] & 0xFFFF0000u) | v;
+          }
+#pragma unroll
+        for (uint32_t r = 0; r < kRounds; ++r)
+          w[r] ^= (w[r] ^ x) & (r == (i ? r1 : 0) + last / kThreads ? ~0u : 0u);
+      }
+    }
   }
-  // visit(round, vector) of every vector; rounds that hold nothing for this
-  // wave are left out.  A loop, whose vectors move up, and not its rounds one
-  // after the other in code.
+  // visit(round, vector) of this wave's vectors.
   template <typename Visit>
   __device__ __forceinline__ void each(const Visit &visit) const {
-    v4u x[kRounds];
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) x[r] = w[r];
-#pragma unroll 1
-    for (uint32_t r = 0; r < kRounds && r * kThreads + wave_number() * 64 < n_vec; ++r) {
-      visit(r, x[0]);
-#pragma unroll
-      for (int i = 1; i < kRounds; ++i) x[i - 1] = x[i];
-    }
-  }
-  // The same with the rounds one after the other in code, for a short visit.
-  template <typename Visit>
-  __device__ __forceinline__ void each_short(const Visit &visit) const {
 #pragma unroll
     for (uint32_t r = 0; r < kRounds; ++r)
-      if (r * kThreads + wave_number() * 64 < n_vec) visit(r, w[r]);
+      if (own >> r & 1) visit(r, w[r]);
   }
-  // one(element) of every element.
+  // The vector of a round that is known at run time.
+  __device__ __forceinline__ v4u of_round(uint32_t round) const {
+    // by masks: the compiler would index memory for a choice
+    v4u x{};
+#pragma unroll
+    for (uint32_t r = 0; r < kRounds; ++r) x |= w[r] & (r == round ? ~0u : 0u);
+    return x;
+  }
+  // one(element) of every element: a loop, to keep the code of rare cases short.
   template <typename One>
   __device__ __forceinline__ void each_one(const One &one) const {
-    each([&](uint32_t, const v4u &x) {
+#pragma unroll 1
+    for (uint32_t r = 0; r < kRounds; ++r) {
+      if (!(own >> r & 1)) continue;
+      const v4u x = of_round(r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         one(x[i] & 0xFFFFu);
         one(x[i] >> 16);
       }
-    });
-    one(last >> 16);
+    }
   }
 };
 
-// Up to eight pieces, one after the other: of a slice, or of two.
-struct Pieces {
-  Slice s[2];
-  uint32_t n0, n;
-  __device__ __forceinline__ Slice operator[](uint32_t i) const {
-    const bool second = i >= n0;
-    const uint32_t c0 = min((second ? i - n0 : i) * kPieceCols, second ? s[1].cols : s[0].cols);
-    const uint16_t *ptr = (second ? s[1].ptr : s[0].ptr) + c0;
-    return {ptr, min(kPieceCols, (second ? s[1].cols : s[0].cols) - c0), (second ? s[1].gid : s[0].gid) + c0};
-  }
-};
-__device__ __forceinline__ static Pieces pieces_of(const Slice &a) {
-  const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
-  return {{a, a}, n, n};
-}
-__device__ __forceinline__ static Pieces pieces_of(const Slice &a, const Slice &b) {
-  const uint32_t n = max(1u, (a.cols + kPieceCols - 1) / kPieceCols);
-  return {{a, b}, n, n + max(1u, (b.cols + kPieceCols - 1) / kPieceCols)};
-}
-
-// Magnitudes from lo to hi (hi 0: none).
+// Magnitudes from lo to hi (hi 0: none), zero left out; the largest pattern
+// above zero (0: none); a pattern above zero that enough elements reach (0:
+// none known).
 struct Span {
-  uint32_t lo, hi;
+  uint32_t lo, hi, top, reached;
 };
-// Widens this lane's span by its elements of a piece, zero and what does not
-// count left out; whether the wave's piece holds any of those.
-__device__ __forceinline__ static bool widen(Span *s, const Held &h) {
-  v2us top = {0, 0}, low = {0xFFFF, 0xFFFF};
-  h.each_short([&](uint32_t, const v4u &x) {
+// This lane's span; whether the wave has a zero or +inf (or a NaN that would
+// pass for it).
+__device__ __forceinline__ static bool span_of(const Held &h, Span *s) {
+  v2us low = {0xFFFF, 0xFFFF}, high = {0, 0};
+  v2s first = {0, 0};
+  h.each([&](uint32_t, const v4u &x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const v2us m = __builtin_bit_cast(v2us, x[i] & 0x7FFF7FFFu);
-      top = __builtin_elementwise_max(top, m);
       low = __builtin_elementwise_min(low, m);
+      // finite magnitudes wrap round to 0x8080 and more, others to less
+      high = __builtin_elementwise_max(high, m - (unsigned short)kInf);
+      first = __builtin_elementwise_max(first, __builtin_bit_cast(v2s, (uint32_t)x[i]));
     }
   });
-  const uint32_t t = max((uint32_t)top.x, (uint32_t)top.y), l = min((uint32_t)low.x, (uint32_t)low.y);
-  if (!__any(t >= kInf || l == 0 || h.last != kMasked)) {
-    s->lo = min(s->lo, l);
-    s->hi = max(s->hi, t);
+  const uint32_t l = min((uint32_t)low.x, (uint32_t)low.y), t = max((uint32_t)high.x, (uint32_t)high.y);
+  const uint32_t f = (uint32_t)max((int)first.x, (int)first.y);
+  *s = Span{kNone, 0, 0, 0};
+  if (!__any(l == 0 || f >= kInf)) {
+    if (t >= 0x10000u - kInf) *s = Span{l, t + kInf - 0x10000u, f, 0};
     return false;
   }
   h.each_one([&](uint32_t v) {
@@ -271,6 +280,7 @@ __device__ __forceinline__ static bool widen(Span *s, const Held &h) {
     if (counts(v) && m) {
       s->lo = min(s->lo, m);
       s->hi = max(s->hi, m);
+      if (v == m) s->top = max(s->top, m);
     }
   });
   return true;
@@ -278,8 +288,9 @@ __device__ __forceinline__ static bool widen(Span *s, const Held &h) {
 
 // ------------------------------------------------------------------ counting
 
+// The words behind the bins, one for each lane, take what does not count.
 struct Bins {
-  uint32_t word[kWords];
+  uint32_t word[kWords + 64];
 };
 
 __device__ __forceinline__ static void clear(Bins *bins) {
@@ -288,16 +299,19 @@ __device__ __forceinline__ static void clear(Bins *bins) {
   for (uint32_t i = 0; i < kWords / 4 / kThreads; ++i) p[i * kThreads + threadIdx.x] = v4u{0, 0, 0, 0};
 }
 
-// Counts a wave's elements of a piece in the bins of magnitudes base .. base +
-// kWords - 1, which have to hold all of them but zero; *zeros takes the zeros.
-__device__ __forceinline__ static void count_held(Bins *bins, const Held &h, bool odd, uint32_t base, uint32_t *zeros) {
+// Counts a wave's elements in the bins of magnitudes base .. base + kWords - 1,
+// which have to hold all of them but zero; *zeros takes the zeros.  `careful`
+// if there may be zeros or infinite ones.
+__device__ __forceinline__ static void count_all(Bins *bins, const Held &h, bool careful, uint32_t base, uint32_t *zeros) {
   uint32_t *word = bins->word;
-  if (!odd) {
-    h.each_short([&](uint32_t, const v4u &x) {
+  if (!careful) {
+    // NaN and -inf lie past the bins' last magnitude
+    const uint32_t none = kWords + threadIdx.x % 64;
+    h.each([&](uint32_t, const v4u &x) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        atomicAdd(&word[(x[i] & 0x7FFFu) - base], (x[i] >> 15 & 1u) * 0xFFFFu + 1u);
-        atomicAdd(&word[(x[i] >> 16 & 0x7FFFu) - base], (x[i] >> 31) * 0xFFFFu + 1u);
+        atomicAdd(&word[min((x[i] & 0x7FFFu) - base, none)], (x[i] >> 15 & 1u) * 0xFFFFu + 1u);
+        atomicAdd(&word[min((x[i] >> 16 & 0x7FFFu) - base, none)], (x[i] >> 31) * 0xFFFFu + 1u);
       }
     });
     return;
@@ -311,6 +325,26 @@ __device__ __forceinline__ static void count_held(Bins *bins, const Held &h, boo
   });
   n = read_lane(scan(n), 63);
   if (n && threadIdx.x % 64 == 0) atomicAdd(zeros, n);
+}
+
+// The same of the elements from pattern lo (above zero) to hi, in the bins from
+// lo on.
+__device__ __forceinline__ static void count_top(Bins *bins, const Held &h, uint32_t lo, uint32_t hi) {
+  uint32_t *word = bins->word;
+  auto one = [&](int v) {
+    if ((uint32_t)v - lo <= hi - lo) atomicAdd(&word[(uint32_t)v - lo], 1u);
+  };
+  h.each([&](uint32_t, const v4u &x) {
+    v2s m = __builtin_bit_cast(v2s, (uint32_t)x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2s, (uint32_t)x[i]));
+    if (!__any(max((int)m.x, (int)m.y) >= (int)lo)) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      one((int)(x[i] << 16) >> 16);
+      one((int)x[i] >> 16);
+    }
+  });
 }
 
 // The entries of the bins, in order.  The words go in groups of 256, a lane
@@ -433,109 +467,135 @@ __device__ __forceinline__ static uint32_t list_in_passes(Bins *bins, uint32_t *
   }
   return n;
 }
-__device__ __forceinline__ static void count_pass(Bins *bins, const Pieces &pieces, uint32_t bin0) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < pieces.n; ++i) {
-    Held h;
-    h.load(pieces[i]);
-    h.each_one([&](uint32_t v) {
-      const uint32_t b = bin_of(v) - bin0;
-      if (counts(v) && b < kWords) atomicAdd(&bins->word[b], 1u);
-    });
-  }
+__device__ __forceinline__ static void count_pass(Bins *bins, const Held &h, uint32_t bin0) {
+  h.each_one([&](uint32_t v) {
+    const uint32_t b = bin_of(v) - bin0;
+    if (counts(v) && b < kWords) atomicAdd(&bins->word[b], 1u);
+  });
 }
 
 // The waves' spans, and the elements that are zero.
 struct Spans {
-  uint32_t lo[kWaves], hi[kWaves], zeros;
+  uint32_t lo[kWaves], hi[kWaves], top[kWaves], reached[kWaves], zeros;
 };
 // This wave's span for the others, before a barrier; from all lanes' spans.
-__device__ __forceinline__ static void share_span(Spans *s, const Span &mine) {
-  const uint32_t hi = wave_max(mine.hi), lo = ~wave_max(~mine.lo);
+// With enough > 0 also the largest pattern that the tops of `enough` lanes
+// reach.
+__device__ __forceinline__ static void share_span(Spans *s, const Span &mine, uint32_t enough) {
+  const uint32_t hi = wave_max(mine.hi), lo = ~wave_max(~mine.lo), top = wave_max(mine.top);
+  uint32_t reached = 0;
+  if (enough) {
+#pragma unroll 1
+    for (uint32_t bit = 1u << 14; bit; bit >>= 1)
+      if (__popcll(__ballot(mine.top >= (reached | bit))) >= enough) reached |= bit;
+  }
   if (threadIdx.x % 64 == 0) {
     s->lo[wave_number()] = lo;
     s->hi[wave_number()] = hi;
+    s->top[wave_number()] = top;
+    s->reached[wave_number()] = reached;
   }
   if (threadIdx.x == 0) s->zeros = 0;
 }
-__device__ __forceinline__ static Span join_spans(const Spans &s) {
-  Span r{kNone, 0};
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    r.lo = min(r.lo, s.lo[w]);
-    r.hi = max(r.hi, s.hi[w]);
-  }
-  return r;
+// All waves' together; `reached` of the first `busy` ones.
+__device__ __forceinline__ static Span join_spans(const Spans &s, uint32_t busy) {
+  const uint32_t lane = threadIdx.x % 64, w = lane % kWaves;
+  const uint32_t lo = s.lo[w], hi = s.hi[w], top = s.top[w], reached = w < busy ? s.reached[w] : kNone;
+  return {~wave_max(~lo), wave_max(hi), wave_max(top), ~wave_max(~reached)};
 }
-// The lowest magnitude of kWords bins that end at hi.
-__device__ __forceinline__ static uint32_t base_of(uint32_t hi) { return hi - min(hi, kWords - 1); }
+// The lowest magnitude, not zero, of kWords bins that reach hi.
+__device__ __forceinline__ static uint32_t base_of(uint32_t hi) { return hi - min(hi, kWords) + 1; }
 __device__ __forceinline__ static bool fits(const Span &s) { return s.hi - min(s.lo, s.hi) < kWords; }
 
-// The span of all pieces, of which `held` is the first, and then the counts:
-// pieces that are not held any more are read again, last first.  True if the
-// bins hold the counts, after a barrier; false if their span is too wide.
-__device__ __forceinline__ static bool count_pieces(Bins *bins, Spans *spans, const Pieces &pieces, Held *held, Span *all) {
+// How many elements of a row matter: top_k, or one to a greedy row.
+__device__ __forceinline__ static uint32_t keep_of(const xfer_sample_params &p) {
+  return !(p.temperature > 0.0f) ? 1 : p.top_k == 0 ? kNone : p.top_k;
+}
+// A pattern above zero below which nothing that min_p keeps lies, `top` being
+// the largest; 0 if there is none, or where top_p asks for every weight.
+__device__ __forceinline__ static uint32_t min_p_cut(const xfer_sample_params &p, uint32_t top) {
+  if (!(p.temperature > 0.0f) || p.top_p < 1.0f || !(p.min_p > 0.0f)) return 0;
+  const float x = __uint_as_float(top << 16);
+  // lowered by more than binary32 loses here; the pattern is cut off downwards
+  const float least = x * (1.0f - 0x1p-18f) + p.temperature * logf(fminf(p.min_p, 1.0f)) * (1.0f + 0x1p-18f);
+  return least > 0.0f ? __float_as_uint(least) >> 16 : 0;
+}
+
+// The span of a slice, and then its counts in bins from magnitude *base on.
+// Elements that the row's settings leave out, whatever other slices hold, are
+// not counted: those below what min_p leaves of the slice's first, and with at
+// most `keep` wanted those below a pattern that the tops of as many lanes
+// reach.  True if the bins hold the counts, after a barrier; false if the span
+// is too wide.
+__device__ __forceinline__ static bool count_slice(Bins *bins, Spans *spans, const Held &h, const xfer_sample_params &p,
+                                            Span *all, uint32_t *base) {
   clear(bins);
-  uint32_t odd = 0;  // bit i: piece i
-  Span mine{kNone, 0};
-  Held &h = *held;
-#pragma unroll 1
-  for (uint32_t i = 0;; ++i) {
-    Held next = h;
-    if (i + 1 < pieces.n) next.load(pieces[i + 1]);
-    odd |= widen(&mine, h) ? 1u << i : 0;
-    if (i + 1 == pieces.n) break;
-    h = next;
-  }
-  share_span(spans, mine);
+  Span mine;
+  const bool careful = span_of(h, &mine);
+  const uint32_t keep = keep_of(p);
+  const uint32_t enough = keep > 1 && keep <= h.busy * 64 ? (keep + h.busy - 1) / h.busy : 0;
+  share_span(spans, mine, enough);
   lds_barrier();
-  *all = join_spans(*spans);
-  if (!fits(*all)) return false;
-  const uint32_t base = base_of(all->hi);
-#pragma unroll 1
-  for (uint32_t i = pieces.n; i-- > 0;) {
-    Held next = h;
-    if (i > 0) next.load(pieces[i - 1]);
-    count_held(bins, h, odd >> i & 1, base, &spans->zeros);
-    h = next;
+  *all = join_spans(*spans, h.busy);
+  uint32_t cut = 0;
+  if (all->top) {
+    cut = max(min_p_cut(p, all->top), all->reached);
+    if (keep == 1) cut = all->top;
   }
+  if (cut) {
+    all->lo = cut;
+    all->hi = all->top;
+  }
+  if (!fits(*all)) return false;
+  *base = cut ? cut : base_of(all->hi);
+  if (cut)
+    count_top(bins, h, cut, all->top);
+  else
+    count_all(bins, h, careful || all->hi == kInf, *base, &spans->zeros);
   lds_barrier();
   return true;
 }
 
-// A workgroup goes from slice to slice, and loads the next one's first piece
-// before it sorts out the counts of the one at hand.
+// A workgroup goes from slice to slice, and loads the next one before it sorts
+// out the counts of the one at hand.
 __device__ __forceinline__ static void count(const Shards &sh, uint32_t n_slices, uint32_t jobs, uint64_t row_cap,
-                                      uint32_t *lists, SliceInfo *infos) {
+                                      const xfer_sample_params *params, uint32_t *lists, SliceInfo *infos) {
   __shared__ __attribute__((aligned(16))) Bins bins;
   __shared__ GroupCounts groups;
   __shared__ Spans spans;
   __shared__ uint32_t most[kWaves];
   const uint32_t lane = threadIdx.x % 64;
   Held held;
+  auto load = [&](uint32_t job) {
+    const Slice part[1] = {slice_of(sh, job / n_slices, job % n_slices)};
+    held.load(part);
+  };
   uint32_t job = blockIdx.x;
-  held.load(pieces_of(slice_of(sh, job / n_slices, job % n_slices))[0]);
+  load(job);
 #pragma unroll 1
   for (; job < jobs; job += gridDim.x) {
     const uint32_t row = job / n_slices, k = job % n_slices, s = k >= sh.slices[0], next = job + gridDim.x;
-    const Pieces pieces = pieces_of(slice_of(sh, row, k));
+    const xfer_sample_params p = params[row];
+    const uint32_t keep = keep_of(p);  // as many entries are enough
     Span all;
-    const bool fit = count_pieces(&bins, &spans, pieces, &held, &all);
-    if (next < jobs) held.load(pieces_of(slice_of(sh, next / n_slices, next % n_slices))[0]);
+    uint32_t base = 0;
+    const bool fit = count_slice(&bins, &spans, held, p, &all, &base);
     uint32_t *list = lists + row * row_cap + (s ? (uint64_t)sh.slices[0] * sh.width[0] : 0) +
                      (uint64_t)(s ? k - sh.slices[0] : k) * sh.width[s];
     uint32_t largest = 0, n;
     auto put = [&](uint32_t i, uint32_t bin, uint32_t count) {
-      list[i] = bin << 16 | count;
+      if (i < keep) list[i] = bin << 16 | count;
       largest = max(largest, count);
     };
+    if (!fit) {
+      lds_barrier();  // the bins are cleared again
+      n = list_in_passes(&bins, groups.pos, [&](uint32_t bin0) { count_pass(&bins, held, bin0); }, put);
+    }
+    if (next < jobs) load(next);
     if (fit) {
       Compact c(&bins, spans.zeros, &groups);
-      c.emit(base_of(all.hi), put);
+      c.emit(base, put);
       n = c.total;
-    } else {
-      lds_barrier();  // the bins are cleared again
-      n = list_in_passes(&bins, groups.pos, [&](uint32_t bin0) { count_pass(&bins, pieces, bin0); }, put);
     }
     largest = wave_max(largest);
     if (lane == 0) most[wave_number()] = largest;
@@ -543,7 +603,7 @@ __device__ __forceinline__ static void count(const Shards &sh, uint32_t n_slices
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) largest = max(largest, most[w]);
-      infos[job] = SliceInfo{n, largest, all.lo, all.hi};
+      infos[job] = SliceInfo{min(n, keep), largest, all.lo, all.hi};
     }
   }
 }
@@ -556,7 +616,6 @@ struct Scratch {
   double mass[kWaves];
   uint32_t count[kWaves];
   uint32_t below[kWaves];  // a wave's first entry whose weight is below min_p's limit
-  uint32_t place[4];
   uint32_t at, rank;       // the drawn entry, and the drawn element's place among its equals
   float prob;
 };
@@ -724,81 +783,60 @@ __device__ __forceinline__ static void search(const First &first, const Entry &e
   }
 }
 
-// Whether one of two patterns is 0 (it may also say so of a pattern of 1 above
-// one of 0).
-__device__ __forceinline__ static uint32_t zero_half(uint32_t x) { return (x - 0x00010001u) & ~x & 0x80008000u; }
-
-// The global id of the rank-th element (from 0) of `bin` in the pieces, which
-// hold one.  `totals` (LDS): a number for each round of a wave.
-__device__ __forceinline__ static uint32_t locate(const Pieces &pieces, uint32_t bin, uint32_t rank, uint32_t *totals,
-                                           uint32_t *place) {
+// Calls found(id) in the lane that holds the rank-th element (from 0) of `bin`
+// in the parts, which hold one; id is its global one.  `totals` (LDS): a number
+// for each round of a wave.
+template <int N, typename Found>
+__device__ __forceinline__ static void locate(const Held &h, const Slice (&part)[N], uint32_t bin, uint32_t rank,
+                                       uint32_t *totals, const Found &found) {
   const uint32_t tid = threadIdx.x, wave = wave_number(), lane = tid % 64;
   // zero has two patterns: without its sign it has one
   const uint32_t keep = bin == kInf ? 0x7FFF7FFFu : 0xFFFFFFFFu, two = pattern_of(bin) * 0x10001u;
-  Held h;
-  h.load(pieces[0]);
+  uint32_t own[2] = {0, 0};  // four bits for each round: its elements in this lane
+  static_assert(kRounds <= 16, "two registers of rounds");
+  h.each([&](uint32_t r, const v4u &x) {
+    uint32_t others = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t d = (x[j] & keep) ^ two;
+      others += __popc((((d & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d) & 0x80008000u);  // a bit where a half is not 0
+    }
+    own[r / 8] |= (8 - others) << (r % 8 * 4);
+  });
+  uint32_t mine = 0;  // of lane r: round r's
 #pragma unroll 1
-  for (uint32_t i = 0;; ++i) {
-    const Slice s = pieces[i];
-    Held next = h;
-    if (i + 1 < pieces.n) next.load(pieces[i + 1]);
-    auto matches = [&](const v4u &x) {
-      uint32_t m = 0;  // bit e: element e of this thread's vector is of the bin
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const uint32_t c = (r < 8 ? own[0] : own[1]) >> (r % 8 * 4) & 15u;
+    if (!__any(c != 0)) continue;
+    const uint32_t all = read_lane(scan(c), 63);
+    if (lane == r) mine = all;
+  }
+  if (lane < kRounds) totals[lane * kWaves + wave] = mine;
+  lds_barrier();
+  static_assert(kRounds * kWaves <= 128, "a lane for two of them");
+  const uint32_t i0 = 2 * lane;
+  const uint32_t c0 = i0 < kRounds * kWaves ? totals[i0] : 0, c1 = i0 + 1 < kRounds * kWaves ? totals[i0 + 1] : 0;
+  const uint32_t incl = scan(c0 + c1), excl = incl - c0 - c1;
+  const uint64_t holds = __ballot(excl <= rank && rank < incl);
+  if (!holds) return;  // does not happen
+  const uint32_t l = (uint32_t)__builtin_ctzll(holds), second = rank - read_lane(excl, l) >= read_lane(c0, l);
+  const uint32_t at = 2 * l + second, round = at / kWaves;
+  if (at % kWaves != wave) return;
+  const v4u x = h.of_round(round);
+  uint32_t m = 0;  // bit e: element e of this lane's vector is of the bin
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t d = (x[j] & keep) ^ two;
-        m |= ((d & 0xFFFFu) == 0) << (2 * j) | (d >> 16 == 0) << (2 * j + 1);
-      }
-      return m;
-    };
-    static_assert(kRounds * kWaves <= 64, "one lane for each round of a wave");
-    if (lane < kRounds) totals[lane * kWaves + wave] = 0;
-    if (tid == 0) place[0] = kNone;
-    h.each_short([&](uint32_t r, const v4u &x) {
-      uint32_t some = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) some |= zero_half((x[j] & keep) ^ two);
-      if (!__any(some != 0)) return;
-      const uint32_t c = scan((uint32_t)__popc(matches(x)));
-      if (lane == 63) totals[r * kWaves + wave] = c;
-    });
-    // the elements of an incomplete last vector, held by the first threads, come last
-    const bool last = ((h.last & keep) ^ two) >> 16 == 0;
-    const uint64_t lasts = __ballot(last);
-    lds_barrier();
-    if (wave == 0) {
-      const uint32_t c = lane < kRounds * kWaves ? totals[lane % (kRounds * kWaves)] : 0, incl = scan(c);
-      if (incl - c <= rank && rank < incl) {
-        place[0] = lane;
-        place[1] = rank - (incl - c);
-      }
-      const uint32_t vectors = read_lane(incl, 63);
-      if (last && vectors + lanes_below(lasts) == rank) {
-        place[0] = 64;
-        place[3] = s.cols / 8 * 8 + lane;
-      }
-      if (lane == 0) place[2] = vectors + __popcll(lasts);
-    }
-    lds_barrier();
-    const uint32_t at = place[0];
-    if (at != kNone) {
-      h.each([&](uint32_t r, const v4u &x) {
-        if (at != r * kWaves + wave) return;
-        uint32_t m = matches(x), left = place[1];
-        const uint32_t c = __popc(m), incl = scan(c);
-        if (incl - c <= left && left < incl) {
-          left -= incl - c;
-          for (; left; --left) m &= m - 1;
-          place[3] = (r * kThreads + tid) * 8 + (uint32_t)__builtin_ctz(m);
-        }
-      });
-      lds_barrier();
-      return s.gid + place[3];
-    }
-    rank -= place[2];
-    if (i + 1 == pieces.n) return s.gid;  // does not happen
-    h = next;
-    lds_barrier();  // totals and place are written again
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t d = (x[j] & keep) ^ two;
+    m |= ((d & 0xFFFFu) == 0) << (2 * j) | (d >> 16 == 0) << (2 * j + 1);
+  }
+  uint32_t left = rank - read_lane(excl, l) - (second ? read_lane(c0, l) : 0);
+  const uint32_t c = __popc(m), up_to = scan(c);
+  if (up_to - c <= left && left < up_to) {
+    left -= up_to - c;
+    for (; left; --left) m &= m - 1;
+    const uint32_t r1 = N == 2 ? second_round(part[0]) : kRounds;
+    const bool b = N == 2 && round >= r1;
+    found(part[b ? N - 1 : 0].gid + ((b ? round - r1 : round) * kThreads + tid) * 8 + (uint32_t)__builtin_ctz(m));
   }
 }
 
@@ -901,13 +939,16 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
   // span (`packed`).
   const Share share = share_of(ONE ? 1 : a.n_slices);
   Ahead ahead{};
-  Pieces pieces = ONE ? pieces_of(slice_of(a.sh, row, 0), slice_of(a.sh, row, 1)) : Pieces{};
+  Held held;
+  Slice part[ONE ? 2 : 1];
   Span all;
+  uint32_t base = 0;
   bool packed;
-  if (ONE) {
-    Held held;
-    held.load(pieces[0]);
-    packed = count_pieces(&lds.bins, &spans, pieces, &held, &all);
+  if constexpr (ONE) {
+    part[0] = slice_of(a.sh, row, 0);
+    part[1] = slice_of(a.sh, row, 1);
+    held.load(part);
+    packed = count_slice(&lds.bins, &spans, held, p, &all, &base);
   } else {
     SliceInfo info{0, 0, kNone, 0};
     if (tid < a.n_slices) info = a.infos[row * a.n_slices + tid];
@@ -916,15 +957,15 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
     if (tid < kMaxSlices) sc.info[tid] = info;
     const uint32_t most = scan(info.most);
     if (lane == 63) sc.count[wave_number()] = most;
-    share_span(&spans, Span{info.lo, info.hi});
+    share_span(&spans, Span{info.lo, info.hi, 0, 0}, 0);
     lds_barrier();
-    all = join_spans(spans);
+    all = join_spans(spans, 0);
     uint32_t sum = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) sum += sc.count[w];
     packed = sum <= 0xFFFFu && fits(all);  // no value can occur more often than that
     if (packed) {
-      const uint32_t base = base_of(all.hi);
+      base = base_of(all.hi);
       for_lists(a, row, sc.info, share, ahead, [&](uint32_t e) {
         const uint32_t b = e >> 16, c = e & 0xFFFFu;
         uint32_t *to = b == kInf ? &spans.zeros : &lds.bins.word[(b < kInf ? kInf - b : b - kInf) - base];
@@ -936,9 +977,11 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
 
   // The row's list: in LDS if it is no longer than kLdsEntries, else in the
   // workspace.
+  const uint32_t keep = keep_of(p);  // as many entries are enough
   uint32_t n;
   bool near = false;
   auto put = [&](uint32_t i, uint32_t bin, uint32_t count) {
+    if (i >= keep) return;
     if (near)
       list[i] = bin << 16 | count;
     else
@@ -946,14 +989,14 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
   };
   if (packed) {
     Compact c(&lds.bins, spans.zeros, &groups);
-    n = c.total;
+    n = min(c.total, keep);
     near = n <= kLdsEntries;
-    c.emit(base_of(all.hi), put);
+    c.emit(base, put);
   } else {
     lds_barrier();  // the bins are cleared again
     n = list_in_passes(&lds.bins, groups.pos, [&](uint32_t bin0) {
-      if (ONE) {
-        count_pass(&lds.bins, pieces, bin0);
+      if constexpr (ONE) {
+        count_pass(&lds.bins, held, bin0);
       } else {
         for_lists(a, row, sc.info, share, ahead, [&](uint32_t e) {
           const uint32_t b = (e >> 16) - bin0;
@@ -961,6 +1004,7 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
         });
       }
     }, put);
+    n = min(n, keep);
   }
   __syncthreads();
   if (n == 0) {
@@ -982,13 +1026,11 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
     *c = near ? list[i] & 0xFFFFu : merged[i].y;
     *w = near ? lds.weights[i] : weight(i);
   };
-  // As many entries as elements that top_k keeps are enough.
-  const uint32_t keep = !(p.temperature > 0.0f) ? 1 : p.top_k == 0 ? kNone : p.top_k;
-  search(first, entry, min(n, keep), keep, p, u, masses, sums, &sc);
+  search(first, entry, n, keep, p, u, masses, sums, &sc);
   __syncthreads();
   const uint32_t bin = bin_at(sc.at);
   uint32_t rank = sc.rank;
-  if (!ONE) {
+  if constexpr (!ONE) {
     // How many of the value each slice holds: its list is in order.
     uint32_t k = 0;
 #pragma unroll 1
@@ -998,18 +1040,19 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
     }
     lds_barrier();
     while (k + 1 < a.n_slices && rank >= sc.slice_count[k]) rank -= sc.slice_count[k++];
-    pieces = pieces_of(slice_of(a.sh, row, k));
+    part[0] = slice_of(a.sh, row, k);
+    held.load(part);
   }
-  const uint32_t id = locate(pieces, bin, rank, totals, sc.place);
-  if (tid == 0) a.out[row] = xfer_sampled{sc.prob, (int32_t)id};
+  locate(held, part, bin, rank, totals, [&](uint32_t id) { a.out[row] = xfer_sampled{sc.prob, (int32_t)id}; });
 }
 
 };  // struct Team
 
 template <int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void sample_count_kernel(Shards sh, uint32_t n_slices, uint32_t jobs,
-                                                                  uint64_t row_cap, uint32_t *lists, SliceInfo *infos) {
-  Team<THREADS>::count(sh, n_slices, jobs, row_cap, lists, infos);
+                                                                  uint64_t row_cap, const xfer_sample_params *params,
+                                                                  uint32_t *lists, SliceInfo *infos) {
+  Team<THREADS>::count(sh, n_slices, jobs, row_cap, params, lists, infos);
 }
 template <int THREADS, bool ONE>
 __global__ __launch_bounds__(THREADS, 4) void sample_draw_kernel(DrawArgs a) {
@@ -1032,7 +1075,7 @@ uint32_t cut(uint32_t cols, uint32_t most) { return cols / most + (cols % most !
 // Slices of the narrower kind that a row is cut into, at most.
 uint32_t sample_slices(uint32_t ncols0, uint32_t ncols1) {
   if ((uint64_t)ncols0 + ncols1 <= kOneCols) return 1;
-  return cut(ncols0, kPieceCols) + cut(ncols1, kPieceCols);
+  return cut(ncols0, kSliceCols) + cut(ncols1, kSliceCols);
 }
 
 namespace {
@@ -1046,7 +1089,7 @@ Sizes sizes_of(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
   Sizes z{};
   z.one = (uint64_t)ncols0 + ncols1 <= kOneCols;
   const uint32_t n[2] = {ncols0, ncols1};
-  uint32_t most = z.one ? kOneCols : kPieceCols;
+  uint32_t most = z.one ? kOneCols : kSliceCols;
   auto slices = [&] { return cut(n[0], most) + cut(n[1], most); };
   while (!z.one && most < kWideSliceCols && (slices() > kMaxSlices || (uint64_t)rows * slices() > kCountWorkgroups))
     most = most * 2 < kWideSliceCols ? most * 2 : kWideSliceCols;
@@ -1102,9 +1145,9 @@ hipError_t launch_sample(const SampleArgs &in, hipStream_t stream) {
   a.lists = lists;
   const dim3 grid(jobs < kCountWorkgroups ? jobs : kCountWorkgroups);
   const hipError_t e = alone(jobs) ? launch(sample_count_kernel<1024>, grid, dim3(1024), 0, stream, a.sh, a.n_slices,
-                                            jobs, a.row_cap, lists, infos)
+                                            jobs, a.row_cap, in.params, lists, infos)
                                    : launch(sample_count_kernel<512>, grid, dim3(512), 0, stream, a.sh, a.n_slices,
-                                            jobs, a.row_cap, lists, infos);
+                                            jobs, a.row_cap, in.params, lists, infos);
   if (e != hipSuccess) return e;
   return launch_draw<false>(a, in.rows, stream);
 }
