@@ -10,8 +10,8 @@
 //
 // Two launches:
 //   1. count: a workgroup counts a slice of one shard in LDS (16 bits for each
-//      value, so a slice has fewer than 65,536 columns) and writes the values
-//      that occur, in order, with their counts;
+//      value; a slice has at most 40,960 columns) and writes the values that
+//      occur, in order, with their counts;
 //   2. draw: a workgroup for each row adds up its slices' lists in LDS the
 //      same way, finds the cuts and the drawn element (its value and how many
 //      equal ones come before it), then looks that one up in the slice that
@@ -20,17 +20,28 @@
 // shards in one workgroup.
 // The kernel boundary orders the two steps, as in the argmax.
 //
-// A slice's range of magnitudes is found before it is counted, and 8,192 bins
-// (64 powers of two, both signs' counts in one word) hold it in 32 KiB of LDS:
-// several workgroups share a compute unit, and clearing and reading the bins
-// costs little.  What bounds the rest is instructions: those that issue (a
-// wave's instruction holds its SIMD for four clocks), so a logit takes two
-// packed operations for each pair and about five more to be counted, the order
-// is made once, when the bins are read, and one wave does the searches, 64
-// probes at a time, without barriers between them; and those that have to be
-// fetched, for a workgroup runs through most of the code once: loops are left
-// as loops (rows of 129,280: 20 us of kernels became __ONE__).  Ranges that are
-// wider, and sums of counts past 16 bits, take a path of eight passes.
+// A workgroup holds its slice in registers, so that all its loads are in
+// flight at once and nothing is read twice (256 rows of 151,936: the count is
+// 20 us, 3.9 TB/s; with pieces of 16,384 columns one after the other, read
+// again to be counted, it was 27).  The slice's range of magnitudes is found
+// before it is counted, and 8,192 bins (64 powers of two, both signs' counts
+// in one word) hold it in 32 KiB of LDS: two workgroups share a compute unit,
+// and clearing and reading the bins costs little.  Ranges that are wider, and
+// sums of counts past 16 bits, take a path of eight passes.
+//
+// What a row's settings leave out whatever the other slices hold is not
+// counted: where top_p does not ask for the sum of all weights, what min_p
+// would drop beside the slice's own first element; and what lies below top_k
+// elements that the slice is known to have.  Its list then has a few entries,
+// and up to 64 of a row are searched by one wave in its registers (rows of
+// 129,280 with all filters: the draw is 8.9 us, with whole lists it was 14.1).
+//
+// What bounds the rest, at one row as at 256, is the chain of steps in a
+// workgroup, each some hundreds of clocks: a load, a barrier, a search.  So the
+// order is made once, when the bins are read, one wave does the searches, 64
+// probes at a time, without barriers between them, and loops of rare cases are
+// left as loops, for a workgroup runs through most of the code once and waits
+// for it to be fetched.
 #include "decode.h"
 
 namespace xfer {
@@ -516,8 +527,10 @@ __device__ __forceinline__ static uint32_t keep_of(const xfer_sample_params &p) 
 __device__ __forceinline__ static uint32_t min_p_cut(const xfer_sample_params &p, uint32_t top) {
   if (!(p.temperature > 0.0f) || p.top_p < 1.0f || !(p.min_p > 0.0f)) return 0;
   const float x = __uint_as_float(top << 16);
-  // lowered by more than binary32 loses here; the pattern is cut off downwards
-  const float least = x * (1.0f - 0x1p-18f) + p.temperature * logf(fminf(p.min_p, 1.0f)) * (1.0f + 0x1p-18f);
+  // lowered by more than binary32 loses here, and by what an exponential in
+  // binary64 still rounds to 1; the pattern is cut off downwards
+  const float exponent = logf(fminf(p.min_p, 1.0f)) * (1.0f + 0x1p-18f) - 0x1p-40f;
+  const float least = x * (1.0f - 0x1p-18f) + p.temperature * exponent;
   return least > 0.0f ? __float_as_uint(least) >> 16 : 0;
 }
 
@@ -620,6 +633,11 @@ struct Scratch {
   float prob;
 };
 
+// The smallest weight that min_p keeps.
+__device__ __forceinline__ static double least_of(const xfer_sample_params &p) {
+  return p.min_p > 1.0f ? 1.0 : (double)p.min_p;
+}
+
 // Smallest r in [1, most] with before + r * w >= target (over: > target).
 __device__ __forceinline__ static uint32_t rank_of(double before, double w, uint32_t most, double target, bool over) {
   const double q = (target - before) / w;
@@ -635,6 +653,63 @@ __device__ __forceinline__ static uint32_t rank_of(double before, double w, uint
   return r;
 }
 
+// The cuts and the draw on a list of up to 64 entries by one wave, an entry
+// (count, weight) to each lane; `keep` elements are left by top_k.
+__device__ __forceinline__ static void search_in_wave(uint32_t count, double weight, uint32_t n, uint32_t keep,
+                                               const xfer_sample_params &p, float u, Scratch *sc) {
+  const uint32_t lane = threadIdx.x % 64;
+  const bool there = lane < n;
+  const uint32_t n_run = scan(there ? count : 0);
+  const double m_run = scan(there ? count * weight : 0.0);
+  const uint64_t below = __ballot(there && weight < least_of(p));
+  keep = min(keep, read_lane(n_run, 63));
+  struct {
+    uint32_t at, rank;
+    double z;  // weights up to there
+  } f = {n - 1, kNone, 0.0};
+#pragma unroll 1
+  for (int border = 0; border < 4; ++border) {  // as in search() below
+    double target = 0;
+    uint32_t last = f.at, last_count = f.rank;
+    if (border == 1) {
+      if (!(p.top_p < 1.0f)) continue;
+      target = (double)p.top_p * f.z;
+    } else if (border == 2) {
+      const uint32_t m_at = below ? (uint32_t)__builtin_ctzll(below) : kNone;
+      if (m_at > f.at) continue;
+      last = m_at - 1;
+      last_count = kNone;
+    } else if (border == 3) {
+      target = u > 0.0f ? (double)u * f.z : 0.0;
+    }
+    const uint64_t hit = __ballot(there && (border == 0   ? n_run >= keep
+                                            : border == 1 ? m_run >= target
+                                                          : border == 3 && m_run > target));
+    const uint32_t at = min(hit ? (uint32_t)__builtin_ctzll(hit) : last, last);
+    const uint32_t c_all = read_lane(count, at), c = at == last ? min(c_all, last_count) : c_all;
+    const double w = read_lane(weight, at), before = at ? read_lane(m_run, at - 1) : 0.0, end = before + c * w;
+    const bool reached = at < last || (border == 1 ? end >= target : end > target);
+    uint32_t rank = c;
+    if (border == 0)
+      rank = keep - (read_lane(n_run, at) - c_all);
+    else if (border == 1 && !reached)
+      continue;  // no cut
+    else if (border != 2 && reached)
+      rank = rank_of(before, w, c, target, border == 3);
+    if (border == 3) {
+      if (lane == 0) {
+        sc->at = at;
+        sc->rank = rank - 1;
+        sc->prob = (float)(w / f.z);
+      }
+    } else {
+      f.at = at;
+      f.rank = rank;
+      f.z = before + rank * w;
+    }
+  }
+}
+
 // The cuts and the draw on a list of n > 0 entries: first(i, &count, &weight)
 // once for each entry, then entry(i, &count, &weight); `keep` elements are left
 // by top_k.  Thread t sums up entries [t * per, (t + 1) * per); `masses` and
@@ -646,10 +721,17 @@ __device__ __forceinline__ static void search(const First &first, const Entry &e
                                        const xfer_sample_params &p, float u, double *masses, uint32_t *counts,
                                        Scratch *sc) {
   const uint32_t tid = threadIdx.x, wave = wave_number(), lane = tid % 64;
-  if (n <= 64 && wave) return;  // the first wave holds all entries
+  if (n <= 64) {
+    if (wave) return;
+    uint32_t c = 0;
+    double w = 0;
+    if (lane < n) first(lane, &c, &w);
+    search_in_wave(c, w, n, keep, p, u, sc);
+    return;
+  }
   const uint32_t per = (n + kThreads - 1) / kThreads;
   const uint32_t i0 = min(tid * per, n), i1 = min(i0 + per, n);
-  const double least = p.min_p > 1.0f ? 1.0 : (double)p.min_p;
+  const double least = least_of(p);
   uint32_t count = 0, below = kNone;
   double mass = 0;
 #pragma unroll 1
@@ -672,12 +754,12 @@ __device__ __forceinline__ static void search(const First &first, const Entry &e
     sc->mass[wave] = mass;
     sc->below[wave] = below;
   }
-  if (n > 64) __syncthreads();
+  __syncthreads();
   if (wave != 0) return;
 
   // Of lane w: the running sums up to wave w's end, and the first entry whose
   // weight is below min_p's limit.
-  const bool is_wave = lane < kWaves && (n > 64 || lane == 0);
+  const bool is_wave = lane < kWaves;
   const uint32_t wave_counts = scan(is_wave ? sc->count[lane % kWaves] : 0);
   const double wave_masses = scan(is_wave ? sc->mass[lane % kWaves] : 0.0);
   const uint32_t m_at = ~wave_max(~(is_wave ? sc->below[lane % kWaves] : kNone));
@@ -783,6 +865,21 @@ __device__ __forceinline__ static void search(const First &first, const Entry &e
   }
 }
 
+// Where the rank-th (from 0) of things lies that are counted in up to 128
+// numbers, of which this lane has the 2l-th and the next: the number's index
+// (kNone: nowhere), and how many lie before it.
+struct Place {
+  uint32_t at, before;
+};
+__device__ __forceinline__ static Place place_of(uint32_t c0, uint32_t c1, uint32_t rank) {
+  const uint32_t incl = scan(c0 + c1), excl = incl - c0 - c1;
+  const uint64_t holds = __ballot(excl <= rank && rank < incl);
+  if (!holds) return {kNone, 0};
+  const uint32_t l = (uint32_t)__builtin_ctzll(holds), before = read_lane(excl, l), first = read_lane(c0, l);
+  const bool second = rank - before >= first;
+  return {2 * l + second, before + (second ? first : 0)};
+}
+
 // Calls found(id) in the lane that holds the rank-th element (from 0) of `bin`
 // in the parts, which hold one; id is its global one.  `totals` (LDS): a number
 // for each round of a wave.
@@ -816,12 +913,9 @@ __device__ __forceinline__ static void locate(const Held &h, const Slice (&part)
   static_assert(kRounds * kWaves <= 128, "a lane for two of them");
   const uint32_t i0 = 2 * lane;
   const uint32_t c0 = i0 < kRounds * kWaves ? totals[i0] : 0, c1 = i0 + 1 < kRounds * kWaves ? totals[i0 + 1] : 0;
-  const uint32_t incl = scan(c0 + c1), excl = incl - c0 - c1;
-  const uint64_t holds = __ballot(excl <= rank && rank < incl);
-  if (!holds) return;  // does not happen
-  const uint32_t l = (uint32_t)__builtin_ctzll(holds), second = rank - read_lane(excl, l) >= read_lane(c0, l);
-  const uint32_t at = 2 * l + second, round = at / kWaves;
-  if (at % kWaves != wave) return;
+  const Place place = place_of(c0, c1, rank);
+  if (place.at % kWaves != wave || place.at == kNone) return;  // kNone does not happen
+  const uint32_t round = place.at / kWaves;
   const v4u x = h.of_round(round);
   uint32_t m = 0;  // bit e: element e of this lane's vector is of the bin
 #pragma unroll
@@ -829,7 +923,7 @@ __device__ __forceinline__ static void locate(const Held &h, const Slice (&part)
     const uint32_t d = (x[j] & keep) ^ two;
     m |= ((d & 0xFFFFu) == 0) << (2 * j) | (d >> 16 == 0) << (2 * j + 1);
   }
-  uint32_t left = rank - read_lane(excl, l) - (second ? read_lane(c0, l) : 0);
+  uint32_t left = rank - place.before;
   const uint32_t c = __popc(m), up_to = scan(c);
   if (up_to - c <= left && left < up_to) {
     left -= up_to - c;
@@ -954,15 +1048,16 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
     if (tid < a.n_slices) info = a.infos[row * a.n_slices + tid];
     ahead = load_ahead(a, row, share);
     clear(&lds.bins);
-    if (tid < kMaxSlices) sc.info[tid] = info;
+    if (tid < kMaxSlices) {
+      sc.info[tid] = info;
+      sc.slice_count[tid] = 0;
+    }
     const uint32_t most = scan(info.most);
     if (lane == 63) sc.count[wave_number()] = most;
     share_span(&spans, Span{info.lo, info.hi, 0, 0}, 0);
     lds_barrier();
     all = join_spans(spans, 0);
-    uint32_t sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += sc.count[w];
+    const uint32_t sum = read_lane(scan(lane < kWaves ? sc.count[lane] : 0), 63);
     packed = sum <= 0xFFFFu && fits(all);  // no value can occur more often than that
     if (packed) {
       base = base_of(all.hi);
@@ -1031,15 +1126,26 @@ __device__ __forceinline__ static void draw(const DrawArgs &a) {
   const uint32_t bin = bin_at(sc.at);
   uint32_t rank = sc.rank;
   if constexpr (!ONE) {
-    // How many of the value each slice holds: its list is in order.
-    uint32_t k = 0;
+    // How many of the value each slice holds.
+    const uint32_t k0 = share.k0;
+    if (a.n_slices <= kWaves && (k0 >= a.n_slices || sc.info[k0].length <= kAtOnce * share.step)) {
+      // the list of the wave's slice is still at hand
+      const uint32_t length = k0 < a.n_slices ? sc.info[k0].length : 0;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (share.i0 + j * share.step < length && ahead.e[j] >> 16 == bin) sc.slice_count[k0] = ahead.e[j] & 0xFFFFu;
+    } else {
+      // it is in order
 #pragma unroll 1
-    for (uint32_t j = wave_number(); j < a.n_slices; j += kWaves) {
-      const uint32_t c = count_in_list(list_of(a, row, j), sc.info[j].length, bin);
-      if (lane == 0) sc.slice_count[j] = c;
+      for (uint32_t j = k0; j < a.n_slices; j += share.groups) {
+        const uint32_t c = count_in_list(list_of(a, row, j), sc.info[j].length, bin);
+        if (lane == 0) sc.slice_count[j] = c;
+      }
     }
     lds_barrier();
-    while (k + 1 < a.n_slices && rank >= sc.slice_count[k]) rank -= sc.slice_count[k++];
+    const Place place = place_of(sc.slice_count[2 * lane], sc.slice_count[2 * lane + 1], rank);
+    const uint32_t k = min(place.at, a.n_slices - 1);
+    rank -= place.before;
     part[0] = slice_of(a.sh, row, k);
     held.load(part);
   }

@@ -259,7 +259,8 @@ typedef struct {
  * id ranges overlap, col_offset + ncols > 2^31, a small workspace, or an
  * output or workspace overlapping an input or one another;
  * XFER_E_UNSUPPORTED for a shard wider than 2,097,152 columns or more than
- * 2^24 - 1 workgroups (one for a row and 32,768 columns).
+ * 2^24 - 1 workgroups (one for a row, and one for each 16,384 columns or part
+ * of a shard where a row has more than 32,768).
  */
 XFER_API size_t xfer_sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1);
 XFER_API int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sample_params *params,

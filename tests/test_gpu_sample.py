@@ -185,6 +185,44 @@ def test_more_distinct_values_than_shared_memory_keeps(cols, n0):
     run(m, n0, params, drawn(rows, 18))
 
 
+CUTS = [(1.0, 0, 1.0, 0.05), (1.0, 0, 1.0, 1.0), (0.3, 0, 1.0, 1e-6), (1.0, 50, 1.0, 0.0), (2.0, 7, 0.9, 0.0),
+        (1.0, 64, 0.8, 0.2), (1.0, 500, 1.0, 0.01), (0.0, 0, 1.0, 0.3), (-2.0, 5, 1.0, 0.3), (1e30, 0, 1.0, 0.5),
+        (float("inf"), 0, 1.0, 0.5), (1e-30, 0, 1.0, 0.5), (1.0, 2000, 1.0, 0.0)]
+
+
+@pytest.mark.parametrize("n0,n1", [(1000, 1200), (40000, 30001), (16385, 16383)])
+@pytest.mark.parametrize("shape", ["apart", "below zero", "about zero", "tiny", "few", "infinite", "equal"])
+def test_settings_that_leave_most_elements_out(shape, n0, n1):
+    """What a part of a row may leave out depends on that part's own first elements: they differ between
+    the parts here, in size and in sign."""
+    rows, cols = len(CUTS), n0 + n1
+    rng = np.random.default_rng(n0 + len(shape))
+    v = rng.standard_normal((rows, cols)) * 2.0
+    if shape == "apart":
+        v[:, :n0] += 3.0
+        v[:, n0 // 2:n0] += 3.0
+    elif shape == "below zero":
+        v -= 20.0
+    elif shape == "about zero":
+        v = -np.abs(v)
+        v[:, ::97] = 0.0
+    elif shape == "tiny":
+        v *= 1e-38
+    elif shape == "few":
+        v[:, :] = -np.inf
+        v[:, 5::cols // 9] = rng.standard_normal(v[:, 5::cols // 9].shape)
+    elif shape == "infinite":
+        v[:, [3, n0 - 1, n0 + 2, cols - 1]] = np.inf
+        v[:, 10:500] = np.nan
+    elif shape == "equal":
+        v = np.round(v)
+    bits = torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16).copy()
+    if shape == "infinite":
+        bits[:, 10:200] = 0x7FC1                       # NaN of both signs
+        bits[:, 200:500] = 0xFFFF
+    run(bits, n0, CUTS, rng.random(rows))
+
+
 def test_odd_settings():
     """Temperatures and limits past their ranges mean what the header says."""
     inf, nan = float("inf"), float("nan")
