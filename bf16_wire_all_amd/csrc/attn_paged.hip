@@ -104,9 +104,13 @@ struct Layout {
 // Waves that stay resident on a SIMD.  Two, where registers allow: more wait
 // on more places of the memory at once, and two rows of 131071 tokens (heads of
 // 128, BF16) take 187 us on three of a SIMD and 169 on two.
+// Heads of 256 leave no registers for the queries beside two waves' or 32
+// heads' results: they are read from LDS for each tile, one step ahead of the
+// products (32 heads, E4M3, 8 rows of up to 20001 tokens: 35 us with them in
+// registers, 32 so; 32 heads of BF16 keep them, at one wave for a SIMD).
 template <int D, int KIND, int TILES>
 struct Residence {
-  static constexpr bool kQInLds = D == 256 && TILES == 1;
+  static constexpr bool kQInLds = D == 256 && (TILES == 1 || KIND == XFER_KV_E4M3);
   static constexpr int kPerSimd = D == 256 && (KIND == XFER_KV_BF16 || TILES == 2) ? 1 : 2;
 };
 
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
                  g = lane / 16;
   // The queries, in the lanes' order, where the exchange lies later.
   v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
-  static_assert(!R::kQInLds || L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
+  static_assert(!R::kQInLds || MR * L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
   uint32_t row = run.row;
   Visible vis = visible_of(a, row);
   uint32_t units = units_of(vis);
@@ -272,7 +276,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
                        : v4u{0, 0, 0, 0};
   };
   if constexpr (R::kQInLds) {
-    for (int k = wave; k < L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(0, k);
+    for (int k = wave; k < MR * L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k / L::kMfmaK, k % L::kMfmaK);
     __syncthreads();
   } else {
 #pragma unroll
@@ -370,22 +374,41 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
     v4f s[MR][2];
 #pragma unroll
     for (int r = 0; r < MR; ++r) s[r][0] = s[r][1] = v4f{0, 0, 0, 0};
+    // The 16 tokens of a half, dims of step kk.
+    auto keys = [&](int half, int kk) {
+      if constexpr (KIND == XFER_KV_BF16) {
+        return k[half][kk];
+      } else {
+        const v4u w = k[half][kk / 2];
+        const uint32_t w0 = kk % 2 ? w.z : w.x, w1 = kk % 2 ? w.w : w.y;
+        return v4u{e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1),
+                   e4m3x2_to_bf16<true>(w1)};
+      }
+    };
+    if constexpr (R::kQInLds) {
+      v4u held[2][MR];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+      for (int r = 0; r < MR; ++r) held[0][r] = lds_q[r * L::kMfmaK * 64 + lane];
 #pragma unroll
       for (int kk = 0; kk < L::kMfmaK; ++kk) {
-        v4u op;
-        if constexpr (KIND == XFER_KV_BF16) {
-          op = k[half][kk];
-        } else {
-          const v4u w = k[half][kk / 2];
-          const uint32_t w0 = kk % 2 ? w.z : w.x, w1 = kk % 2 ? w.w : w.y;
-          op = v4u{e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1),
-                   e4m3x2_to_bf16<true>(w1)};
+        if (kk + 1 < L::kMfmaK) {
+#pragma unroll
+          for (int r = 0; r < MR; ++r) held[(kk + 1) % 2][r] = lds_q[(r * L::kMfmaK + kk + 1) * 64 + lane];
         }
-        if constexpr (R::kQInLds) {
-          s[0][half] = mfma(op, lds_q[kk * 64 + lane], s[0][half]);
-        } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const v4u op = keys(half, kk);
+#pragma unroll
+          for (int r = 0; r < MR; ++r) s[r][half] = mfma(op, held[kk % 2][r], s[r][half]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // or all reads would be made first, and held
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int kk = 0; kk < L::kMfmaK; ++kk) {
+          const v4u op = keys(half, kk);
 #pragma unroll
           for (int r = 0; r < MR; ++r) s[r][half] = mfma(op, q[r][kk], s[r][half]);
         }
