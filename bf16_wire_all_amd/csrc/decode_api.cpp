@@ -29,6 +29,7 @@ int cache_checks(const xfer_kv_cache *c, uint64_t *extent) {
   if (c->n_pages == 0 || c->page_tokens == 0 || c->kv_heads == 0) return XFER_E_INVAL;
   if (c->page_tokens & (c->page_tokens - 1)) return XFER_E_INVAL;
   if (c->kind == XFER_KV_BF16 && (c->k_scale || c->v_scale)) return XFER_E_INVAL;
+  if ((uintptr_t)c->k_scale % 4 || (uintptr_t)c->v_scale % 4) return XFER_E_INVAL;
   if (c->reserved) return XFER_E_INVAL;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return XFER_E_UNSUPPORTED;
   if (c->page_tokens > 65536) return XFER_E_UNSUPPORTED;
@@ -59,6 +60,33 @@ bool slots_disjoint(const xfer_kv_cache *c) {
     extent += t.stride * (t.count - 1);
   }
   return true;
+}
+
+// Whether an element of the values shares a byte with one of the keys, whose
+// elements are disjoint among themselves: `by` bytes lie between two elements,
+// and from stride `level` of s (in descending order) inwards each may still be
+// moved either way.
+struct Stride {
+  uint64_t bytes, count;
+};
+bool values_touch(const Stride *s, int level, int64_t by, int64_t row) {
+  if (level == 3) return by < row && -by < row;
+  const int64_t step = (int64_t)s[level].bytes, most = (int64_t)s[level].count - 1;
+  if (most == 0) return values_touch(s, level + 1, by, row);
+  int64_t inner = row;  // bytes of what lies inside one step
+  for (int i = level + 1; i < 3; ++i) inner += (int64_t)s[i].bytes * ((int64_t)s[i].count - 1);
+  const int64_t near = -by / step;  // only steps about there can bring them together
+  for (int64_t t = std::max(near - 1, -most); t <= std::min(near + 1, most); ++t) {
+    const int64_t d = by + t * step;
+    if (d < inner && -d < inner && values_touch(s, level + 1, d, row)) return true;
+  }
+  return false;
+}
+bool values_apart(const xfer_kv_cache *c) {
+  Stride s[3] = {{c->page_stride, c->n_pages}, {c->token_stride, c->page_tokens}, {c->head_stride, c->kv_heads}};
+  std::sort(s, s + 3, [](const Stride &a, const Stride &b) { return a.bytes > b.bytes; });
+  return !values_touch(s, 0, (int64_t)((uintptr_t)c->v - (uintptr_t)c->k),
+                       (int64_t)c->head_dim * element_bytes(c->kind));
 }
 
 // Rows of `len` bytes, `pitch` apart.
@@ -125,7 +153,7 @@ int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xf
   uint64_t extent = 0;
   const int st = cache_checks(cache, &extent);
   if (st != XFER_OK) return st;
-  if (!slots_disjoint(cache) || cache->v == cache->k) return XFER_E_OVERLAP;
+  if (!slots_disjoint(cache) || !values_apart(cache)) return XFER_E_OVERLAP;
   if (!in || !rope || in->reserved || rope->reserved) return XFER_E_INVAL;
   if (rope->style != XFER_ROPE_HALVES && rope->style != XFER_ROPE_PAIRS) return XFER_E_INVAL;
   if (!(in->eps >= 0.0f) || !std::isfinite(in->eps)) return XFER_E_INVAL;
@@ -133,9 +161,10 @@ int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xf
   if (in->tokens == 0) return XFER_OK;
   const uint64_t T = in->tokens, q_row = (uint64_t)in->q_heads * cache->head_dim;
   const uint64_t kv_row = (uint64_t)cache->kv_heads * cache->head_dim;
-  if (rope->rot_dim && (!rope->cos_sin || !aligned16(rope->cos_sin) || !rope->positions || !rope->max_pos))
+  if (rope->rot_dim && (!rope->cos_sin || !aligned16(rope->cos_sin) || !rope->positions ||
+                        (uintptr_t)rope->positions % 4 || !rope->max_pos))
     return XFER_E_INVAL;
-  if (!slots || !in->k || !in->v || !aligned16(in->k) || !aligned16(in->v)) return XFER_E_INVAL;
+  if (!slots || (uintptr_t)slots % 8 || !in->k || !in->v || !aligned16(in->k) || !aligned16(in->v)) return XFER_E_INVAL;
   if (in->q_heads && (!in->q || !q_out || !aligned16(in->q) || !aligned16(q_out))) return XFER_E_INVAL;
   if (!aligned16(in->q_weight) || !aligned16(in->k_weight)) return XFER_E_INVAL;
   if (!ld_ok(in->k_ld, T, kv_row) || !ld_ok(in->v_ld, T, kv_row)) return XFER_E_INVAL;
@@ -154,6 +183,23 @@ int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xf
     if (overlaps(c, extent, out.at, out.extent())) return XFER_E_INVAL;
     for (const Rows &r : ins)
       if (overlaps(c, extent, r.at, r.extent())) return XFER_E_INVAL;
+  }
+  const uint64_t dim_bytes = cache->head_dim * 2ull, scale_bytes = cache->kv_heads * 4ull;
+  const struct {
+    const void *at;
+    uint64_t bytes;
+  } others[7] = {{slots, T * 8},
+                 {rope->rot_dim ? rope->positions : nullptr, T * 4},
+                 {rope->rot_dim ? rope->cos_sin : nullptr, (uint64_t)rope->max_pos * rope->rot_dim * 4},
+                 {in->q_weight, dim_bytes},
+                 {in->k_weight, dim_bytes},
+                 {cache->k_scale, scale_bytes},
+                 {cache->v_scale, scale_bytes}};
+  for (const auto &o : others) {
+    if (!o.at) continue;
+    if (rows_touch(out, Rows{(uintptr_t)o.at, 0, o.bytes, 1})) return XFER_E_INVAL;
+    for (uintptr_t c : caches)
+      if (overlaps(c, extent, (uintptr_t)o.at, o.bytes)) return XFER_E_INVAL;
   }
   const uint64_t heads = (uint64_t)in->q_heads + 2ull * cache->kv_heads;
   if (heads > UINT32_MAX ||
@@ -223,6 +269,10 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
     if (rows_touch(o, r) || overlaps(w, need, r.at, r.extent())) return XFER_E_INVAL;
   for (uintptr_t c : caches)
     if (overlaps(c, extent, o.at, o.extent()) || overlaps(c, extent, w, need)) return XFER_E_INVAL;
+  for (const float *scales : {cache->k_scale, cache->v_scale})
+    if (scales && (overlaps((uintptr_t)scales, cache->kv_heads * 4ull, o.at, o.extent()) ||
+                   overlaps((uintptr_t)scales, cache->kv_heads * 4ull, w, need)))
+      return XFER_E_INVAL;
   if (overlaps(w, need, o.at, o.extent())) return XFER_E_INVAL;
   if (s.workgroups > xfer::kMaxGridBlocks || R * q_heads > xfer::kMaxGridBlocks) return XFER_E_UNSUPPORTED;
 

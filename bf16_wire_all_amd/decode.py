@@ -158,7 +158,7 @@ def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_
             raise ValueError("one weight for each element of a head")
     rope = RopeC(0, 0, 0, 0, ROPE_PAIRS if interleaved else ROPE_HALVES, 0)
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or positions.numel() != tokens:
+        if positions is None or cos_sin.dim() != 2 or positions.numel() != tokens:
             raise ValueError("cos_sin must be [max_pos, rot_dim], with a position for each token")
         rope.cos_sin = _flat(cos_sin, 4, dev, "cos_sin")
         rope.positions = _flat(positions, 4, dev, "positions")

@@ -67,8 +67,8 @@ typedef struct {
  * The checks that every call makes of a cache: XFER_E_INVAL for a NULL cache,
  * NULL or misaligned k or v, a stride that is not a multiple of 16,
  * n_pages, page_tokens or kv_heads 0, page_tokens not a power of two, an
- * unknown kind, scales with XFER_KV_BF16, reserved not 0, or an extent that
- * passes 2^47 bytes; XFER_E_UNSUPPORTED for another head_dim or page_tokens
+ * unknown kind, scales with XFER_KV_BF16, misaligned scales (4 bytes),
+ * reserved not 0, or an extent that passes 2^47 bytes; XFER_E_UNSUPPORTED for another head_dim or page_tokens
  * above 65,536.
  */
 
@@ -128,12 +128,13 @@ typedef struct {
  * stored.  No byte of the cache outside the named slots is written.
  *
  * Errors: those of the cache; XFER_E_OVERLAP if two slots of the cache share
- * bytes or v == k; XFER_E_INVAL for NULL or misaligned pointers (k, v, q and
- * q_out where there are heads; slots), lds that are not multiples of 8 or
+ * bytes, of keys, of values or one of each; XFER_E_INVAL for NULL or
+ * misaligned pointers (k, v, q and q_out where there are heads; slots, 8
+ * bytes), lds that are not multiples of 8 or
  * smaller than a row, a q_out row that overlaps a row of q, k or v (except in
- * place) or the cache, an input overlapping the cache, eps negative or not
+ * place), another input or the cache, an input overlapping the cache, eps negative or not
  * finite, rot_dim not a multiple of 8 or above head_dim, a rotation with NULL
- * or misaligned table, NULL positions or max_pos 0, an unknown style, or a
+ * or misaligned table, NULL or misaligned positions (4 bytes) or max_pos 0, an unknown style, or a
  * reserved field that is not 0; XFER_E_UNSUPPORTED if the call needs more
  * than 2^24 - 1 workgroups (about one for 16 heads of a token).
  */
@@ -167,7 +168,8 @@ typedef struct {
  *   s_j = scale * q[r][h] . k_j        (k_j times k_scale[g] if there is one)
  *   out[r][h] = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s)
  *                                      (v_j times v_scale[g])
- * A row with no visible token (length 0, or holes alone) gets zeros.  A page
+ * A row with no visible token (length 0, or holes alone) gets zeros, and so
+ * does a head whose scores are all -inf.  A page
  * number that is not below n_pages is a hole: its tokens are not visible and
  * nothing is read for them.  What pages hold past a row's length, and tokens
  * outside the window, has no influence, NaN and infinities included.
@@ -195,8 +197,8 @@ typedef struct {
  * a scale that is not finite, sinks without a window, max_len 0 or above
  * 2^31 - 1, a table_ld below ceil(max_len / page_tokens) (rows > 1), lds that
  * are not multiples of 8 or smaller than a row, an unknown out_mode, a small
- * workspace, or an output or workspace that overlaps q, the cache, the table,
- * the lengths or one another; XFER_E_UNSUPPORTED for more than 2^24 - 1
+ * workspace, or an output or workspace that overlaps q, the cache, its scales,
+ * the table, the lengths or one another; XFER_E_UNSUPPORTED for more than 2^24 - 1
  * workgroups.
  *
  * xfer_attn_workspace_bytes - the bytes that such a call needs (0 also for a

@@ -8,6 +8,7 @@ import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 import bf16_wire_all_amd as x
@@ -132,6 +133,41 @@ def test_store_refuses_overlapping_slots():
     assert store(cache(n_pages=1, page_stride=0), empty) == x.OK  # one page: its stride is never walked
 
 
+def test_store_refuses_values_over_keys():
+    """Every way of laying small caches of keys and values into one another, against their bytes."""
+    rng = np.random.default_rng(4)
+    seen = {x.OK: 0, x.E_OVERLAP: 0}
+    for _ in range(3000):
+        counts = [int(n) for n in rng.integers(1, 4, 2)] + [int(2 ** rng.integers(0, 3))]   # pages, heads, slots
+        # nested strides in any order, with room for the other half somewhere, or a little too small
+        strides, extent = [0, 0, 0], 64
+        for i in rng.permutation(3):
+            strides[i] = extent + 16 * int(rng.integers(-1 if rng.random() < 0.1 else 0, 2)) + extent * int(
+                rng.integers(0, 2))
+            extent = strides[i] * counts[i] if rng.random() < 0.5 else extent + strides[i] * (counts[i] - 1)
+        by = 16 * int(rng.integers(-2 * extent // 16, 2 * extent // 16))
+        if rng.random() < 0.5:                                     # a likely place: a multiple of a part
+            by = int(rng.choice([64, -64, *strides, *[-s for s in strides]])) * int(rng.integers(1, 3))
+        c = cache(k=K, v=K + by, page_stride=strides[0], head_stride=strides[1], token_stride=strides[2],
+                  n_pages=counts[0], kv_heads=counts[1], page_tokens=counts[2], head_dim=64, kind=decode.KV_E4M3)
+        at = [p * strides[0] + h * strides[1] + t * strides[2] for p in range(counts[0]) for h in range(counts[1])
+              for t in range(counts[2])]
+        starts = sorted(at + [a + by for a in at])
+        touch = any(b - a < 64 for a, b in zip(starts, starts[1:]))
+        got = store(c, qkv(tokens=0), rope(rot_dim=64))
+        seen[got] += 1
+        if touch:
+            assert got == x.E_OVERLAP, (counts, strides, by)
+        else:
+            # slots that are disjoint without being nested are refused too
+            nested, e = True, 64
+            for st, n in sorted(zip(strides, counts)):
+                nested &= n == 1 or st >= e
+                e += st * (n - 1) if n > 1 else 0
+            assert got == (x.OK if nested else x.E_OVERLAP), (counts, strides, by)
+    assert min(seen.values()) > 500, seen
+
+
 @pytest.mark.parametrize("q,r,more,status", [
     (dict(reserved=1), {}, {}, x.E_INVAL), ({}, dict(reserved=1), {}, x.E_INVAL), ({}, dict(style=2), {}, x.E_INVAL),
     (dict(eps=-1e-6), {}, {}, x.E_INVAL), (dict(eps=float("nan")), {}, {}, x.E_INVAL),
@@ -153,6 +189,27 @@ def test_store_refuses_overlapping_slots():
 ])
 def test_store_refusals(q, r, more, status):
     assert store(q=qkv(**q), r=rope(**r), **more) == status
+
+
+@pytest.mark.parametrize("q,r,c,more", [
+    ({}, dict(positions=66), {}, {}), ({}, {}, {}, dict(slots=68)),                 # misaligned
+    ({}, {}, dict(kind=decode.KV_E4M3, k_scale=66), {}), ({}, {}, dict(kind=decode.KV_E4M3, v_scale=65), {}),
+    ({}, {}, {}, dict(slots=QO + 64)), ({}, dict(positions=QO), {}, {}),            # q_out over what is read
+    ({}, dict(cos_sin=QO + 4096), {}, {}), (dict(q_weight=QO), {}, {}, {}), (dict(k_weight=QO + 16), {}, {}, {}),
+    ({}, {}, dict(kind=decode.KV_E4M3, k_scale=QO + 4), {}), ({}, {}, {}, dict(slots=K + 64)),   # the cache over it
+    ({}, dict(positions=V + 8), {}, {}), ({}, dict(cos_sin=K), {}, {}), (dict(q_weight=V), {}, {}, {}),
+    ({}, {}, dict(kind=decode.KV_E4M3, v_scale=K + 4), {}),
+])
+def test_store_refuses_misaligned_and_overlapping_inputs(q, r, c, more):
+    assert store(cache(**c), qkv(**q), rope(**r), **more) == x.E_INVAL
+
+
+@pytest.mark.parametrize("c,more", [
+    (dict(k_scale=66), {}), (dict(v_scale=67), {}), (dict(k_scale=QO), {}), (dict(v_scale=QO + 2048), {}),
+    (dict(k_scale=0xC0_0000), {}), (dict(v_scale=0xC0_0010), {}),
+])
+def test_attn_refuses_misaligned_scales_and_an_output_over_them(c, more):
+    assert attn(cache(kind=decode.KV_E4M3, **c), **more) == x.E_INVAL
 
 
 def test_store_in_a_fused_buffer():
