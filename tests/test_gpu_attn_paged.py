@@ -166,6 +166,15 @@ def test_many_short_rows_and_one_long():
     run(World([1 + 7 * i % 60 for i in range(200)] + [3000], 4, 1, 64, 16, seed=4))
 
 
+@pytest.mark.parametrize("d,kind", [(64, "e4m3"), (128, "bf16")])
+def test_more_rows_than_threads(d, kind):
+    """Rows beyond one for each thread of a workgroup, in runs and as a whole."""
+    lens = [(i * 37) % 90 for i in range(701)]
+    run(World(lens, 2, 1, d, 16, kind, seed=17))
+    lens[300] = 9000
+    run(World(lens, 2, 1, d, 16, kind, seed=18))
+
+
 def test_lengths_below_the_bound_and_above_it():
     """max_len is a bound: shorter rows are served, longer ones are cut to it."""
     run(World([10, 500, 999], 4, 2, 64, 16, max_len=40000, seed=5))

@@ -5,6 +5,8 @@ stores one token of each request, attends, multiplies by a head and samples
 the token that the next step takes.  Each operator's result is compared with
 its formulas in 64 bits, from what it read on the device; the step captured
 in a graph and replayed has to give the eager run's bits."""
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -215,3 +217,48 @@ def test_prompts_moved_and_continued(d, kind, window, sinks):
             assert torch.equal(a, b), ("replay", i)
         step.attn_ws.fill_(0xFF)
         step.sample_ws.fill_(0xFF)
+
+
+def test_two_workers_at_once():
+    """Two threads with streams, caches and workspaces of their own: each gets the bits that it gets alone."""
+    say("decode step, two workers")
+    d, rows, steps = 128, 3, 12
+    g = torch.Generator().manual_seed(9)
+    embed = torch.randn((VOCAB, (HQ + 2 * HKV) * d), generator=g).to(torch.bfloat16).to(DEV)
+    head = (torch.randn((HQ * d, VOCAB), generator=g) * 0.2).to(torch.bfloat16).to(DEV)
+    angle = torch.arange(4096)[:, None] * 10000.0 ** (-torch.arange(d // 2) / (d // 2))
+    cs = torch.cat([angle.cos(), angle.sin()], 1).float().contiguous().to(DEV)
+    workers = []
+    for w in range(2):
+        decoder = Worker(rows * 200 + 3, d, "bf16", (None, None))
+        fill = torch.randn(decoder.pages.shape, generator=g).to(torch.bfloat16)
+        decoder.pages.copy_(fill)
+        numbers = torch.randperm(rows * 200 + 3, generator=g)[:rows * 200].view(rows, 200).int().to(DEV)
+        lens = torch.tensor([2900 - 7 * w, 5 + w, 900], dtype=torch.int32, device=DEV)
+        workers.append(Step(decoder, numbers, lens, embed, head, cs, (None, None), d, 0, 0))
+    us = torch.rand((steps, rows), generator=g).to(DEV)
+
+    def go(step, stream):
+        with torch.cuda.stream(stream):
+            got = []
+            for i in range(steps):
+                step.u.copy_(us[i])
+                step.run()
+                got.append(step.results())
+            stream.synchronize()
+        return got
+
+    begins = [s.state() for s in workers]
+    streams = [torch.cuda.Stream() for _ in workers]
+    torch.cuda.synchronize()
+    alone = []
+    for s, stream in zip(workers, streams):
+        alone.append(go(s, stream))
+    for s, b in zip(workers, begins):
+        s.restore(b)
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(2) as ex:
+        both = list(ex.map(go, workers, streams))
+    for a, b in zip(alone, both):
+        for i in range(steps):
+            assert all(torch.equal(p, q) for p, q in zip(a[i], b[i])), ("step", i)

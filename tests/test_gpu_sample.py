@@ -17,6 +17,9 @@ DEV = "cuda:0"
 GUARD = 64
 SETTINGS = [(1.0, 0, 1.0, 0.0), (0.7, 40, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.05), (0.8, 50, 0.95, 0.02),
             (0.0, 0, 1.0, 0.0), (1.3, 0, 0.999, 0.001), (2.0, 1000, 0.5, 0.0), (1.0, 1, 1.0, 0.0), (5.0, 0, 1.0, 0.5)]
+CUTS = [(1.0, 0, 1.0, 0.05), (1.0, 0, 1.0, 1.0), (0.3, 0, 1.0, 1e-6), (1.0, 50, 1.0, 0.0), (2.0, 7, 0.9, 0.0),
+        (1.0, 64, 0.8, 0.2), (1.0, 500, 1.0, 0.01), (0.0, 0, 1.0, 0.3), (-2.0, 5, 1.0, 0.3), (1e30, 0, 1.0, 0.5),
+        (float("inf"), 0, 1.0, 0.5), (1e-30, 0, 1.0, 0.5), (1.0, 2000, 1.0, 0.0)]
 
 
 def values_of(bits):
@@ -93,6 +96,15 @@ def test_settings(setting):
 
 def test_the_widest_shards():
     run(logits(2, 2097152 + 2000000, 7), 2097152, [SETTINGS[0], SETTINGS[4]], drawn(2, 8))
+
+
+@pytest.mark.parametrize("rows,n0,n1", [(300, 20001, 20003), (70, 40960, 40961), (100, 33000, 40001)])
+def test_more_slices_than_workgroups(rows, n0, n1):
+    """Workgroups of the count go from slice to slice; every seventh row is masked but for a few elements."""
+    bits = logits(rows, n0 + n1, rows)
+    bits[3::7, 100::] = 0xFF80
+    bits[5::7, :n0 + 50] = 0xFF80
+    run(bits, n0, [(SETTINGS + CUTS)[r % (len(SETTINGS) + len(CUTS))] for r in range(rows)], drawn(rows, rows + 1))
 
 
 def test_masked_rows():
@@ -183,11 +195,6 @@ def test_more_distinct_values_than_shared_memory_keeps(cols, n0):
     params = [((64.0, 0, 1.0, 0.0), (200.0, 30000, 1.0, 0.0), (100.0, 0, 0.7, 0.0), (300.0, 0, 1.0, 0.3))[r % 4]
               for r in range(rows)]
     run(m, n0, params, drawn(rows, 18))
-
-
-CUTS = [(1.0, 0, 1.0, 0.05), (1.0, 0, 1.0, 1.0), (0.3, 0, 1.0, 1e-6), (1.0, 50, 1.0, 0.0), (2.0, 7, 0.9, 0.0),
-        (1.0, 64, 0.8, 0.2), (1.0, 500, 1.0, 0.01), (0.0, 0, 1.0, 0.3), (-2.0, 5, 1.0, 0.3), (1e30, 0, 1.0, 0.5),
-        (float("inf"), 0, 1.0, 0.5), (1e-30, 0, 1.0, 0.5), (1.0, 2000, 1.0, 0.0)]
 
 
 @pytest.mark.parametrize("n0,n1", [(1000, 1200), (40000, 30001), (16385, 16383)])
