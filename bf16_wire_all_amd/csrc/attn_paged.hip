@@ -147,9 +147,12 @@ __device__ __forceinline__ void load_v(uint32_t *dst, const uint8_t *row, uint32
   }
 }
 
-// Weights of eight tokens as two BF16 numbers each, high and low.
+// Weights of eight tokens as PARTS BF16 numbers each, whose sum is the weight
+// to 2^-9 of itself for each: two (2^-18) are far below a BF16 result's own
+// rounding, three (2^-27) below that of F32.
+template <int PARTS>
 struct Weights {
-  v4u hi, lo;
+  v4u part[PARTS];
 };
 
 // What a (row, kv head) that fell to several workgroups leaves: its first
@@ -215,7 +218,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   return run;
 }
 
-template <int D, int KIND, int TILES>
+template <int D, int KIND, int TILES, int PARTS>
 __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
                                                                                              uint32_t m_groups) {
   using L = Layout<D, KIND>;
@@ -422,7 +425,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
       next = look_up(t + 2 * kStep);
     }
 
-    Weights w[MR];
+    Weights<PARTS> w[MR];
 #pragma unroll
     for (int r = 0; r < MR; ++r) {
       float x[8];
@@ -453,9 +456,14 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[r].hi[i] = bf16x2(p[2 * i], p[2 * i + 1]);
-        w[r].lo[i] = bf16x2(p[2 * i] - __uint_as_float(w[r].hi[i] << 16),
-                            p[2 * i + 1] - __uint_as_float(w[r].hi[i] & 0xFFFF0000u));
+        float x0 = p[2 * i], x1 = p[2 * i + 1];
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) {
+          const uint32_t two = bf16x2(x0, x1);
+          w[r].part[c][i] = two;
+          x0 -= __uint_as_float(two << 16);
+          x1 -= __uint_as_float(two & 0xFFFF0000u);
+        }
       }
     }
 
@@ -485,10 +493,10 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
       }
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
-        o[r][2 * i] = mfma(even, w[r].hi, o[r][2 * i]);
-        o[r][2 * i] = mfma(even, w[r].lo, o[r][2 * i]);
-        o[r][2 * i + 1] = mfma(odd, w[r].hi, o[r][2 * i + 1]);
-        o[r][2 * i + 1] = mfma(odd, w[r].lo, o[r][2 * i + 1]);
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) o[r][2 * i] = mfma(even, w[r].part[c], o[r][2 * i]);
+#pragma unroll
+        for (int c = 0; c < PARTS; ++c) o[r][2 * i + 1] = mfma(odd, w[r].part[c], o[r][2 * i + 1]);
       }
     }
     off = off_next;
@@ -653,11 +661,17 @@ uint32_t resident(uint32_t head_dim, uint32_t tiles) {
                            : resident<256, KIND>(tiles);
 }
 
+template <int D, int KIND, int TILES>
+hipError_t launch_parts(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
+  const dim3 grid((uint32_t)s.workgroups);
+  if (a.out_mode == XFER_OUT_F32)
+    return launch(attn_kernel<D, KIND, TILES, 3>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  return launch(attn_kernel<D, KIND, TILES, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+}
+
 template <int D, int KIND>
 hipError_t launch_tiles(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
-  const dim3 grid((uint32_t)s.workgroups);
-  if (s.m_tiles == 1) return launch(attn_kernel<D, KIND, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
-  return launch(attn_kernel<D, KIND, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  return s.m_tiles == 1 ? launch_parts<D, KIND, 1>(a, s, stream) : launch_parts<D, KIND, 2>(a, s, stream);
 }
 
 template <int D>
