@@ -638,19 +638,16 @@ __device__ __forceinline__ static double least_of(const xfer_sample_params &p) {
   return p.min_p > 1.0f ? 1.0 : (double)p.min_p;
 }
 
-// Smallest r in [1, most] with before + r * w >= target (over: > target).
+// Smallest r in [1, most] with before + r * w >= target (over: > target), or
+// most.
 __device__ __forceinline__ static uint32_t rank_of(double before, double w, uint32_t most, double target, bool over) {
   const double q = (target - before) / w;
-  uint32_t r = q > 1.0 ? (q < (double)most ? (uint32_t)q : most) : 1;
-  auto reached = [&](uint32_t k) {
-    const double c = before + k * w;
-    return over ? c > target : c >= target;
-  };
-  // the quotient is off by one step at most
-  if (r > 1 && reached(r - 1)) --r;
-  if (!reached(r) && r < most) ++r;
-  if (!reached(r) && r < most) ++r;
-  return r;
+  const uint32_t r = q > 1.0 ? (q < (double)most ? (uint32_t)q : most) : 1;
+  // the quotient is off by one step at most: a lane for each number about it
+  const uint32_t k = min(max(r, 2u) - 1 + threadIdx.x % 4, most);
+  const double c = before + k * w;
+  const uint64_t reached = __ballot(over ? c > target : c >= target) & 0xF;
+  return reached ? read_lane(k, (uint32_t)__builtin_ctzll(reached)) : most;
 }
 
 // The cuts and the draw on a list of up to 64 entries by one wave, an entry
@@ -662,13 +659,12 @@ __device__ __forceinline__ static void search_in_wave(uint32_t count, double wei
   const uint32_t n_run = scan(there ? count : 0);
   const double m_run = scan(there ? count * weight : 0.0);
   const uint64_t below = __ballot(there && weight < least_of(p));
-  keep = min(keep, read_lane(n_run, 63));
   struct {
     uint32_t at, rank;
     double z;  // weights up to there
-  } f = {n - 1, kNone, 0.0};
+  } f = {n - 1, kNone, read_lane(m_run, 63)};
 #pragma unroll 1
-  for (int border = 0; border < 4; ++border) {  // as in search() below
+  for (int border = keep < read_lane(n_run, 63) ? 0 : 1; border < 4; ++border) {  // as in search() below
     double target = 0;
     uint32_t last = f.at, last_count = f.rank;
     if (border == 1) {
@@ -764,16 +760,16 @@ __device__ __forceinline__ static void search(const First &first, const Entry &e
   const double wave_masses = scan(is_wave ? sc->mass[lane % kWaves] : 0.0);
   const uint32_t m_at = ~wave_max(~(is_wave ? sc->below[lane % kWaves] : kNone));
 
-  // Four borders, one after the other: the last element that top_k keeps, the
-  // first that reaches top_p, the last before min_p's limit, and the drawn one.
-  // f is the last entry kept so far, with `rank` of its elements.
-  keep = min(keep, read_lane(wave_counts, 63));
+  // Four borders, one after the other: the last element that top_k keeps (if
+  // it does not keep all), the first that reaches top_p, the last before
+  // min_p's limit, and the drawn one.  f is the last entry kept so far, with
+  // `rank` of its elements.
   struct {
     uint32_t at, rank;
     double z;  // weights up to there
-  } f = {n - 1, kNone, 0.0};
+  } f = {n - 1, kNone, read_lane(wave_masses, 63)};
 #pragma unroll 1
-  for (int border = 0; border < 4; ++border) {
+  for (int border = keep < read_lane(wave_counts, 63) ? 0 : 1; border < 4; ++border) {
     double target = 0;
     uint32_t t, last = f.at, last_count = f.rank;
     if (border == 1) {
