@@ -12,7 +12,7 @@
 //     (max, sum, weighted sum) of each part in the workspace, at most two for a
 //     workgroup, and a second launch joins them;
 //   - a workgroup takes all query heads of a kv head, so a key is read from
-//     memory once for all of them.  Four waves take tiles of 32 tokens in turn,
+//     memory once for all of them.  Its waves take tiles of 32 tokens in turn,
 //     each with a running maximum and sum of its own, and meet once for each
 //     (row, kv head), in LDS.  Heads beyond 16 take more registers of these
 //     waves (up to 32 heads; the next 32 are a kv head of their own);
@@ -44,12 +44,14 @@
 namespace xfer {
 namespace {
 
-constexpr int kWaves = 4;                        // that share the tokens
-constexpr int kThreads = 64 * kWaves;            // for 16 query heads
+constexpr int kWaves = 4;                        // that share the tokens of a run
+constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kTile = 32;                   // tokens of a wave's tile
-constexpr uint32_t kStep = kTile * kWaves;       // tokens of a workgroup's round
+constexpr uint32_t kStep = kTile * kWaves;       // tokens of a unit
 constexpr uint32_t kWholeUnits = 16;             // of a row that need not be cut up
 constexpr uint32_t kJoinUnits = 3;               // that the join is worth
+constexpr int kManyWaves = 8;                    // that share the tokens of a row with a compute unit to itself
+constexpr uint32_t kAloneBytes = 2048;           // of such a row's units, one row of each, at most
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
@@ -223,27 +225,30 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   return run;
 }
 
-template <int D, int KIND, int TILES, int PARTS>
-__global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
-                                                                                             uint32_t m_groups) {
+// WAVES: kWaves, or kManyWaves without runs.
+template <int D, int KIND, int TILES, int PARTS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
+                                                                                               uint32_t m_groups) {
   using L = Layout<D, KIND>;
   using R = Residence<D, KIND, TILES>;
   constexpr int MR = TILES;
   // A line holds the rows of two heads where they are shorter than it.
   constexpr bool kStream = D * L::kBytes >= 128;
+  constexpr uint32_t kRound = kTile * WAVES;  // tokens of a round
   constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
-  __shared__ float lds_o[kWaves][16][D + kPad];
-  __shared__ float lds_all_m[MR][kWaves][16], lds_all_l[MR][kWaves][16];
+  __shared__ float lds_o[WAVES][16][D + kPad];
+  __shared__ float lds_all_m[MR][WAVES][16], lds_all_l[MR][WAVES][16];
 
   const uint32_t inner_n = a.cache.kv_heads * m_groups;
   const uint32_t xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
+  const bool runs = WAVES == kWaves && a.parts;
   uint32_t wg = 0;
   Run run;
-  if (a.parts) {
+  if (runs) {
     // Neighbouring runs on one XCD: its L2 then serves the lines that two
     // heads share.
     wg = xcd * (gridDim.x / kXcds) + rest;
-    run = run_of(a, inner_n, wg, gridDim.x);
+    if constexpr (WAVES == kWaves) run = run_of(a, inner_n, wg, gridDim.x);
     if (run.length == 0) return;
   } else {
     // A workgroup for each (row, kv head): rows go round the XCDs, and the
@@ -262,7 +267,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
   uint32_t units = units_of(vis);
   uint32_t inner = rest % inner_n, unit = 0;
   uint64_t left = units;
-  if (a.parts) {
+  if (runs) {
     inner = __builtin_amdgcn_readfirstlane((uint32_t)(run.at / units));
     unit = __builtin_amdgcn_readfirstlane((uint32_t)(run.at % units));
     left = run.length;
@@ -284,7 +289,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
                        : v4u{0, 0, 0, 0};
   };
   if constexpr (R::kQInLds) {
-    for (int k = wave; k < MR * L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k / L::kMfmaK, k % L::kMfmaK);
+    for (int k = wave; k < MR * L::kMfmaK; k += WAVES) lds_q[k * 64 + lane] = load_q(k / L::kMfmaK, k % L::kMfmaK);
     __syncthreads();
   } else {
 #pragma unroll
@@ -369,9 +374,9 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
   if (t < v1) {
     off = offset_of(look_up(t));
     load_k(off);
-    next = look_up(t + kStep);
+    next = look_up(t + kRound);
   }
-  for (; t < v1; t += kStep) {
+  for (; t < v1; t += kRound) {
     // keep the queries where they are: read anew from LDS for each tile
     if constexpr (R::kQInLds) asm volatile("" ::: "memory");
     uint32_t vr[8][L::kDwordsV];
@@ -425,9 +430,9 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
 
     // The next tile's keys, while this one's weights are computed.
     const int64_t off_next = offset_of(next);
-    if (t + kStep < v1) {
+    if (t + kRound < v1) {
       load_k(off_next);
-      next = look_up(t + 2 * kStep);
+      next = look_up(t + 2 * kRound);
     }
 
     Weights<PARTS> w[MR];
@@ -507,10 +512,10 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
     off = off_next;
   }
 
-  // The four waves' results, joined in LDS.
+  // The waves' results, joined in LDS.
   const bool whole = take == units;
   const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
-  if (unit == 0 && threadIdx.x == 0 && a.parts)
+  if (unit == 0 && threadIdx.x == 0 && runs)
     reinterpret_cast<Parts *>(a.parts)[(uint64_t)row * inner_n + inner] =
         whole ? Parts{kWhole, 1} : Parts{slot, 1 + (uint32_t)((units - take + run.per - 1) / run.per)};
 #pragma unroll
@@ -532,7 +537,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
     {
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_m[w][n]);
       const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - top);
 #pragma unroll
       for (int j = 0; j < L::kMfmaV; ++j)
@@ -541,16 +546,16 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
     }
     __syncthreads();
 #pragma unroll
-    for (int it = 0; it < D / 64; ++it) {
-      const uint32_t at = it * kThreads + tid, hq = at / (D / 4), d = at % (D / 4) * 4;
+    for (uint32_t at = tid; at < 4 * D; at += 64 * WAVES) {
+      const uint32_t hq = at / (D / 4), d = at % (D / 4) * 4;
       const uint32_t h = h0 + 16 * r + hq;
       if (h >= a.group) continue;
       float top = -INFINITY, total = 0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_m[w][hq]);
       v4f v = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         const float mw = lds_m[w][hq];
         total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
         v += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
@@ -666,12 +671,20 @@ uint32_t resident(uint32_t head_dim, uint32_t tiles) {
                            : resident<256, KIND>(tiles);
 }
 
+template <int D, int KIND, int TILES, int PARTS>
+hipError_t launch_waves(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
+  const dim3 grid((uint32_t)s.workgroups);
+  if constexpr (Residence<D, KIND, TILES>::kPerSimd > 1) {
+    if (s.waves == kManyWaves)
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves>, grid, dim3(64 * kManyWaves), 0, stream, a, s.m_groups);
+  }
+  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+}
+
 template <int D, int KIND, int TILES>
 hipError_t launch_parts(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
-  const dim3 grid((uint32_t)s.workgroups);
-  if (a.out_mode == XFER_OUT_F32)
-    return launch(attn_kernel<D, KIND, TILES, 3>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
-  return launch(attn_kernel<D, KIND, TILES, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  return a.out_mode == XFER_OUT_F32 ? launch_waves<D, KIND, TILES, 3>(a, s, stream)
+                                    : launch_waves<D, KIND, TILES, 2>(a, s, stream);
 }
 
 template <int D, int KIND>
@@ -707,7 +720,22 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   // workgroup no more units than the second launch costs; else equal runs.
   const uint64_t most =
       kind == XFER_KV_BF16 ? resident<XFER_KV_BF16>(head_dim, s.m_tiles) : resident<XFER_KV_E4M3>(head_dim, s.m_tiles);
+  s.waves = kWaves;
   s.joined = steps > kWholeUnits || steps > rows * inner * steps / most + kJoinUnits;
+  // Where compute units have no more than one (row, kv head) each, twice the
+  // waves take a whole one, in half the rounds.  A compute unit takes in only so
+  // much at once, so the longer the rows of a key, the fewer units it may hold up
+  // the others for: beyond what an equal share would be, `wait` of them cost as
+  // much as the join (1.2, 2.3 and 3.5 us for each two units of 64, 128 and 256
+  // bytes a key; 5 us).  256 rows of 1000 tokens, 64 bytes: 9.5 us, 14.5 with
+  // four waves and 13.3 joined (128 bytes: 15.0, 20.3).
+  const uint32_t row_bytes = head_dim * (kind == XFER_KV_BF16 ? 2 : 1);
+  const uint32_t wait = row_bytes <= 64 ? 10 : row_bytes <= 128 ? 6 : 3;
+  if (most > kComputeUnits && rows * inner <= kComputeUnits && steps > 1 && steps * row_bytes <= kAloneBytes &&
+      steps <= 2 * rows * inner * steps / most + wait) {
+    s.waves = kManyWaves;
+    s.joined = false;
+  }
   if (!s.joined) {
     s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
     return s;

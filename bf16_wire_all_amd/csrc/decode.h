@@ -30,10 +30,10 @@ hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStr
 
 // ---- attention of one new token over a paged cache (attn_paged.hip)
 // How a call's work is cut up: query heads of a kv head in m_groups of 16 *
-// m_tiles, workgroups that share the visible tokens (of vis_max a row, at
+// m_tiles, workgroups (of `waves`) that share the visible tokens (of vis_max a row, at
 // most) evenly, and whether a (row, kv head) may fall to several of them.
 struct AttnShape {
-  uint32_t m_tiles, m_groups, part_heads;
+  uint32_t m_tiles, m_groups, part_heads, waves;
   uint64_t workgroups;
   bool joined;
 };

@@ -175,6 +175,20 @@ def test_more_rows_than_threads(d, kind):
     run(World(lens, 2, 1, d, 16, kind, seed=18))
 
 
+@pytest.mark.parametrize("d,kind,hq,hkv,top", [(64, "e4m3", 8, 2, 1100), (64, "bf16", 20, 1, 700), (128, "e4m3", 5, 1, 700),
+                                              (128, "bf16", 24, 1, 380), (256, "e4m3", 4, 2, 380)])
+def test_a_whole_row_to_each_compute_unit(d, kind, hq, hkv, top):
+    """Few rows of middling length: no row is cut up, and more waves share it."""
+    lens = [top, 0, 1, 129, 255, 256, 257, top - 1]
+    w = World(lens, hq, hkv, d, 16, kind, seed=19, out="f32" if hq == 5 else "bf16")
+    assert w.workspace()[1] == 0
+    run(w, calls=2)
+    w = World([9000, 40, 5000], hq, hkv, d, 32, kind, "heads", window=top - 3, sinks=3, seed=20)
+    assert w.workspace()[1] == 0
+    run(w)
+    run(World(lens, hq, hkv, d, 16, kind, holes=[(0, 0), (0, 9), (7, 3), (6, 15), (6, 16)], seed=21))
+
+
 def test_lengths_below_the_bound_and_above_it():
     """max_len is a bound: shorter rows are served, longer ones are cut to it."""
     run(World([10, 500, 999], 4, 2, 64, 16, max_len=40000, seed=5))
