@@ -52,6 +52,11 @@ constexpr uint32_t kWholeUnits = 16;             // of a row that need not be cu
 constexpr uint32_t kJoinUnits = 3;               // that the join is worth
 constexpr int kManyWaves = 8;                    // that share the tokens of a row with a compute unit to itself
 constexpr uint32_t kAloneBytes = 2048;           // of such a row's units, one row of each, at most
+// Keys and values are read past the caches where a call may read more than
+// they hold (two rows of 131071 tokens 169 us, 188 through them); fewer may be
+// there still, from the call before or from rows that share pages (128 (row, kv
+// head)s of 1000 tokens, 65 MB, called in turn: 17.9 us, 19 past them).
+constexpr uint64_t kCachedBytes = 96ull << 20;
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
@@ -129,7 +134,7 @@ __device__ __forceinline__ uint32_t dim_of(uint32_t j, uint32_t n) {
   return n * (D / 16) + j;
 }
 
-// STREAM: each line is read once and by one workgroup.
+// STREAM: past the caches.
 template <bool STREAM, typename T>
 __device__ __forceinline__ T load(const uint8_t *p) {
   if (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
@@ -226,14 +231,12 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
 }
 
 // WAVES: kWaves, or kManyWaves without runs.
-template <int D, int KIND, int TILES, int PARTS, int WAVES>
+template <int D, int KIND, int TILES, int PARTS, int WAVES, bool STREAM>
 __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
                                                                                                uint32_t m_groups) {
   using L = Layout<D, KIND>;
   using R = Residence<D, KIND, TILES>;
   constexpr int MR = TILES;
-  // A line holds the rows of two heads where they are shorter than it.
-  constexpr bool kStream = D * L::kBytes >= 128;
   constexpr uint32_t kRound = kTile * WAVES;  // tokens of a round
   constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
   __shared__ float lds_o[WAVES][16][D + kPad];
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
       const uint64_t o = ((uint64_t)(uint32_t)__shfl((int)hi, from) << 32) | (uint32_t)__shfl((int)lo, from);
       const uint8_t *p = kbase + ((int64_t)o < 0 ? 0 : o);  // a hole's scores are replaced: any row will do
 #pragma unroll
-      for (int i = 0; i < L::kLoadsK; ++i) k[s][i] = load<kStream, v4u>(p + 64 * i);
+      for (int i = 0; i < L::kLoadsK; ++i) k[s][i] = load<STREAM, v4u>(p + 64 * i);
     }
   };
 
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
     const uint32_t h = row_lane<E>(hi);                                                    \
     const bool no = (int32_t)h < 0;                                                        \
     gone |= no ? 1u << E : 0;                                                              \
-    load_v<D, KIND, kStream>(vr[E], vbase + (no ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo)), n);   \
+    load_v<D, KIND, STREAM>(vr[E], vbase + (no ? 0 : ((uint64_t)h << 32) | row_lane<E>(lo)), n);   \
   }
     XFER_ROW(0) XFER_ROW(1) XFER_ROW(2) XFER_ROW(3) XFER_ROW(4) XFER_ROW(5) XFER_ROW(6) XFER_ROW(7)
 #undef XFER_ROW
@@ -676,9 +679,15 @@ hipError_t launch_waves(const AttnArgs &a, const AttnShape &s, hipStream_t strea
   const dim3 grid((uint32_t)s.workgroups);
   if constexpr (Residence<D, KIND, TILES>::kPerSimd > 1) {
     if (s.waves == kManyWaves)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves>, grid, dim3(64 * kManyWaves), 0, stream, a, s.m_groups);
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves, false>, grid, dim3(64 * kManyWaves), 0, stream, a,
+                    s.m_groups);
   }
-  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  // a line holds the rows of two heads where they are shorter than it
+  if constexpr (D * Layout<D, KIND>::kBytes >= 128) {
+    if (s.stream)
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, true>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  }
+  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, false>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
 }
 
 template <int D, int KIND, int TILES>
@@ -730,6 +739,7 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   // bytes a key; 5 us).  256 rows of 1000 tokens, 64 bytes: 9.5 us, 14.5 with
   // four waves and 13.3 joined (128 bytes: 15.0, 20.3).
   const uint32_t row_bytes = head_dim * (kind == XFER_KV_BF16 ? 2 : 1);
+  s.stream = vis_max > kCachedBytes / (2 * row_bytes) / ((uint64_t)rows * kv_heads);
   const uint32_t wait = row_bytes <= 64 ? 10 : row_bytes <= 128 ? 6 : 3;
   if (most > kComputeUnits && rows * inner <= kComputeUnits && steps > 1 && steps * row_bytes <= kAloneBytes &&
       steps <= 2 * rows * inner * steps / most + wait) {

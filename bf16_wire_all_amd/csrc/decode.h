@@ -30,12 +30,13 @@ hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStr
 
 // ---- attention of one new token over a paged cache (attn_paged.hip)
 // How a call's work is cut up: query heads of a kv head in m_groups of 16 *
-// m_tiles, workgroups (of `waves`) that share the visible tokens (of vis_max a row, at
-// most) evenly, and whether a (row, kv head) may fall to several of them.
+// m_tiles; workgroups of `waves` that share the visible tokens (of vis_max a
+// row, at most) evenly; whether a (row, kv head) may fall to several of them;
+// whether the cache is read past the caches.
 struct AttnShape {
   uint32_t m_tiles, m_groups, part_heads, waves;
   uint64_t workgroups;
-  bool joined;
+  bool joined, stream;
 };
 AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind,
                      uint64_t vis_max);
