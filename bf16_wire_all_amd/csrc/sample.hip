@@ -22,7 +22,7 @@
 //
 // A workgroup holds its slice in registers, so that all its loads are in
 // flight at once and nothing is read twice (256 rows of 151,936: the count is
-// 20 us, 3.9 TB/s; with pieces of 16,384 columns one after the other, read
+// 22 us, 3.5 TB/s; with pieces of 16,384 columns one after the other, read
 // again to be counted, it was 27).  The slice's range of magnitudes is found
 // before it is counted, and 8,192 bins (64 powers of two, both signs' counts
 // in one word) hold it in 32 KiB of LDS: two workgroups share a compute unit,
