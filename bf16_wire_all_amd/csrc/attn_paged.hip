@@ -57,6 +57,7 @@ constexpr uint32_t kAloneBytes = 2048;           // of such a row's units, one r
 // there still, from the call before or from rows that share pages (128 (row, kv
 // head)s of 1000 tokens, 65 MB, called in turn: 17.9 us, 19 past them).
 constexpr uint64_t kCachedBytes = 96ull << 20;
+constexpr int kSideBytes = 256;                  // of a key that is read beside the next head's, at most
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
@@ -174,7 +175,10 @@ struct Parts {
 };
 constexpr uint32_t kWhole = 0xFFFFFFFFu;
 
-__device__ __forceinline__ uint32_t units_of(const Visible &v) { return v.n ? (v.n + kStep - 1) / kStep : 1; }
+template <uint32_t UNIT>
+__device__ __forceinline__ uint32_t units_of(const Visible &v) {
+  return v.n ? (v.n + UNIT - 1) / UNIT : 1;
+}
 
 // A workgroup's run of units: where it starts, and how long it is.
 struct Run {
@@ -185,6 +189,7 @@ struct Run {
 
 // Adds up the rows' units (a row has units_of() for each of `inner_n` heads)
 // and cuts them into equal runs; by all threads.
+template <uint32_t UNIT>
 __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint32_t wg, uint32_t n_wg) {
   __shared__ uint64_t totals[kWaves];
   __shared__ uint64_t start[2];
@@ -192,7 +197,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   const uint32_t each = (a.rows + kThreads - 1) / kThreads;
   const uint32_t r0 = min(tid * each, a.rows), r1 = min(r0 + each, a.rows);
   uint64_t mine = 0;
-  for (uint32_t r = r0; r < r1; ++r) mine += (uint64_t)units_of(visible_of(a, r)) * inner_n;
+  for (uint32_t r = r0; r < r1; ++r) mine += (uint64_t)units_of<UNIT>(visible_of(a, r)) * inner_n;
   uint64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
@@ -217,7 +222,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
     uint64_t before = incl - mine;
     uint32_t r = r0;
     for (; r + 1 < r1; ++r) {
-      const uint64_t u = (uint64_t)units_of(visible_of(a, r)) * inner_n;
+      const uint64_t u = (uint64_t)units_of<UNIT>(visible_of(a, r)) * inner_n;
       if (from < before + u) break;
       before += u;
     }
@@ -230,28 +235,36 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   return run;
 }
 
-// WAVES: kWaves, or kManyWaves without runs.
-template <int D, int KIND, int TILES, int PARTS, int WAVES, bool STREAM>
-__global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(AttnArgs a,
-                                                                                               uint32_t m_groups) {
+// HEADS kv heads side by side, WAVES waves for each: kWaves together, or
+// kManyWaves without runs.
+template <int D, int KIND, int TILES, int PARTS, int WAVES, bool STREAM, int HEADS>
+__global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(
+    AttnArgs a, uint32_t m_groups) {
   using L = Layout<D, KIND>;
   using R = Residence<D, KIND, TILES>;
   constexpr int MR = TILES;
-  constexpr uint32_t kRound = kTile * WAVES;  // tokens of a round
+  constexpr bool kRuns = WAVES * HEADS == kWaves;
+  constexpr uint32_t kRound = kTile * WAVES;         // tokens of a round
+  constexpr uint32_t kUnit = kRuns ? kRound : kStep;  // and of a unit
   constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
-  __shared__ float lds_o[WAVES][16][D + kPad];
-  __shared__ float lds_all_m[MR][WAVES][16], lds_all_l[MR][WAVES][16];
+  __shared__ float lds_heads_o[HEADS][WAVES][16][D + kPad];
+  __shared__ float lds_heads_m[HEADS][MR][WAVES][16], lds_heads_l[HEADS][MR][WAVES][16];
+  static_assert(HEADS == 1 || !R::kQInLds, "the queries in LDS are one head's");
+  const uint32_t side = HEADS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * WAVES));
+  auto &lds_o = lds_heads_o[side];
+  auto &lds_all_m = lds_heads_m[side];
+  auto &lds_all_l = lds_heads_l[side];
 
-  const uint32_t inner_n = a.cache.kv_heads * m_groups;
+  const uint32_t inner_n = a.cache.kv_heads / HEADS * m_groups;
   const uint32_t xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
-  const bool runs = WAVES == kWaves && a.parts;
+  const bool runs = kRuns && a.parts;
   uint32_t wg = 0;
   Run run;
   if (runs) {
     // Neighbouring runs on one XCD: its L2 then serves the lines that two
     // heads share.
     wg = xcd * (gridDim.x / kXcds) + rest;
-    if constexpr (WAVES == kWaves) run = run_of(a, inner_n, wg, gridDim.x);
+    if constexpr (kRuns) run = run_of<kUnit>(a, inner_n, wg, gridDim.x);
     if (run.length == 0) return;
   } else {
     // A workgroup for each (row, kv head): rows go round the XCDs, and the
@@ -260,14 +273,14 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
     if (run.row >= a.rows) return;
   }
 
-  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16,
-                 g = lane / 16;
+  const uint32_t tid = threadIdx.x % (64 * WAVES), wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64,
+                 n = lane % 16, g = lane / 16;
   // The queries, in the lanes' order, where the exchange lies later.
   v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
   static_assert(!R::kQInLds || MR * L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
   uint32_t row = run.row;
   Visible vis = visible_of(a, row);
-  uint32_t units = units_of(vis);
+  uint32_t units = units_of<kUnit>(vis);
   uint32_t inner = rest % inner_n, unit = 0;
   uint64_t left = units;
   if (runs) {
@@ -280,8 +293,8 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
 #pragma unroll 1
   while (left) {
   const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
-  const uint32_t kvh = inner / m_groups, h0 = inner % m_groups * (16 * MR);  // first query head within the group
-  const uint32_t v0 = unit * kStep, v1 = min((unit + take) * kStep, vis.n);
+  const uint32_t kvh = inner / m_groups * HEADS + side, h0 = inner % m_groups * (16 * MR);  // first query head within the group
+  const uint32_t v0 = unit * kUnit, v1 = min((unit + take) * kUnit, vis.n);
 
   // Q: query head h0 + 16 * r + n, the dims that this lane's K loads hold.
   v4u q[R::kQInLds ? 1 : MR][L::kMfmaK];
@@ -518,8 +531,8 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
   // The waves' results, joined in LDS.
   const bool whole = take == units;
   const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
-  if (unit == 0 && threadIdx.x == 0 && runs)
-    reinterpret_cast<Parts *>(a.parts)[(uint64_t)row * inner_n + inner] =
+  if (unit == 0 && tid == 0 && runs)
+    reinterpret_cast<Parts *>(a.parts)[((uint64_t)row * a.cache.kv_heads + kvh) * m_groups + inner % m_groups] =
         whole ? Parts{kWhole, 1} : Parts{slot, 1 + (uint32_t)((units - take + run.per - 1) / run.per)};
 #pragma unroll
   for (int r = 0; r < MR; ++r) {
@@ -571,7 +584,7 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
         else
           *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at_out) = v2u{bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
       } else {
-        const uint64_t part = (uint64_t)slot * min(a.group, (uint32_t)TILES * 16) + 16 * r + hq;
+        const uint64_t part = ((uint64_t)slot * HEADS + side) * min(a.group, (uint32_t)TILES * 16) + 16 * r + hq;
         *reinterpret_cast<v4f *>(a.part_o + part * D + d) = v;
         if (d == 0) {
           a.part_ml[2 * part] = top;
@@ -589,7 +602,7 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
     inner = 0;
     if (++row == a.rows) break;
     vis = visible_of(a, row);
-    units = units_of(vis);
+    units = units_of<kUnit>(vis);
   }
   if (left) __syncthreads();  // LDS is written again
   }
@@ -598,7 +611,8 @@ __global__ __launch_bounds__(64 * WAVES, (Residence<D, KIND, TILES>::kPerSimd)) 
 // One workgroup for each (row, query head): the weighted sums of its parts, each
 // scaled to the largest maximum, in the parts' order.
 template <int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t m_tile, uint32_t m_groups) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t m_tile, uint32_t m_groups,
+                                                               uint32_t heads) {
   constexpr uint32_t kLanes = D / 4, kAtOnce = kThreads / kLanes;
   constexpr int kEach = kMaxWorkgroups / kThreads;  // parts of a thread
   __shared__ float lds_w[kMaxWorkgroups];
@@ -610,7 +624,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
   if (parts.slot == kWhole) return;
   // Part p > 0 is the first thing that the workgroup p further on did.
   auto place = [&](uint32_t p) {
-    return (uint64_t)(p ? (parts.slot / 2 + p) * 2 : parts.slot) * min(a.group, m_tile) + h % m_tile;
+    return ((uint64_t)(p ? (parts.slot / 2 + p) * 2 : parts.slot) * heads + kvh % heads) * min(a.group, m_tile) + h % m_tile;
   };
 
   float m[kEach], l[kEach], top = -INFINITY;
@@ -677,17 +691,24 @@ uint32_t resident(uint32_t head_dim, uint32_t tiles) {
 template <int D, int KIND, int TILES, int PARTS>
 hipError_t launch_waves(const AttnArgs &a, const AttnShape &s, hipStream_t stream) {
   const dim3 grid((uint32_t)s.workgroups);
+  // a line holds the rows of two heads where they are shorter than it
+  constexpr bool kLines = D * Layout<D, KIND>::kBytes >= 128;
   if constexpr (Residence<D, KIND, TILES>::kPerSimd > 1) {
     if (s.waves == kManyWaves)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves, false>, grid, dim3(64 * kManyWaves), 0, stream, a,
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves, false, 1>, grid, dim3(64 * kManyWaves), 0, stream, a,
                     s.m_groups);
   }
-  // a line holds the rows of two heads where they are shorter than it
-  if constexpr (D * Layout<D, KIND>::kBytes >= 128) {
-    if (s.stream)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, true>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  if constexpr (D * Layout<D, KIND>::kBytes <= kSideBytes && D < 256) {
+    if (s.heads == 4)
+      return launch(attn_kernel<D, KIND, TILES, PARTS, 1, kLines, 4>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+    if (s.heads == 2)
+      return launch(attn_kernel<D, KIND, TILES, PARTS, 2, kLines, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
   }
-  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, false>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  if constexpr (kLines) {
+    if (s.stream)
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, true, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  }
+  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, false, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
 }
 
 template <int D, int KIND, int TILES>
@@ -707,17 +728,17 @@ hipError_t launch_dim(const AttnArgs &a, int kind, const AttnShape &s, hipStream
       kind == XFER_KV_BF16 ? launch_tiles<D, XFER_KV_BF16>(a, s, stream) : launch_tiles<D, XFER_KV_E4M3>(a, s, stream);
   if (e != hipSuccess || !s.joined) return e;
   return launch(attn_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a, 16 * s.m_tiles,
-                s.m_groups);
+                s.m_groups, s.heads);
 }
 
 uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
 // Query heads of all the workgroups' parts: two parts for each.
-uint64_t parts_of(const AttnShape &s) { return 2ull * s.workgroups * s.part_heads; }
+uint64_t parts_of(const AttnShape &s) { return 2ull * s.workgroups * s.heads * s.part_heads; }
 
 }  // namespace
 
 AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind,
-                     uint64_t vis_max) {
+                     uint64_t vis_max, uint64_t head_stride) {
   AttnShape s{};
   if (rows == 0) return s;
   s.m_tiles = group <= 16 ? 1 : 2;
@@ -730,6 +751,7 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   const uint64_t most =
       kind == XFER_KV_BF16 ? resident<XFER_KV_BF16>(head_dim, s.m_tiles) : resident<XFER_KV_E4M3>(head_dim, s.m_tiles);
   s.waves = kWaves;
+  s.heads = 1;
   s.joined = steps > kWholeUnits || steps > rows * inner * steps / most + kJoinUnits;
   // Where compute units have no more than one (row, kv head) each, twice the
   // waves take a whole one, in half the rounds.  A compute unit takes in only so
@@ -750,6 +772,12 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
     s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
     return s;
   }
+  // Where a token's heads lie one after the other, rows of up to 256 bytes are
+  // read four heads (or two) at a time, a wave or two for each: scattered by
+  // the tokens' distance, such rows cost more than their bytes (256,000 tokens
+  // of 8 heads of 128 bytes: 94 us, 121 one head at a time).
+  if (s.stream && head_dim < 256 && row_bytes <= kSideBytes && head_stride == row_bytes && kv_heads % 2 == 0)
+    s.heads = kv_heads % 4 == 0 ? 4 : 2;
   uint64_t n;
   if (__builtin_mul_overflow(rows * inner, steps, &n)) n = UINT64_MAX;
   s.workgroups = n < most ? (n + kXcds - 1) / kXcds * kXcds : most;

@@ -30,16 +30,16 @@ hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStr
 
 // ---- attention of one new token over a paged cache (attn_paged.hip)
 // How a call's work is cut up: query heads of a kv head in m_groups of 16 *
-// m_tiles; workgroups of `waves` that share the visible tokens (of vis_max a
+// m_tiles; workgroups of `waves`, of `heads` kv heads side by side, that share the visible tokens (of vis_max a
 // row, at most) evenly; whether a (row, kv head) may fall to several of them;
 // whether the cache is read past the caches.
 struct AttnShape {
-  uint32_t m_tiles, m_groups, part_heads, waves;
+  uint32_t m_tiles, m_groups, part_heads, waves, heads;
   uint64_t workgroups;
   bool joined, stream;
 };
 AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind,
-                     uint64_t vis_max);
+                     uint64_t vis_max, uint64_t head_stride);
 uint64_t attn_workspace_bytes(const AttnShape &s, uint32_t rows, uint32_t kv_heads, uint32_t head_dim);
 struct AttnArgs {
   CacheView cache;

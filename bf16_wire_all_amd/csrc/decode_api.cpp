@@ -140,7 +140,7 @@ int attn_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, uint32_t q_hea
   if (b->max_len == 0 || b->max_len > 0x7FFFFFFFu) return XFER_E_INVAL;
   uint64_t vis = b->max_len;
   if (b->window) vis = std::min<uint64_t>(vis, (uint64_t)b->window + b->sinks);
-  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, c->head_dim, c->kind, vis);
+  *s = xfer::attn_shape(b->rows, c->kv_heads, q_heads / c->kv_heads, c->head_dim, c->kind, vis, c->head_stride);
   return XFER_OK;
 }
 

@@ -189,6 +189,21 @@ def test_a_whole_row_to_each_compute_unit(d, kind, hq, hkv, top):
     run(World(lens, hq, hkv, d, 16, kind, holes=[(0, 0), (0, 9), (7, 3), (6, 15), (6, 16)], seed=21))
 
 
+@pytest.mark.parametrize("d,kind,hq,hkv,out", [(64, "e4m3", 8, 4, "bf16"), (64, "bf16", 6, 2, "f32"), (128, "e4m3", 16, 8, "f32"),
+                                              (128, "bf16", 12, 12, "bf16"), (128, "bf16", 40, 2, "f32"),
+                                              (64, "e4m3", 132, 4, "bf16")])
+def test_heads_side_by_side(d, kind, hq, hkv, out):
+    """Tokens whose heads lie one after the other, under a bound that a large batch would need."""
+    lens = [3000, 0, 1, 31, 32, 33, 127, 700, 2, 1025]
+    bound = 100 * 2 ** 20 // (len(lens) * hkv * d * (2 if kind == "bf16" else 1) * 2) + 1000
+    w = World(lens, hq, hkv, d, 16, kind, seed=22, max_len=bound, out=out)
+    assert w.workspace()[1] > 0
+    run(w, calls=2)
+    run(World(lens, hq, hkv, d, 8, kind, seed=23, max_len=bound, out=out, holes=[(0, 3), (7, 0), (7, 87), (9, 127), (9, 128)]))
+    lens = [9000] + lens
+    run(World(lens, hq, hkv, d, 16, kind, seed=24, max_len=2 * bound, window=5000, sinks=33, out=out))
+
+
 def test_lengths_below_the_bound_and_above_it():
     """max_len is a bound: shorter rows are served, longer ones are cut to it."""
     run(World([10, 500, 999], 4, 2, 64, 16, max_len=40000, seed=5))
