@@ -203,8 +203,8 @@ typedef struct {
  * workgroups.
  *
  * xfer_attn_workspace_bytes - the bytes that such a call needs (0 also for a
- * batch or cache that xfer_attn_paged refuses).  They depend on the sizes
- * alone, not on pointers.
+ * batch or cache that xfer_attn_paged refuses).  They depend on the sizes and
+ * strides alone, not on pointers.
  */
 XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch,
                                           uint32_t q_heads);
