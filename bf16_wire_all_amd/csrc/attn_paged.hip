@@ -57,7 +57,8 @@ constexpr uint32_t kAloneBytes = 2048;           // of such a row's units, one r
 // there still, from the call before or from rows that share pages (128 (row, kv
 // head)s of 1000 tokens, 65 MB, called in turn: 17.9 us, 19 past them).
 constexpr uint64_t kCachedBytes = 96ull << 20;
-constexpr int kSideBytes = 256;                  // of a key that is read beside the next head's, at most
+// Bytes of a key that is read beside the next heads', at most.
+constexpr int side_bytes(int heads, int tiles) { return heads == 4 && tiles == 1 ? 256 : 128; }
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kMaxWorkgroups = 4 * kComputeUnits;
 constexpr float kRaise = 8.0f;                   // in powers of two
@@ -249,7 +250,6 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
   constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
   __shared__ float lds_heads_o[HEADS][WAVES][16][D + kPad];
   __shared__ float lds_heads_m[HEADS][MR][WAVES][16], lds_heads_l[HEADS][MR][WAVES][16];
-  static_assert(HEADS == 1 || !R::kQInLds, "the queries in LDS are one head's");
   const uint32_t side = HEADS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * WAVES));
   auto &lds_o = lds_heads_o[side];
   auto &lds_all_m = lds_heads_m[side];
@@ -697,12 +697,14 @@ hipError_t launch_waves(const AttnArgs &a, const AttnShape &s, hipStream_t strea
     if (s.waves == kManyWaves)
       return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves, false, 1>, grid, dim3(64 * kManyWaves), 0, stream, a,
                     s.m_groups);
-  }
-  if constexpr (D * Layout<D, KIND>::kBytes <= kSideBytes && D < 256) {
-    if (s.heads == 4)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, 1, kLines, 4>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
-    if (s.heads == 2)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, 2, kLines, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+    if constexpr (D * Layout<D, KIND>::kBytes <= side_bytes(4, TILES)) {
+      if (s.heads == 4)
+        return launch(attn_kernel<D, KIND, TILES, PARTS, 1, kLines, 4>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+    }
+    if constexpr (D * Layout<D, KIND>::kBytes <= side_bytes(2, TILES)) {
+      if (s.heads == 2)
+        return launch(attn_kernel<D, KIND, TILES, PARTS, 2, kLines, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+    }
   }
   if constexpr (kLines) {
     if (s.stream)
@@ -772,12 +774,16 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
     s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
     return s;
   }
-  // Where a token's heads lie one after the other, rows of up to 256 bytes are
-  // read four heads (or two) at a time, a wave or two for each: scattered by
-  // the tokens' distance, such rows cost more than their bytes (256,000 tokens
-  // of 8 heads of 128 bytes: 94 us, 121 one head at a time).
-  if (s.stream && head_dim < 256 && row_bytes <= kSideBytes && head_stride == row_bytes && kv_heads % 2 == 0)
-    s.heads = kv_heads % 4 == 0 ? 4 : 2;
+  // Where a token's heads lie one after the other, short rows are read four
+  // heads (or two) at a time, a wave or two for each: scattered by the tokens'
+  // distance they cost more than their bytes (256,000 tokens of 8 heads of 128
+  // bytes: 94 us, 121 one head at a time; of 256 bytes 92, 101).  Not where a wave
+  // has enough to do with 32 query heads (256 bytes: 68 us, 61), or with two
+  // heads of 256 bytes (36 us, 33).
+  const uint32_t heads = kv_heads % 4 == 0 ? 4 : 2;
+  if (s.stream && most > kComputeUnits && kv_heads % 2 == 0 && head_stride == row_bytes &&
+      row_bytes <= (uint32_t)side_bytes(heads, s.m_tiles))
+    s.heads = heads;
   uint64_t n;
   if (__builtin_mul_overflow(rows * inner, steps, &n)) n = UINT64_MAX;
   s.workgroups = n < most ? (n + kXcds - 1) / kXcds * kXcds : most;

@@ -191,7 +191,8 @@ def test_a_whole_row_to_each_compute_unit(d, kind, hq, hkv, top):
 
 @pytest.mark.parametrize("d,kind,hq,hkv,out", [(64, "e4m3", 8, 4, "bf16"), (64, "bf16", 6, 2, "f32"), (128, "e4m3", 16, 8, "f32"),
                                               (128, "bf16", 12, 12, "bf16"), (128, "bf16", 40, 2, "f32"),
-                                              (64, "e4m3", 132, 4, "bf16")])
+                                              (64, "e4m3", 132, 4, "bf16"), (256, "e4m3", 12, 4, "f32"),
+                                              (256, "e4m3", 40, 2, "bf16")])
 def test_heads_side_by_side(d, kind, hq, hkv, out):
     """Tokens whose heads lie one after the other, under a bound that a large batch would need."""
     lens = [3000, 0, 1, 31, 32, 33, 127, 700, 2, 1025]
