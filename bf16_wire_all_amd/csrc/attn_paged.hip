@@ -48,7 +48,6 @@ constexpr int kWaves = 4;                        // that share the tokens of a r
 constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kTile = 32;                   // tokens of a wave's tile
 constexpr uint32_t kStep = kTile * kWaves;       // tokens of a unit
-constexpr uint32_t kWholeUnits = 16;             // of a row that need not be cut up
 constexpr uint32_t kJoinUnits = 3;               // that the join is worth
 constexpr int kManyWaves = 8;                    // that share the tokens of a row with a compute unit to itself
 constexpr uint32_t kAloneBytes = 2048;           // of such a row's units, one row of each, at most
@@ -748,13 +747,29 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   s.m_groups = group / tile + (group % tile != 0);
   s.part_heads = group < tile ? group : tile;
   const uint64_t inner = (uint64_t)kv_heads * s.m_groups, steps = (vis_max + kStep - 1) / kStep;
-  // Whole (row, kv head)s where none is long, and cutting them up would spare a
-  // workgroup no more units than the second launch costs; else equal runs.
   const uint64_t most =
       kind == XFER_KV_BF16 ? resident<XFER_KV_BF16>(head_dim, s.m_tiles) : resident<XFER_KV_E4M3>(head_dim, s.m_tiles);
+  const uint32_t row_bytes = head_dim * (kind == XFER_KV_BF16 ? 2 : 1);
+  s.stream = vis_max > kCachedBytes / (2 * row_bytes) / ((uint64_t)rows * kv_heads);
+  // Where a token's heads lie one after the other, short rows are read four
+  // heads (or two) at a time, a wave or two for each: scattered by the tokens'
+  // distance they cost more than their bytes (256,000 tokens of 8 heads of 128
+  // bytes: 94 us, 121 one head at a time; of 256 bytes 92, 101).  Not where a wave
+  // has enough to do with 32 query heads (256 bytes: 68 us, 61), or with two
+  // heads of 256 bytes (36 us, 33).
+  const uint32_t heads = kv_heads % 4 == 0 ? 4 : 2;
+  const bool beside = s.stream && most > kComputeUnits && kv_heads % 2 == 0 && head_stride == row_bytes &&
+                      row_bytes <= (uint32_t)side_bytes(heads, s.m_tiles);
+  // Whole (row, kv head)s where none is long, and cutting them up would spare a
+  // workgroup no more units than the second launch costs; else equal runs.  What
+  // is long depends on what the runs are worth: 768 (row, kv head)s of up to 2800
+  // tokens, 64 bytes, take 31 us whole and 45 in runs (128 bytes: 55, 56; 256
+  // bytes: 90, 74), with heads side by side 36 and 39 (of up to 1400, 256 bytes:
+  // 55, 44).
+  const uint32_t whole = beside ? (row_bytes <= 64 ? 24 : row_bytes <= 128 ? 16 : 8) : row_bytes <= 64 ? 32 : 16;
   s.waves = kWaves;
   s.heads = 1;
-  s.joined = steps > kWholeUnits || steps > rows * inner * steps / most + kJoinUnits;
+  s.joined = steps > whole || steps > rows * inner * steps / most + kJoinUnits;
   // Where compute units have no more than one (row, kv head) each, twice the
   // waves take a whole one, in half the rounds.  A compute unit takes in only so
   // much at once, so the longer the rows of a key, the fewer units it may hold up
@@ -762,8 +777,6 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   // much as the join (1.2, 2.3 and 3.5 us for each two units of 64, 128 and 256
   // bytes a key; 5 us).  256 rows of 1000 tokens, 64 bytes: 9.5 us, 14.5 with
   // four waves and 13.3 joined (128 bytes: 15.0, 20.3).
-  const uint32_t row_bytes = head_dim * (kind == XFER_KV_BF16 ? 2 : 1);
-  s.stream = vis_max > kCachedBytes / (2 * row_bytes) / ((uint64_t)rows * kv_heads);
   const uint32_t wait = row_bytes <= 64 ? 10 : row_bytes <= 128 ? 6 : 3;
   if (most > kComputeUnits && rows * inner <= kComputeUnits && steps > 1 && steps * row_bytes <= kAloneBytes &&
       steps <= 2 * rows * inner * steps / most + wait) {
@@ -774,16 +787,7 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
     s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
     return s;
   }
-  // Where a token's heads lie one after the other, short rows are read four
-  // heads (or two) at a time, a wave or two for each: scattered by the tokens'
-  // distance they cost more than their bytes (256,000 tokens of 8 heads of 128
-  // bytes: 94 us, 121 one head at a time; of 256 bytes 92, 101).  Not where a wave
-  // has enough to do with 32 query heads (256 bytes: 68 us, 61), or with two
-  // heads of 256 bytes (36 us, 33).
-  const uint32_t heads = kv_heads % 4 == 0 ? 4 : 2;
-  if (s.stream && most > kComputeUnits && kv_heads % 2 == 0 && head_stride == row_bytes &&
-      row_bytes <= (uint32_t)side_bytes(heads, s.m_tiles))
-    s.heads = heads;
+  if (beside) s.heads = heads;
   uint64_t n;
   if (__builtin_mul_overflow(rows * inner, steps, &n)) n = UINT64_MAX;
   s.workgroups = n < most ? (n + kXcds - 1) / kXcds * kXcds : most;
