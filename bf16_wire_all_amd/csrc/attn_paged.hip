@@ -383,6 +383,32 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
     return gone;
   };
 
+  // Four sums from dim d on, some of them NaN.  Where no value is NaN but one is
+  // infinite, the products made it so: a part of a weight is often 0 or negative.
+  // The sum is that infinity then, unless there are both.  A loop over all of the
+  // run's values: calls without an infinity never take it.
+  auto with_infinities = [&](v4f v, uint32_t d) -> v4f {
+    uint32_t nan = 0, up = 0, down = 0;  // a bit for each dim
+#pragma unroll 1
+    for (uint32_t at = v0; at < v1; ++at) {
+      const uint32_t token = at < vis.first ? at : at + vis.gap, page = table[token >> a.cache.page_log2];
+      if (page >= a.cache.n_pages) continue;
+      const v2u w = *reinterpret_cast<const v2u *>(vbase + page * a.cache.page_stride +
+                                                   (token & slot_mask) * a.cache.token_stride + 2 * d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+        nan |= ((x & 0x7FFFu) > 0x7F80u) << i;
+        up |= (x == 0x7F80u) << i;
+        down |= (x == 0xFF80u) << i;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (isnan(v[i]) && !(nan >> i & 1) && (up >> i & 1) != (down >> i & 1)) v[i] = up >> i & 1 ? INFINITY : -INFINITY;
+    return v;
+  };
+
   uint32_t t = v0 + wave * kTile;
   int64_t off = -1;
   Place next{};
@@ -575,8 +601,11 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
         total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
         v += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
       }
+      if constexpr (KIND == XFER_KV_BF16) {
+        if (isnan(v.x + v.y + v.z + v.w)) v = with_infinities(v, d);
+      }
       if (whole) {
-        v *= total == 0.0f ? 0.0f : v_scale / total;
+        v = total == 0.0f ? v4f{0, 0, 0, 0} : v * (v_scale / total);
         const uint64_t at_out = row * a.out_ld + (uint64_t)(kvh * a.group + h) * D + d;
         if (a.out_mode == XFER_OUT_F32)
           *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at_out) = v;
@@ -648,7 +677,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
   for (int i = 0; i < kEach; ++i) {
     const uint32_t p = i * kThreads + tid;
     const float f = m[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
-    if (p < parts.n) lds_w[p] = f;
+    // not 0: a part's infinity stays one, however small its weights
+    if (p < parts.n) lds_w[p] = f == 0.0f ? __uint_as_float(1) : f;
     total += m[i] == -INFINITY ? l[i] : l[i] * f;
   }
 #pragma unroll
@@ -667,7 +697,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
   for (uint32_t s = 1; s < kAtOnce; ++s) r += lds_o[s][d4];
   total = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
   const float v_scale = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
-  r *= total == 0.0f ? 0.0f : v_scale / total;
+  r = total == 0.0f ? v4f{0, 0, 0, 0} : r * (v_scale / total);
   const uint64_t at = row * a.out_ld + (uint64_t)head * D + 4 * d4;
   if (a.out_mode == XFER_OUT_F32)
     *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at) = r;

@@ -174,6 +174,13 @@ typedef struct {
  * nothing is read for them.  What pages hold past a row's length, and tokens
  * outside the window, has no influence, NaN and infinities included.
  *
+ * Among a row's visible tokens, an infinite value makes its dim of every head
+ * of its kv head that infinity, however small its weight; a NaN, or infinities
+ * of both signs, make it NaN.  A score of NaN or +inf makes its head NaN.
+ * Neither reaches another dim, head or row.  Finite inputs give finite results
+ * where q . k_j, the score and the sum of a dim's values, each times up to 2^8,
+ * stay within binary32.
+ *
  * Several new tokens of one request are rows of their own, with the same
  * page numbers and increasing lengths.
  *
