@@ -160,9 +160,9 @@ __device__ __forceinline__ void load_v(uint32_t *dst, const uint8_t *row, uint32
   }
 }
 
-// Weights of eight tokens as PARTS BF16 numbers each, whose sum is the weight
-// to 2^-9 of itself for each: two (2^-18) are far below a BF16 result's own
-// rounding, three (2^-27) below that of F32.
+// Weights of eight tokens as PARTS BF16 numbers each.  The first is off by up to
+// 2^-8 of the weight, and each rounds what is left: two come to 2^-17 of it, far
+// below a BF16 result's own 2^-8, and three hold all 24 bits.
 template <int PARTS>
 struct Weights {
   v4u part[PARTS];

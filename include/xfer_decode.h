@@ -185,9 +185,9 @@ typedef struct {
  * page numbers and increasing lengths.
  *
  * Scores, maxima, sums and the weighted sum are held in binary32; a weight
- * is split into BF16 numbers for the product with v, which keeps it to 2^-18
- * of itself (two numbers, for XFER_OUT_BF16) or 2^-27 (three, for
- * XFER_OUT_F32).  The result is rounded once, to nearest even, for
+ * is split into BF16 numbers for the product with v, which keep it to 2^-17
+ * of itself (two numbers, for XFER_OUT_BF16) or, from 2^-100 on, exactly
+ * (three, for XFER_OUT_F32).  The result is rounded once, to nearest even, for
  * XFER_OUT_BF16.
  *
  *   q         (device) BF16 bit patterns, row r at q + r * q_ld, q_heads
