@@ -20,9 +20,13 @@ def test_two_parts_hold_a_weight_to_2_17_and_three_hold_it_whole():
     assert off[2] == 0
 
 
-def test_the_lowest_part_of_a_weight_of_2_100_is_a_normal_number():
-    """Its last bit is 2^-23 of it, and BF16 has normal numbers from 2^-126 on."""
-    assert -100 - 23 > -126
+def test_weights_from_2_100_on_need_no_subnormal_part():
+    w = (torch.arange(1 << 23, dtype=torch.int32) + 0x3F800000).view(torch.float32) * 2.0 ** -100
+    for _ in range(3):
+        part = w.to(torch.bfloat16).float()
+        assert float(part[part != 0].abs().min()) >= 2.0 ** -126
+        w = w - part
+    assert float(w.abs().max()) == 0
 
 
 def test_the_header_states_these_figures():
