@@ -239,7 +239,7 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
 // kManyWaves without runs.
 template <int D, int KIND, int TILES, int PARTS, int WAVES, bool STREAM, int HEADS>
 __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPerSimd)) void attn_kernel(
-    AttnArgs a, uint32_t m_groups) {
+    AttnArgs a, uint32_t m_groups, uint32_t deal) {
   using L = Layout<D, KIND>;
   using R = Residence<D, KIND, TILES>;
   constexpr int MR = TILES;
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
   const uint32_t inner_n = a.cache.kv_heads / HEADS * m_groups;
   const uint32_t xcd = blockIdx.x % kXcds, rest = blockIdx.x / kXcds;
   const bool runs = kRuns && a.parts;
-  uint32_t wg = 0;
+  uint32_t wg = 0, item = 0;
   Run run;
   if (runs) {
     // Neighbouring runs on one XCD: its L2 then serves the lines that two
@@ -266,10 +266,11 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
     if constexpr (kRuns) run = run_of<kUnit>(a, inner_n, wg, gridDim.x);
     if (run.length == 0) return;
   } else {
-    // A workgroup for each (row, kv head): rows go round the XCDs, and the
-    // heads of a row follow one another on one.
-    run.row = rest / inner_n * kXcds + xcd;
-    if (run.row >= a.rows) return;
+    // A workgroup for each (row, kv head) and group of its query heads, `deal`
+    // of them to each XCD in turn.
+    item = (rest / deal * kXcds + xcd) * deal + rest % deal;
+    if (item >= a.rows * inner_n) return;
+    run.row = item / inner_n;
   }
 
   const uint32_t tid = threadIdx.x % (64 * WAVES), wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64,
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(64 * WAVES * HEADS, (Residence<D, KIND, TILES>::kPe
   uint32_t row = run.row;
   Visible vis = visible_of(a, row);
   uint32_t units = units_of<kUnit>(vis);
-  uint32_t inner = rest % inner_n, unit = 0;
+  uint32_t inner = item % inner_n, unit = 0;
   uint64_t left = units;
   if (runs) {
     inner = __builtin_amdgcn_readfirstlane((uint32_t)(run.at / units));
@@ -725,21 +726,25 @@ hipError_t launch_waves(const AttnArgs &a, const AttnShape &s, hipStream_t strea
   if constexpr (Residence<D, KIND, TILES>::kPerSimd > 1) {
     if (s.waves == kManyWaves)
       return launch(attn_kernel<D, KIND, TILES, PARTS, kManyWaves, false, 1>, grid, dim3(64 * kManyWaves), 0, stream, a,
-                    s.m_groups);
+                    s.m_groups, s.deal);
     if constexpr (D * Layout<D, KIND>::kBytes <= side_bytes(4, TILES)) {
       if (s.heads == 4)
-        return launch(attn_kernel<D, KIND, TILES, PARTS, 1, kLines, 4>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+        return launch(attn_kernel<D, KIND, TILES, PARTS, 1, kLines, 4>, grid, dim3(kThreads), 0, stream, a, s.m_groups,
+                      s.deal);
     }
     if constexpr (D * Layout<D, KIND>::kBytes <= side_bytes(2, TILES)) {
       if (s.heads == 2)
-        return launch(attn_kernel<D, KIND, TILES, PARTS, 2, kLines, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+        return launch(attn_kernel<D, KIND, TILES, PARTS, 2, kLines, 2>, grid, dim3(kThreads), 0, stream, a, s.m_groups,
+                      s.deal);
     }
   }
   if constexpr (kLines) {
     if (s.stream)
-      return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, true, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+      return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, true, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups,
+                    s.deal);
   }
-  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, false, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups);
+  return launch(attn_kernel<D, KIND, TILES, PARTS, kWaves, false, 1>, grid, dim3(kThreads), 0, stream, a, s.m_groups,
+                s.deal);
 }
 
 template <int D, int KIND, int TILES>
@@ -800,8 +805,8 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   s.waves = kWaves;
   s.heads = 1;
   s.joined = steps > whole || steps > rows * inner * steps / most + kJoinUnits;
-  // Where compute units have no more than one (row, kv head) each, twice the
-  // waves take a whole one, in half the rounds.  A compute unit takes in only so
+  // Where there are no more of them than compute units, twice the waves take a
+  // whole one, in half the rounds.  A compute unit takes in only so
   // much at once, so the longer the rows of a key, the fewer units it may hold up
   // the others for: beyond what an equal share would be, `wait` of them cost as
   // much as the join (1.2, 2.3 and 3.5 us for each two units of 64, 128 and 256
@@ -814,7 +819,13 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
     s.joined = false;
   }
   if (!s.joined) {
-    s.workgroups = ((uint64_t)rows + kXcds - 1) / kXcds * kXcds * inner;
+    const uint64_t items = rows * inner;
+    // What reads the same lines stays on one XCD: a kv head's groups, and two heads
+    // of 64 bytes (77 rows of 8 such heads: 20 us, 27 apart).  With whole rows dealt
+    // out, few of them left XCDs without work (one row of 40 kv heads of 128 bytes,
+    // 350 tokens: 6.1 us, 10.8 so; 9 rows of 28, 256 bytes, 900 tokens: 24 us, 36).
+    s.deal = s.m_groups * (row_bytes < 128 && kv_heads % 2 == 0 ? 2 : 1);
+    s.workgroups = ((items + s.deal - 1) / s.deal + kXcds - 1) / kXcds * kXcds * s.deal;
     return s;
   }
   if (beside) s.heads = heads;

@@ -32,9 +32,10 @@ hipError_t launch_rope_store(const RopeStoreArgs &a, int kind, int style, hipStr
 // How a call's work is cut up: query heads of a kv head in m_groups of 16 *
 // m_tiles; workgroups of `waves`, of `heads` kv heads side by side, that share the visible tokens (of vis_max a
 // row, at most) evenly; whether a (row, kv head) may fall to several of them;
-// whether the cache is read past the caches.
+// how many of these an XCD gets at a time if not; whether the cache is read past
+// the caches.
 struct AttnShape {
-  uint32_t m_tiles, m_groups, part_heads, waves, heads;
+  uint32_t m_tiles, m_groups, part_heads, waves, heads, deal;
   uint64_t workgroups;
   bool joined, stream;
 };
