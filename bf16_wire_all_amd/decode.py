@@ -76,24 +76,38 @@ def lib():
     return _lib
 
 
+# What a tensor may be of to stand for each format: the type itself, or whole
+# numbers of its size as bit patterns.  Another float type would be read as if
+# it were this one.
+_BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+_E4M3 = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
+_F32 = frozenset((torch.float32,))
+_INT32 = frozenset((torch.int32, torch.uint32))
+_INT64 = frozenset((torch.int64, torch.uint64))
+
+
+def _names(types) -> str:
+    return " or ".join(sorted(str(t) for t in types))
+
+
 # The checks below run at every call, in front of kernels of a few
 # microseconds: each asks a tensor as few things as it can.
 
-def _flat(t, itemsize: int, device: int, what: str) -> int:
-    """Pointer of a contiguous tensor of the call's device (None: NULL)."""
+def _flat(t, types, device: int, what: str) -> int:
+    """Pointer of a contiguous tensor of the call's device (None: NULL); types None: any."""
     if t is None:
         return 0
-    if t.get_device() != device or t.element_size() != itemsize or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {itemsize}-byte tensor on cuda:{device}")
+    if t.get_device() != device or (types is not None and t.dtype not in types) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor{' of ' + _names(types) if types else ''} on cuda:{device}")
     return t.data_ptr()
 
 
-def _rows(t, heads, head_dim: int, itemsize: int, device: int, what: str):
+def _rows(t, heads, head_dim: int, types, device: int, what: str):
     """(pointer, rows, heads, ld in elements) of a [rows, heads, head_dim] tensor whose rows are dense."""
     rows, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if t.get_device() != device or t.element_size() != itemsize or d != head_dim or (heads is not None and h != heads):
-        raise ValueError(f"{what}: expected [rows, {heads or 'heads'}, {head_dim}] of {itemsize} bytes on cuda:{device}")
+    if t.get_device() != device or t.dtype not in types or d != head_dim or (heads is not None and h != heads):
+        raise ValueError(f"{what}: expected [rows, {heads or 'heads'}, {head_dim}] of {_names(types)} on cuda:{device}")
     if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{what}: a row's heads must lie one after the other")
     return t.data_ptr(), rows, h, s0 if rows > 1 else h * d
@@ -111,9 +125,10 @@ class KVCache:
     """A paged cache of keys and values; keeps its tensors alive."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or v.element_size() != k.element_size():
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
             raise ValueError("k and v must be alike: [pages, page_tokens, heads, head_dim] with the same strides")
-        if k.element_size() not in (1, 2) or v.device != k.device or k.device.type != "cuda":
+        types = next((t for t in (_BF16, _E4M3) if k.dtype in t and v.dtype in t), None)
+        if types is None or v.device != k.device or k.device.type != "cuda":
             raise ValueError("k and v must be BF16 or E4M3 CUDA tensors of one device")
         n, p, h, d = k.shape
         s, e = k.stride(), k.element_size()
@@ -126,31 +141,32 @@ class KVCache:
         self.tensors = (k, v, k_scale, v_scale)
         # the stride of a dimension of one element is never walked: any multiple of 16 will do
         stride = [s[i] * e if k.shape[i] > 1 else 0 for i in range(3)]
-        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, 4, self.device, "k_scale") or None,
-                          _flat(v_scale, 4, self.device, "v_scale") or None, stride[0], stride[1], stride[2], n, p, h, d,
-                          KV_BF16 if e == 2 else KV_E4M3, 0)
+        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, _F32, self.device, "k_scale") or None,
+                          _flat(v_scale, _F32, self.device, "v_scale") or None, stride[0], stride[1], stride[2], n, p, h,
+                          d, KV_BF16 if types is _BF16 else KV_E4M3, 0)
 
 
 def kv_cache(k, v, k_scale=None, v_scale=None) -> KVCache:
     """k, v: [pages, page_tokens, heads, head_dim] CUDA tensors or views (BF16 or
-    2-byte patterns, or E4M3 bytes), any strides but a dense last dimension;
+    float8_e4m3fn, or int16, uint16, int8 or uint8 as their bit patterns), any
+    strides but a dense last dimension;
     k_scale, v_scale: F32[heads] of an E4M3 cache."""
     return KVCache(k, v, k_scale, v_scale)
 
 
 def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_weight=None, k_weight=None,
                    eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
-    """q: [tokens, q_heads, head_dim], k, v: [tokens, kv_heads, head_dim] (2-byte
-    elements; slices of a fused projection will do); positions: int32[tokens]
+    """q: [tokens, q_heads, head_dim], k, v: [tokens, kv_heads, head_dim] (BF16 or
+    its patterns; slices of a fused projection will do); positions: int32[tokens]
     and cos_sin: F32[max_pos, rot_dim] (both None: no rotation); slots:
     int64[tokens]; q_out like q (q itself is computed in place);
     interleaved: dims 2i and 2i + 1 form a pair, not i and i + rot_dim / 2."""
     dev, d = cache.device, cache.head_dim
     stream = _stream_on(dev, stream)
-    kp, tokens, _, k_ld = _rows(k, cache.kv_heads, d, 2, dev, "k")
-    vp, vt, _, v_ld = _rows(v, cache.kv_heads, d, 2, dev, "v")
-    qp, qt, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
-    op, ot, _, o_ld = _rows(q_out, q_heads, d, 2, dev, "q_out")
+    kp, tokens, _, k_ld = _rows(k, cache.kv_heads, d, _BF16, dev, "k")
+    vp, vt, _, v_ld = _rows(v, cache.kv_heads, d, _BF16, dev, "v")
+    qp, qt, q_heads, q_ld = _rows(q, None, d, _BF16, dev, "q")
+    op, ot, _, o_ld = _rows(q_out, q_heads, d, _BF16, dev, "q_out")
     if not (vt == qt == ot == tokens == slots.numel()):
         raise ValueError("q, k, v, q_out and slots must have one row for each token")
     for w in (q_weight, k_weight):
@@ -160,13 +176,13 @@ def qkv_rope_store(cache: KVCache, q, k, v, positions, cos_sin, slots, q_out, q_
     if cos_sin is not None:
         if positions is None or cos_sin.dim() != 2 or positions.numel() != tokens:
             raise ValueError("cos_sin must be [max_pos, rot_dim], with a position for each token")
-        rope.cos_sin = _flat(cos_sin, 4, dev, "cos_sin")
-        rope.positions = _flat(positions, 4, dev, "positions")
+        rope.cos_sin = _flat(cos_sin, _F32, dev, "cos_sin")
+        rope.positions = _flat(positions, _INT32, dev, "positions")
         rope.max_pos, rope.rot_dim = cos_sin.shape
-    qkv = QKVC(qp, kp, vp, q_ld, k_ld, v_ld, _flat(q_weight, 2, dev, "q_weight"), _flat(k_weight, 2, dev, "k_weight"),
-               tokens, q_heads, eps, 0)
+    qkv = QKVC(qp, kp, vp, q_ld, k_ld, v_ld, _flat(q_weight, _BF16, dev, "q_weight"),
+               _flat(k_weight, _BF16, dev, "k_weight"), tokens, q_heads, eps, 0)
     status = lib().xfer_qkv_rope_store(ctypes.byref(cache.c), ctypes.byref(qkv), ctypes.byref(rope),
-                                       _flat(slots, 8, dev, "slots"), op, o_ld, stream)
+                                       _flat(slots, _INT64, dev, "slots"), op, o_ld, stream)
     if status != OK:
         _check(status, "xfer_qkv_rope_store")
 
@@ -188,32 +204,30 @@ def attn_workspace_bytes(cache: KVCache, rows: int, q_heads: int, max_len: int, 
 
 def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
                sinks: int = 0, stream=None) -> None:
-    """q: [rows, q_heads, head_dim] (2-byte elements); page_table: int32 or uint32
-    [rows, at least ceil(max_len / page_tokens)], dense within a row; lens:
-    int32 or uint32 [rows]; out: like q, BF16 (2-byte) or F32; workspace: a
-    CUDA tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
+    """q: [rows, q_heads, head_dim] (BF16 or its patterns); page_table: int32 or
+    uint32 [rows, at least ceil(max_len / page_tokens)], dense within a row;
+    lens: int32 or uint32 [rows] (a negative one is a large length, cut to
+    max_len); out: like q, BF16 (or its patterns) or F32; workspace: a CUDA
+    tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
     dev, d = cache.device, cache.head_dim
     stream = _stream_on(dev, stream)
-    qp, rows, q_heads, q_ld = _rows(q, None, d, 2, dev, "q")
-    size = out.element_size()
-    if size not in (2, 4):
-        raise ValueError("out must have 2-byte (BF16) or 4-byte (F32) elements")
-    op, o_rows, _, o_ld = _rows(out, q_heads, d, size, dev, "out")
+    qp, rows, q_heads, q_ld = _rows(q, None, d, _BF16, dev, "q")
+    f32 = out.dtype in _F32
+    op, o_rows, _, o_ld = _rows(out, q_heads, d, _F32 if f32 else _BF16, dev, "out")
     if o_rows != rows or lens.numel() != rows or page_table.dim() != 2 or page_table.shape[0] != rows:
         raise ValueError("q, page_table, lens and out must have the same rows")
     width, ts = page_table.shape[1], page_table.stride()
-    if page_table.get_device() != dev or page_table.element_size() != 4 or (width > 1 and ts[1] != 1):
-        raise ValueError("page_table: expected 4-byte page numbers, dense within a row")
+    if page_table.get_device() != dev or page_table.dtype not in _INT32 or (width > 1 and ts[1] != 1):
+        raise ValueError(f"page_table: expected {_names(_INT32)} on cuda:{dev}, dense within a row")
     if width * cache.page_tokens < max_len:
         raise ValueError("page_table is too narrow for max_len")
     ws, ws_bytes = 0, 0
     if workspace is not None:
-        size_w = workspace.element_size()
-        ws_bytes, ws = workspace.numel() * size_w, _flat(workspace, size_w, dev, "workspace")
-    batch = PagedBatchC(page_table.data_ptr(), _flat(lens, 4, dev, "lens"), ts[0] if rows > 1 else width, rows,
+        ws_bytes, ws = workspace.numel() * workspace.element_size(), _flat(workspace, None, dev, "workspace")
+    batch = PagedBatchC(page_table.data_ptr(), _flat(lens, _INT32, dev, "lens"), ts[0] if rows > 1 else width, rows,
                         max_len, window, sinks)
     status = lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
-                                   OUT_F32 if size == 4 else OUT_BF16, ws, ws_bytes, stream)
+                                   OUT_F32 if f32 else OUT_BF16, ws, ws_bytes, stream)
     if status != OK:
         _check(status, "xfer_attn_paged")
 
@@ -228,12 +242,13 @@ def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q
 # ------------------------------------------------------------------ sampling
 
 def shard(logits, ncols: int, col_offset: int) -> Shard:
-    """A column shard of BF16 logits: a CUDA tensor [rows, at least ncols] whose
-    rows are dense; the shard keeps it alive."""
+    """A column shard of BF16 logits (or their patterns): a CUDA tensor [rows, at
+    least ncols] whose rows are dense, and a multiple of 8 elements apart; the
+    shard keeps it alive."""
     rows, width = logits.shape
     ts = logits.stride()
-    if not logits.is_cuda or logits.element_size() != 2 or width < ncols or (width > 1 and ts[1] != 1):
-        raise ValueError("expected a CUDA tensor of 2-byte elements, dense within a row and ncols wide")
+    if not logits.is_cuda or logits.dtype not in _BF16 or width < ncols or (width > 1 and ts[1] != 1):
+        raise ValueError(f"expected a CUDA tensor of {_names(_BF16)}, dense within a row and ncols wide")
     s = Shard(logits.data_ptr(), ts[0] if rows > 1 else width, rows, ncols, col_offset)
     s.tensor = logits
     return s
@@ -249,14 +264,14 @@ def sample_merge(s0: Shard, s1: Shard, params, u, out, workspace, stream=None) -
     at least sample_workspace_bytes() bytes, any contents."""
     dev, rows = u.get_device(), s0.rows
     stream = _stream_on(dev, stream)
-    ps, os_, ws = params.element_size(), out.element_size(), workspace.element_size()
-    if params.numel() * ps != rows * 16 or u.numel() != rows:
+    if params.numel() * params.element_size() != rows * 16 or u.numel() != rows:
         raise ValueError("params and u must have one record for each row")
-    if out.numel() * os_ != rows * 8:
+    if out.numel() * out.element_size() != rows * 8:
         raise ValueError("out must have 8 bytes for each row")
-    status = lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1), _flat(params, ps, dev, "params"),
-                                     _flat(u, 4, dev, "u"), _flat(out, os_, dev, "out"),
-                                     _flat(workspace, ws, dev, "workspace"), workspace.numel() * ws, stream)
+    status = lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1), _flat(params, None, dev, "params"),
+                                     _flat(u, _F32, dev, "u"), _flat(out, None, dev, "out"),
+                                     _flat(workspace, None, dev, "workspace"),
+                                     workspace.numel() * workspace.element_size(), stream)
     if status != OK:
         _check(status, "xfer_sample_merge")
 
