@@ -250,7 +250,7 @@ def shard(logits, ncols: int, col_offset: int) -> Shard:
     if not logits.is_cuda or logits.dtype not in _BF16 or width < ncols or (width > 1 and ts[1] != 1):
         raise ValueError(f"expected a CUDA tensor of {_names(_BF16)}, dense within a row and ncols wide")
     s = Shard(logits.data_ptr(), ts[0] if rows > 1 else width, rows, ncols, col_offset)
-    s.tensor = logits
+    s.tensor, s.device = logits, logits.get_device()
     return s
 
 
@@ -264,6 +264,9 @@ def sample_merge(s0: Shard, s1: Shard, params, u, out, workspace, stream=None) -
     at least sample_workspace_bytes() bytes, any contents."""
     dev, rows = u.get_device(), s0.rows
     stream = _stream_on(dev, stream)
+    # a shard made from a pointer alone does not say where it lies
+    if getattr(s0, "device", dev) != dev or getattr(s1, "device", dev) != dev:
+        raise ValueError(f"expected shards on cuda:{dev}, where u is")
     if params.numel() * params.element_size() != rows * 16 or u.numel() != rows:
         raise ValueError("params and u must have one record for each row")
     if out.numel() * out.element_size() != rows * 8:

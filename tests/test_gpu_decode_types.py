@@ -1,5 +1,5 @@
 """GPU: what the decode-step binding takes for which format.  Tensors of another
-type of the same size are refused before the
+type of the same size, and shards on another device, are refused before the
 call."""
 import numpy as np
 import pytest
@@ -124,3 +124,17 @@ def test_patterns_as_whole_numbers_are_taken():
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs[:3]) and all(torch.equal(o, outs[3]) for o in outs[3:])
     assert bool(torch.isfinite(outs[0].float()).all()) and not torch.equal(outs[0], outs[3])
+
+
+def test_shards_on_another_device_are_refused():
+    b = torch.zeros((R, 64), dtype=torch.bfloat16, device=DEV)
+    args = draw(b, b, R)
+    for s in args[:2]:
+        here = s.device
+        s.device = here + 1                                # as a shard of another GPU's tensor has it
+        with pytest.raises(ValueError):
+            decode.sample_merge(*args)
+        s.device = here
+    decode.sample_merge(*args)
+    torch.cuda.synchronize()
+    assert bool((args[4][:, 1] != 9).all())
