@@ -249,7 +249,8 @@ def shard(logits, ncols: int, col_offset: int) -> Shard:
     ts = logits.stride()
     if not logits.is_cuda or logits.dtype not in _BF16 or width < ncols or (width > 1 and ts[1] != 1):
         raise ValueError(f"expected a CUDA tensor of {_names(_BF16)}, dense within a row and ncols wide")
-    s = Shard(logits.data_ptr(), ts[0] if rows > 1 else width, rows, ncols, col_offset)
+    # a single row has no distance to the next: any multiple of 8 that holds it will do
+    s = Shard(logits.data_ptr(), ts[0] if rows > 1 else -(-width // 8) * 8, rows, ncols, col_offset)
     s.tensor, s.device = logits, logits.get_device()
     return s
 

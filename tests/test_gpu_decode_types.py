@@ -1,11 +1,13 @@
 """GPU: what the decode-step binding takes for which format.  Tensors of another
 type of the same size, and shards on another device, are refused before the
-call."""
+call; a single row may be of any width."""
 import numpy as np
 import pytest
 import torch
 
 from bf16_wire_all_amd import decode
+from tests import decode_reference as ref
+from tests.gpu_util import say
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +140,18 @@ def test_shards_on_another_device_are_refused():
     decode.sample_merge(*args)
     torch.cuda.synchronize()
     assert bool((args[4][:, 1] != 9).all())
+
+
+@pytest.mark.parametrize("n0,n1", [(1, 1), (1001, 500), (40003, 20001), (7, 32770)])
+def test_one_row_of_any_width(n0, n1):
+    """A single row has no distance to a next one that could be odd."""
+    say("sample, one row", n0, n1)
+    g = torch.Generator().manual_seed(n0)
+    l0, l1 = (torch.randn((1, n), generator=g).to(torch.bfloat16) for n in (n0, n1))
+    args = draw(l0.to(DEV), l1.to(DEV), 1)
+    decode.sample_merge(*args)
+    torch.cuda.synchronize()
+    got = args[4].cpu().numpy().view(decode.SAMPLED)[0, 0]
+    x = torch.cat([l0, l1], 1)[0].double().numpy()
+    idx, prob, margin = ref.sample(x, np.arange(n0 + n1), 1.0, 0, 1.0, 0.0, 0.5)
+    assert margin > 1e-12 and got["idx"] == idx and abs(got["prob"] - prob) <= 2.0 ** -23 * prob
