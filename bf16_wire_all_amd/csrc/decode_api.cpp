@@ -144,6 +144,11 @@ int attn_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, uint32_t q_hea
   return XFER_OK;
 }
 
+// Whether both launches of an attention call are within a grid's limit.
+bool attn_launches(const xfer::AttnShape &s, uint64_t rows, uint32_t q_heads) {
+  return s.workgroups <= xfer::kMaxGridBlocks && rows * q_heads <= xfer::kMaxGridBlocks;
+}
+
 }  // namespace
 
 extern "C" {
@@ -233,7 +238,9 @@ int xfer_qkv_rope_store(const xfer_kv_cache *cache, const xfer_qkv *in, const xf
 size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch, uint32_t q_heads) {
   uint64_t extent = 0;
   xfer::AttnShape s{};
-  if (!batch || cache_checks(cache, &extent) != XFER_OK || attn_sizes(cache, batch, q_heads, &s) != XFER_OK) return 0;
+  if (!batch || cache_checks(cache, &extent) != XFER_OK || attn_sizes(cache, batch, q_heads, &s) != XFER_OK ||
+      !attn_launches(s, batch->rows, q_heads))
+    return 0;
   return (size_t)xfer::attn_workspace_bytes(s, batch->rows, cache->kv_heads, cache->head_dim);
 }
 
@@ -274,7 +281,7 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
                    overlaps((uintptr_t)scales, cache->kv_heads * 4ull, w, need)))
       return XFER_E_INVAL;
   if (overlaps(w, need, o.at, o.extent())) return XFER_E_INVAL;
-  if (s.workgroups > xfer::kMaxGridBlocks || R * q_heads > xfer::kMaxGridBlocks) return XFER_E_UNSUPPORTED;
+  if (!attn_launches(s, R, q_heads)) return XFER_E_UNSUPPORTED;
 
   xfer::AttnArgs a{};
   a.cache = view_of(cache);

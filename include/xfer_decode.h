@@ -209,8 +209,8 @@ typedef struct {
  * the table, the lengths or one another; XFER_E_UNSUPPORTED for more than 2^24 - 1
  * workgroups.
  *
- * xfer_attn_workspace_bytes - the bytes that such a call needs (0 also for a
- * batch or cache that xfer_attn_paged refuses).  They depend on the sizes and
+ * xfer_attn_workspace_bytes - the bytes that such a call needs (0 also for
+ * sizes and caches that xfer_attn_paged refuses).  They depend on the sizes and
  * strides alone, not on pointers.
  */
 XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch,

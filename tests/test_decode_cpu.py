@@ -290,6 +290,16 @@ def test_attn_empty_work_and_workspace_sizes():
             assert need <= max(1 << 20, rows * n * 2 * 2 * 128 * 2 // 16), (rows, n, need)
 
 
+def test_attn_workspace_of_batches_past_the_launch_limit():
+    """A batch that the call refuses for its size needs no workspace."""
+    far = 1 << 44
+    b = batch(rows=1 << 22, max_len=100000, table_ld=6250, page_table=3 * far, lens=4 * far)
+    assert attn(b=b, q=far, out=2 * far, heads=8, ws=6 * far, ws_bytes=1 << 40) == x.E_UNSUPPORTED
+    assert _need(cache(), b, 8) == 0
+    b.rows = 1 << 20
+    assert _need(cache(), b, 8) > 0
+
+
 # ---------------------------------------------------------------- sampling
 
 def shards(n0=1000, n1=900, ld0=1000, ld1=904, rows=3, off0=0, off1=1000, p0=K, p1=V):
