@@ -325,3 +325,10 @@ def test_refused_call_leaves_the_output_untouched():
                             torch.zeros(2, device=DEV), out, torch.zeros(1 << 16, dtype=torch.uint8, device=DEV))
     torch.cuda.synchronize()
     assert bool((out == 9).all())
+
+
+def test_the_largest_number_below_one_takes_the_definition_s_element():
+    u = np.float32(0.99999994)
+    m = logits(4, 3000, 21)
+    got = run(m, 1504, [(1.0, 0, 1.0, 0.0)] * 4, [u] * 4)
+    assert np.all(got["idx"] >= 0)
