@@ -7,8 +7,8 @@
 //   - the work is one line of units, 128 visible tokens of a (row, kv head)
 //     each, row after row; every workgroup adds up the rows' lengths for itself
 //     and takes an equal run of it.  So rows of any mixture of lengths keep all
-//     compute units busy for the same time, and no more workgroups start than
-//     stay resident.  A (row, kv head) that falls to several workgroups leaves
+//     compute units busy for the same time, and all workgroups that start are
+//     resident at once.  A (row, kv head) that falls to several workgroups leaves
 //     (max, sum, weighted sum) of each part in the workspace, at most two for a
 //     workgroup, and a second launch joins them;
 //   - a workgroup takes all query heads of a kv head, so a key is read from
@@ -31,10 +31,11 @@
 // tiles of a window are as full as any others; a token's place is looked up
 // by one lane and handed to the lanes that read it.
 //
-// Two rows of 131071 tokens (8 kv heads of 128, BF16, 1074 MB) take 165 us, 6.5
-// TB/s, and 4.7 us to be joined; 48 rows of up to 8192 tokens 94 us, 6.0 TB/s.
+// Two rows of 131071 tokens (8 kv heads of 128, BF16, 1074 MB) take 164 us, 6.5
+// TB/s, and 4.6 us to be joined; 48 rows of up to 8192 tokens 94 us, 6.0 TB/s.
 // Where a workgroup has a few units only, the rounds of one after the other
-// bound it: 96 windows of 1028 tokens (64, E4M3) 23.5 us, 3.7 TB/s.
+// bound it: 96 windows of 1028 tokens (64, E4M3) 23.2 us, 3.7 TB/s, the last
+// of nine rounds for four tokens.
 //
 // The running maximum is raised only when a score passes it by more than 2^8
 // (weights stay below 256, far from binary32's limits), which leaves out most
@@ -114,9 +115,12 @@ struct Layout {
   static constexpr int kMfmaV = D / 16;
 };
 
-// Waves that stay resident on a SIMD.  Two, where registers allow: more wait
-// on more places of the memory at once, and two rows of 131071 tokens (heads of
-// 128, BF16) take 187 us on three of a SIMD and 169 on two.
+// Waves that the runs give a SIMD: two, where registers allow.  Three or four
+// would fit for heads of 64 with up to 16 of them, three for E4M3 of 128; they
+// wait on more places of the memory at once, which serves some calls and costs
+// others (heads of 64, E4M3, four for two: 48 rows of up to 8192 tokens 45 us, 58,
+// but two rows of 100,000, tokens first, 55, 51, and 768 (row, kv head)s of up to
+// 2800 39, 37; heads of 128, BF16, three for two, two rows of 131071: 187, 169).
 // Heads of 256 leave no registers for the queries beside two waves' or 32
 // heads' results: they are read from LDS for each tile, one step ahead of the
 // products (32 heads, E4M3, 8 rows of up to 20001 tokens: 35 us with them in
@@ -215,8 +219,10 @@ __device__ __forceinline__ Run run_of(const AttnArgs &a, uint32_t inner_n, uint3
   Run run;
   run.per = (all + n_wg - 1) / n_wg;
   const uint64_t from = wg * run.per;
-  // No guarded subtraction here: the compiler has taken such a guard away
-  // (from < all ? min(per, all - from) : 0 became min(per, all - from)).
+  // No guarded subtraction here: hipcc 7.2 compiles
+  //   from < all ? min(per, all - from) : 0
+  // to min(per, all - from) without the guard (also alone, in a kernel of its
+  // own), since it may assume that what min() is called with is defined.
   run.length = min(run.per, all - min(from, all));
   if (incl - mine <= from && from < incl) {
     uint64_t before = incl - mine;
@@ -706,7 +712,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
     *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
 }
 
-// Workgroups that stay resident.
+// Workgroups of four waves that the runs are cut for.
 template <int D, int KIND>
 uint32_t resident(uint32_t tiles) {
   return kComputeUnits * (tiles == 1 ? Residence<D, KIND, 1>::kPerSimd : Residence<D, KIND, 2>::kPerSimd);
@@ -805,10 +811,10 @@ AttnShape attn_shape(uint32_t rows, uint32_t kv_heads, uint32_t group, uint32_t 
   s.waves = kWaves;
   s.heads = 1;
   s.joined = steps > whole || steps > rows * inner * steps / most + kJoinUnits;
-  // Where there are no more of them than compute units, twice the waves take a
-  // whole one, in half the rounds.  A compute unit takes in only so
-  // much at once, so the longer the rows of a key, the fewer units it may hold up
-  // the others for: beyond what an equal share would be, `wait` of them cost as
+  // Where there are no more (row, kv head)s than compute units, twice the waves
+  // take a whole one, in half the rounds.  A compute unit takes in only so much
+  // at once, so the longer the rows of a key, the fewer units it may hold up the
+  // others for: beyond what an equal share would be, `wait` of them cost as
   // much as the join (1.2, 2.3 and 3.5 us for each two units of 64, 128 and 256
   // bytes a key; 5 us).  256 rows of 1000 tokens, 64 bytes: 9.5 us, 14.5 with
   // four waves and 13.3 joined (128 bytes: 15.0, 20.3).

@@ -16,7 +16,7 @@
 //     within a row of 16 lanes (and one lane permute for 32).
 // Everything is held in binary32 and rounded once, at the store.
 //
-// 16384 tokens of 56 heads of 128 (BF16) take 71 us, 6.6 TB/s read and written;
+// 16384 tokens of 56 heads of 128 (BF16) take 73 us, 6.6 TB/s read and written;
 // one token 2.4 us, a launch.
 #include "decode.h"
 
@@ -31,9 +31,10 @@ constexpr int kThreads = 256;
 constexpr int kHeadsPerLane = 4;
 constexpr uint64_t kManyWorkgroups = 1024;
 // The queries are stored past the caches (88 us became 71; cache rows the same
-// way: 78).  Projections are read past them where the call moves more than they
-// hold (80 us became 71); smaller ones have just been written and are still
-// there (2000 tokens: 10.5 us, 12.5 past the caches).
+// way: 78; of calls that follow one another).  Projections are read past them
+// where the call moves more than they hold (80 us became 71); smaller ones have
+// just been written and are still there (2000 tokens: 10.5 us, 12.5 past the
+// caches).
 constexpr uint64_t kCachedBytes = 128ull << 20;
 
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));

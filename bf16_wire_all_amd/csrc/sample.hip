@@ -32,7 +32,8 @@
 // What a row's settings leave out whatever the other slices hold is not
 // counted: where top_p does not ask for the sum of all weights, what min_p
 // would drop beside the slice's own first element; and what lies below top_k
-// elements that the slice is known to have.  Its list then has a few entries,
+// elements that the slice is known to have.  That needs a largest value above
+// zero: slices all below it are counted whole.  The list then has a few entries,
 // and up to 64 of a row are searched by one wave in its registers (rows of
 // 129,280 with all filters: the draw is 8.9 us, with whole lists it was 14.1).
 //

@@ -112,9 +112,10 @@ typedef struct {
  * with the cosines and sines of the token's position.  The queries go to
  * q_out (BF16, row t at q_out + t * q_out_ld, heads one after the other), the
  * keys to slot slots[t] of the cache, and the values, unchanged, to the same
- * slot.  Everything is computed in binary32 and rounded once, to nearest
- * even: to BF16, or to E4M3 of (value / the head's scale) limited to +-448.
- * NaN stays NaN.
+ * slot.  Everything is computed in binary32 (the sum of a head's squares too,
+ * which has to stay within it: |x| below 2^59 does) and rounded once, to
+ * nearest even: to BF16, or to E4M3 of (value / the head's scale) limited to
+ * +-448.  NaN stays NaN, though not always the same one.
  *
  *   slots  (device) int64[tokens]: page * page_tokens + slot.  A token whose
  *          slot is negative, or not below n_pages * page_tokens, is not
