@@ -135,3 +135,27 @@ def test_nan_in_an_8_bit_cache_reaches_its_dim_alone():
     bad[1, 4:, 9] = bad[0, :4, 100] = True
     assert np.array_equal(np.isnan(got), bad)
     assert np.all(np.abs(got - o)[~bad] <= tol[~bad])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_scores(form):
+    """A score of +inf makes its heads NaN; one of -inf takes its token out."""
+    w = world(form, "f32", 36)
+    group, n = w.hq // w.hkv, [w.lens[0] - 1, 5]
+    for r in (0, 1):                                # heads of the first kv head: a key's infinity keeps its sign
+        w.q[r, :group, 2] = 1.5
+        w.dq[r, :group, 2] = 1.5
+    o, tol = w.want()                               # of row 0 and the other heads
+    pages, slots = w.at[1]
+    keep = torch.arange(len(pages)) != n[1]
+    w.at[1] = pages[keep], slots[keep]
+    without, without_tol = w.want()                 # row 1 without that token
+    w.at[1] = pages, slots
+    o[1, :group], tol[1, :group] = without[1, :group], without_tol[1, :group]
+    put(w, 0, 0, n[0], 0, 2, INF16)
+    put(w, 0, 1, n[1], 0, 2, NINF16)
+    got = call(w)
+    bad = np.zeros(got.shape, bool)
+    bad[0, :group] = True
+    assert np.array_equal(np.isnan(got), bad)
+    assert np.all(np.abs(got - o)[~bad] <= tol[~bad])
