@@ -58,6 +58,17 @@ struct AttnArgs {
 };
 hipError_t launch_attn(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream);
 
+// ---- a cache's slots as records for the wire, and back (kv_wire.hip)
+struct WireArgs {
+  CacheView cache;
+  const int64_t *slots;
+  uint8_t *records;  // written by quantize, read by restore
+  uint64_t record_ld;
+  uint32_t tokens, lanes_log2;  // log2 of the lanes that share a head's row (set by the launch)
+};
+uint64_t wire_workgroups(uint32_t tokens, uint32_t kv_heads, uint32_t head_dim);
+hipError_t launch_wire(const WireArgs &a, int kind, int bits, bool restore, hipStream_t stream);
+
 // ---- sampling (sample.hip)
 // Workgroups of the widest launch for each row, and the workspace.
 uint32_t sample_slices(uint32_t ncols0, uint32_t ncols1);

@@ -149,6 +149,51 @@ bool attn_launches(const xfer::AttnShape &s, uint64_t rows, uint32_t q_heads) {
   return s.workgroups <= xfer::kMaxGridBlocks && rows * q_heads <= xfer::kMaxGridBlocks;
 }
 
+// Bytes of a token's record: its elements, a scale for each 32 of them, and
+// zeros up to a multiple of 16.
+uint64_t record_bytes(const xfer_kv_cache *c, int bits) {
+  const uint64_t n = 2ull * c->kv_heads * c->head_dim;
+  return (n * (uint64_t)bits / 8 + n / 32 + 15) / 16 * 16;
+}
+
+// Both directions of the wire; the records are read by one and written by the other.
+int wire_call(const xfer_kv_cache *cache, const int64_t *slots, uint32_t tokens, int bits, void *records,
+              uint64_t record_ld, bool restore, hipStream_t stream) {
+  uint64_t extent = 0;
+  const int st = cache_checks(cache, &extent);
+  if (st != XFER_OK) return st;
+  if (bits != XFER_WIRE_E4M3 && bits != XFER_WIRE_E2M1) return XFER_E_INVAL;
+  if (restore && (!slots_disjoint(cache) || !values_apart(cache))) return XFER_E_OVERLAP;
+  if (tokens == 0) return XFER_OK;
+  const uint64_t need = record_bytes(cache, bits);
+  if (need > 0x7FFFFFFFu || xfer::wire_workgroups(tokens, cache->kv_heads, cache->head_dim) > xfer::kMaxGridBlocks)
+    return XFER_E_UNSUPPORTED;
+  if (!slots || (uintptr_t)slots % 8 || !records || !aligned16(records) || record_ld % 16) return XFER_E_INVAL;
+  if (tokens > 1 && (record_ld < need || record_ld > kMaxExtent || tokens - 1 > kMaxExtent / record_ld))
+    return XFER_E_INVAL;
+  const Rows rec{(uintptr_t)records, record_ld, need, tokens};
+  const Rows others[3] = {{(uintptr_t)slots, 8, 8, tokens},
+                          {(uintptr_t)cache->k_scale, 4, 4, cache->k_scale ? cache->kv_heads : 0},
+                          {(uintptr_t)cache->v_scale, 4, 4, cache->v_scale ? cache->kv_heads : 0}};
+  const uintptr_t caches[2] = {(uintptr_t)cache->k, (uintptr_t)cache->v};
+  for (uintptr_t c : caches) {
+    if (overlaps(c, extent, rec.at, rec.extent())) return XFER_E_INVAL;
+    for (const Rows &o : others)
+      if (restore && overlaps(c, extent, o.at, o.extent())) return XFER_E_INVAL;
+  }
+  for (const Rows &o : others)
+    if (!restore && rows_touch(rec, Rows{o.at, 0, o.extent(), o.n ? 1u : 0u})) return XFER_E_INVAL;
+
+  xfer::WireArgs a{};
+  a.cache = view_of(cache);
+  a.slots = slots;
+  a.records = static_cast<uint8_t *>(records);
+  a.record_ld = record_ld;
+  a.tokens = tokens;
+  if (xfer::launch_wire(a, cache->kind, bits, restore, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -303,6 +348,23 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   a.part_ml = static_cast<float *>(workspace);
   if (xfer::launch_attn(a, cache->kind, s, stream) != hipSuccess) return XFER_E_DEVICE;
   return XFER_OK;
+}
+
+size_t xfer_kv_record_bytes(const xfer_kv_cache *cache, int bits) {
+  uint64_t extent = 0;
+  if (cache_checks(cache, &extent) != XFER_OK || (bits != XFER_WIRE_E4M3 && bits != XFER_WIRE_E2M1)) return 0;
+  const uint64_t need = record_bytes(cache, bits);
+  return need > 0x7FFFFFFFu ? 0 : (size_t)need;
+}
+
+int xfer_kv_quantize(const xfer_kv_cache *cache, const int64_t *slots, uint32_t tokens, int bits, void *records,
+                     uint64_t record_ld, hipStream_t stream) {
+  return wire_call(cache, slots, tokens, bits, records, record_ld, false, stream);
+}
+
+int xfer_kv_restore(const void *records, uint64_t record_ld, uint32_t tokens, int bits, const xfer_kv_cache *cache,
+                    const int64_t *slots, hipStream_t stream) {
+  return wire_call(cache, slots, tokens, bits, const_cast<void *>(records), record_ld, true, stream);
 }
 
 size_t xfer_sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {

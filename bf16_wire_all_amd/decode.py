@@ -17,8 +17,8 @@ from . import OK, OUT_BF16, OUT_F32, Shard, _check, _stream, lib as _base_lib
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
-EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged", "xfer_sample_workspace_bytes",
-            "xfer_sample_merge"]
+EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged", "xfer_kv_record_bytes",
+            "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge"]
 
 SAMPLE_PARAMS = np.dtype([("temperature", "<f4"), ("top_k", "<u4"), ("top_p", "<f4"), ("min_p", "<f4")])
 SAMPLED = np.dtype([("prob", "<f4"), ("idx", "<i4")])
@@ -68,6 +68,12 @@ def lib():
         L.xfer_attn_paged.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, U64, U32, F, P, U64, I,
                                       P, S, P]
         L.xfer_attn_paged.restype = I
+        L.xfer_kv_record_bytes.argtypes = [ctypes.POINTER(KVCacheC), I]
+        L.xfer_kv_record_bytes.restype = S
+        L.xfer_kv_quantize.argtypes = [ctypes.POINTER(KVCacheC), P, U32, I, P, U64, P]
+        L.xfer_kv_quantize.restype = I
+        L.xfer_kv_restore.argtypes = [P, U64, U32, I, ctypes.POINTER(KVCacheC), P, P]
+        L.xfer_kv_restore.restype = I
         L.xfer_sample_workspace_bytes.argtypes = [U32, U32, U32]
         L.xfer_sample_workspace_bytes.restype = S
         L.xfer_sample_merge.argtypes = [ctypes.POINTER(Shard), ctypes.POINTER(Shard), P, P, P, P, S, P]
@@ -237,6 +243,60 @@ def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q
     """Raw-pointer form; returns the status without raising."""
     return lib().xfer_attn_paged(ctypes.byref(cache), ctypes.byref(batch), q_ptr, q_ld, q_heads, scale, out_ptr,
                                  out_ld, out_mode, ws_ptr, ws_bytes, _stream(stream))
+
+
+# ------------------------------------------- a cache's slots in 8 or 4 bits
+
+_BYTES = frozenset((torch.uint8, torch.int8))
+
+
+def kv_record_bytes(cache: KVCache, bits: int) -> int:
+    """Bytes of a token's record; bits: 8 (E4M3) or 4 (E2M1)."""
+    return int(lib().xfer_kv_record_bytes(ctypes.byref(cache.c), bits))
+
+
+def _records(records, slots, cache: KVCache, bits: int):
+    """(pointer, bytes between records, tokens) of a [tokens, bytes] tensor whose rows are dense."""
+    tokens, width = records.shape
+    s0, s1 = records.stride()
+    if records.get_device() != cache.device or records.dtype not in _BYTES or (width > 1 and s1 != 1):
+        raise ValueError(f"records: expected {_names(_BYTES)} on cuda:{cache.device}, dense within a row")
+    if tokens != slots.numel() or width < kv_record_bytes(cache, bits):
+        raise ValueError("records must have a row of at least kv_record_bytes() for each slot")
+    return records.data_ptr(), s0 if tokens > 1 else 0, tokens
+
+
+def kv_quantize(cache: KVCache, slots, records, bits: int, stream=None) -> None:
+    """slots: int64[tokens]; records: uint8 [tokens, at least kv_record_bytes()],
+    rows a multiple of 16 bytes apart; bits: 8 or 4."""
+    stream = _stream_on(cache.device, stream)
+    rp, ld, tokens = _records(records, slots, cache, bits)
+    status = lib().xfer_kv_quantize(ctypes.byref(cache.c), _flat(slots, _INT64, cache.device, "slots"), tokens, bits, rp,
+                                    ld, stream)
+    if status != OK:
+        _check(status, "xfer_kv_quantize")
+
+
+def kv_restore(records, bits: int, cache: KVCache, slots, stream=None) -> None:
+    """The records of kv_quantize into slots of this cache, of either kind."""
+    stream = _stream_on(cache.device, stream)
+    rp, ld, tokens = _records(records, slots, cache, bits)
+    status = lib().xfer_kv_restore(rp, ld, tokens, bits, ctypes.byref(cache.c),
+                                   _flat(slots, _INT64, cache.device, "slots"), stream)
+    if status != OK:
+        _check(status, "xfer_kv_restore")
+
+
+def kv_quantize_raw(cache: KVCacheC, slots_ptr: int, tokens: int, bits: int, records_ptr: int, record_ld: int,
+                    stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_kv_quantize(ctypes.byref(cache), slots_ptr, tokens, bits, records_ptr, record_ld, _stream(stream))
+
+
+def kv_restore_raw(records_ptr: int, record_ld: int, tokens: int, bits: int, cache: KVCacheC, slots_ptr: int,
+                   stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_kv_restore(records_ptr, record_ld, tokens, bits, ctypes.byref(cache), slots_ptr, _stream(stream))
 
 
 # ------------------------------------------------------------------ sampling

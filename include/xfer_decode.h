@@ -8,6 +8,8 @@
  *   xfer_attn_paged      attention of one new token of every request over
  *                        such a cache, the whole of it or a window and the
  *                        first tokens
+ *   xfer_kv_quantize,    a cache's slots as records of 8 or 4 bits an
+ *   xfer_kv_restore      element for the wire, and back into another cache
  *   xfer_sample_merge    sampling with temperature, top-k, top-p and min-p
  *                        from logits in two column shards, beside
  *                        xfer_argmax_merge
@@ -219,6 +221,68 @@ XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer
 XFER_API int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q,
                              uint64_t q_ld, uint32_t q_heads, float scale, void *out, uint64_t out_ld, int out_mode,
                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------ a cache's slots in 8 or 4 bits */
+
+/* Bits of an element on the wire. */
+enum {
+  XFER_WIRE_E4M3 = 8, /* 8-bit floats, 448 the largest                        */
+  XFER_WIRE_E2M1 = 4  /* 4-bit floats (2 exponent bits, 1 mantissa bit):
+                         0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; the
+                         magnitude's place in this list is its code, the sign
+                         the highest bit                                      */
+};
+
+/*
+ * A token's record, xfer_kv_record_bytes() bytes: the elements of its keys,
+ * head after head, and of its values, then one byte for each 32 of these
+ * elements, and zeros up to a multiple of 16.  Byte b after the elements
+ * stands for the scale 2^(b - 127) of its 32; 255 makes all of them NaN.  Of
+ * two 4-bit elements in a byte the first is in the low bits.
+ *
+ * xfer_kv_quantize - the records of the tokens in the cache's slots
+ * slots[0 .. tokens - 1], token t's at records + t * record_ld: for each 32
+ * neighbouring elements x of a head (of an E4M3 cache: an element times its
+ * head's scale, in binary32), with L the largest 448 or 6,
+ *   e = the smallest whole number from -127 on with max |x| <= L * 2^e
+ *   element = x / 2^e, rounded to nearest even         (the sign of a zero kept)
+ * 32 elements with a NaN or an infinity among them get byte 255 and zeros.
+ * A slot that is negative, or not below n_pages * page_tokens, gives a record
+ * of zeros, which stands for zeros.  A slot may be named any number of times.
+ *
+ * xfer_kv_restore - the inverse: the values element * 2^(b - 127) go to slot
+ * slots[t] of the cache, of either kind and any layout.  In a BF16 cache they
+ * are exact, but for values that are no BF16 numbers: below its subnormal ones
+ * (which quantising a BF16 cache never makes) they are rounded to nearest even,
+ * and 2^128 or more (to which magnitudes from 1.75 * 2^127 on may have been
+ * rounded) becomes infinite.  In an E4M3 cache value / the head's scale, in
+ * binary32, is limited to +-448 and rounded to nearest even, as
+ * xfer_qkv_rope_store does.  NaN stays NaN, though not
+ * always the same one.  A token whose slot is negative or out of range is not
+ * stored; the slots that are stored to must be distinct (as for
+ * xfer_qkv_rope_store).  Any bytes are valid records.
+ *
+ *   slots    (device) int64[tokens], 8-byte aligned.
+ *   records  (device) 16-byte aligned; record_ld bytes between records, a
+ *            multiple of 16.  Bytes between records are not written.
+ *   bits     XFER_WIRE_*.
+ *
+ * Quantising what was restored into a BF16 cache, and is finite, gives records
+ * of the same values.
+ *
+ * Errors: those of the cache; XFER_E_INVAL for unknown bits, NULL or
+ * misaligned pointers, a record_ld that is not a multiple of 16 or smaller
+ * than a record (tokens > 1), or records, or the cache where it is written,
+ * that overlap another buffer; XFER_E_OVERLAP (restore) if two slots of the
+ * cache share bytes; XFER_E_UNSUPPORTED for a record of 2 GiB or more or more than
+ * 2^24 - 1 workgroups (one for each 8,192 elements).
+ * xfer_kv_record_bytes: 0 for caches and bits that the calls refuse.
+ */
+XFER_API size_t xfer_kv_record_bytes(const xfer_kv_cache *cache, int bits);
+XFER_API int xfer_kv_quantize(const xfer_kv_cache *cache, const int64_t *slots, uint32_t tokens, int bits,
+                              void *records, uint64_t record_ld, hipStream_t stream);
+XFER_API int xfer_kv_restore(const void *records, uint64_t record_ld, uint32_t tokens, int bits,
+                             const xfer_kv_cache *cache, const int64_t *slots, hipStream_t stream);
 
 /* --------------------------------------------------------------- sampling */
 
