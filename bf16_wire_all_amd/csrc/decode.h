@@ -83,4 +83,24 @@ struct SampleArgs {
 };
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
 
+// ---- log probabilities (logprobs.hip)
+constexpr uint32_t kMaxTokens = 16, kMaxTop = 32;  // of a row
+struct LogprobArgs {
+  ArgmaxShard s[2];
+  uint32_t rows, n_tokens, n_top;
+  const float *temperature;
+  const int32_t *tokens;
+  xfer_token_logprob *token_out;
+  xfer_top_logprob *top_out;
+  float *entropy;
+  // set by the launch: how rows are cut up, and the workspace of rows in several parts
+  uint32_t parts, slices[2], width[2];
+  void *sums;
+  uint64_t *keys;
+  uint32_t *ranks;
+};
+uint64_t logprobs_workgroups(uint32_t rows, uint32_t ncols0, uint32_t ncols1);
+uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1, uint32_t n_tokens, uint32_t n_top);
+hipError_t launch_logprobs(const LogprobArgs &a, void *workspace, hipStream_t stream);
+
 }  // namespace xfer

@@ -149,6 +149,19 @@ bool attn_launches(const xfer::AttnShape &s, uint64_t rows, uint32_t q_heads) {
   return s.workgroups <= xfer::kMaxGridBlocks && rows * q_heads <= xfer::kMaxGridBlocks;
 }
 
+// The checks of two logit shards that xfer_sample_merge and xfer_logprobs_merge
+// share, up to their pointers'.
+int shard_checks(const xfer_shard *const (&s)[2]) {
+  for (const xfer_shard *x : s)
+    if (x->ncols == 0 || (uint64_t)x->col_offset + x->ncols > (1ull << 31)) return XFER_E_INVAL;
+  if (s[0]->col_offset < s[1]->col_offset + (uint64_t)s[1]->ncols &&
+      s[1]->col_offset < s[0]->col_offset + (uint64_t)s[0]->ncols)
+    return XFER_E_INVAL;
+  for (const xfer_shard *x : s)
+    if (x->ncols > xfer::kArgmaxMaxShardCols) return XFER_E_UNSUPPORTED;
+  return XFER_OK;
+}
+
 // Bytes of a token's record: its elements, a scale for each 32 of them, and
 // zeros up to a multiple of 16.
 uint64_t record_bytes(const xfer_kv_cache *c, int bits) {
@@ -378,12 +391,8 @@ int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sam
   const uint64_t R = s0->rows;
   if (R == 0) return XFER_OK;
   const xfer_shard *s[2] = {s0, s1};
-  for (const xfer_shard *x : s)
-    if (x->ncols == 0 || (uint64_t)x->col_offset + x->ncols > (1ull << 31)) return XFER_E_INVAL;
-  if (s0->col_offset < s1->col_offset + (uint64_t)s1->ncols && s1->col_offset < s0->col_offset + (uint64_t)s0->ncols)
-    return XFER_E_INVAL;
-  for (const xfer_shard *x : s)
-    if (x->ncols > xfer::kArgmaxMaxShardCols) return XFER_E_UNSUPPORTED;
+  const int st = shard_checks(s);
+  if (st != XFER_OK) return st;
   if (R * xfer::sample_slices(s0->ncols, s1->ncols) > xfer::kMaxGridBlocks) return XFER_E_UNSUPPORTED;
   for (const xfer_shard *x : s)
     if (!x->ptr || !aligned16(x->ptr) || !ld_ok(x->ld, R, x->ncols)) return XFER_E_INVAL;
@@ -408,6 +417,67 @@ int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sam
   a.out = static_cast<xfer_sampled *>(out);
   a.workspace = workspace;
   if (xfer::launch_sample(a, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
+size_t xfer_logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1, uint32_t n_tokens,
+                                     uint32_t n_top) {
+  if (!rows || !ncols0 || !ncols1 || ncols0 > xfer::kArgmaxMaxShardCols || ncols1 > xfer::kArgmaxMaxShardCols ||
+      n_tokens > xfer::kMaxTokens || n_top > xfer::kMaxTop ||
+      xfer::logprobs_workgroups(rows, ncols0, ncols1) > xfer::kMaxGridBlocks)
+    return 0;
+  return (size_t)xfer::logprobs_workspace_bytes(rows, ncols0, ncols1, n_tokens, n_top);
+}
+
+int xfer_logprobs_merge(const xfer_shard *s0, const xfer_shard *s1, const float *temperature, const int32_t *tokens,
+                        uint32_t n_tokens, uint32_t n_top, void *token_out, void *top_out, float *entropy,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!s0 || !s1 || s0->rows != s1->rows) return XFER_E_INVAL;
+  const uint64_t R = s0->rows;
+  if (R == 0) return XFER_OK;
+  const xfer_shard *s[2] = {s0, s1};
+  const int st = shard_checks(s);
+  if (st != XFER_OK) return st;
+  if (n_tokens > xfer::kMaxTokens || n_top > xfer::kMaxTop ||
+      xfer::logprobs_workgroups((uint32_t)R, s0->ncols, s1->ncols) > xfer::kMaxGridBlocks)
+    return XFER_E_UNSUPPORTED;
+  for (const xfer_shard *x : s)
+    if (!x->ptr || !aligned16(x->ptr) || !ld_ok(x->ld, R, x->ncols)) return XFER_E_INVAL;
+  if ((uintptr_t)temperature % 4 || (uintptr_t)entropy % 4) return XFER_E_INVAL;
+  if (n_tokens && (!tokens || (uintptr_t)tokens % 4 || !token_out || (uintptr_t)token_out % 8)) return XFER_E_INVAL;
+  if (n_top && (!top_out || (uintptr_t)top_out % 8)) return XFER_E_INVAL;
+  const uint64_t need = xfer::logprobs_workspace_bytes((uint32_t)R, s0->ncols, s1->ncols, n_tokens, n_top);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return XFER_E_INVAL;
+  struct Buffer {
+    uintptr_t at;
+    uint64_t bytes;
+  };
+  const Buffer outs[4] = {{(uintptr_t)token_out, R * n_tokens * sizeof(xfer_token_logprob)},
+                          {(uintptr_t)top_out, R * n_top * sizeof(xfer_top_logprob)},
+                          {(uintptr_t)entropy, entropy ? R * 4 : 0},
+                          {(uintptr_t)workspace, need}};
+  const Rows ins[4] = {{(uintptr_t)s0->ptr, s0->ld * 2, (uint64_t)s0->ncols * 2, R},
+                       {(uintptr_t)s1->ptr, s1->ld * 2, (uint64_t)s1->ncols * 2, R},
+                       {(uintptr_t)temperature, 4, 4, temperature ? R : 0},
+                       {(uintptr_t)tokens, 4ull * n_tokens, 4ull * n_tokens, n_tokens ? R : 0}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Rows &r : ins)
+      if (overlaps(outs[i].at, outs[i].bytes, r.at, r.extent())) return XFER_E_INVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return XFER_E_INVAL;
+  }
+
+  xfer::LogprobArgs a{};
+  for (int i = 0; i < 2; ++i) a.s[i] = xfer::ArgmaxShard{s[i]->ptr, s[i]->ld, s[i]->ncols, s[i]->col_offset};
+  a.rows = (uint32_t)R;
+  a.n_tokens = n_tokens;
+  a.n_top = n_top;
+  a.temperature = temperature;
+  a.tokens = tokens;
+  a.token_out = static_cast<xfer_token_logprob *>(token_out);
+  a.top_out = static_cast<xfer_top_logprob *>(top_out);
+  a.entropy = entropy;
+  if (xfer::launch_logprobs(a, workspace, stream) != hipSuccess) return XFER_E_DEVICE;
   return XFER_OK;
 }
 

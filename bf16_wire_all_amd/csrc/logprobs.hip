@@ -1,0 +1,515 @@
+// Log probabilities of given tokens with their ranks, the best elements and the
+// entropy of rows of BF16 logits in two column shards.
+//
+// With m the row's largest logit, x_i = (l_i - m) / T <= 0 and w_i = exp(x_i):
+//   Z = 1 + R, R the weights of all elements but the first of the row's order,
+//   logprob_i = x_i - log1p(R), entropy = log1p(R) - sum w_i x_i / Z.
+// Keeping the largest element out of the sum leaves R's own digits where it is
+// small (a token of probability 1 - 1e-9 has a log probability of -1e-9, not
+// 0), and both terms of the entropy are positive, so neither cancels.
+//
+// The logits are read once.  A workgroup holds a slice of a row in registers
+// and makes its passes there:
+//   1. the largest: packed 16-bit maxima of the patterns as they stand (as
+//      whole numbers positive BF16 numbers are in order, negative ones below
+//      them; rows without a positive element, or with NaN, are looked at again);
+//   2. the best elements: each lane's own largest gives a bound that enough
+//      elements reach (the n-th largest of a wave's 64 lanes), and the few
+//      elements that reach it go to a list in LDS, where their places are
+//      counted;
+//   3. the ranks: comparisons, counted a wave at a time;
+//   4. the weights: 2^(l c - m c), c = log2(e) / T, by one fused multiply-add
+//      and the hardware's power.  m c is rounded to binary32; what that moves
+//      all weights by is a factor that is put right afterwards.
+// Thread sums are binary32 (of up to 64 elements), everything above binary64.
+//
+// Where rows are few, each is cut into several workgroups' parts, which a
+// second launch folds: (largest, R, sum w x) scaled to the row's largest.
+#include "decode.h"
+
+namespace xfer {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kRounds = 8;                                // vectors of 8 elements that a thread holds
+constexpr uint32_t kSliceCols = kThreads * 8 * kRounds;   // 16,384
+constexpr uint32_t kMinCols = 2048;                       // of a slice where rows are cut into parts
+constexpr uint32_t kWorkgroups = 1024;                    // that a call is cut up for
+constexpr uint32_t kMaxParts = 128;                       // of a row: two for each lane of the fold's wave
+constexpr uint32_t kList = 1024;                          // elements that reach the bound, at most
+constexpr uint32_t kMasked = 0xFF80FF80u;
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef short v2s __attribute__((ext_vector_type(2)));
+
+// A place in the row's order: 0 for what is not in it (NaN, -inf), larger for
+// larger values, -0 as +0.
+__device__ __forceinline__ uint32_t ord(uint32_t v) {
+  const uint32_t mag = v & 0x7FFFu;
+  if (mag > 0x7F80u || v == 0xFF80u) return 0;
+  return v & 0x8000u ? 0x8000u - mag : 0x8000u + mag;
+}
+// The value of a place that is not 0.
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float((o >= 0x8000u ? o - 0x8000u : 0x8000u | (0x8000u - o)) << 16);
+}
+// An element: its place, then its id, the lower first.
+__device__ __forceinline__ uint64_t key_of(uint32_t o, uint32_t id) { return o ? (uint64_t)o << 32 | (0xFFFFFFFFu - id) : 0; }
+__device__ __forceinline__ uint32_t ord_of(uint64_t key) { return (uint32_t)(key >> 32); }
+__device__ __forceinline__ uint32_t id_of(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
+
+__device__ __forceinline__ uint32_t half(uint32_t w, int h) { return h ? w >> 16 : w & 0xFFFFu; }
+__device__ __forceinline__ float as_float(uint32_t w, int h) {
+  return __uint_as_float(h ? w & 0xFFFF0000u : w << 16);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int x, int old) {
+  return __builtin_amdgcn_update_dpp(old, x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_max(int x) {
+  constexpr int kLow = -0x7FFFFFFF - 1;
+  x = max(x, dpp<0x111, 0xF>(x, kLow));
+  x = max(x, dpp<0x112, 0xF>(x, kLow));
+  x = max(x, dpp<0x114, 0xF>(x, kLow));
+  x = max(x, dpp<0x118, 0xF>(x, kLow));
+  x = max(x, dpp<0x142, 0xA>(x, kLow));
+  x = max(x, dpp<0x143, 0xC>(x, kLow));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x = max(x, (uint64_t)__shfl_xor((unsigned long long)x, d));
+  return x;
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+  return x;
+}
+
+// What a set of elements comes to: its first element, and of all others the sum
+// of weights and of weights times x, relative to that first one.
+struct Sum {
+  double rest, wx;
+  uint64_t top;
+};
+// (l - m) / T of a row, in binary64.
+__device__ __forceinline__ double scaled(float l, float m, float T) {
+  if (l == m) return 0.0;
+  return __builtin_isinf(m) ? -INFINITY : ((double)l - (double)m) / (double)T;
+}
+__device__ __forceinline__ Sum join(const Sum &a, const Sum &b, float T) {
+  if (!a.top || !b.top) return a.top ? a : b;
+  const Sum &hi = a.top > b.top ? a : b, &lo = a.top > b.top ? b : a;
+  const double x = scaled(value_of(ord_of(lo.top)), value_of(ord_of(hi.top)), T), f = exp(x);
+  Sum s = hi;
+  if (f > 0) {  // not so where x is -inf
+    s.rest += f * (1.0 + lo.rest);
+    s.wx += f * (lo.wx + (1.0 + lo.rest) * x);
+  }
+  return s;
+}
+
+// The next BF16 number above v (NaN above +inf, which nothing reaches).
+__device__ __forceinline__ float above(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return __uint_as_float(v == 0.0f ? 0x10000u : u & 0x80000000u ? u - 0x10000u : u + 0x10000u);
+}
+
+struct Slice {
+  const uint16_t *ptr;
+  uint32_t cols, gid;
+};
+__device__ __forceinline__ Slice slice_of(const LogprobArgs &a, uint32_t row, uint32_t k) {
+  const uint32_t s = k >= a.slices[0];
+  const uint32_t c0 = min((s ? k - a.slices[0] : k) * a.width[s], a.s[s].ncols);
+  return {a.s[s].ptr + row * a.s[s].ld + c0, min(a.width[s], a.s[s].ncols - c0), a.s[s].col_offset + c0};
+}
+
+// A given token's place in the order (0: it has none).
+__device__ __forceinline__ uint64_t token_key(const LogprobArgs &a, uint32_t row, int32_t id) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const uint32_t c = (uint32_t)id - a.s[s].col_offset;
+    if (id >= 0 && (uint32_t)id >= a.s[s].col_offset && c < a.s[s].ncols)
+      return key_of(ord(a.s[s].ptr[row * a.s[s].ld + c]), (uint32_t)id);
+  }
+  return 0;
+}
+
+// The row's results from its sum, its tokens' ranks and its best elements; by
+// the threads of a workgroup.
+__device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sum &sum, float T,
+                                       const uint32_t *ranks, const uint64_t *best) {
+  const uint32_t tid = threadIdx.x;
+  const bool greedy = !(T > 0.0f);
+  const double log_z = greedy ? 0.0 : log1p(sum.rest);
+  const float m = sum.top ? value_of(ord_of(sum.top)) : 0.0f;
+  auto logprob = [&](uint64_t key) -> float {
+    if (!key) return -INFINITY;
+    if (greedy) return key == sum.top ? 0.0f : -INFINITY;
+    return (float)(scaled(value_of(ord_of(key)), m, T) - log_z);
+  };
+  if (tid == 0 && a.entropy) a.entropy[row] = !sum.top || greedy ? 0.0f : (float)(log_z - sum.wx / (1.0 + sum.rest));
+  if (tid < a.n_tokens) {
+    const uint64_t at = (uint64_t)row * a.n_tokens + tid, key = token_key(a, row, a.tokens[at]);
+    a.token_out[at] = xfer_token_logprob{logprob(key), key ? (int32_t)ranks[tid] : -1};
+  }
+  if (tid < a.n_top) {
+    const uint64_t key = best[tid];
+    a.top_out[(uint64_t)row * a.n_top + tid] = xfer_top_logprob{logprob(key), key ? (int32_t)id_of(key) : -1};
+  }
+}
+
+struct Shared {
+  uint64_t list[kList];           // what reaches the bound
+  uint64_t best[kMaxTop];         // the best so far, in order
+  uint64_t token[kMaxTokens];
+  uint32_t rank[kMaxTokens];
+  int32_t wave_top[kWaves], wave_bound[kWaves];
+  double wave_rest[kWaves], wave_wx[kWaves];
+  uint64_t wave_key[kWaves];
+  uint32_t listed, equal, first;  // elements listed; elements equal to the largest, and the first one's column
+};
+
+// What reaches `bound` and is in the row's order.
+__device__ __forceinline__ float bound_value(int32_t o) {
+  return o > 0 ? value_of((uint32_t)o) : __uint_as_float(0xFF7F0000u);  // or the lowest finite number
+}
+
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
+  __shared__ Shared sh;
+  const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const uint32_t n_slices = a.slices[0] + a.slices[1];
+  const uint32_t k0 = (uint32_t)((uint64_t)n_slices * part / a.parts), k1 = (uint32_t)((uint64_t)n_slices * (part + 1) / a.parts);
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  const bool greedy = !(T > 0.0f);
+  if (tid < a.n_tokens) {
+    sh.token[tid] = token_key(a, row, a.tokens[(uint64_t)row * a.n_tokens + tid]);
+    sh.rank[tid] = 0;
+  }
+  if (tid < a.n_top) sh.best[tid] = 0;
+  Sum total = {0, 0, 0};  // thread 0's
+
+#pragma unroll 1
+  for (uint32_t k = k0; k < k1; ++k) {
+    const Slice s = slice_of(a, row, k);
+    v4u w[kRounds];
+    {
+      // The vector that the slice ends in, by the thread that holds it.
+      const uint32_t end = s.cols / 8;
+      v4u last = v4u{kMasked, kMasked, kMasked, kMasked};
+      if (s.cols % 8 && tid == end % kThreads) {
+        for (uint32_t i = 0; i < s.cols % 8; ++i) {
+          const uint32_t v = s.ptr[8 * end + i], low = 16 * (i % 2);
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q)
+            if (i / 2 == q) last[q] = (last[q] & ~(0xFFFFu << low)) | v << low;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const uint32_t at = r * kThreads + tid;
+        w[r] = at == end ? last : v4u{kMasked, kMasked, kMasked, kMasked};
+        if (at < end) w[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(s.ptr) + at);
+      }
+    }
+    // f(word, half, column) for each element that this thread holds
+    auto each = [&](auto &&f) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        if ((uint32_t)r * kThreads * 8 >= s.cols) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x = w[r][q];
+          f(x, 0, 8 * (r * kThreads + tid) + 2 * q);
+          f(x, 1, 8 * (r * kThreads + tid) + 2 * q + 1);
+        }
+      }
+    };
+    // f(pattern, column) for each element, read again: for what is rare
+    auto again = [&](auto &&f) {
+#pragma unroll 1
+      for (uint32_t c = tid; c < s.cols; c += kThreads) f((uint32_t)s.ptr[c], c);
+    };
+
+    // 1. The largest, and a bound that n_top elements of a wave reach.
+    v2s two = {-0x8000, -0x8000};
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = w[r][q];
+        two = __builtin_elementwise_max(two, __builtin_bit_cast(v2s, x));
+      }
+    const int mine = max((int)two.x, (int)two.y);
+    int top = wave_max(mine);
+    int own = mine >= 0 ? 0x8000 + mine : 0;  // this lane's largest in the order; 0: not known
+    const bool plain = top > 0 && top <= 0x7F80 && (uint32_t)__popcll(__ballot(mine >= 0)) >= a.n_top;
+    if (!plain) {
+      own = 0;
+      again([&](uint32_t v, uint32_t) { own = max(own, (int)ord(v)); });
+      top = wave_max(own) - 0x8000;
+    }
+    int bound = 0;
+    if (a.n_top) {
+#pragma unroll
+      for (int b = 0x8000; b; b >>= 1)
+        if ((uint32_t)__popcll(__ballot(own >= bound + b)) >= a.n_top) bound += b;
+    }
+    __syncthreads();  // the slice before this one is done with LDS
+    if (lane == 0) {
+      sh.wave_top[wave] = top + 0x8000;
+      sh.wave_bound[wave] = bound;
+    }
+    if (tid == 0) sh.listed = a.n_top, sh.equal = 0, sh.first = 0xFFFFFFFFu;
+    if (tid < a.n_top) sh.list[tid] = sh.best[tid];
+    __syncthreads();
+    uint32_t o = 0;
+    int32_t reach = a.n_top ? (int32_t)ord_of(sh.best[a.n_top - 1]) : 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      o = max(o, (uint32_t)sh.wave_top[i]);
+      reach = max(reach, sh.wave_bound[i]);
+    }
+    if (o == 0) continue;  // nothing here is in the order
+    const float m = value_of(o);
+
+    // 2. What reaches the bound.
+    if (a.n_top) {
+      const float at_least = bound_value(reach);
+      each([&](uint32_t x, int h, uint32_t c) {
+        const bool in = as_float(x, h) >= at_least;
+        const uint64_t mask = __ballot(in);
+        if (!mask) return;
+        uint32_t base = 0;
+        if (lane == 0) base = atomicAdd(&sh.listed, (uint32_t)__popcll(mask));
+        base = __builtin_amdgcn_readfirstlane(base);
+        const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (in && at < kList) sh.list[at] = key_of(ord(half(x, h)), s.gid + c);
+      });
+    }
+
+    // 3. The elements before each token.
+    for (uint32_t i = 0; i < a.n_tokens; ++i) {
+      const uint64_t key = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(sh.token[i] >> 32)) << 32 |
+                           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)sh.token[i]);
+      if (!key) continue;
+      const uint32_t id = id_of(key);
+      const float g = value_of(ord_of(key));
+      uint32_t n = 0;
+      if (id > s.gid && id < s.gid + s.cols) {
+        each([&](uint32_t x, int h, uint32_t c) {
+          const float l = as_float(x, h);
+          n += (uint32_t)__popcll(__ballot(l > g || (l == g && s.gid + c < id)));
+        });
+      } else {
+        // equal ones come before it where their ids do
+        const float from = id > s.gid ? g : above(g);
+        each([&](uint32_t x, int h, uint32_t) { n += (uint32_t)__popcll(__ballot(as_float(x, h) >= from)); });
+      }
+      if (lane == 0 && n) atomicAdd(&sh.rank[i], n);
+    }
+
+    // 4. The weights.  Elements equal to the largest are taken out and counted.
+    if (own == (int)o || !plain) {
+      uint32_t n = 0, first = 0xFFFFFFFFu;
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x = w[r][q];
+          const bool lo = as_float(x, 0) == m, hi = as_float(x, 1) == m;
+          n += lo + hi;
+          first = min(first, lo || hi ? 8 * (r * kThreads + tid) + 2 * q + (lo ? 0 : 1) : 0xFFFFFFFFu);
+          x = lo ? (x & 0xFFFF0000u) | (kMasked & 0xFFFFu) : x;
+          w[r][q] = hi ? (x & 0xFFFFu) | (kMasked & 0xFFFF0000u) : x;
+        }
+      atomicAdd(&sh.equal, n);
+      atomicMin(&sh.first, first);
+    }
+    double rest = 0, wx = 0;
+    const float c = 1.4426950408889634f / T;
+    if (greedy || __builtin_isinf(m)) {
+      // all weight is the largest elements'
+    } else if (__builtin_fabsf(m) * c <= 0x1p20f && c <= 0x1p64f) {
+      const float mc = m * c;
+      float sum_w = 0, sum_wt = 0;
+      each([&](uint32_t x, int h, uint32_t) {
+        // what is masked or NaN, and what is 2^-200 or less, has no weight
+        const float t = fmaxf(fmaf(as_float(x, h), c, -mc), -200.0f);
+        const float e = __builtin_amdgcn_exp2f(t);
+        sum_w += e;
+        sum_wt = fmaf(e, t, sum_wt);
+      });
+      const double off = (double)mc - (double)m * (double)c;  // t is too small by this
+      const double f = exp2(off);
+      rest = sum_w * f;
+      wx = f * ((double)sum_wt + off * sum_w) * 0.6931471805599453;
+    } else {
+      again([&](uint32_t v, uint32_t) {
+        if (!ord(v) || as_float(v, 0) == m) return;
+        const double t = scaled(as_float(v, 0), m, T), e = exp(t);
+        if (e > 0) rest += e, wx += e * t;
+      });
+    }
+    rest = wave_sum(rest);
+    wx = wave_sum(wx);
+    if (lane == 0) sh.wave_rest[wave] = rest, sh.wave_wx[wave] = wx;
+    __syncthreads();
+    if (tid == 0) {
+      Sum one = {(double)sh.equal - 1.0, 0, key_of(o, s.gid + sh.first)};
+      for (int i = 0; i < kWaves; ++i) one.rest += sh.wave_rest[i], one.wx += sh.wave_wx[i];
+      total = greedy ? (one.top > total.top ? one : total) : join(total, one, T);
+    }
+    // The best of what is listed.
+    if (a.n_top) {
+      const uint32_t n = sh.listed;
+      if (n <= kList) {
+        for (uint32_t i = tid; i < n; i += kThreads) {
+          const uint64_t key = sh.list[i];
+          uint32_t before = 0;
+          for (uint32_t j = 0; j < n; ++j) before += sh.list[j] > key;
+          if (key && before < a.n_top) sh.best[before] = key;
+        }
+      } else {
+        // Very many equal elements, or few lanes with all of them: one after
+        // the other, the largest below the one before.
+        uint64_t below = ~0ull;
+        for (uint32_t i = 0; i < a.n_top; ++i) {
+          uint64_t key = tid < a.n_top && sh.list[tid] < below ? sh.list[tid] : 0;
+          again([&](uint32_t v, uint32_t c) {
+            const uint64_t y = key_of(ord(v), s.gid + c);
+            if (y < below && y > key) key = y;
+          });
+          key = wave_max(key);
+          __syncthreads();
+          if (lane == 0) sh.wave_key[wave] = key;
+          __syncthreads();
+          for (int j = 0; j < kWaves; ++j) key = max(key, sh.wave_key[j]);
+          below = key;
+          if (tid == 0) sh.best[i] = key;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (a.parts > 1) {
+    const uint64_t at = (uint64_t)row * a.parts + part;
+    if (tid == 0) static_cast<Sum *>(a.sums)[at] = total;
+    if (tid < a.n_tokens) a.ranks[at * a.n_tokens + tid] = sh.rank[tid];
+    if (tid < a.n_top) a.keys[at * a.n_top + tid] = sh.best[tid];
+    return;
+  }
+  __shared__ Sum all;
+  if (tid == 0) all = total;
+  __syncthreads();
+  finish(a, row, all, T, sh.rank, sh.best);
+}
+
+// One wave for each row.
+__global__ __launch_bounds__(64) void logprobs_fold_kernel(LogprobArgs a) {
+  __shared__ uint32_t rank[kMaxTokens];
+  __shared__ uint64_t best[kMaxTop];
+  const uint32_t row = blockIdx.x, lane = threadIdx.x;
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  const uint64_t at = (uint64_t)row * a.parts;
+  Sum s = {0, 0, 0};
+  for (uint32_t p = lane; p < a.parts; p += 64) {
+    const Sum b = static_cast<const Sum *>(a.sums)[at + p];
+    s = T > 0.0f ? join(s, b, T) : b.top > s.top ? b : s;
+  }
+#pragma unroll 1
+  for (int d = 1; d < 64; d *= 2) {
+    Sum b;
+    b.rest = __shfl_xor(s.rest, d);
+    b.wx = __shfl_xor(s.wx, d);
+    b.top = __shfl_xor((unsigned long long)s.top, d);
+    s = T > 0.0f ? join(s, b, T) : b.top > s.top ? b : s;
+  }
+  for (uint32_t i = 0; i < a.n_tokens; ++i) {
+    uint32_t n = 0;
+    for (uint32_t p = lane; p < a.parts; p += 64) n += a.ranks[(at + p) * a.n_tokens + i];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+    if (lane == 0) rank[i] = n;
+  }
+  // The parts' lists are in order: each lane shows the first of its two.
+  uint32_t used[2] = {0, 0};
+  auto head = [&](uint32_t j) -> uint64_t {
+    const uint32_t p = lane + 64 * j;
+    return p < a.parts && used[j] < a.n_top ? a.keys[(at + p) * a.n_top + used[j]] : 0;
+  };
+  uint64_t h[2] = {a.n_top ? head(0) : 0, a.n_top ? head(1) : 0};
+  for (uint32_t i = 0; i < a.n_top; ++i) {
+    const uint64_t key = wave_max(max(h[0], h[1]));
+    if (lane == 0) best[i] = key;
+#pragma unroll
+    for (uint32_t j = 0; j < 2; ++j)
+      if (key && h[j] == key) {
+        ++used[j];
+        h[j] = head(j);
+      }
+  }
+  __syncthreads();
+  finish(a, row, s, T, rank, best);
+}
+
+struct Shape {
+  uint32_t parts, slices[2], width[2];
+};
+Shape shape_of(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
+  // As many parts as give kWorkgroups, of at least kMinCols.
+  const uint64_t cols = (uint64_t)ncols0 + ncols1;
+  uint64_t want = rows < kWorkgroups ? (kWorkgroups + rows - 1) / rows : 1;
+  want = want < kMaxParts - 1 ? want : kMaxParts - 1;
+  uint64_t width = (cols + want - 1) / want;
+  width = width < kMinCols ? kMinCols : width > kSliceCols ? kSliceCols : (width + 7) / 8 * 8;
+  Shape s{};
+  const uint32_t n[2] = {ncols0, ncols1};
+  for (int i = 0; i < 2; ++i) {
+    s.slices[i] = (uint32_t)((n[i] + width - 1) / width);
+    s.width[i] = (uint32_t)(((n[i] + s.slices[i] - 1) / s.slices[i] + 7) / 8 * 8);
+  }
+  const uint64_t slices = (uint64_t)s.slices[0] + s.slices[1];
+  s.parts = (uint32_t)(want < slices ? want : slices);
+  return s;
+}
+
+uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+uint64_t logprobs_workgroups(uint32_t rows, uint32_t ncols0, uint32_t ncols1) {
+  return (uint64_t)rows * shape_of(rows, ncols0, ncols1).parts;
+}
+
+// Layout: the parts' sums, their best elements, their ranks.
+uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1, uint32_t n_tokens, uint32_t n_top) {
+  const Shape s = shape_of(rows, ncols0, ncols1);
+  if (s.parts == 1) return 0;
+  const uint64_t n = (uint64_t)rows * s.parts;
+  return up16(n * sizeof(Sum)) + up16(n * n_top * 8) + up16(n * n_tokens * 4);
+}
+
+hipError_t launch_logprobs(const LogprobArgs &in, void *workspace, hipStream_t stream) {
+  LogprobArgs a = in;
+  const Shape s = shape_of(a.rows, a.s[0].ncols, a.s[1].ncols);
+  a.parts = s.parts;
+  for (int i = 0; i < 2; ++i) a.slices[i] = s.slices[i], a.width[i] = s.width[i];
+  if (s.parts > 1) {
+    const uint64_t n = (uint64_t)a.rows * s.parts;
+    uint8_t *at = static_cast<uint8_t *>(workspace);
+    a.sums = at;
+    a.keys = reinterpret_cast<uint64_t *>(at += up16(n * sizeof(Sum)));
+    a.ranks = reinterpret_cast<uint32_t *>(at + up16(n * a.n_top * 8));
+  }
+  const hipError_t e = launch(logprobs_kernel, dim3(a.rows * s.parts), dim3(kThreads), 0, stream, a);
+  if (e != hipSuccess || s.parts == 1) return e;
+  return launch(logprobs_fold_kernel, dim3(a.rows), dim3(64), 0, stream, a);
+}
+
+}  // namespace xfer

@@ -18,10 +18,13 @@ KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
 EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged", "xfer_kv_record_bytes",
-            "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge"]
+            "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge",
+            "xfer_logprobs_workspace_bytes", "xfer_logprobs_merge"]
 
 SAMPLE_PARAMS = np.dtype([("temperature", "<f4"), ("top_k", "<u4"), ("top_p", "<f4"), ("min_p", "<f4")])
 SAMPLED = np.dtype([("prob", "<f4"), ("idx", "<i4")])
+TOKEN_LOGPROB = np.dtype([("logprob", "<f4"), ("rank", "<i4")])
+TOP_LOGPROB = np.dtype([("logprob", "<f4"), ("idx", "<i4")])
 
 
 class KVCacheC(ctypes.Structure):
@@ -78,6 +81,10 @@ def lib():
         L.xfer_sample_workspace_bytes.restype = S
         L.xfer_sample_merge.argtypes = [ctypes.POINTER(Shard), ctypes.POINTER(Shard), P, P, P, P, S, P]
         L.xfer_sample_merge.restype = I
+        L.xfer_logprobs_workspace_bytes.argtypes = [U32, U32, U32, U32, U32]
+        L.xfer_logprobs_workspace_bytes.restype = S
+        L.xfer_logprobs_merge.argtypes = [ctypes.POINTER(Shard), ctypes.POINTER(Shard), P, P, U32, U32, P, P, P, P, S, P]
+        L.xfer_logprobs_merge.restype = I
         _lib = L
     return _lib
 
@@ -345,3 +352,56 @@ def sample_merge_raw(s0: Shard, s1: Shard, params_ptr: int, u_ptr: int, out_ptr:
     """Raw-pointer form; returns the status without raising."""
     return lib().xfer_sample_merge(ctypes.byref(s0), ctypes.byref(s1), params_ptr, u_ptr, out_ptr, ws_ptr, ws_bytes,
                                    _stream(stream))
+
+
+# --------------------------------------------------------- log probabilities
+
+def logprobs_workspace_bytes(rows: int, ncols0: int, ncols1: int, n_tokens: int, n_top: int) -> int:
+    return int(lib().xfer_logprobs_workspace_bytes(rows, ncols0, ncols1, n_tokens, n_top))
+
+
+def logprobs_merge(s0: Shard, s1: Shard, tokens, token_out, top_out, entropy, workspace, temperature=None,
+                   stream=None) -> None:
+    """tokens: int32 [rows, n_tokens]; token_out: CUDA tensor of rows * n_tokens *
+    8 bytes (TOKEN_LOGPROB records); top_out: one of rows * n_top * 8 bytes
+    (TOP_LOGPROB records), its size says n_top; entropy: F32[rows]; each of the
+    four may be None; workspace: at least logprobs_workspace_bytes() bytes
+    (None if that is 0); temperature: F32[rows] (None: 1)."""
+    given = [t for t in (tokens, token_out, top_out, entropy) if t is not None]
+    if not given:
+        raise ValueError("no output asked for")
+    dev, rows = given[0].get_device(), s0.rows
+    stream = _stream_on(dev, stream)
+    # a shard made from a pointer alone does not say where it lies
+    if getattr(s0, "device", dev) != dev or getattr(s1, "device", dev) != dev:
+        raise ValueError(f"expected shards on cuda:{dev}, where the outputs are")
+    n_tokens = 0
+    if tokens is not None or token_out is not None:
+        if tokens is None or token_out is None or tokens.dim() != 2 or tokens.shape[0] != rows:
+            raise ValueError("tokens must be [rows, n_tokens], with a token_out")
+        n_tokens = tokens.shape[1]
+        if token_out.numel() * token_out.element_size() != rows * n_tokens * 8:
+            raise ValueError("token_out must have 8 bytes for each token")
+    n_top, left = divmod(top_out.numel() * top_out.element_size(), max(rows, 1) * 8) if top_out is not None else (0, 0)
+    if left:
+        raise ValueError("top_out must have the same number of 8-byte records for each row")
+    for t in (entropy, temperature):
+        if t is not None and t.numel() != rows:
+            raise ValueError("entropy and temperature must have one number for each row")
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws_bytes, ws = workspace.numel() * workspace.element_size(), _flat(workspace, None, dev, "workspace")
+    status = lib().xfer_logprobs_merge(ctypes.byref(s0), ctypes.byref(s1), _flat(temperature, _F32, dev, "temperature"),
+                                       _flat(tokens, _INT32, dev, "tokens"), n_tokens, n_top,
+                                       _flat(token_out, None, dev, "token_out"), _flat(top_out, None, dev, "top_out"),
+                                       _flat(entropy, _F32, dev, "entropy"), ws, ws_bytes, stream)
+    if status != OK:
+        _check(status, "xfer_logprobs_merge")
+
+
+def logprobs_merge_raw(s0: Shard, s1: Shard, temperature_ptr: int, tokens_ptr: int, n_tokens: int, n_top: int,
+                       token_out_ptr: int, top_out_ptr: int, entropy_ptr: int, ws_ptr: int, ws_bytes: int,
+                       stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_logprobs_merge(ctypes.byref(s0), ctypes.byref(s1), temperature_ptr, tokens_ptr, n_tokens, n_top,
+                                     token_out_ptr, top_out_ptr, entropy_ptr, ws_ptr, ws_bytes, _stream(stream))

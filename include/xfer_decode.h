@@ -13,6 +13,8 @@
  *   xfer_sample_merge    sampling with temperature, top-k, top-p and min-p
  *                        from logits in two column shards, beside
  *                        xfer_argmax_merge
+ *   xfer_logprobs_merge  log probabilities of given tokens, the best
+ *                        alternatives and the entropy from such shards
  *
  * The caches are the ones that xfer_gather_runs, xfer_scatter_runs and
  * xfer_paged_copy move.  All conventions of xfer.h hold (host checks first,
@@ -341,6 +343,68 @@ XFER_API size_t xfer_sample_workspace_bytes(uint32_t rows, uint32_t ncols0, uint
 XFER_API int xfer_sample_merge(const xfer_shard *s0, const xfer_shard *s1, const xfer_sample_params *params,
                                const float *u, void *out, void *workspace, size_t workspace_bytes,
                                hipStream_t stream);
+
+/* ------------------------------------------------------ log probabilities */
+
+typedef struct {
+  float logprob; /* of the given token                                         */
+  int32_t rank;  /* how many elements of the row's order come before it, -1 if
+                    it is not in it                                           */
+} xfer_token_logprob; /* 8 bytes */
+
+typedef struct {
+  float logprob;
+  int32_t idx; /* the element's global id, -1 past the end of the row's order */
+} xfer_top_logprob; /* 8 bytes */
+
+/*
+ * xfer_logprobs_merge - for every row of a block of logit rows split by columns
+ * between two ranks: the log probabilities of given tokens and their ranks,
+ * the first elements of the row's order with theirs, and the entropy.
+ *
+ * Row order and weights are those of xfer_sample_merge without filters: larger
+ * value first (numeric, -0 == +0), then the lower global id; elements that are
+ * -inf or NaN are not in the order and count nowhere; with l_0 the first
+ * element and T the row's temperature,
+ *   x_i = (l_i - l_0) / T    (0 where l_i == l_0, infinite ones included, and
+ *                             -inf for all others where l_0 is +inf)
+ *   Z = sum_i exp(x_i)       logprob_i = x_i - log Z
+ *   entropy = log Z - sum_i exp(x_i) x_i / Z             (in nats)
+ * A token that is not in the order (masked, or an id of neither shard) has
+ * logprob -inf and rank -1.  A row without any element in its order has
+ * entropy 0.  T not above 0, or NaN (greedy): the first element has all the
+ * weight, logprob 0, every other one -inf, and the entropy is 0.
+ *
+ * Weights are computed in binary32, and summed in binary32 over up to 64
+ * elements, in binary64 from there on; Z is held as 1 + the weights of all
+ * but the first element, so that a logprob near 0 keeps its own digits.
+ * Results are rounded to binary32 once.
+ *
+ *   temperature (device) F32[rows]; NULL: 1 for all.
+ *   tokens      (device) int32[rows][n_tokens], global ids; n_tokens up to 16.
+ *   token_out   (device) xfer_token_logprob[rows][n_tokens], 8-byte aligned.
+ *   top_out     (device) xfer_top_logprob[rows][n_top], 8-byte aligned, in the
+ *               row's order; n_top up to 32.
+ *   entropy     (device) F32[rows]; may be NULL.
+ *   workspace   (device) at least xfer_logprobs_workspace_bytes() bytes,
+ *               16-byte aligned, any contents.  May be NULL if that is 0.
+ *               Calls that may run concurrently must use different workspaces.
+ * tokens and token_out are not used if n_tokens is 0, nor top_out if n_top is.
+ *
+ * Errors: those of the shards in xfer_sample_merge; XFER_E_INVAL for NULL or
+ * misaligned pointers (temperature, tokens and entropy 4 bytes), a small
+ * workspace, or an output or workspace overlapping an input or one another;
+ * XFER_E_UNSUPPORTED for more tokens or alternatives than stated, a shard wider
+ * than 2,097,152 columns or more than 2^24 - 1 workgroups (a row each, or up to
+ * 127 where rows are few).
+ * xfer_logprobs_workspace_bytes: 0 also for sizes that the call refuses.
+ */
+XFER_API size_t xfer_logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols1, uint32_t n_tokens,
+                                              uint32_t n_top);
+XFER_API int xfer_logprobs_merge(const xfer_shard *s0, const xfer_shard *s1, const float *temperature,
+                                 const int32_t *tokens, uint32_t n_tokens, uint32_t n_top, void *token_out,
+                                 void *top_out, float *entropy, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
 
 #ifdef __cplusplus
 }
