@@ -1,0 +1,456 @@
+// Attention of one new token over a paged cache for rows in groups that begin
+// with the same tokens: what a group shares is read once for all its rows.
+//
+// A softmax over a row's tokens splits into sums over any parts of them, each
+// with a maximum of its own, so a row is its group's shared tokens and the
+// rest of its own, and three steps make it up:
+//   1. plan: one workgroup turns the groups and lengths into two lists of
+//      entries, a run of tokens with the query heads that see all of it: a row's
+//      own tokens with its heads, a group's shared tokens with the heads of
+//      all its rows.  Rows that do not see all of the shared tokens are kept
+//      out of them and read theirs alone, so no entry needs a mask;
+//   2. walk: the entries' units (128 tokens of a kv head and up to 16 or 32
+//      query heads) are one line that is cut into equal runs, as the attention
+//      of one token cuts its rows, and with the same walk;
+//   3. join: a workgroup for each (row, query head) scales the parts of the
+//      shared tokens and of the row's own to the largest maximum and adds
+//      them up, in a fixed order.
+#include "attn_tile.h"
+
+namespace xfer {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr uint32_t kUnit = kTile * kWaves;       // tokens of a unit
+constexpr uint32_t kComputeUnits = 256;
+constexpr uint32_t kMaxParts = 2 * 2 * kComputeUnits;  // of a (row, query head)
+constexpr uint32_t kXcds = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, since the memory bounds the walk
+
+// ------------------------------------------------------------------- plan
+
+__device__ __forceinline__ uint64_t entry_units(const SharedArgs &a, const SharedEntry &e) {
+  const uint64_t heads = (uint64_t)e.q_rows * a.group;
+  return (uint64_t)((e.n + kUnit - 1) / kUnit) * a.cache.kv_heads * ((heads + a.tile - 1) / a.tile);
+}
+
+// Inclusive scans over the threads of the plan's workgroup.
+template <typename T, typename F>
+__device__ __forceinline__ T block_scan(T x, T *waves, F &&op) {
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const T y = __shfl_up(x, d);
+    if ((int)lane >= d) x = op(y, x);
+  }
+  __syncthreads();
+  if (lane == 63) waves[wave] = x;
+  __syncthreads();
+  T before = waves[0];
+  for (uint32_t w = 1; w < wave; ++w) before = op(before, waves[w]);
+  return wave ? op(before, x) : x;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a) {
+  __shared__ uint32_t start[kMaxGroups + 1], prefix[kMaxGroups];
+  __shared__ unsigned long long waves[kPlanThreads / 64];
+  const uint32_t tid = threadIdx.x;
+  // The groups' first rows: a start below the one before counts as that one,
+  // so that no row is in two groups, whatever the caller's numbers are.
+  {
+    const uint32_t n = a.groups + 1, each = (n + kPlanThreads - 1) / kPlanThreads;
+    const uint32_t i0 = min(tid * each, n), i1 = min(i0 + each, n);
+    uint32_t top = 0;
+    auto given = [&](uint32_t i) { return a.groups ? min(a.starts[i], a.rows) : a.rows; };
+    for (uint32_t i = i0; i < i1; ++i) top = max(top, given(i));
+    auto *w = reinterpret_cast<uint32_t *>(waves);
+    uint32_t mine = block_scan(top, w, [](uint32_t x, uint32_t y) { return max(x, y); });
+    // what comes before this thread's: the inclusive result of the thread before
+    const uint32_t before = __shfl_up(mine, 1);
+    uint32_t run = tid % 64 ? before : 0;
+    if (tid % 64 == 0)
+      for (uint32_t i = 0; i < tid / 64; ++i) run = max(run, w[i]);
+    for (uint32_t i = i0; i < i1; ++i) {
+      run = max(run, given(i));
+      start[i] = run;
+    }
+  }
+  __syncthreads();
+  for (uint32_t g = tid; g < a.groups; g += kPlanThreads) {
+    const uint32_t row = start[g], n = start[g + 1] - row;
+    uint32_t p = n > 1 ? min(a.shared[g], a.max_len) : 0;
+    if (p) p = min(p, a.lens[row]);  // the first row's pages are read
+    prefix[g] = p;
+  }
+  __syncthreads();
+  const uint32_t n = a.rows + a.groups, each = (n + kPlanThreads - 1) / kPlanThreads;
+  const uint32_t i0 = min(tid * each, n), i1 = min(i0 + each, n);
+  auto entry = [&](uint32_t i) {
+    SharedEntry e{};
+    if (i < a.rows) {
+      uint32_t lo = 0, hi = a.groups + 1;  // the first start past row i
+      while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (start[mid] <= i)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      const uint32_t len = min(a.lens[i], a.max_len);
+      const bool in = lo > 0 && lo <= a.groups;
+      const uint32_t p = in ? prefix[lo - 1] : 0;
+      e.first = p <= len ? p : 0;
+      e.n = len - e.first;
+      e.row = e.q_row = i;
+      e.q_rows = 1;
+      e.group = e.first ? lo - 1 : kNoGroup;
+    } else {
+      const uint32_t g = i - a.rows;
+      e.n = prefix[g];
+      e.row = e.q_row = start[g];
+      e.q_rows = e.n ? start[g + 1] - start[g] : 0;
+      e.group = g;
+    }
+    return e;
+  };
+  uint64_t units = 0, tiles = 0;
+  for (uint32_t i = i0; i < i1; ++i) {
+    const SharedEntry e = entry(i);
+    units += entry_units(a, e);
+    tiles += ((uint64_t)e.q_rows * a.group + a.tile - 1) / a.tile;
+  }
+  auto add = [](unsigned long long x, unsigned long long y) { return x + y; };
+  uint64_t unit0 = block_scan((unsigned long long)units, waves, add) - units;
+  uint64_t tile0 = block_scan((unsigned long long)tiles, waves, add) - tiles;
+  for (uint32_t i = i0; i < i1; ++i) {
+    SharedEntry e = entry(i);
+    e.unit0 = unit0;
+    e.part0 = (uint32_t)(tile0 * a.cache.kv_heads);
+    a.entries[i] = e;
+    unit0 += entry_units(a, e);
+    tile0 += ((uint64_t)e.q_rows * a.group + a.tile - 1) / a.tile;
+  }
+  if (i0 < n && i1 == n) {
+    SharedEntry e{};
+    e.unit0 = unit0;
+    a.entries[n] = e;
+  }
+}
+
+// ------------------------------------------------------------------- walk
+
+// What a (entry, kv head, tile of heads) that fell to several workgroups leaves:
+// its first part's slot (kWhole: one workgroup did it all), and how many parts.
+constexpr uint32_t kWhole = 0xFFFFFFFFu;
+
+template <int D, int KIND, int TILES>
+__global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void shared_walk_kernel(SharedArgs a) {
+  using L = Layout<D, KIND>;
+  using R = Residence<D, KIND, TILES>;
+  constexpr int MR = TILES, kPad = 4;
+  constexpr uint32_t kHeads = 16 * TILES;
+  __shared__ float lds_o[kWaves][16][D + kPad];
+  __shared__ float lds_all_m[MR][kWaves][16], lds_all_l[MR][kWaves][16];
+  __shared__ uint32_t start;
+  const uint32_t n_entries = a.rows + a.groups;
+  // Neighbouring runs on one XCD: its L2 then serves the tokens that the heads
+  // of an entry have in common.
+  const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  const uint64_t all = a.entries[n_entries].unit0, per = (all + gridDim.x - 1) / gridDim.x, from = wg * per;
+  if (from >= all) return;
+  uint64_t left = min(per, all - from);
+  for (uint32_t i = threadIdx.x; i < n_entries; i += kThreads)
+    if (a.entries[i].unit0 <= from && from < a.entries[i + 1].unit0) start = i;
+  __syncthreads();
+  uint32_t index = __builtin_amdgcn_readfirstlane(start);
+  SharedEntry e = a.entries[index];
+  uint64_t at = from - e.unit0;
+
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16,
+                 g = lane / 16;
+  // The queries, in the lanes' order, where the exchange lies later.
+  v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
+  static_assert(!R::kQInLds || MR * L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
+  bool first_segment = true;
+
+#pragma unroll 1
+  while (left) {
+    const uint32_t heads = e.q_rows * a.group, m_groups = (heads + kHeads - 1) / kHeads;
+    const uint32_t units = (e.n + kUnit - 1) / kUnit, inner_n = m_groups * a.cache.kv_heads;
+    uint32_t inner = __builtin_amdgcn_readfirstlane((uint32_t)(at / units));
+    uint32_t unit = __builtin_amdgcn_readfirstlane((uint32_t)(at % units));
+#pragma unroll 1
+    for (; inner < inner_n && left; ++inner, unit = 0) {
+      const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
+      const uint32_t kvh = inner / m_groups, h0 = inner % m_groups * kHeads;
+      const uint32_t v0 = unit * kUnit, v1 = min((unit + take) * kUnit, e.n);
+      const Visible vis{e.n, 0, e.first};
+      // Q: query head h0 + 16 * r + n of the entry, the dims that this lane's K loads hold.
+      v4u q[R::kQInLds ? 1 : MR][L::kMfmaK];
+      auto load_q = [&](int r, int k) {
+        const uint32_t h = h0 + 16 * r + n;
+        const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
+        if (h >= heads) return v4u{0, 0, 0, 0};
+        return *reinterpret_cast<const v4u *>(a.q + (e.q_row + h / a.group) * a.q_ld +
+                                              (uint64_t)(kvh * a.group + h % a.group) * D + d);
+      };
+      if constexpr (R::kQInLds) {
+        for (int k = wave; k < MR * L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k / L::kMfmaK, k % L::kMfmaK);
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int r = 0; r < MR; ++r)
+#pragma unroll
+          for (int k = 0; k < L::kMfmaK; ++k) q[r][k] = load_q(r, k);
+      }
+      float scale2 = a.scale * 1.4426950408889634f;
+      if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
+      const uint32_t *table = a.page_table + e.row * a.table_ld;
+      v4f o[MR][L::kMfmaV];
+      float mx[MR], sum[MR];
+      attn_walk<D, KIND, MR, kParts, kUnit, false>(a.cache, kvh, table, vis, v0 + wave * kTile, v1, scale2, n, g, lane, q,
+                                                   lds_q, o, mx, sum);
+
+      // The waves' results, joined in LDS.
+      const bool whole = take == units;
+      const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
+      if (unit == 0 && tid == 0)
+        a.parts[e.part0 + inner] = whole ? SharedParts{kWhole, 1} : SharedParts{slot, 1 + (uint32_t)((units - take + per - 1) / per)};
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+        sum[r] += __shfl_xor(sum[r], 16);
+        sum[r] += __shfl_xor(sum[r], 32);
+        if (g == 0) {
+          lds_all_m[r][wave][n] = mx[r];
+          lds_all_l[r][wave][n] = sum[r];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
+        auto &lds_m = lds_all_m[r];
+        auto &lds_l = lds_all_l[r];
+        if (r) __syncthreads();
+        {
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
+          const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - top);
+#pragma unroll
+          for (int j = 0; j < L::kMfmaV; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[r][j][i] * f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t i = tid; i < 4 * D; i += kThreads) {
+          const uint32_t hq = i / (D / 4), d = i % (D / 4) * 4, h = h0 + 16 * r + hq;
+          if (h >= heads) continue;
+          float top = -INFINITY, total = 0;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
+          v4f v = {0, 0, 0, 0};
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float mw = lds_m[w][hq];
+            total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
+            v += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
+          }
+          if constexpr (KIND == XFER_KV_BF16) {
+            if (isnan(v.x + v.y + v.z + v.w)) v = with_infinities<KIND>(a.cache, kvh, table, vis, v0, v1, v, d);
+          }
+          // a whole one's place is its row's and head's, in the half for shared or own tokens
+          const uint64_t mine = (uint64_t)(e.q_row + h / a.group) * a.q_heads + kvh * a.group + h % a.group;
+          const uint64_t to = whole ? a.whole0 + (index < a.rows ? 0 : (uint64_t)a.rows * a.q_heads) + mine
+                                    : (uint64_t)slot * kHeads + 16 * r + hq;
+          *reinterpret_cast<v4f *>(a.part_o + to * D + d) = v;
+          if (d == 0) {
+            a.part_ml[2 * to] = top;
+            a.part_ml[2 * to + 1] = total;
+          }
+        }
+      }
+      left -= take;
+      first_segment = false;
+      if (left) __syncthreads();  // LDS is written again
+    }
+    at = 0;
+    if (left) {
+      do e = a.entries[++index];
+      while (e.n == 0);  // there is one with tokens as long as units are left
+    }
+  }
+}
+
+// ------------------------------------------------------------------- join
+
+// One workgroup for each (row, query head): its parts of the shared tokens, then
+// of its own.
+template <int D>
+__global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
+  constexpr uint32_t kLanes = D / 4, kAtOnce = kThreads / kLanes;
+  constexpr int kEach = kMaxParts / kThreads;  // parts of a thread
+  __shared__ float lds_w[kMaxParts];
+  __shared__ float lds_red[2][kWaves];
+  __shared__ v4f lds_o[kAtOnce][kLanes];
+  const uint32_t row = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads, tid = threadIdx.x;
+  const uint32_t kvh = head / a.group, h = head % a.group;
+  const SharedEntry own = a.entries[row];
+  struct Source {
+    uint32_t n;                 // parts
+    uint64_t at0, at1, stride;  // places: part 0's; part p's at1 + p * stride
+  };
+  auto source = [&](const SharedEntry &e, bool prefix) {
+    Source s{};
+    if (!e.n) return s;
+    const uint32_t heads = e.q_rows * a.group, m_groups = (heads + a.tile - 1) / a.tile;
+    const uint32_t i = (row - e.q_row) * a.group + h;
+    const SharedParts p = a.parts[e.part0 + kvh * m_groups + i / a.tile];
+    s.n = p.n;
+    if (p.slot == kWhole) {
+      s.at0 = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
+    } else {
+      // Part p > 0 is the first thing that the workgroup p further on did.
+      s.at0 = (uint64_t)p.slot * a.tile + i % a.tile;
+      s.at1 = (uint64_t)(p.slot / 2 * 2) * a.tile + i % a.tile;
+      s.stride = 2 * a.tile;
+    }
+    return s;
+  };
+  Source pre{};
+  if (own.group != kNoGroup) pre = source(a.entries[a.rows + own.group], true);
+  const Source mine = source(own, false);
+  const uint32_t n = pre.n + mine.n;
+  auto place = [&](uint32_t p) -> uint64_t {
+    const Source &s = p < pre.n ? pre : mine;
+    const uint32_t k = p < pre.n ? p : p - pre.n;
+    return k ? s.at1 + k * s.stride : s.at0;
+  };
+
+  float m[kEach], l[kEach], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t p = i * kThreads + tid;
+    m[i] = -INFINITY;
+    l[i] = 0;
+    if (p < n) {
+      const uint64_t at = place(p);
+      m[i] = a.part_ml[2 * at];
+      l[i] = a.part_ml[2 * at + 1];
+    }
+    top = fmaxf(top, m[i]);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if (tid % 64 == 0) lds_red[0][tid / 64] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(lds_red[0][0], lds_red[0][1]), fmaxf(lds_red[0][2], lds_red[0][3]));
+  float total = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t p = i * kThreads + tid;
+    const float f = m[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
+    // not 0: a part's infinity stays one, however small its weights
+    if (p < n) lds_w[p] = f == 0.0f ? __uint_as_float(1) : f;
+    total += m[i] == -INFINITY ? l[i] : l[i] * f;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+  if (tid % 64 == 0) lds_red[1][tid / 64] = total;
+  __syncthreads();
+  const uint32_t d4 = tid % kLanes, p0 = tid / kLanes;
+  v4f r = {0, 0, 0, 0};
+#pragma unroll 4
+  for (uint32_t p = p0; p < n; p += kAtOnce) r += lds_w[p] * *reinterpret_cast<const v4f *>(a.part_o + place(p) * D + 4 * d4);
+  lds_o[p0][d4] = r;
+  __syncthreads();
+  if (p0 != 0) return;
+#pragma unroll
+  for (uint32_t s = 1; s < kAtOnce; ++s) r += lds_o[s][d4];
+  total = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
+  const float v_scale = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
+  r = total == 0.0f ? v4f{0, 0, 0, 0} : r * (v_scale / total);
+  const uint64_t at = row * a.out_ld + (uint64_t)head * D + 4 * d4;
+  if (a.out_mode == XFER_OUT_F32)
+    *reinterpret_cast<v4f *>(static_cast<float *>(a.out) + at) = r;
+  else
+    *reinterpret_cast<v2u *>(static_cast<uint16_t *>(a.out) + at) = v2u{bf16x2(r.x, r.y), bf16x2(r.z, r.w)};
+}
+
+// ----------------------------------------------------------------- launches
+
+template <int D, int KIND, int TILES>
+hipError_t launch_walk(const SharedArgs &a, uint32_t workgroups, hipStream_t stream) {
+  return launch(shared_walk_kernel<D, KIND, TILES>, dim3(workgroups), dim3(kThreads), 0, stream, a);
+}
+template <int D>
+hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, hipStream_t stream) {
+  hipError_t e = launch(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+  if (e != hipSuccess) return e;
+  if (kind == XFER_KV_BF16)
+    e = a.tile == 16 ? launch_walk<D, XFER_KV_BF16, 1>(a, workgroups, stream) : launch_walk<D, XFER_KV_BF16, 2>(a, workgroups, stream);
+  else
+    e = a.tile == 16 ? launch_walk<D, XFER_KV_E4M3, 1>(a, workgroups, stream) : launch_walk<D, XFER_KV_E4M3, 2>(a, workgroups, stream);
+  if (e != hipSuccess) return e;
+  return launch(shared_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a);
+}
+
+struct Shape {
+  uint32_t tile, workgroups;
+  uint64_t parts, places, whole0;  // (entry, kv head, tile)s at most; query heads of all parts; the first whole one's
+};
+template <int D, int KIND>
+uint32_t per_simd(uint32_t tile) {
+  return tile == 16 ? Residence<D, KIND, 1>::kPerSimd : Residence<D, KIND, 2>::kPerSimd;
+}
+template <int KIND>
+uint32_t per_simd(uint32_t head_dim, uint32_t tile) {
+  return head_dim == 64 ? per_simd<64, KIND>(tile) : head_dim == 128 ? per_simd<128, KIND>(tile) : per_simd<256, KIND>(tile);
+}
+Shape shape_of(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind) {
+  Shape s{};
+  // 32 heads at a time where a row or the average group has more than 16
+  s.tile = group > 16 || (groups && (uint64_t)rows * group > 16ull * groups) ? 32 : 16;
+  s.workgroups = kComputeUnits * (kind == XFER_KV_BF16 ? per_simd<XFER_KV_BF16>(head_dim, s.tile)
+                                                       : per_simd<XFER_KV_E4M3>(head_dim, s.tile));
+  const uint64_t row_tiles = (group + s.tile - 1) / s.tile;
+  s.parts = kv_heads * (rows * row_tiles + (uint64_t)rows * group / s.tile + groups);
+  s.whole0 = 2ull * s.workgroups * s.tile;
+  s.places = s.whole0 + 2ull * rows * kv_heads * group;
+  return s;
+}
+uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind) {
+  return groups <= kMaxGroups && (uint64_t)rows * kv_heads * group <= kMaxGridBlocks &&
+         shape_of(rows, groups, kv_heads, group, head_dim, kind).parts <= UINT32_MAX;
+}
+
+// Layout: the entries, the parts of each (entry, kv head, tile), (max, sum) of each part, the weighted sums.
+uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
+                                int kind) {
+  const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
+  return up16(((uint64_t)rows + groups + 1) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
+         s.places * head_dim * 4;
+}
+
+hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStream_t stream) {
+  SharedArgs a = in;
+  const Shape s = shape_of(a.rows, a.groups, a.cache.kv_heads, a.group, a.cache.head_dim, kind);
+  a.tile = s.tile;
+  a.whole0 = s.whole0;
+  uint8_t *at = static_cast<uint8_t *>(workspace);
+  a.entries = reinterpret_cast<SharedEntry *>(at);
+  a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + a.groups + 1) * sizeof(SharedEntry)));
+  a.part_ml = reinterpret_cast<float *>(at += up16(s.parts * sizeof(SharedParts)));
+  a.part_o = reinterpret_cast<float *>(at + up16(s.places * 8));
+  if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s.workgroups, stream);
+  if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s.workgroups, stream);
+  return launch_dim<256>(a, kind, s.workgroups, stream);
+}
+
+}  // namespace xfer

@@ -58,6 +58,47 @@ struct AttnArgs {
 };
 hipError_t launch_attn(const AttnArgs &a, int kind, const AttnShape &s, hipStream_t stream);
 
+// ---- attention of rows with shared prefixes (attn_shared.hip)
+constexpr uint32_t kMaxGroups = 4096;
+constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
+// Tokens first .. first + n - 1 of a row's pages, seen by all query heads of
+// q_rows rows from q_row on: a row's own tokens, or a group's shared ones.
+struct SharedEntry {
+  uint64_t unit0;  // the first of its units, over all entries
+  uint32_t row, first, n, q_row, q_rows;
+  uint32_t part0;  // its first (kv head, tile of heads) among all entries'
+  uint32_t group;  // whose shared tokens the row also sees (kNoGroup: none)
+  uint32_t reserved;
+};
+static_assert(sizeof(SharedEntry) % 8 == 0, "entries lie one after the other");
+struct SharedParts {
+  uint32_t slot, n;
+};
+struct SharedArgs {
+  CacheView cache;
+  const uint32_t *page_table, *lens;
+  uint64_t table_ld;
+  uint32_t rows, max_len;
+  const uint32_t *starts, *shared;
+  uint32_t groups;
+  const uint16_t *q;
+  uint64_t q_ld, out_ld;
+  uint32_t q_heads, group;  // group = q_heads / kv_heads
+  float scale;
+  void *out;
+  int out_mode;
+  // set by the launch
+  uint32_t tile;  // query heads that a workgroup takes at a time
+  SharedEntry *entries;
+  SharedParts *parts;
+  float *part_ml, *part_o;
+  uint64_t whole0;  // the place of the first result that one workgroup has whole
+};
+bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind);
+uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
+                                int kind);
+hipError_t launch_shared(const SharedArgs &a, int kind, void *workspace, hipStream_t stream);
+
 // ---- a cache's slots as records for the wire, and back (kv_wire.hip)
 struct WireArgs {
   CacheView cache;

@@ -149,6 +149,42 @@ bool attn_launches(const xfer::AttnShape &s, uint64_t rows, uint32_t q_heads) {
   return s.workgroups <= xfer::kMaxGridBlocks && rows * q_heads <= xfer::kMaxGridBlocks;
 }
 
+// The pointers and row distances that attention's calls share.
+int attn_pointers(const xfer_kv_cache *c, const xfer_paged_batch *b, const void *q, uint64_t q_ld, const void *out,
+                  uint64_t out_ld, uint64_t row) {
+  const uint64_t R = b->rows, pages = ((uint64_t)b->max_len + c->page_tokens - 1) / c->page_tokens;
+  if (!b->page_table || !b->lens || (uintptr_t)b->page_table % 4 || (uintptr_t)b->lens % 4) return XFER_E_INVAL;
+  if (R > 1 && (b->table_ld < pages || b->table_ld > kMaxExtent / 4 || R - 1 > kMaxExtent / 4 / b->table_ld))
+    return XFER_E_INVAL;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !ld_ok(q_ld, R, row) || !ld_ok(out_ld, R, row))
+    return XFER_E_INVAL;
+  return XFER_OK;
+}
+
+// Whether the output or the workspace (w, need bytes) shares a byte with an
+// input, the cache, its scales or one another.
+bool attn_outputs_touch(const xfer_kv_cache *c, uint64_t extent, const Rows &o, uintptr_t w, uint64_t need,
+                        const Rows *ins, int n) {
+  for (int i = 0; i < n; ++i)
+    if (rows_touch(o, ins[i]) || overlaps(w, need, ins[i].at, ins[i].extent())) return true;
+  for (uintptr_t k : {(uintptr_t)c->k, (uintptr_t)c->v})
+    if (overlaps(k, extent, o.at, o.extent()) || overlaps(k, extent, w, need)) return true;
+  for (const float *scales : {c->k_scale, c->v_scale})
+    if (scales && (overlaps((uintptr_t)scales, c->kv_heads * 4ull, o.at, o.extent()) ||
+                   overlaps((uintptr_t)scales, c->kv_heads * 4ull, w, need)))
+      return true;
+  return overlaps(w, need, o.at, o.extent());
+}
+
+// The sizes of a call with shared prefixes.
+int shared_sizes(const xfer_kv_cache *c, const xfer_paged_batch *b, const xfer_prefix_groups *g, uint32_t q_heads) {
+  if (q_heads == 0 || q_heads % c->kv_heads || g->reserved) return XFER_E_INVAL;
+  if (b->max_len == 0 || b->max_len > 0x7FFFFFFFu || (b->sinks && !b->window)) return XFER_E_INVAL;
+  if (b->window || !xfer::shared_launches(b->rows, g->groups, c->kv_heads, q_heads / c->kv_heads, c->head_dim, c->kind))
+    return XFER_E_UNSUPPORTED;
+  return XFER_OK;
+}
+
 // The checks of two logit shards that xfer_sample_merge and xfer_logprobs_merge
 // share, up to their pointers'.
 int shard_checks(const xfer_shard *const (&s)[2]) {
@@ -315,12 +351,7 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   if (batch->rows == 0) return XFER_OK;
   const uint64_t R = batch->rows, row = (uint64_t)q_heads * cache->head_dim;
   const uint64_t pages = ((uint64_t)batch->max_len + cache->page_tokens - 1) / cache->page_tokens;
-  if (!batch->page_table || !batch->lens || (uintptr_t)batch->page_table % 4 || (uintptr_t)batch->lens % 4)
-    return XFER_E_INVAL;
-  if (R > 1 && (batch->table_ld < pages || batch->table_ld > kMaxExtent / 4 || R - 1 > kMaxExtent / 4 / batch->table_ld))
-    return XFER_E_INVAL;
-  if (!q || !out || !aligned16(q) || !aligned16(out) || !ld_ok(q_ld, R, row) || !ld_ok(out_ld, R, row))
-    return XFER_E_INVAL;
+  if ((st = attn_pointers(cache, batch, q, q_ld, out, out_ld, row)) != XFER_OK) return st;
   const uint64_t need = xfer::attn_workspace_bytes(s, batch->rows, cache->kv_heads, cache->head_dim);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return XFER_E_INVAL;
 
@@ -329,16 +360,7 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   const Rows ins[3] = {{(uintptr_t)q, q_ld * 2, row * 2, R},
                        {(uintptr_t)batch->page_table, batch->table_ld * 4, pages * 4, R},
                        {(uintptr_t)batch->lens, 4, 4, R}};
-  const uintptr_t w = (uintptr_t)workspace, caches[2] = {(uintptr_t)cache->k, (uintptr_t)cache->v};
-  for (const Rows &r : ins)
-    if (rows_touch(o, r) || overlaps(w, need, r.at, r.extent())) return XFER_E_INVAL;
-  for (uintptr_t c : caches)
-    if (overlaps(c, extent, o.at, o.extent()) || overlaps(c, extent, w, need)) return XFER_E_INVAL;
-  for (const float *scales : {cache->k_scale, cache->v_scale})
-    if (scales && (overlaps((uintptr_t)scales, cache->kv_heads * 4ull, o.at, o.extent()) ||
-                   overlaps((uintptr_t)scales, cache->kv_heads * 4ull, w, need)))
-      return XFER_E_INVAL;
-  if (overlaps(w, need, o.at, o.extent())) return XFER_E_INVAL;
+  if (attn_outputs_touch(cache, extent, o, (uintptr_t)workspace, need, ins, 3)) return XFER_E_INVAL;
   if (!attn_launches(s, R, q_heads)) return XFER_E_UNSUPPORTED;
 
   xfer::AttnArgs a{};
@@ -360,6 +382,65 @@ int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, c
   a.out_mode = out_mode;
   a.part_ml = static_cast<float *>(workspace);
   if (xfer::launch_attn(a, cache->kind, s, stream) != hipSuccess) return XFER_E_DEVICE;
+  return XFER_OK;
+}
+
+size_t xfer_attn_shared_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch,
+                                        const xfer_prefix_groups *groups, uint32_t q_heads) {
+  uint64_t extent = 0;
+  if (!batch || !groups || cache_checks(cache, &extent) != XFER_OK ||
+      shared_sizes(cache, batch, groups, q_heads) != XFER_OK || batch->rows == 0)
+    return 0;
+  return (size_t)xfer::shared_workspace_bytes(batch->rows, groups->groups, cache->kv_heads, q_heads / cache->kv_heads,
+                                              cache->head_dim, cache->kind);
+}
+
+int xfer_attn_shared(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const xfer_prefix_groups *groups,
+                     const uint16_t *q, uint64_t q_ld, uint32_t q_heads, float scale, void *out, uint64_t out_ld,
+                     int out_mode, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  uint64_t extent = 0;
+  int st = cache_checks(cache, &extent);
+  if (st != XFER_OK) return st;
+  if (!batch || !groups || (out_mode != XFER_OUT_F32 && out_mode != XFER_OUT_BF16) || !std::isfinite(scale))
+    return XFER_E_INVAL;
+  if ((st = shared_sizes(cache, batch, groups, q_heads)) != XFER_OK) return st;
+  if (batch->rows == 0) return XFER_OK;
+  const uint64_t R = batch->rows, G = groups->groups, row = (uint64_t)q_heads * cache->head_dim;
+  const uint64_t pages = ((uint64_t)batch->max_len + cache->page_tokens - 1) / cache->page_tokens;
+  if ((st = attn_pointers(cache, batch, q, q_ld, out, out_ld, row)) != XFER_OK) return st;
+  if (G && (!groups->starts || !groups->shared || (uintptr_t)groups->starts % 4 || (uintptr_t)groups->shared % 4))
+    return XFER_E_INVAL;
+  const uint64_t need = xfer::shared_workspace_bytes(batch->rows, groups->groups, cache->kv_heads,
+                                                     q_heads / cache->kv_heads, cache->head_dim, cache->kind);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return XFER_E_INVAL;
+  const uint64_t ob = out_mode == XFER_OUT_F32 ? 4 : 2;
+  const Rows o{(uintptr_t)out, out_ld * ob, row * ob, R};
+  const Rows ins[5] = {{(uintptr_t)q, q_ld * 2, row * 2, R},
+                       {(uintptr_t)batch->page_table, batch->table_ld * 4, pages * 4, R},
+                       {(uintptr_t)batch->lens, 4, 4, R},
+                       {(uintptr_t)groups->starts, 4, 4, G ? G + 1 : 0},
+                       {(uintptr_t)groups->shared, 4, 4, G}};
+  if (attn_outputs_touch(cache, extent, o, (uintptr_t)workspace, need, ins, 5)) return XFER_E_INVAL;
+
+  xfer::SharedArgs a{};
+  a.cache = view_of(cache);
+  a.page_table = batch->page_table;
+  a.lens = batch->lens;
+  a.table_ld = batch->table_ld;
+  a.rows = batch->rows;
+  a.max_len = batch->max_len;
+  a.starts = groups->starts;
+  a.shared = groups->shared;
+  a.groups = groups->groups;
+  a.q = q;
+  a.q_ld = q_ld;
+  a.out_ld = out_ld;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->kv_heads;
+  a.scale = scale;
+  a.out = out;
+  a.out_mode = out_mode;
+  if (xfer::launch_shared(a, cache->kind, workspace, stream) != hipSuccess) return XFER_E_DEVICE;
   return XFER_OK;
 }
 

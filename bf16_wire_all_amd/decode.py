@@ -17,8 +17,8 @@ from . import OK, OUT_BF16, OUT_F32, Shard, _check, _stream, lib as _base_lib
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
-EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged", "xfer_kv_record_bytes",
-            "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge",
+EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged",
+            "xfer_attn_shared_workspace_bytes", "xfer_attn_shared", "xfer_kv_record_bytes", "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge",
             "xfer_logprobs_workspace_bytes", "xfer_logprobs_merge"]
 
 SAMPLE_PARAMS = np.dtype([("temperature", "<f4"), ("top_k", "<u4"), ("top_p", "<f4"), ("min_p", "<f4")])
@@ -53,6 +53,11 @@ class PagedBatchC(ctypes.Structure):
                 ("sinks", ctypes.c_uint32)]
 
 
+class PrefixGroupsC(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("shared", ctypes.c_void_p), ("groups", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -71,6 +76,11 @@ def lib():
         L.xfer_attn_paged.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, U64, U32, F, P, U64, I,
                                       P, S, P]
         L.xfer_attn_paged.restype = I
+        L.xfer_attn_shared_workspace_bytes.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, U32]
+        L.xfer_attn_shared_workspace_bytes.restype = S
+        L.xfer_attn_shared.argtypes = [ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedBatchC), P, P, U64, U32, F, P, U64, I,
+                                       P, S, P]
+        L.xfer_attn_shared.restype = I
         L.xfer_kv_record_bytes.argtypes = [ctypes.POINTER(KVCacheC), I]
         L.xfer_kv_record_bytes.restype = S
         L.xfer_kv_quantize.argtypes = [ctypes.POINTER(KVCacheC), P, U32, I, P, U64, P]
@@ -215,15 +225,10 @@ def attn_workspace_bytes(cache: KVCache, rows: int, q_heads: int, max_len: int, 
     return int(lib().xfer_attn_workspace_bytes(ctypes.byref(cache.c), ctypes.byref(batch), q_heads))
 
 
-def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
-               sinks: int = 0, stream=None) -> None:
-    """q: [rows, q_heads, head_dim] (BF16 or its patterns); page_table: int32 or
-    uint32 [rows, at least ceil(max_len / page_tokens)], dense within a row;
-    lens: int32 or uint32 [rows] (a negative one is a large length, cut to
-    max_len); out: like q, BF16 (or its patterns) or F32; workspace: a CUDA
-    tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
+def _attn_call(cache: KVCache, q, page_table, lens, max_len: int, out, workspace, window: int, sinks: int):
+    """What both attention calls make of their arguments: (batch, q, q_ld, q_heads, out, out_ld, out_mode, workspace,
+    its bytes)."""
     dev, d = cache.device, cache.head_dim
-    stream = _stream_on(dev, stream)
     qp, rows, q_heads, q_ld = _rows(q, None, d, _BF16, dev, "q")
     f32 = out.dtype in _F32
     op, o_rows, _, o_ld = _rows(out, q_heads, d, _F32 if f32 else _BF16, dev, "out")
@@ -239,8 +244,21 @@ def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, 
         ws_bytes, ws = workspace.numel() * workspace.element_size(), _flat(workspace, None, dev, "workspace")
     batch = PagedBatchC(page_table.data_ptr(), _flat(lens, _INT32, dev, "lens"), ts[0] if rows > 1 else width, rows,
                         max_len, window, sinks)
+    return batch, qp, q_ld, q_heads, op, o_ld, OUT_F32 if f32 else OUT_BF16, ws, ws_bytes
+
+
+def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
+               sinks: int = 0, stream=None) -> None:
+    """q: [rows, q_heads, head_dim] (BF16 or its patterns); page_table: int32 or
+    uint32 [rows, at least ceil(max_len / page_tokens)], dense within a row;
+    lens: int32 or uint32 [rows] (a negative one is a large length, cut to
+    max_len); out: like q, BF16 (or its patterns) or F32; workspace: a CUDA
+    tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
+    stream = _stream_on(cache.device, stream)
+    batch, qp, q_ld, q_heads, op, o_ld, mode, ws, ws_bytes = _attn_call(cache, q, page_table, lens, max_len, out, workspace,
+                                                                        window, sinks)
     status = lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
-                                   OUT_F32 if f32 else OUT_BF16, ws, ws_bytes, stream)
+                                   mode, ws, ws_bytes, stream)
     if status != OK:
         _check(status, "xfer_attn_paged")
 
@@ -250,6 +268,41 @@ def attn_paged_raw(cache: KVCacheC, batch: PagedBatchC, q_ptr: int, q_ld: int, q
     """Raw-pointer form; returns the status without raising."""
     return lib().xfer_attn_paged(ctypes.byref(cache), ctypes.byref(batch), q_ptr, q_ld, q_heads, scale, out_ptr,
                                  out_ld, out_mode, ws_ptr, ws_bytes, _stream(stream))
+
+
+# ------------------------------------------------- rows with a shared prefix
+
+def attn_shared_workspace_bytes(cache: KVCache, rows: int, groups: int, q_heads: int, max_len: int) -> int:
+    """Bytes of workspace that attn_shared needs for these sizes."""
+    batch, g = PagedBatchC(0, 0, 0, rows, max_len, 0, 0), PrefixGroupsC(0, 0, groups, 0)
+    return int(lib().xfer_attn_shared_workspace_bytes(ctypes.byref(cache.c), ctypes.byref(batch), ctypes.byref(g), q_heads))
+
+
+def attn_shared(cache: KVCache, q, page_table, lens, max_len: int, starts, shared, scale: float, out, workspace,
+                stream=None) -> None:
+    """q, page_table, lens, max_len, scale and out as attn_paged's; starts: int32 or
+    uint32 [groups + 1], the groups' first rows and the end of the last one's;
+    shared: int32 or uint32 [groups], how many tokens a group's rows have in
+    common (a negative one is a large number, cut to what there is);
+    workspace: at least attn_shared_workspace_bytes() bytes."""
+    stream = _stream_on(cache.device, stream)
+    batch, qp, q_ld, q_heads, op, o_ld, mode, ws, ws_bytes = _attn_call(cache, q, page_table, lens, max_len, out, workspace,
+                                                                        0, 0)
+    groups = shared.numel()
+    if starts.numel() != groups + 1:
+        raise ValueError("starts must have one number more than shared")
+    g = PrefixGroupsC(_flat(starts, _INT32, cache.device, "starts"), _flat(shared, _INT32, cache.device, "shared"), groups, 0)
+    status = lib().xfer_attn_shared(ctypes.byref(cache.c), ctypes.byref(batch), ctypes.byref(g), qp, q_ld, q_heads, scale,
+                                    op, o_ld, mode, ws, ws_bytes, stream)
+    if status != OK:
+        _check(status, "xfer_attn_shared")
+
+
+def attn_shared_raw(cache: KVCacheC, batch: PagedBatchC, groups: PrefixGroupsC, q_ptr: int, q_ld: int, q_heads: int,
+                    scale: float, out_ptr: int, out_ld: int, out_mode: int, ws_ptr: int, ws_bytes: int, stream=None) -> int:
+    """Raw-pointer form; returns the status without raising."""
+    return lib().xfer_attn_shared(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(groups), q_ptr, q_ld, q_heads,
+                                  scale, out_ptr, out_ld, out_mode, ws_ptr, ws_bytes, _stream(stream))
 
 
 # ------------------------------------------- a cache's slots in 8 or 4 bits

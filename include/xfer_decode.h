@@ -8,6 +8,8 @@
  *   xfer_attn_paged      attention of one new token of every request over
  *                        such a cache, the whole of it or a window and the
  *                        first tokens
+ *   xfer_attn_shared     the same for rows in groups that begin with the same
+ *                        tokens, which are read once for all of them
  *   xfer_kv_quantize,    a cache's slots as records of 8 or 4 bits an
  *   xfer_kv_restore      element for the wire, and back into another cache
  *   xfer_sample_merge    sampling with temperature, top-k, top-p and min-p
@@ -223,6 +225,57 @@ XFER_API size_t xfer_attn_workspace_bytes(const xfer_kv_cache *cache, const xfer
 XFER_API int xfer_attn_paged(const xfer_kv_cache *cache, const xfer_paged_batch *batch, const uint16_t *q,
                              uint64_t q_ld, uint32_t q_heads, float scale, void *out, uint64_t out_ld, int out_mode,
                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------- rows with a shared prefix */
+
+/*
+ * Groups of neighbouring rows whose requests begin with the same tokens in the
+ * same pages: several answers to one prompt, requests under one system prompt,
+ * drafted positions of one request.  Group i is rows starts[i] ..
+ * starts[i + 1] - 1; the first shared[i] tokens of all of them lie in the
+ * pages of the group's first row.  Rows outside every group share nothing.
+ */
+typedef struct {
+  const uint32_t *starts; /* (device) uint32[groups + 1], not decreasing       */
+  const uint32_t *shared; /* (device) uint32[groups]: any number of tokens,
+                             whole pages or not                                */
+  uint32_t groups;        /* up to 4,096; 0: no row shares anything            */
+  uint32_t reserved;      /* 0                                                 */
+} xfer_prefix_groups;
+
+/*
+ * xfer_attn_shared - xfer_attn_paged, its formula and everything said there of
+ * lengths, holes and numbers that are not finite, with the shared tokens of a
+ * group read once for all its rows.  A row's shared tokens are read from the
+ * pages of its group's first row, the others from its own; of these, only the
+ * page numbers from token shared[i] on are used, unless the row is shorter
+ * than that: then it is read as if it were in no group, and so is every row of
+ * a group of one.  shared[i] counts up to the length of the group's first row.
+ * The device's numbers cannot be checked on the host: a start below the one
+ * before counts as that one, and one past the rows as the rows' end.
+ *
+ * Weights are split as for XFER_OUT_F32 there, or into two BF16 numbers (2^-17
+ * of the weight) for XFER_OUT_BF16.  Results of a row may differ in their last
+ * bits with the rows it is grouped with.
+ *
+ *   batch      as xfer_attn_paged's; windows are not supported.
+ *   workspace  (device) at least xfer_attn_shared_workspace_bytes() bytes,
+ *              16-byte aligned, any contents.  Calls that may run concurrently
+ *              must use different workspaces.
+ *
+ * Errors: those of xfer_attn_paged; XFER_E_INVAL for NULL or misaligned starts
+ * or shared (4 bytes) where there are groups, or a reserved field that is not 0;
+ * XFER_E_UNSUPPORTED for a window, or more than 4,096 groups or 2^24 - 1
+ * (row, query head)s.
+ * xfer_attn_shared_workspace_bytes - 0 for sizes and caches that the call
+ * refuses, and for no rows.  The bytes depend on the sizes alone.
+ */
+XFER_API size_t xfer_attn_shared_workspace_bytes(const xfer_kv_cache *cache, const xfer_paged_batch *batch,
+                                                 const xfer_prefix_groups *groups, uint32_t q_heads);
+XFER_API int xfer_attn_shared(const xfer_kv_cache *cache, const xfer_paged_batch *batch,
+                              const xfer_prefix_groups *groups, const uint16_t *q, uint64_t q_ld, uint32_t q_heads,
+                              float scale, void *out, uint64_t out_ld, int out_mode, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------ a cache's slots in 8 or 4 bits */
 
