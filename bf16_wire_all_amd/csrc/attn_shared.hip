@@ -29,11 +29,19 @@ constexpr uint32_t kXcds = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, since the memory bounds the walk
 
+// Groups of more than kFewHeads query heads for a kv head go another way, kManyHeads of them and
+// kManyUnit tokens at a time, and at least kManyLeast such units to a workgroup.
+constexpr uint32_t kFewHeads = 32, kManyHeads = 128, kManyUnit = 64, kManyLeast = 4;
+
 // ------------------------------------------------------------------- plan
 
-__device__ __forceinline__ uint64_t entry_units(const SharedArgs &a, const SharedEntry &e) {
-  const uint64_t heads = (uint64_t)e.q_rows * a.group;
-  return (uint64_t)((e.n + kUnit - 1) / kUnit) * a.cache.kv_heads * ((heads + a.tile - 1) / a.tile);
+// Units and tiles of heads (of a kv head) of an entry in the list whose
+// workgroups take `tile` heads and `unit` tokens at a time.
+__device__ __forceinline__ uint64_t entry_tiles(const SharedArgs &a, const SharedEntry &e, uint32_t tile) {
+  return ((uint64_t)e.q_rows * a.group + tile - 1) / tile;
+}
+__device__ __forceinline__ uint64_t entry_units(const SharedArgs &a, const SharedEntry &e, uint32_t tile, uint32_t unit) {
+  return (uint64_t)((e.n + unit - 1) / unit) * a.cache.kv_heads * entry_tiles(a, e, tile);
 }
 
 // Inclusive scans over the threads of the plan's workgroup.
@@ -85,58 +93,60 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
     prefix[g] = p;
   }
   __syncthreads();
-  const uint32_t n = a.rows + a.groups, each = (n + kPlanThreads - 1) / kPlanThreads;
-  const uint32_t i0 = min(tid * each, n), i1 = min(i0 + each, n);
-  auto entry = [&](uint32_t i) {
+  // A group's shared tokens, if its rows' heads are in the list of many or the other.
+  auto of_group = [&](uint32_t g, bool many) {
     SharedEntry e{};
-    if (i < a.rows) {
-      uint32_t lo = 0, hi = a.groups + 1;  // the first start past row i
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (start[mid] <= i)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      const uint32_t len = min(a.lens[i], a.max_len);
-      const bool in = lo > 0 && lo <= a.groups;
-      const uint32_t p = in ? prefix[lo - 1] : 0;
-      e.first = p <= len ? p : 0;
-      e.n = len - e.first;
-      e.row = e.q_row = i;
-      e.q_rows = 1;
-      e.group = e.first ? lo - 1 : kNoGroup;
-    } else {
-      const uint32_t g = i - a.rows;
-      e.n = prefix[g];
-      e.row = e.q_row = start[g];
-      e.q_rows = e.n ? start[g + 1] - start[g] : 0;
-      e.group = g;
-    }
+    const uint32_t rows = start[g + 1] - start[g];
+    if (!prefix[g] || ((uint64_t)rows * a.group > kFewHeads) != many) return e;
+    e.n = prefix[g];
+    e.row = e.q_row = start[g];
+    e.q_rows = rows;
     return e;
   };
-  uint64_t units = 0, tiles = 0;
-  for (uint32_t i = i0; i < i1; ++i) {
-    const SharedEntry e = entry(i);
-    units += entry_units(a, e);
-    tiles += ((uint64_t)e.q_rows * a.group + a.tile - 1) / a.tile;
-  }
-  auto add = [](unsigned long long x, unsigned long long y) { return x + y; };
-  uint64_t unit0 = block_scan((unsigned long long)units, waves, add) - units;
-  uint64_t tile0 = block_scan((unsigned long long)tiles, waves, add) - tiles;
-  for (uint32_t i = i0; i < i1; ++i) {
-    SharedEntry e = entry(i);
-    e.unit0 = unit0;
-    e.part0 = (uint32_t)(tile0 * a.cache.kv_heads);
-    a.entries[i] = e;
-    unit0 += entry_units(a, e);
-    tile0 += ((uint64_t)e.q_rows * a.group + a.tile - 1) / a.tile;
-  }
-  if (i0 < n && i1 == n) {
+  auto of_row = [&](uint32_t i) {
     SharedEntry e{};
-    e.unit0 = unit0;
-    a.entries[n] = e;
-  }
+    uint32_t lo = 0, hi = a.groups + 1;  // the first start past row i
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (start[mid] <= i)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const uint32_t len = min(a.lens[i], a.max_len);
+    const uint32_t p = lo > 0 && lo <= a.groups ? prefix[lo - 1] : 0;
+    e.first = p <= len ? p : 0;
+    e.n = len - e.first;
+    e.row = e.q_row = i;
+    e.q_rows = 1;
+    e.group = e.first ? lo - 1 : kNoGroup;
+    return e;
+  };
+  // Lists of n entries: where each one's units and parts begin.
+  auto list = [&](SharedEntry *to, uint32_t n, uint32_t tile, uint32_t unit, uint32_t part0, auto &&entry) {
+    const uint32_t each = (n + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
+    uint64_t units = 0, tiles = 0;
+    for (uint32_t i = i0; i < i1; ++i) {
+      const SharedEntry e = entry(i);
+      units += entry_units(a, e, tile, unit);
+      tiles += entry_tiles(a, e, tile);
+    }
+    auto add = [](unsigned long long x, unsigned long long y) { return x + y; };
+    uint64_t unit0 = block_scan((unsigned long long)units, waves, add) - units;
+    uint64_t tile0 = block_scan((unsigned long long)tiles, waves, add) - tiles;
+    for (uint32_t i = i0; i < i1; ++i) {
+      SharedEntry e = entry(i);
+      e.unit0 = unit0;
+      e.part0 = part0 + (uint32_t)(tile0 * a.cache.kv_heads);
+      to[i] = e;
+      unit0 += entry_units(a, e, tile, unit);
+      tile0 += entry_tiles(a, e, tile);
+    }
+    if (i0 < n && i1 == n) to[n].unit0 = unit0;
+  };
+  list(a.entries, a.rows + a.groups, a.tile, kUnit, 0,
+       [&](uint32_t i) { return i < a.rows ? of_row(i) : of_group(i - a.rows, false); });
+  if (a.many) list(a.many, a.groups, kManyHeads, kManyUnit, a.many_part0, [&](uint32_t g) { return of_group(g, true); });
 }
 
 // ------------------------------------------------------------------- walk
@@ -284,6 +294,304 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
   }
 }
 
+// --------------------------------------------------- many heads' shared tokens
+
+// Four waves take 32 query heads each of the same tokens, 64 at a time, which go
+// through LDS: keys as rows, values as columns (a lane's operand is eight tokens
+// of one dim), both in BF16.  Scores are K Q^T (32x32x16), so a lane holds 16 tokens'
+// scores of one query in each of two blocks; in the order in which it holds them they are
+// the operand of V^T P^T, and the values' columns are laid down in that order of tokens:
+// nothing crosses lanes but the two halves' maxima.  Pieces of 16 bytes are placed so that
+// eight lanes side by side, reading rows or columns one apart, touch all banks.
+template <int D, int KIND>
+struct Many {
+  static constexpr int kBytes = KIND == XFER_KV_BF16 ? 2 : 1;
+  static constexpr int kPieces = D / 8;                            // of a key's row
+  static constexpr int kUnits = 2 * D;                             // four tokens' eight dims each, of a tile
+  static constexpr int kEach = kUnits / kThreads ? kUnits / kThreads : 1;  // of a thread, of keys and of values
+  static constexpr bool kSplit = kUnits < kThreads;                // half the threads take keys, the others values
+  static constexpr int kBuffers = D == 256 ? 1 : 2;
+  static constexpr int kPerSimd = D == 256 ? 1 : 2;
+  static constexpr uint32_t kTileBytes = kManyUnit * D * 2;        // of keys, and of values
+};
+
+template <int BYTES>
+struct Piece {
+  typedef v4u type;
+};
+template <>
+struct Piece<8> {
+  typedef v2u type;
+};
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// Bytes from a tile's start: piece c of token t's key; piece c (eight tokens) of dim d's values.
+template <int D>
+__device__ __forceinline__ uint32_t key_at(uint32_t t, uint32_t c) {
+  return (t * (D / 8) + (c ^ (t & 7))) * 16;
+}
+__device__ __forceinline__ uint32_t value_at(uint32_t d, uint32_t c) { return (d * 8 + (c ^ ((d ^ d >> 3) & 7))) * 16; }
+
+template <int D, int KIND, int PARTS>
+__global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_many_kernel(SharedArgs a) {
+  using M = Many<D, KIND>;
+  constexpr int kDims = D / 32;   // blocks of dims
+  constexpr int kSteps = D / 16;  // of a score
+  __shared__ __align__(16) uint8_t lds[M::kBuffers][2 * M::kTileBytes];
+  __shared__ __align__(16) uint8_t lds_gone[M::kBuffers][16];  // a bit for each token of four that is not there
+  __shared__ uint32_t start;
+  const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  const uint64_t all = a.many[a.groups].unit0, share = (all + gridDim.x - 1) / gridDim.x;
+  const uint64_t per = share < kManyLeast ? kManyLeast : share, from = wg * per;
+  if (from >= all) return;
+  uint64_t left = min(per, all - from);
+  for (uint32_t i = threadIdx.x; i < a.groups; i += kThreads)
+    if (a.many[i].unit0 <= from && from < a.many[i + 1].unit0) start = i;
+  __syncthreads();
+  uint32_t index = __builtin_amdgcn_readfirstlane(start);
+  SharedEntry e = a.many[index];
+  uint64_t at = from - e.unit0;
+
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 32,
+                 hf = lane / 32;
+  // This thread's place in a tile: tokens 4 * quad .. + 3, pieces piece and (256 dims) piece + 16.
+  constexpr uint32_t kAcross = M::kPieces < 16 ? M::kPieces : 16;
+  const uint32_t unit_of = M::kSplit ? tid % M::kUnits : tid;
+  const uint32_t quad = unit_of / kAcross, piece = unit_of % kAcross;
+  const bool takes_k = !M::kSplit || tid < M::kUnits, takes_v = !M::kSplit || tid >= M::kUnits;
+  const uint32_t slot_mask = (1u << a.cache.page_log2) - 1;
+  bool first_segment = true;
+
+#pragma unroll 1
+  while (left) {
+    const uint32_t heads = e.q_rows * a.group, tiles = (heads + kManyHeads - 1) / kManyHeads;
+    const uint32_t units = (e.n + kManyUnit - 1) / kManyUnit, inner_n = tiles * a.cache.kv_heads;
+    uint32_t inner = __builtin_amdgcn_readfirstlane((uint32_t)(at / units));
+    uint32_t unit = __builtin_amdgcn_readfirstlane((uint32_t)(at % units));
+#pragma unroll 1
+    for (; inner < inner_n && left; ++inner, unit = 0) {
+      const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
+      const uint32_t kvh = inner / tiles, h = inner % tiles * kManyHeads + 32 * wave + n;  // this lane's query head
+      float scale2 = a.scale * 1.4426950408889634f;
+      if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
+      // a negative scale's sign goes to the queries, so that the largest product is the largest score
+      const uint32_t flip = scale2 < 0 ? 0x80008000u : 0;
+      scale2 = __builtin_fabsf(scale2);
+      const uint64_t head = (uint64_t)kvh * a.group + h % a.group;
+      v4u q[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        q[k] = v4u{0, 0, 0, 0};
+        if (h < heads) q[k] = *reinterpret_cast<const v4u *>(a.q + (e.q_row + h / a.group) * a.q_ld + head * D + 16 * k + 8 * hf);
+        q[k] ^= flip;
+      }
+      const uint32_t *table = a.page_table + e.row * a.table_ld;
+      const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride + piece * 8 * M::kBytes;
+      const uint8_t *vbase = a.cache.v + kvh * a.cache.head_stride + piece * 8 * M::kBytes;
+
+      // The pages of this thread's four tokens of the tile from token t on.
+      struct Pages {
+        uint32_t page[4];
+      };
+      auto look_up = [&](uint32_t t) {
+        Pages p;
+        t += 4 * quad;
+        if (a.cache.page_log2 >= 2) {  // all four are in one
+          const uint32_t x = t < e.n ? table[t >> a.cache.page_log2] : 0;
+          for (uint32_t i = 0; i < 4; ++i) p.page[i] = x;
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) p.page[i] = t + i < e.n ? table[(t + i) >> a.cache.page_log2] : 0;
+        }
+        return p;
+      };
+      uint32_t k[M::kEach][4][2 * M::kBytes], v[M::kEach][4][2 * M::kBytes], gone = 0;
+      auto fetch = [&](uint32_t t, const Pages &p) {
+        gone = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t token = t + 4 * quad + i;
+          const bool there = token < e.n && p.page[i] < a.cache.n_pages;
+          gone |= there ? 0 : 1u << i;
+          // one that is not there is read from the cache's first slot, and replaced
+          const uint64_t off = there ? p.page[i] * a.cache.page_stride + (token & slot_mask) * a.cache.token_stride : 0;
+#pragma unroll
+          for (int u = 0; u < M::kEach; ++u) {
+            typedef typename Piece<8 * M::kBytes>::type T;
+            if (takes_k) {
+              const T w = *reinterpret_cast<const T *>(kbase + off + u * 128 * M::kBytes);
+              __builtin_memcpy(k[u][i], &w, sizeof(T));
+            }
+            if (takes_v) {
+              const T w = *reinterpret_cast<const T *>(vbase + off + u * 128 * M::kBytes);
+              __builtin_memcpy(v[u][i], &w, sizeof(T));
+            }
+          }
+        }
+      };
+      // Eight elements as BF16.
+      auto widen = [&](const uint32_t (&w)[2 * M::kBytes]) -> v4u {
+        if constexpr (KIND == XFER_KV_BF16)
+          return v4u{w[0], w[1], w[2], w[3]};
+        else
+          return v4u{e4m3x2_to_bf16<false>(w[0]), e4m3x2_to_bf16<true>(w[0]), e4m3x2_to_bf16<false>(w[1]),
+                     e4m3x2_to_bf16<true>(w[1])};
+      };
+      auto put = [&](uint32_t b) {
+        uint8_t *keys = lds[b], *values = lds[b] + M::kTileBytes;
+        if (piece == 0 && takes_k) lds_gone[b][quad] = (uint8_t)gone;
+#pragma unroll
+        for (int u = 0; u < M::kEach; ++u) {
+          if (takes_k) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+              *reinterpret_cast<v4u *>(keys + key_at<D>(4 * quad + i, piece + 16 * u)) = widen(k[u][i]);
+          }
+          if (takes_v) {
+            v4u x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = gone >> i & 1 ? v4u{0, 0, 0, 0} : widen(v[u][i]);
+            // tokens 8j + 4f + i of 16 are element 4j + i of piece f
+            const uint32_t c = quad / 4 * 2 + quad % 2, j = quad % 4 / 2;
+#pragma unroll
+            for (uint32_t d = 0; d < 8; ++d) {
+              const uint32_t sel = d % 2 ? 0x07060302 : 0x05040100;
+              const v2u w = {__builtin_amdgcn_perm(x[1][d / 2], x[0][d / 2], sel),
+                             __builtin_amdgcn_perm(x[3][d / 2], x[2][d / 2], sel)};
+              *reinterpret_cast<v2u *>(values + value_at(8 * (piece + 16 * u) + d, c) + 8 * j) = w;
+            }
+          }
+        }
+      };
+
+      v16f o[kDims];
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[d] = v16f{};
+      float mx = -INFINITY, sum = 0;
+      const uint32_t t0 = unit * kManyUnit, t1 = t0 + take * kManyUnit;
+      fetch(t0, look_up(t0));
+      Pages next = look_up(t0 + kManyUnit);
+      put(0);
+      __syncthreads();
+      uint32_t b = 0;
+#pragma unroll 1
+      for (uint32_t t = t0; t < t1; t += kManyUnit) {
+        const bool more = t + kManyUnit < t1;
+        if (more) {
+          fetch(t + kManyUnit, next);
+          next = look_up(t + 2 * kManyUnit);
+        }
+        const uint8_t *keys = lds[b], *values = lds[b] + M::kTileBytes;
+        const v4u out = *reinterpret_cast<const v4u *>(lds_gone[b]);
+        v16f s[2] = {v16f{}, v16f{}};
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk)
+            s[blk] = mfma32(*reinterpret_cast<const v4u *>(keys + key_at<D>(32 * blk + n, 2 * kk + hf)), q[kk], s[blk]);
+        const bool holes = (out.x | out.y | out.z | out.w) != 0;
+        if (holes) {
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t four = 8 * blk + 2 * (i / 4) + hf;  // tokens 32 blk + 8 (i / 4) + 4 hf + i % 4
+              const uint32_t w = out[2 * blk + i / 8];
+              if (w >> (8 * (four % 4) + i % 4) & 1) s[blk][i] = -INFINITY;
+            }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
+        top *= scale2;
+        if (__any(top > mx + kRaise)) {
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float raised = fmaxf(mx, top);
+          const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - raised);
+          mx = raised;
+          sum *= f;
+#pragma unroll
+          for (int d = 0; d < kDims; ++d) o[d] *= f;
+        }
+        const float base = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          v4u w[PARTS][2];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x0 = __builtin_amdgcn_exp2f(fmaf(s[blk][2 * i], scale2, -base));
+            float x1 = __builtin_amdgcn_exp2f(fmaf(s[blk][2 * i + 1], scale2, -base));
+            sum += x0 + x1;
+#pragma unroll
+            for (int c = 0; c < PARTS; ++c) {
+              const uint32_t two = bf16x2(x0, x1);
+              w[c][i / 4][i % 4] = two;
+              x0 -= __uint_as_float(two << 16);
+              x1 -= __uint_as_float(two & 0xFFFF0000u);
+            }
+          }
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) {
+              const v4u col = *reinterpret_cast<const v4u *>(values + value_at(32 * d + n, 4 * blk + 2 * st + hf));
+#pragma unroll
+              for (int c = 0; c < PARTS; ++c) o[d] = mfma32(col, w[c][st], o[d]);
+            }
+        }
+        if (more) {
+          if constexpr (M::kBuffers == 1) {
+            __syncthreads();  // the tile has been read
+          } else {
+            b ^= 1;
+          }
+          put(b);
+        }
+        __syncthreads();
+      }
+
+      // This wave's results: lane n, hf holds dims 32 d + 8 (i / 4) + 4 hf + i % 4 of query n.
+      const bool whole = take == units;
+      const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
+      if (unit == 0 && tid == 0)
+        a.parts[e.part0 + inner] = whole ? SharedParts{kWhole, 1} : SharedParts{slot, 1 + (uint32_t)((units - take + per - 1) / per)};
+      sum += __shfl_xor(sum, 32);
+      if (h < heads) {
+        const uint64_t to = whole ? a.whole0 + ((uint64_t)a.rows + e.q_row + h / a.group) * a.q_heads + head
+                                  : a.many_place0 + (uint64_t)slot * kManyHeads + 32 * wave + n;
+        if (hf == 0) {
+          a.part_ml[2 * to] = mx;
+          a.part_ml[2 * to + 1] = sum;
+        }
+        const Visible vis{e.n, 0, 0};
+#pragma unroll
+        for (int d = 0; d < kDims; ++d)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v4f x = {o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]};
+            const uint32_t dim = 32 * d + 8 * j + 4 * hf;
+            if constexpr (KIND == XFER_KV_BF16) {
+              if (isnan(x.x + x.y + x.z + x.w) && !isnan(sum))
+                x = with_infinities<KIND>(a.cache, kvh, table, vis, t0, min(t1, e.n), x, dim);
+            }
+            *reinterpret_cast<v4f *>(a.part_o + to * D + dim) = x;
+          }
+      }
+      left -= take;
+      first_segment = false;
+    }
+    at = 0;
+    if (left) {
+      do e = a.many[++index];
+      while (e.n == 0);  // there is one with tokens as long as units are left
+    }
+  }
+}
+
 // ------------------------------------------------------------------- join
 
 // One workgroup for each (row, query head): its parts of the shared tokens, then
@@ -302,26 +610,29 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
     uint32_t n;                 // parts
     uint64_t at0, at1, stride;  // places: part 0's; part p's at1 + p * stride
   };
-  auto source = [&](const SharedEntry &e, bool prefix) {
+  auto source = [&](const SharedEntry &e, bool prefix, uint32_t tile, uint64_t cut0) {
     Source s{};
     if (!e.n) return s;
-    const uint32_t heads = e.q_rows * a.group, m_groups = (heads + a.tile - 1) / a.tile;
+    const uint32_t heads = e.q_rows * a.group, m_groups = (heads + tile - 1) / tile;
     const uint32_t i = (row - e.q_row) * a.group + h;
-    const SharedParts p = a.parts[e.part0 + kvh * m_groups + i / a.tile];
+    const SharedParts p = a.parts[e.part0 + kvh * m_groups + i / tile];
     s.n = p.n;
     if (p.slot == kWhole) {
       s.at0 = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
     } else {
       // Part p > 0 is the first thing that the workgroup p further on did.
-      s.at0 = (uint64_t)p.slot * a.tile + i % a.tile;
-      s.at1 = (uint64_t)(p.slot / 2 * 2) * a.tile + i % a.tile;
-      s.stride = 2 * a.tile;
+      s.at0 = cut0 + (uint64_t)p.slot * tile + i % tile;
+      s.at1 = cut0 + (uint64_t)(p.slot / 2 * 2) * tile + i % tile;
+      s.stride = 2 * tile;
     }
     return s;
   };
   Source pre{};
-  if (own.group != kNoGroup) pre = source(a.entries[a.rows + own.group], true);
-  const Source mine = source(own, false);
+  if (own.group != kNoGroup) {
+    const SharedEntry e = a.entries[a.rows + own.group];
+    pre = e.n ? source(e, true, a.tile, 0) : source(a.many[own.group], true, kManyHeads, a.many_place0);
+  }
+  const Source mine = source(own, false, a.tile, 0);
   const uint32_t n = pre.n + mine.n;
   auto place = [&](uint32_t p) -> uint64_t {
     const Source &s = p < pre.n ? pre : mine;
@@ -381,25 +692,29 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
 
 // ----------------------------------------------------------------- launches
 
-template <int D, int KIND, int TILES>
-hipError_t launch_walk(const SharedArgs &a, uint32_t workgroups, hipStream_t stream) {
-  return launch(shared_walk_kernel<D, KIND, TILES>, dim3(workgroups), dim3(kThreads), 0, stream, a);
+template <int D, int KIND>
+hipError_t launch_kind(const SharedArgs &a, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
+  hipError_t e = a.tile == 16 ? launch(shared_walk_kernel<D, KIND, 1>, dim3(workgroups), dim3(kThreads), 0, stream, a)
+                              : launch(shared_walk_kernel<D, KIND, 2>, dim3(workgroups), dim3(kThreads), 0, stream, a);
+  if (e != hipSuccess || !a.many) return e;
+  return a.out_mode == XFER_OUT_F32
+             ? launch(shared_many_kernel<D, KIND, 3>, dim3(many_workgroups), dim3(kThreads), 0, stream, a)
+             : launch(shared_many_kernel<D, KIND, 2>, dim3(many_workgroups), dim3(kThreads), 0, stream, a);
 }
 template <int D>
-hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, hipStream_t stream) {
+hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
   hipError_t e = launch(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
   if (e != hipSuccess) return e;
-  if (kind == XFER_KV_BF16)
-    e = a.tile == 16 ? launch_walk<D, XFER_KV_BF16, 1>(a, workgroups, stream) : launch_walk<D, XFER_KV_BF16, 2>(a, workgroups, stream);
-  else
-    e = a.tile == 16 ? launch_walk<D, XFER_KV_E4M3, 1>(a, workgroups, stream) : launch_walk<D, XFER_KV_E4M3, 2>(a, workgroups, stream);
+  e = kind == XFER_KV_BF16 ? launch_kind<D, XFER_KV_BF16>(a, workgroups, many_workgroups, stream)
+                           : launch_kind<D, XFER_KV_E4M3>(a, workgroups, many_workgroups, stream);
   if (e != hipSuccess) return e;
   return launch(shared_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a);
 }
 
 struct Shape {
-  uint32_t tile, workgroups;
-  uint64_t parts, places, whole0;  // (entry, kv head, tile)s at most; query heads of all parts; the first whole one's
+  uint32_t tile, workgroups, many_workgroups;
+  uint64_t parts, many_part0;             // (entry, kv head, tile)s at most, and where those of many heads begin
+  uint64_t places, many_place0, whole0;   // query heads of all parts, and where those of many heads and whole ones begin
 };
 template <int D, int KIND>
 uint32_t per_simd(uint32_t tile) {
@@ -416,8 +731,15 @@ Shape shape_of(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group
   s.workgroups = kComputeUnits * (kind == XFER_KV_BF16 ? per_simd<XFER_KV_BF16>(head_dim, s.tile)
                                                        : per_simd<XFER_KV_E4M3>(head_dim, s.tile));
   const uint64_t row_tiles = (group + s.tile - 1) / s.tile;
-  s.parts = kv_heads * (rows * row_tiles + (uint64_t)rows * group / s.tile + groups);
-  s.whole0 = 2ull * s.workgroups * s.tile;
+  s.many_part0 = kv_heads * (rows * row_tiles + (uint64_t)rows * group / s.tile + groups);
+  s.parts = s.many_part0;
+  s.many_place0 = 2ull * s.workgroups * s.tile;
+  s.whole0 = s.many_place0;
+  if (groups && (uint64_t)rows * group > kFewHeads) {  // some group may be that large
+    s.many_workgroups = kComputeUnits * (head_dim == 256 ? 1 : 2);
+    s.parts += kv_heads * ((uint64_t)rows * group / kManyHeads + groups);
+    s.whole0 += 2ull * s.many_workgroups * kManyHeads;
+  }
   s.places = s.whole0 + 2ull * rows * kv_heads * group;
   return s;
 }
@@ -434,7 +756,7 @@ bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
                                 int kind) {
   const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
-  return up16(((uint64_t)rows + groups + 1) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
+  return up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
          s.places * head_dim * 4;
 }
 
@@ -445,12 +767,15 @@ hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStr
   a.whole0 = s.whole0;
   uint8_t *at = static_cast<uint8_t *>(workspace);
   a.entries = reinterpret_cast<SharedEntry *>(at);
-  a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + a.groups + 1) * sizeof(SharedEntry)));
+  a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + 2ull * a.groups + 2) * sizeof(SharedEntry)));
+  if (s.many_workgroups) a.many = a.entries + a.rows + a.groups + 1;
+  a.many_part0 = (uint32_t)s.many_part0;
+  a.many_place0 = s.many_place0;
   a.part_ml = reinterpret_cast<float *>(at += up16(s.parts * sizeof(SharedParts)));
   a.part_o = reinterpret_cast<float *>(at + up16(s.places * 8));
-  if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s.workgroups, stream);
-  if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s.workgroups, stream);
-  return launch_dim<256>(a, kind, s.workgroups, stream);
+  if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s.workgroups, s.many_workgroups, stream);
+  if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s.workgroups, s.many_workgroups, stream);
+  return launch_dim<256>(a, kind, s.workgroups, s.many_workgroups, stream);
 }
 
 }  // namespace xfer

@@ -89,10 +89,12 @@ struct SharedArgs {
   int out_mode;
   // set by the launch
   uint32_t tile;  // query heads that a workgroup takes at a time
-  SharedEntry *entries;
+  SharedEntry *entries;  // of rows, then of groups of few query heads
+  SharedEntry *many;     // of groups of many (NULL: there is none)
   SharedParts *parts;
+  uint32_t many_part0;
   float *part_ml, *part_o;
-  uint64_t whole0;  // the place of the first result that one workgroup has whole
+  uint64_t many_place0, whole0;  // the first places of groups of many, and of results that one workgroup has whole
 };
 bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind);
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
