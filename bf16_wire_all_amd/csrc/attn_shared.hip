@@ -33,6 +33,8 @@ constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, si
 // kManyUnit tokens at a time, and at least kManyLeast such units to a workgroup.
 constexpr uint32_t kFewHeads = 32, kManyHeads = 128, kManyUnit = 64, kManyLeast = 4;
 
+constexpr uint32_t kZeros = 16;  // bytes that stand for tokens that are not there
+
 // ------------------------------------------------------------------- plan
 
 // Units and tiles of heads (of a kv head) of an entry in the list whose
@@ -65,6 +67,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
   __shared__ uint32_t start[kMaxGroups + 1], prefix[kMaxGroups];
   __shared__ unsigned long long waves[kPlanThreads / 64];
   const uint32_t tid = threadIdx.x;
+  if (tid < kZeros / 4) reinterpret_cast<uint32_t *>(a.zeros)[tid] = 0;
   // The groups' first rows: a start below the one before counts as that one,
   // so that no row is in two groups, whatever the caller's numbers are.
   {
@@ -297,52 +300,44 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
 // --------------------------------------------------- many heads' shared tokens
 
 // Four waves take 32 query heads each of the same tokens, 64 at a time, which go
-// through LDS: keys as rows, values as columns (a lane's operand is eight tokens
-// of one dim), both in BF16.  Scores are K Q^T (32x32x16), so a lane holds 16 tokens'
-// scores of one query in each of two blocks; in the order in which it holds them they are
-// the operand of V^T P^T, and the values' columns are laid down in that order of tokens:
-// nothing crosses lanes but the two halves' maxima.  Pieces of 16 bytes are placed so that
-// eight lanes side by side, reading rows or columns one apart, touch all banks.
+// through LDS in BF16, a row for each token.  Scores are K Q^T (32x32x16), so a lane
+// holds 16 tokens' scores of one query in each of two blocks, and in the order in
+// which it holds them they are the operand of V^T P^T: a lane's eight tokens are two
+// fours, and each four of a dim is what one transposing read of LDS (4 rows of 16
+// columns for 16 lanes) gives.  Nothing crosses lanes but the two halves' maxima.
+// BF16 rows go from memory to LDS without a register; the next tile is on its way
+// while one is used.  A row's pieces of 16 bytes are placed by the token's last three
+// bits, so that eight lanes side by side that read a column of pieces touch all banks.
 template <int D, int KIND>
 struct Many {
   static constexpr int kBytes = KIND == XFER_KV_BF16 ? 2 : 1;
-  static constexpr int kPieces = D / 8;                            // of a key's row
-  static constexpr int kUnits = 2 * D;                             // four tokens' eight dims each, of a tile
-  static constexpr int kEach = kUnits / kThreads ? kUnits / kThreads : 1;  // of a thread, of keys and of values
-  static constexpr bool kSplit = kUnits < kThreads;                // half the threads take keys, the others values
-  static constexpr int kBuffers = D == 256 ? 1 : 2;
+  static constexpr int kEach = D / 32;                             // pieces of keys, and of values, of a thread
+  static constexpr uint32_t kRowLanes = D / 8;                     // that hold a row of pieces
+  static constexpr uint32_t kRows = 64 / kRowLanes;                // rows that a wave moves at once
   static constexpr int kPerSimd = D == 256 ? 1 : 2;
   static constexpr uint32_t kTileBytes = kManyUnit * D * 2;        // of keys, and of values
 };
 
-template <int BYTES>
-struct Piece {
-  typedef v4u type;
-};
-template <>
-struct Piece<8> {
-  typedef v2u type;
-};
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ v16f mfma32(v4u a, v4u b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
-
-// Bytes from a tile's start: piece c of token t's key; piece c (eight tokens) of dim d's values.
-template <int D>
-__device__ __forceinline__ uint32_t key_at(uint32_t t, uint32_t c) {
-  return (t * (D / 8) + (c ^ (t & 7))) * 16;
+// Element `lane % 16` of the rows that the lanes of 16 point into, four lanes to a row.
+__device__ __forceinline__ v2u column4(const uint8_t *p) {
+  typedef __attribute__((address_space(3))) v4s *Lds;
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p));
 }
-__device__ __forceinline__ uint32_t value_at(uint32_t d, uint32_t c) { return (d * 8 + (c ^ ((d ^ d >> 3) & 7))) * 16; }
 
 template <int D, int KIND, int PARTS>
 __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_many_kernel(SharedArgs a) {
   using M = Many<D, KIND>;
   constexpr int kDims = D / 32;   // blocks of dims
   constexpr int kSteps = D / 16;  // of a score
-  __shared__ __align__(16) uint8_t lds[M::kBuffers][2 * M::kTileBytes];
-  __shared__ __align__(16) uint8_t lds_gone[M::kBuffers][16];  // a bit for each token of four that is not there
+  // two variables, not one of two: then the compiler knows that what is on its way to one does not change the other
+  __shared__ __align__(16) uint8_t lds0[2 * M::kTileBytes], lds1[2 * M::kTileBytes];
+  __shared__ __align__(8) uint16_t lds_gone[2][kWaves];  // a bit for each token of 16 that is not there
   __shared__ uint32_t start;
   const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
   const uint64_t all = a.many[a.groups].unit0, share = (all + gridDim.x - 1) / gridDim.x;
@@ -358,12 +353,14 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
 
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 32,
                  hf = lane / 32;
-  // This thread's place in a tile: tokens 4 * quad .. + 3, pieces piece and (256 dims) piece + 16.
-  constexpr uint32_t kAcross = M::kPieces < 16 ? M::kPieces : 16;
-  const uint32_t unit_of = M::kSplit ? tid % M::kUnits : tid;
-  const uint32_t quad = unit_of / kAcross, piece = unit_of % kAcross;
-  const bool takes_k = !M::kSplit || tid < M::kUnits, takes_v = !M::kSplit || tid >= M::kUnits;
+  // This lane moves tokens 16 * wave + kRows * i + row of a tile, the pieces that lie at its place.
+  const uint32_t row = lane / M::kRowLanes, place = lane % M::kRowLanes;
   const uint32_t slot_mask = (1u << a.cache.page_log2) - 1;
+  // Where its operands lie: a step's keys at key0 ^ 32 * step, a dim block's values at value0 ^ 64 * block; other tokens' 2 D
+  // bytes further on for each.
+  const uint32_t key0 = n * 2 * D + (hf ^ (n & 7)) * 16;
+  const uint32_t four = 4 * hf + lane % 16 / 4, column = 2 * (lane / 16 & 1) + lane % 4 / 2;
+  const uint32_t value0 = four * 2 * D + (column ^ four) * 16 + lane % 2 * 8;
   bool first_segment = true;
 
 #pragma unroll 1
@@ -376,12 +373,76 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
     for (; inner < inner_n && left; ++inner, unit = 0) {
       const uint32_t take = (uint32_t)min(left, (uint64_t)(units - unit));
       const uint32_t kvh = inner / tiles, h = inner % tiles * kManyHeads + 32 * wave + n;  // this lane's query head
+      const uint64_t head = (uint64_t)kvh * a.group + h % a.group;
+      const uint32_t *table = a.page_table + e.row * a.table_ld;
+      const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride, *vbase = a.cache.v + kvh * a.cache.head_stride;
+
+      // The pages of this lane's tokens of the tile from token t on.
+      struct Pages {
+        uint32_t page[M::kEach];
+      };
+      auto look_up = [&](uint32_t t) {
+        Pages p;
+#pragma unroll
+        for (int i = 0; i < M::kEach; ++i)
+          p.page[i] = table[min(t + 16 * wave + M::kRows * i + row, e.n - 1) >> a.cache.page_log2];
+        return p;
+      };
+      // Moves a tile to buffer b: BF16 at once, E4M3 by way of registers and put().
+      uint32_t held[2][M::kEach][2];
+      auto fetch = [&](uint32_t t, const Pages &p, uint8_t *lds, uint16_t *lds_gone) {
+        uint32_t gone = 0;
+#pragma unroll
+        for (int i = 0; i < M::kEach; ++i) {
+          const uint32_t local = 16 * wave + M::kRows * i + row, token = t + local;
+          const bool there = token < e.n && p.page[i] < a.cache.n_pages;
+          const uint64_t absent = __ballot(!there);
+          if (absent) {
+#pragma unroll
+            for (uint32_t r = 0; r < M::kRows; ++r) gone |= (uint32_t)(absent >> (r * M::kRowLanes) & 1) << (M::kRows * i + r);
+          }
+          const uint64_t off = p.page[i] * a.cache.page_stride + (token & slot_mask) * a.cache.token_stride +
+                               (place ^ (local & 7)) * 8 * M::kBytes;
+          // one that is not there is all zeros: no weight times it is NaN
+          const uint8_t *key = there ? kbase + off : a.zeros, *value = there ? vbase + off : a.zeros;
+          if constexpr (KIND == XFER_KV_BF16) {
+            typedef const __attribute__((address_space(1))) void *Global;
+            typedef __attribute__((address_space(3))) void *Lds;
+            uint8_t *to = lds + (wave * M::kEach + i) * 1024;
+            __builtin_amdgcn_global_load_lds((Global)key, (Lds)to, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((Global)value, (Lds)(to + M::kTileBytes), 16, 0, 0);
+          } else {
+            const v2u k = *reinterpret_cast<const v2u *>(key), v = *reinterpret_cast<const v2u *>(value);
+            held[0][i][0] = k.x, held[0][i][1] = k.y;
+            held[1][i][0] = v.x, held[1][i][1] = v.y;
+          }
+        }
+        if (lane == 0) lds_gone[wave] = (uint16_t)gone;
+      };
+      auto put = [&](uint8_t *lds) {
+        if constexpr (KIND == XFER_KV_E4M3) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int i = 0; i < M::kEach; ++i) {
+              const uint32_t w0 = held[kv][i][0], w1 = held[kv][i][1];
+              *reinterpret_cast<v4u *>(lds + kv * M::kTileBytes + (wave * M::kEach + i) * 1024 + lane * 16) =
+                  v4u{e4m3x2_to_bf16<false>(w0), e4m3x2_to_bf16<true>(w0), e4m3x2_to_bf16<false>(w1), e4m3x2_to_bf16<true>(w1)};
+            }
+        }
+        // What goes to LDS on its own counts as a load, which a barrier need not wait for.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+      };
+
+      const uint32_t t0 = unit * kManyUnit, t1 = t0 + take * kManyUnit;
+      fetch(t0, look_up(t0), lds0, lds_gone[0]);
+      Pages next = look_up(t0 + kManyUnit);
       float scale2 = a.scale * 1.4426950408889634f;
       if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
       // a negative scale's sign goes to the queries, so that the largest product is the largest score
       const uint32_t flip = scale2 < 0 ? 0x80008000u : 0;
       scale2 = __builtin_fabsf(scale2);
-      const uint64_t head = (uint64_t)kvh * a.group + h % a.group;
       v4u q[kSteps];
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
@@ -389,120 +450,31 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
         if (h < heads) q[k] = *reinterpret_cast<const v4u *>(a.q + (e.q_row + h / a.group) * a.q_ld + head * D + 16 * k + 8 * hf);
         q[k] ^= flip;
       }
-      const uint32_t *table = a.page_table + e.row * a.table_ld;
-      const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride + piece * 8 * M::kBytes;
-      const uint8_t *vbase = a.cache.v + kvh * a.cache.head_stride + piece * 8 * M::kBytes;
-
-      // The pages of this thread's four tokens of the tile from token t on.
-      struct Pages {
-        uint32_t page[4];
-      };
-      auto look_up = [&](uint32_t t) {
-        Pages p;
-        t += 4 * quad;
-        if (a.cache.page_log2 >= 2) {  // all four are in one
-          const uint32_t x = t < e.n ? table[t >> a.cache.page_log2] : 0;
-          for (uint32_t i = 0; i < 4; ++i) p.page[i] = x;
-        } else {
-#pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) p.page[i] = t + i < e.n ? table[(t + i) >> a.cache.page_log2] : 0;
-        }
-        return p;
-      };
-      uint32_t k[M::kEach][4][2 * M::kBytes], v[M::kEach][4][2 * M::kBytes], gone = 0;
-      auto fetch = [&](uint32_t t, const Pages &p) {
-        gone = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t token = t + 4 * quad + i;
-          const bool there = token < e.n && p.page[i] < a.cache.n_pages;
-          gone |= there ? 0 : 1u << i;
-          // one that is not there is read from the cache's first slot, and replaced
-          const uint64_t off = there ? p.page[i] * a.cache.page_stride + (token & slot_mask) * a.cache.token_stride : 0;
-#pragma unroll
-          for (int u = 0; u < M::kEach; ++u) {
-            typedef typename Piece<8 * M::kBytes>::type T;
-            if (takes_k) {
-              const T w = *reinterpret_cast<const T *>(kbase + off + u * 128 * M::kBytes);
-              __builtin_memcpy(k[u][i], &w, sizeof(T));
-            }
-            if (takes_v) {
-              const T w = *reinterpret_cast<const T *>(vbase + off + u * 128 * M::kBytes);
-              __builtin_memcpy(v[u][i], &w, sizeof(T));
-            }
-          }
-        }
-      };
-      // Eight elements as BF16.
-      auto widen = [&](const uint32_t (&w)[2 * M::kBytes]) -> v4u {
-        if constexpr (KIND == XFER_KV_BF16)
-          return v4u{w[0], w[1], w[2], w[3]};
-        else
-          return v4u{e4m3x2_to_bf16<false>(w[0]), e4m3x2_to_bf16<true>(w[0]), e4m3x2_to_bf16<false>(w[1]),
-                     e4m3x2_to_bf16<true>(w[1])};
-      };
-      auto put = [&](uint32_t b) {
-        uint8_t *keys = lds[b], *values = lds[b] + M::kTileBytes;
-        if (piece == 0 && takes_k) lds_gone[b][quad] = (uint8_t)gone;
-#pragma unroll
-        for (int u = 0; u < M::kEach; ++u) {
-          if (takes_k) {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-              *reinterpret_cast<v4u *>(keys + key_at<D>(4 * quad + i, piece + 16 * u)) = widen(k[u][i]);
-          }
-          if (takes_v) {
-            v4u x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = gone >> i & 1 ? v4u{0, 0, 0, 0} : widen(v[u][i]);
-            // tokens 8j + 4f + i of 16 are element 4j + i of piece f
-            const uint32_t c = quad / 4 * 2 + quad % 2, j = quad % 4 / 2;
-#pragma unroll
-            for (uint32_t d = 0; d < 8; ++d) {
-              const uint32_t sel = d % 2 ? 0x07060302 : 0x05040100;
-              const v2u w = {__builtin_amdgcn_perm(x[1][d / 2], x[0][d / 2], sel),
-                             __builtin_amdgcn_perm(x[3][d / 2], x[2][d / 2], sel)};
-              *reinterpret_cast<v2u *>(values + value_at(8 * (piece + 16 * u) + d, c) + 8 * j) = w;
-            }
-          }
-        }
-      };
-
       v16f o[kDims];
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[d] = v16f{};
       float mx = -INFINITY, sum = 0;
-      const uint32_t t0 = unit * kManyUnit, t1 = t0 + take * kManyUnit;
-      fetch(t0, look_up(t0));
-      Pages next = look_up(t0 + kManyUnit);
-      put(0);
-      __syncthreads();
-      uint32_t b = 0;
-#pragma unroll 1
-      for (uint32_t t = t0; t < t1; t += kManyUnit) {
-        const bool more = t + kManyUnit < t1;
-        if (more) {
-          fetch(t + kManyUnit, next);
+      put(lds0);
+      // The tile from token t on, which is in `tile`, while the next goes to `other`.
+      auto step = [&](uint32_t t, const uint8_t *tile, const uint16_t *tile_gone, uint8_t *other, uint16_t *other_gone) {
+        if (t + kManyUnit < t1) {
+          fetch(t + kManyUnit, next, other, other_gone);
           next = look_up(t + 2 * kManyUnit);
         }
-        const uint8_t *keys = lds[b], *values = lds[b] + M::kTileBytes;
-        const v4u out = *reinterpret_cast<const v4u *>(lds_gone[b]);
+        const uint8_t *keys = tile, *values = tile + M::kTileBytes;
+        const v2u out = *reinterpret_cast<const v2u *>(tile_gone);
         v16f s[2] = {v16f{}, v16f{}};
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk)
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
-            s[blk] = mfma32(*reinterpret_cast<const v4u *>(keys + key_at<D>(32 * blk + n, 2 * kk + hf)), q[kk], s[blk]);
-        const bool holes = (out.x | out.y | out.z | out.w) != 0;
-        if (holes) {
+            s[blk] = mfma32(*reinterpret_cast<const v4u *>(keys + (key0 ^ 32 * kk) + blk * 64 * D), q[kk], s[blk]);
+        if ((out.x | out.y) != 0) {
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t four = 8 * blk + 2 * (i / 4) + hf;  // tokens 32 blk + 8 (i / 4) + 4 hf + i % 4
-              const uint32_t w = out[2 * blk + i / 8];
-              if (w >> (8 * (four % 4) + i % 4) & 1) s[blk][i] = -INFINITY;
-            }
+            for (int i = 0; i < 16; ++i)
+              if (out[blk] >> (8 * (i / 4) + 4 * hf + i % 4) & 1) s[blk][i] = -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll
@@ -538,20 +510,19 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int d = 0; d < kDims; ++d) {
-              const v4u col = *reinterpret_cast<const v4u *>(values + value_at(32 * d + n, 4 * blk + 2 * st + hf));
+              const uint8_t *p = values + (value0 ^ 64 * d) + (32 * blk + 16 * st) * 2 * D;
+              const v2u lo = column4(p), hi = column4(p + 8 * 2 * D);
+              const v4u col = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
               for (int c = 0; c < PARTS; ++c) o[d] = mfma32(col, w[c][st], o[d]);
             }
         }
-        if (more) {
-          if constexpr (M::kBuffers == 1) {
-            __syncthreads();  // the tile has been read
-          } else {
-            b ^= 1;
-          }
-          put(b);
-        }
-        __syncthreads();
+        put(other);
+      };
+#pragma unroll 1
+      for (uint32_t t = t0; t < t1; t += 2 * kManyUnit) {
+        step(t, lds0, lds_gone[0], lds1, lds_gone[1]);
+        if (t + kManyUnit < t1) step(t + kManyUnit, lds1, lds_gone[1], lds0, lds_gone[0]);
       }
 
       // This wave's results: lane n, hf holds dims 32 d + 8 (i / 4) + 4 hf + i % 4 of query n.
@@ -756,7 +727,7 @@ bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
                                 int kind) {
   const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
-  return up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
+  return kZeros + up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
          s.places * head_dim * 4;
 }
 
@@ -766,7 +737,8 @@ hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStr
   a.tile = s.tile;
   a.whole0 = s.whole0;
   uint8_t *at = static_cast<uint8_t *>(workspace);
-  a.entries = reinterpret_cast<SharedEntry *>(at);
+  a.zeros = at;
+  a.entries = reinterpret_cast<SharedEntry *>(at += kZeros);
   a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + 2ull * a.groups + 2) * sizeof(SharedEntry)));
   if (s.many_workgroups) a.many = a.entries + a.rows + a.groups + 1;
   a.many_part0 = (uint32_t)s.many_part0;

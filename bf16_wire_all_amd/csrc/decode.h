@@ -89,6 +89,7 @@ struct SharedArgs {
   int out_mode;
   // set by the launch
   uint32_t tile;  // query heads that a workgroup takes at a time
+  uint8_t *zeros;
   SharedEntry *entries;  // of rows, then of groups of few query heads
   SharedEntry *many;     // of groups of many (NULL: there is none)
   SharedParts *parts;
