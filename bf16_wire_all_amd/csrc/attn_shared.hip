@@ -37,61 +37,69 @@ constexpr uint32_t kZeros = 16;  // bytes that stand for tokens that are not the
 
 // ------------------------------------------------------------------- plan
 
-// Units and tiles of heads (of a kv head) of an entry in the list whose
-// workgroups take `tile` heads and `unit` tokens at a time.
-__device__ __forceinline__ uint64_t entry_tiles(const SharedArgs &a, const SharedEntry &e, uint32_t tile) {
-  return ((uint64_t)e.q_rows * a.group + tile - 1) / tile;
-}
-__device__ __forceinline__ uint64_t entry_units(const SharedArgs &a, const SharedEntry &e, uint32_t tile, uint32_t unit) {
-  return (uint64_t)((e.n + unit - 1) / unit) * a.cache.kv_heads * entry_tiles(a, e, tile);
+// What a number of entries comes to, in the list whose workgroups take `tile`
+// heads and `unit` tokens at a time: units, and tiles of heads of a kv head.
+struct Extent {
+  uint64_t units;
+  uint32_t tiles;
+};
+__device__ __forceinline__ Extent operator+(const Extent &x, const Extent &y) { return {x.units + y.units, x.tiles + y.tiles}; }
+__device__ __forceinline__ Extent extent_of(const SharedArgs &a, const SharedEntry &e, uint32_t tile, uint32_t unit) {
+  const uint32_t tiles = (uint32_t)(((uint64_t)e.q_rows * a.group + tile - 1) / tile);
+  return {(uint64_t)((e.n + unit - 1) / unit) * a.cache.kv_heads * tiles, tiles};
 }
 
-// Inclusive scans over the threads of the plan's workgroup.
+// Sums (or maxima) over the lanes up to each, by DPP moves; lanes that a move does not reach give 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ Extent dpp(const Extent &x) {
+  const uint32_t lo = dpp<CTRL, ROWS>((uint32_t)x.units), hi = dpp<CTRL, ROWS>((uint32_t)(x.units >> 32));
+  return {(uint64_t)hi << 32 | lo, dpp<CTRL, ROWS>(x.tiles)};
+}
 template <typename T, typename F>
-__device__ __forceinline__ T block_scan(T x, T *waves, F &&op) {
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const T y = __shfl_up(x, d);
-    if ((int)lane >= d) x = op(y, x);
-  }
-  __syncthreads();
-  if (lane == 63) waves[wave] = x;
-  __syncthreads();
-  T before = waves[0];
-  for (uint32_t w = 1; w < wave; ++w) before = op(before, waves[w]);
-  return wave ? op(before, x) : x;
+__device__ __forceinline__ T wave_scan(T x, F &&op) {
+  x = op(x, dpp<0x111, 0xF>(x));
+  x = op(x, dpp<0x112, 0xF>(x));
+  x = op(x, dpp<0x114, 0xF>(x));
+  x = op(x, dpp<0x118, 0xF>(x));
+  x = op(x, dpp<0x142, 0xA>(x));
+  return op(x, dpp<0x143, 0xC>(x));
 }
 
 __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a) {
+  constexpr uint32_t kPlanWaves = kPlanThreads / 64;
   __shared__ uint32_t start[kMaxGroups + 1], prefix[kMaxGroups];
-  __shared__ unsigned long long waves[kPlanThreads / 64];
-  const uint32_t tid = threadIdx.x;
+  __shared__ uint32_t wave_top[kPlanWaves];
+  __shared__ Extent wave_sum[3][kPlanWaves];
+  const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   if (tid < kZeros / 4) reinterpret_cast<uint32_t *>(a.zeros)[tid] = 0;
+  // This thread's starts, groups and rows.  Loads that depend on nothing first.
+  const uint32_t n_starts = a.groups + 1, s_each = (n_starts + kPlanThreads - 1) / kPlanThreads;
+  const uint32_t s0 = min(tid * s_each, n_starts), s1 = min(s0 + s_each, n_starts);
+  const uint32_t g0 = min(s0, a.groups), g1 = min(s1, a.groups);
+  const uint32_t r_each = (a.rows + kPlanThreads - 1) / kPlanThreads;
+  const uint32_t r0 = min(tid * r_each, a.rows), r1 = min(r0 + r_each, a.rows);
+  const uint32_t first_len = r0 < r1 ? a.lens[r0] : 0, first_shared = g0 < g1 ? a.shared[g0] : 0;
   // The groups' first rows: a start below the one before counts as that one,
   // so that no row is in two groups, whatever the caller's numbers are.
-  {
-    const uint32_t n = a.groups + 1, each = (n + kPlanThreads - 1) / kPlanThreads;
-    const uint32_t i0 = min(tid * each, n), i1 = min(i0 + each, n);
-    uint32_t top = 0;
-    auto given = [&](uint32_t i) { return a.groups ? min(a.starts[i], a.rows) : a.rows; };
-    for (uint32_t i = i0; i < i1; ++i) top = max(top, given(i));
-    auto *w = reinterpret_cast<uint32_t *>(waves);
-    uint32_t mine = block_scan(top, w, [](uint32_t x, uint32_t y) { return max(x, y); });
-    // what comes before this thread's: the inclusive result of the thread before
-    const uint32_t before = __shfl_up(mine, 1);
-    uint32_t run = tid % 64 ? before : 0;
-    if (tid % 64 == 0)
-      for (uint32_t i = 0; i < tid / 64; ++i) run = max(run, w[i]);
-    for (uint32_t i = i0; i < i1; ++i) {
-      run = max(run, given(i));
-      start[i] = run;
-    }
-  }
+  auto given = [&](uint32_t i) { return a.groups ? min(a.starts[i], a.rows) : a.rows; };
+  auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
+  uint32_t top = 0;
+  for (uint32_t i = s0; i < s1; ++i) start[i] = top = max(top, given(i));
+  const uint32_t through = wave_scan(top, larger);
+  if (lane == 63) wave_top[wave] = through;
   __syncthreads();
-  for (uint32_t g = tid; g < a.groups; g += kPlanThreads) {
+  uint32_t before = __shfl_up(through, 1);  // by all lanes: one that sits out gives nothing
+  if (lane == 0) before = 0;
+  for (uint32_t w = 0; w < wave; ++w) before = max(before, wave_top[w]);
+  for (uint32_t i = s0; i < s1; ++i) start[i] = max(start[i], before);
+  __syncthreads();
+  for (uint32_t g = g0; g < g1; ++g) {
     const uint32_t row = start[g], n = start[g + 1] - row;
-    uint32_t p = n > 1 ? min(a.shared[g], a.max_len) : 0;
+    uint32_t p = n > 1 ? min(g == g0 ? first_shared : a.shared[g], a.max_len) : 0;
     if (p) p = min(p, a.lens[row]);  // the first row's pages are read
     prefix[g] = p;
   }
@@ -108,7 +116,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
   };
   auto of_row = [&](uint32_t i) {
     SharedEntry e{};
-    uint32_t lo = 0, hi = a.groups + 1;  // the first start past row i
+    uint32_t lo = 0, hi = n_starts;  // the first start past row i
     while (lo < hi) {
       const uint32_t mid = (lo + hi) / 2;
       if (start[mid] <= i)
@@ -116,7 +124,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
       else
         hi = mid;
     }
-    const uint32_t len = min(a.lens[i], a.max_len);
+    const uint32_t len = min(i == r0 ? first_len : a.lens[i], a.max_len);
     const uint32_t p = lo > 0 && lo <= a.groups ? prefix[lo - 1] : 0;
     e.first = p <= len ? p : 0;
     e.n = len - e.first;
@@ -125,31 +133,49 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
     e.group = e.first ? lo - 1 : kNoGroup;
     return e;
   };
-  // Lists of n entries: where each one's units and parts begin.
-  auto list = [&](SharedEntry *to, uint32_t n, uint32_t tile, uint32_t unit, uint32_t part0, auto &&entry) {
-    const uint32_t each = (n + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, n), i1 = min(i0 + each, n);
-    uint64_t units = 0, tiles = 0;
-    for (uint32_t i = i0; i < i1; ++i) {
-      const SharedEntry e = entry(i);
-      units += entry_units(a, e, tile, unit);
-      tiles += entry_tiles(a, e, tile);
-    }
-    auto add = [](unsigned long long x, unsigned long long y) { return x + y; };
-    uint64_t unit0 = block_scan((unsigned long long)units, waves, add) - units;
-    uint64_t tile0 = block_scan((unsigned long long)tiles, waves, add) - tiles;
-    for (uint32_t i = i0; i < i1; ++i) {
-      SharedEntry e = entry(i);
-      e.unit0 = unit0;
-      e.part0 = part0 + (uint32_t)(tile0 * a.cache.kv_heads);
-      to[i] = e;
-      unit0 += entry_units(a, e, tile, unit);
-      tile0 += entry_tiles(a, e, tile);
-    }
-    if (i0 < n && i1 == n) to[n].unit0 = unit0;
+  // Where each entry's units and parts begin: rows, groups of few heads after them, and groups of many.
+  Extent mine[3] = {};
+  for (uint32_t i = r0; i < r1; ++i) mine[0] = mine[0] + extent_of(a, of_row(i), a.tile, kUnit);
+  for (uint32_t g = g0; g < g1; ++g) {
+    mine[1] = mine[1] + extent_of(a, of_group(g, false), a.tile, kUnit);
+    mine[2] = mine[2] + extent_of(a, of_group(g, true), kManyHeads, kManyUnit);
+  }
+  Extent at[3], all[3];
+  auto add = [](const Extent &x, const Extent &y) { return x + y; };
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    at[k] = wave_scan(mine[k], add);
+    if (lane == 63) wave_sum[k][wave] = at[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const Extent waves = wave_scan(lane < kPlanWaves ? wave_sum[k][lane] : Extent{}, add);  // up to each wave
+    auto of_wave = [&](uint32_t w) -> Extent {
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)waves.units, w),
+                     hi = __builtin_amdgcn_readlane((uint32_t)(waves.units >> 32), w);
+      return {(uint64_t)hi << 32 | lo, (uint32_t)__builtin_amdgcn_readlane(waves.tiles, w)};
+    };
+    all[k] = of_wave(kPlanWaves - 1);
+    const Extent before_wave = wave ? of_wave(wave - 1) : Extent{};
+    at[k] = {at[k].units - mine[k].units + before_wave.units, at[k].tiles - mine[k].tiles + before_wave.tiles};
+  }
+  at[1] = at[1] + all[0];
+  auto put = [&](SharedEntry &to, SharedEntry e, Extent &from, uint32_t part0, uint32_t tile, uint32_t unit) {
+    e.unit0 = from.units;
+    e.part0 = part0 + from.tiles * a.cache.kv_heads;
+    to = e;
+    from = from + extent_of(a, e, tile, unit);
   };
-  list(a.entries, a.rows + a.groups, a.tile, kUnit, 0,
-       [&](uint32_t i) { return i < a.rows ? of_row(i) : of_group(i - a.rows, false); });
-  if (a.many) list(a.many, a.groups, kManyHeads, kManyUnit, a.many_part0, [&](uint32_t g) { return of_group(g, true); });
+  for (uint32_t i = r0; i < r1; ++i) put(a.entries[i], of_row(i), at[0], 0, a.tile, kUnit);
+  for (uint32_t g = g0; g < g1; ++g) {
+    put(a.entries[a.rows + g], of_group(g, false), at[1], 0, a.tile, kUnit);
+    if (a.many) put(a.many[g], of_group(g, true), at[2], a.many_part0, kManyHeads, kManyUnit);
+  }
+  if (tid == 0) {
+    a.entries[a.rows + a.groups].unit0 = all[0].units + all[1].units;
+    if (a.many) a.many[a.groups].unit0 = all[2].units;
+  }
 }
 
 // ------------------------------------------------------------------- walk
@@ -463,12 +489,33 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
         }
         const uint8_t *keys = tile, *values = tile + M::kTileBytes;
         const v2u out = *reinterpret_cast<const v2u *>(tile_gone);
+        // Operands are read from LDS a group of products ahead; the barriers keep the compiler from reading each where it is used.
         v16f s[2] = {v16f{}, v16f{}};
+        v4u key[2][4];
+        auto read_keys = [&](int g) {
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk)
+          for (int i = 0; i < 4; ++i)
+            key[g % 2][i] = *reinterpret_cast<const v4u *>(keys + (key0 ^ 32 * (2 * g + i / 2)) + i % 2 * 64 * D);
+        };
+        read_keys(0);
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk)
-            s[blk] = mfma32(*reinterpret_cast<const v4u *>(keys + (key0 ^ 32 * kk) + blk * 64 * D), q[kk], s[blk]);
+        for (int g = 0; g < kSteps / 2; ++g) {
+          if (g + 1 < kSteps / 2) read_keys(g + 1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i % 2] = mfma32(key[g % 2][i], q[2 * g + i / 2], s[i % 2]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        v4u value[2][kDims];
+        auto read_values = [&](int g) {  // 16 tokens
+#pragma unroll
+          for (int d = 0; d < kDims; ++d) {
+            const uint8_t *p = values + (value0 ^ 64 * d) + 16 * g * 2 * D;
+            const v2u lo = column4(p), hi = column4(p + 8 * 2 * D);
+            value[g % 2][d] = v4u{lo.x, lo.y, hi.x, hi.y};
+          }
+        };
+        read_values(0);
         if ((out.x | out.y) != 0) {
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
@@ -476,27 +523,32 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
             for (int i = 0; i < 16; ++i)
               if (out[blk] >> (8 * (i / 4) + 4 * hf + i % 4) & 1) s[blk][i] = -INFINITY;
         }
-        float top = -INFINITY;
+        // Scores above the running maximum; where one passes it by kRaise, the maximum moves and they with it.
+        float base = mx == -INFINITY ? 0.0f : mx, top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
-        top *= scale2;
-        if (__any(top > mx + kRaise)) {
-          top = fmaxf(top, __shfl_xor(top, 32));
+        for (int i = 0; i < 16; ++i) {
+          s[0][i] = fmaf(s[0][i], scale2, -base);
+          s[1][i] = fmaf(s[1][i], scale2, -base);
+          top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
+        }
+        if (__any(top + base > mx + kRaise)) {
+          top = fmaxf(top, __shfl_xor(top, 32)) + base;
           const float raised = fmaxf(mx, top);
           const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - raised);
+          const float by = base - (raised == -INFINITY ? 0.0f : raised);
           mx = raised;
           sum *= f;
 #pragma unroll
           for (int d = 0; d < kDims; ++d) o[d] *= f;
+          s[0] += by;
+          s[1] += by;
         }
-        const float base = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           v4u w[PARTS][2];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float x0 = __builtin_amdgcn_exp2f(fmaf(s[blk][2 * i], scale2, -base));
-            float x1 = __builtin_amdgcn_exp2f(fmaf(s[blk][2 * i + 1], scale2, -base));
+            float x0 = __builtin_amdgcn_exp2f(s[blk][2 * i]), x1 = __builtin_amdgcn_exp2f(s[blk][2 * i + 1]);
             sum += x0 + x1;
 #pragma unroll
             for (int c = 0; c < PARTS; ++c) {
@@ -507,15 +559,16 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
             }
           }
 #pragma unroll
-          for (int st = 0; st < 2; ++st)
+          for (int st = 0; st < 2; ++st) {
+            const int g = 2 * blk + st;
+            if (g < 3) read_values(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int d = 0; d < kDims; ++d) {
-              const uint8_t *p = values + (value0 ^ 64 * d) + (32 * blk + 16 * st) * 2 * D;
-              const v2u lo = column4(p), hi = column4(p + 8 * 2 * D);
-              const v4u col = {lo.x, lo.y, hi.x, hi.y};
+            for (int c = 0; c < PARTS; ++c)
 #pragma unroll
-              for (int c = 0; c < PARTS; ++c) o[d] = mfma32(col, w[c][st], o[d]);
-            }
+              for (int d = 0; d < kDims; ++d) o[d] = mfma32(value[g % 2][d], w[c][st], o[d]);
+            if (g == 0) __builtin_amdgcn_sched_barrier(0);
+          }
         }
         put(other);
       };
