@@ -24,7 +24,6 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kUnit = kTile * kWaves;       // tokens of a unit
 constexpr uint32_t kComputeUnits = 256;
-constexpr uint32_t kMaxParts = 2 * 2 * kComputeUnits;  // of a (row, query head)
 constexpr uint32_t kXcds = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, since the memory bounds the walk
@@ -174,7 +173,15 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
   }
   if (tid == 0) {
     a.entries[a.rows + a.groups].unit0 = all[0].units + all[1].units;
-    if (a.many) a.many[a.groups].unit0 = all[2].units;
+    if (a.many) {
+      a.many[a.groups].unit0 = all[2].units;
+      // Both lists' workgroups are to end together, by what a unit of each costs.
+      const double few = (double)(all[0].units + all[1].units) * a.unit_cost, many = (double)all[2].units * a.many_unit_cost;
+      uint32_t n = few + many > 0 ? (uint32_t)(a.places_of_xcd * (many / (few + many)) + 0.5) : 0;
+      if (all[2].units) n = max(n, 1u);
+      if (few > 0) n = min(n, a.places_of_xcd - 1);
+      *a.many_places = n;
+    }
   }
 }
 
@@ -184,26 +191,37 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
 // its first part's slot (kWhole: one workgroup did it all), and how many parts.
 constexpr uint32_t kWhole = 0xFFFFFFFFu;
 
+template <int D, int TILES>
+struct WalkLds {
+  static constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
+  float o[kWaves][16][D + kPad];
+  float m[TILES][kWaves][16], l[TILES][kWaves][16];
+};
+
+// The entry that unit `from` of a list falls to; by all threads.
+__device__ __forceinline__ uint32_t entry_at(const SharedEntry *entries, uint32_t n, uint64_t from) {
+  __shared__ uint32_t start;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+    if (entries[i].unit0 <= from && from < entries[i + 1].unit0) start = i;
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(start);
+}
+
+// The run of workgroup wg of n_wg.
 template <int D, int KIND, int TILES>
-__global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void shared_walk_kernel(SharedArgs a) {
+__device__ __forceinline__ void walk(const SharedArgs &a, uint32_t wg, uint32_t n_wg, WalkLds<D, TILES> &lds) {
   using L = Layout<D, KIND>;
   using R = Residence<D, KIND, TILES>;
-  constexpr int MR = TILES, kPad = 4;
+  constexpr int MR = TILES;
   constexpr uint32_t kHeads = 16 * TILES;
-  __shared__ float lds_o[kWaves][16][D + kPad];
-  __shared__ float lds_all_m[MR][kWaves][16], lds_all_l[MR][kWaves][16];
-  __shared__ uint32_t start;
+  auto &lds_o = lds.o;
+  auto &lds_all_m = lds.m;
+  auto &lds_all_l = lds.l;
   const uint32_t n_entries = a.rows + a.groups;
-  // Neighbouring runs on one XCD: its L2 then serves the tokens that the heads
-  // of an entry have in common.
-  const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-  const uint64_t all = a.entries[n_entries].unit0, per = (all + gridDim.x - 1) / gridDim.x, from = wg * per;
+  const uint64_t all = a.entries[n_entries].unit0, per = (all + n_wg - 1) / n_wg, from = wg * per;
   if (from >= all) return;
   uint64_t left = min(per, all - from);
-  for (uint32_t i = threadIdx.x; i < n_entries; i += kThreads)
-    if (a.entries[i].unit0 <= from && from < a.entries[i + 1].unit0) start = i;
-  __syncthreads();
-  uint32_t index = __builtin_amdgcn_readfirstlane(start);
+  uint32_t index = entry_at(a.entries, n_entries, from);
   SharedEntry e = a.entries[index];
   uint64_t at = from - e.unit0;
 
@@ -340,7 +358,7 @@ struct Many {
   static constexpr int kEach = D / 32;                             // pieces of keys, and of values, of a thread
   static constexpr uint32_t kRowLanes = D / 8;                     // that hold a row of pieces
   static constexpr uint32_t kRows = 64 / kRowLanes;                // rows that a wave moves at once
-  static constexpr int kPerSimd = D == 256 ? 1 : 2;
+  static constexpr int kPerSimd = D == 256 ? 1 : D == 128 ? 2 : 3;
   static constexpr uint32_t kTileBytes = kManyUnit * D * 2;        // of keys, and of values
 };
 
@@ -356,24 +374,19 @@ __device__ __forceinline__ v2u column4(const uint8_t *p) {
   return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p));
 }
 
+// The run of workgroup wg of n_wg; lds0 and lds1 are two variables, not one of two: then the compiler knows that what
+// is on its way to one does not change the other.
 template <int D, int KIND, int PARTS>
-__global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_many_kernel(SharedArgs a) {
+__device__ __forceinline__ void walk_many(const SharedArgs &a, uint32_t wg, uint32_t n_wg, uint8_t *lds0, uint8_t *lds1) {
   using M = Many<D, KIND>;
   constexpr int kDims = D / 32;   // blocks of dims
   constexpr int kSteps = D / 16;  // of a score
-  // two variables, not one of two: then the compiler knows that what is on its way to one does not change the other
-  __shared__ __align__(16) uint8_t lds0[2 * M::kTileBytes], lds1[2 * M::kTileBytes];
   __shared__ __align__(8) uint16_t lds_gone[2][kWaves];  // a bit for each token of 16 that is not there
-  __shared__ uint32_t start;
-  const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-  const uint64_t all = a.many[a.groups].unit0, share = (all + gridDim.x - 1) / gridDim.x;
+  const uint64_t all = a.many[a.groups].unit0, share = (all + n_wg - 1) / n_wg;
   const uint64_t per = share < kManyLeast ? kManyLeast : share, from = wg * per;
   if (from >= all) return;
   uint64_t left = min(per, all - from);
-  for (uint32_t i = threadIdx.x; i < a.groups; i += kThreads)
-    if (a.many[i].unit0 <= from && from < a.many[i + 1].unit0) start = i;
-  __syncthreads();
-  uint32_t index = __builtin_amdgcn_readfirstlane(start);
+  uint32_t index = entry_at(a.many, a.groups, from);
   SharedEntry e = a.many[index];
   uint64_t at = from - e.unit0;
 
@@ -616,19 +629,46 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_ma
   }
 }
 
+// Neighbouring runs on one XCD: its L2 then serves the tokens that the heads of an entry have in common.
+template <int D, int KIND, int TILES>
+__global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void shared_walk_kernel(SharedArgs a) {
+  __shared__ WalkLds<D, TILES> lds;
+  walk<D, KIND, TILES>(a, blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds, gridDim.x, lds);
+}
+
+// Both lists at once, so that one's loads and the other's products share the compute units: of the workgroups
+// that are resident, as many take the list of many heads as the plan found, spread evenly over the others.
+template <int D, int KIND, int TILES, int PARTS>
+__global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_both_kernel(SharedArgs a) {
+  constexpr uint32_t kTile = 2 * Many<D, KIND>::kTileBytes;
+  __shared__ __align__(16) uint8_t lds0[kTile < sizeof(WalkLds<D, TILES>) ? sizeof(WalkLds<D, TILES>) : kTile];
+  __shared__ __align__(16) uint8_t lds1[kTile];
+  const uint32_t xcd = blockIdx.x % kXcds, place = blockIdx.x / kXcds, places = gridDim.x / kXcds;
+  const uint32_t many = *a.many_places;  // of an XCD's places
+  const uint32_t before = place * many / places;
+  if ((place + 1) * many / places > before)
+    walk_many<D, KIND, PARTS>(a, xcd * many + before, kXcds * many, lds0, lds1);
+  else
+    walk<D, KIND, TILES>(a, xcd * (places - many) + place - before, kXcds * (places - many),
+                         *reinterpret_cast<WalkLds<D, TILES> *>(lds0));
+}
+
 // ------------------------------------------------------------------- join
 
-// One workgroup for each (row, query head): its parts of the shared tokens, then
-// of its own.
-template <int D>
+// kJoinWaves (or one) for each (row, query head): its parts of the shared tokens, then of its own, each scaled to
+// the largest maximum, in a fixed order.  One wave where there are many heads to join, since each has few parts then
+// (6336 heads of 64: 6 us with a wave each, 18 with four); four where few heads are cut into many parts.
+constexpr uint32_t kJoinHeads = 4096;  // from which on a wave takes a whole one
+
+template <int D, int WAVES>
 __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
-  constexpr uint32_t kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  constexpr int kEach = kMaxParts / kThreads;  // parts of a thread
-  __shared__ float lds_w[kMaxParts];
-  __shared__ float lds_red[2][kWaves];
-  __shared__ v4f lds_o[kAtOnce][kLanes];
-  const uint32_t row = blockIdx.x / a.q_heads, head = blockIdx.x % a.q_heads, tid = threadIdx.x;
-  const uint32_t kvh = head / a.group, h = head % a.group;
+  constexpr uint32_t kLanes = D / 4, kAtOnce = 64 / kLanes;  // of a part, and parts of a wave at once
+  __shared__ float lds_top[kWaves], lds_total[kWaves];
+  __shared__ v4f lds_o[WAVES][kLanes];
+  const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) % WAVES;
+  const uint32_t item = WAVES == 1 ? blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : blockIdx.x;
+  if (item >= a.rows * a.q_heads) return;  // by waves that share nothing
+  const uint32_t row = item / a.q_heads, head = item % a.q_heads, kvh = head / a.group, h = head % a.group;
   const SharedEntry own = a.entries[row];
   struct Source {
     uint32_t n;                 // parts
@@ -664,47 +704,63 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
     return k ? s.at1 + k * s.stride : s.at0;
   };
 
-  float m[kEach], l[kEach], top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t p = i * kThreads + tid;
-    m[i] = -INFINITY;
-    l[i] = 0;
-    if (p < n) {
-      const uint64_t at = place(p);
-      m[i] = a.part_ml[2 * at];
-      l[i] = a.part_ml[2 * at + 1];
-    }
-    top = fmaxf(top, m[i]);
+  // Lane l of wave w has part p0 + l * WAVES + w of every 64 * WAVES.
+  float top = -INFINITY;
+#pragma unroll 1
+  for (uint32_t p0 = 0; p0 < n; p0 += 64 * WAVES) {
+    const uint32_t p = p0 + lane * WAVES + wave;
+    top = fmaxf(top, p < n ? a.part_ml[2 * place(p)] : -INFINITY);
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if (tid % 64 == 0) lds_red[0][tid / 64] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(lds_red[0][0], lds_red[0][1]), fmaxf(lds_red[0][2], lds_red[0][3]));
-  float total = 0;
+  if constexpr (WAVES > 1) {
+    if (lane == 0) lds_top[wave] = top;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t p = i * kThreads + tid;
-    const float f = m[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
-    // not 0: a part's infinity stays one, however small its weights
-    if (p < n) lds_w[p] = f == 0.0f ? __uint_as_float(1) : f;
-    total += m[i] == -INFINITY ? l[i] : l[i] * f;
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, lds_top[w]);
+  }
+  float total = 0;
+  v4f r = {0, 0, 0, 0};
+  const uint32_t sub = lane / kLanes, d4 = lane % kLanes;
+#pragma unroll 1
+  for (uint32_t p0 = 0; p0 < n; p0 += 64 * WAVES) {
+    const uint32_t p = p0 + lane * WAVES + wave;
+    float f = 0;
+    if (p < n) {
+      const uint64_t at = place(p);
+      const float m = a.part_ml[2 * at], l = a.part_ml[2 * at + 1];
+      f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+      total += m == -INFINITY ? l : l * f;
+      if (f == 0.0f) f = __uint_as_float(1);  // a part's infinity stays one, however small its weights
+    }
+    const uint32_t count = wave < n - p0 ? min((n - p0 - wave + WAVES - 1) / WAVES, 64u) : 0;
+#pragma unroll 4
+    for (uint32_t k0 = 0; k0 < count; k0 += kAtOnce) {
+      const uint32_t k = k0 + sub;
+      const float fk = __shfl(f, k);
+      if (k < count) r += fk * *reinterpret_cast<const v4f *>(a.part_o + place(p0 + k * WAVES + wave) * D + 4 * d4);
+    }
   }
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-  if (tid % 64 == 0) lds_red[1][tid / 64] = total;
-  __syncthreads();
-  const uint32_t d4 = tid % kLanes, p0 = tid / kLanes;
-  v4f r = {0, 0, 0, 0};
-#pragma unroll 4
-  for (uint32_t p = p0; p < n; p += kAtOnce) r += lds_w[p] * *reinterpret_cast<const v4f *>(a.part_o + place(p) * D + 4 * d4);
-  lds_o[p0][d4] = r;
-  __syncthreads();
-  if (p0 != 0) return;
+  for (uint32_t d = kLanes; d < 64; d *= 2)
 #pragma unroll
-  for (uint32_t s = 1; s < kAtOnce; ++s) r += lds_o[s][d4];
-  total = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
+    for (int i = 0; i < 4; ++i) r[i] += __shfl_xor(r[i], d);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+  if constexpr (WAVES > 1) {
+    if (lane == 0) lds_total[wave] = total;
+    if (sub == 0) lds_o[wave][d4] = r;
+    __syncthreads();
+    if (wave != 0) return;
+    total = lds_total[0];
+    if (sub == 0) {
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) r += lds_o[w][d4];
+    }
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) total += lds_total[w];
+  }
+  if (sub != 0) return;
   const float v_scale = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.0f;
   r = total == 0.0f ? v4f{0, 0, 0, 0} : r * (v_scale / total);
   const uint64_t at = row * a.out_ld + (uint64_t)head * D + 4 * d4;
@@ -718,12 +774,16 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
 
 template <int D, int KIND>
 hipError_t launch_kind(const SharedArgs &a, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
-  hipError_t e = a.tile == 16 ? launch(shared_walk_kernel<D, KIND, 1>, dim3(workgroups), dim3(kThreads), 0, stream, a)
-                              : launch(shared_walk_kernel<D, KIND, 2>, dim3(workgroups), dim3(kThreads), 0, stream, a);
-  if (e != hipSuccess || !a.many) return e;
-  return a.out_mode == XFER_OUT_F32
-             ? launch(shared_many_kernel<D, KIND, 3>, dim3(many_workgroups), dim3(kThreads), 0, stream, a)
-             : launch(shared_many_kernel<D, KIND, 2>, dim3(many_workgroups), dim3(kThreads), 0, stream, a);
+  const dim3 block(kThreads);
+  if (!a.many)
+    return a.tile == 16 ? launch(shared_walk_kernel<D, KIND, 1>, dim3(workgroups), block, 0, stream, a)
+                        : launch(shared_walk_kernel<D, KIND, 2>, dim3(workgroups), block, 0, stream, a);
+  const dim3 grid(many_workgroups);
+  if (a.out_mode == XFER_OUT_F32)
+    return a.tile == 16 ? launch(shared_both_kernel<D, KIND, 1, 3>, grid, block, 0, stream, a)
+                        : launch(shared_both_kernel<D, KIND, 2, 3>, grid, block, 0, stream, a);
+  return a.tile == 16 ? launch(shared_both_kernel<D, KIND, 1, 2>, grid, block, 0, stream, a)
+                      : launch(shared_both_kernel<D, KIND, 2, 2>, grid, block, 0, stream, a);
 }
 template <int D>
 hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
@@ -732,7 +792,10 @@ hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, uint32
   e = kind == XFER_KV_BF16 ? launch_kind<D, XFER_KV_BF16>(a, workgroups, many_workgroups, stream)
                            : launch_kind<D, XFER_KV_E4M3>(a, workgroups, many_workgroups, stream);
   if (e != hipSuccess) return e;
-  return launch(shared_join_kernel<D>, dim3(a.rows * a.q_heads), dim3(kThreads), 0, stream, a);
+  const uint32_t items = a.rows * a.q_heads;
+  if (items >= kJoinHeads)
+    return launch(shared_join_kernel<D, 1>, dim3((items + kWaves - 1) / kWaves), dim3(kThreads), 0, stream, a);
+  return launch(shared_join_kernel<D, kWaves>, dim3(items), dim3(kThreads), 0, stream, a);
 }
 
 struct Shape {
@@ -751,7 +814,7 @@ uint32_t per_simd(uint32_t head_dim, uint32_t tile) {
 Shape shape_of(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind) {
   Shape s{};
   // 32 heads at a time where a row or the average group has more than 16
-  s.tile = group > 16 || (groups && (uint64_t)rows * group > 16ull * groups) ? 32 : 16;
+  s.tile = group > 16 ? 32 : 16;
   s.workgroups = kComputeUnits * (kind == XFER_KV_BF16 ? per_simd<XFER_KV_BF16>(head_dim, s.tile)
                                                        : per_simd<XFER_KV_E4M3>(head_dim, s.tile));
   const uint64_t row_tiles = (group + s.tile - 1) / s.tile;
@@ -760,7 +823,9 @@ Shape shape_of(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group
   s.many_place0 = 2ull * s.workgroups * s.tile;
   s.whole0 = s.many_place0;
   if (groups && (uint64_t)rows * group > kFewHeads) {  // some group may be that large
-    s.many_workgroups = kComputeUnits * (head_dim == 256 ? 1 : 2);
+    s.workgroups = s.many_workgroups = kComputeUnits * (head_dim == 256 ? 1 : head_dim == 128 ? 2 : 3);
+    s.many_place0 = 2ull * s.workgroups * s.tile;
+    s.whole0 = s.many_place0;
     s.parts += kv_heads * ((uint64_t)rows * group / kManyHeads + groups);
     s.whole0 += 2ull * s.many_workgroups * kManyHeads;
   }
@@ -780,7 +845,7 @@ bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
                                 int kind) {
   const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
-  return kZeros + up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
+  return 2 * kZeros + up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
          s.places * head_dim * 4;
 }
 
@@ -791,7 +856,11 @@ hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStr
   a.whole0 = s.whole0;
   uint8_t *at = static_cast<uint8_t *>(workspace);
   a.zeros = at;
-  a.entries = reinterpret_cast<SharedEntry *>(at += kZeros);
+  a.many_places = reinterpret_cast<uint32_t *>(at + kZeros);
+  a.places_of_xcd = s.many_workgroups / kXcds;
+  a.unit_cost = kUnit * 2 * a.cache.head_dim * (kind == XFER_KV_BF16 ? 2 : 1) / 64;
+  a.many_unit_cost = a.cache.head_dim * (a.out_mode == XFER_OUT_F32 ? 4 : 3) * 2;
+  a.entries = reinterpret_cast<SharedEntry *>(at += 2 * kZeros);
   a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + 2ull * a.groups + 2) * sizeof(SharedEntry)));
   if (s.many_workgroups) a.many = a.entries + a.rows + a.groups + 1;
   a.many_part0 = (uint32_t)s.many_part0;

@@ -90,6 +90,8 @@ struct SharedArgs {
   // set by the launch
   uint32_t tile;  // query heads that a workgroup takes at a time
   uint8_t *zeros;
+  uint32_t *many_places;  // workgroups of each XCD that take groups of many query heads
+  uint32_t places_of_xcd, unit_cost, many_unit_cost;
   SharedEntry *entries;  // of rows, then of groups of few query heads
   SharedEntry *many;     // of groups of many (NULL: there is none)
   SharedParts *parts;
