@@ -22,6 +22,7 @@
 //      and the hardware's power.  m c is rounded to binary32; what that moves
 //      all weights by is a factor that is put right afterwards.
 // Thread sums are binary32 (of up to 64 elements), everything above binary64.
+// The slices' sums are put together at the end, a slice to a lane.
 //
 // Where rows are few, each is cut into several workgroups' parts, which a
 // second launch folds: (largest, R, sum w x) scaled to the row's largest.
@@ -36,8 +37,10 @@ constexpr int kRounds = 8;                                // vectors of 8 elemen
 constexpr uint32_t kSliceCols = kThreads * 8 * kRounds;   // 16,384
 constexpr uint32_t kMinCols = 2048;                       // of a slice where rows are cut into parts
 constexpr uint32_t kWorkgroups = 1024;                    // that a call is cut up for
-constexpr uint32_t kMaxParts = 128;                       // of a row: two for each lane of the fold's wave
+constexpr uint32_t kMaxParts = 128;                       // of a row
+constexpr uint32_t kMaxSlices = 2 * (kArgmaxMaxShardCols / kSliceCols);
 constexpr uint32_t kList = 1024;                          // elements that reach the bound, at most
+static_assert(kList >= kMaxTop * kMaxTop, "the fold's, of as many parts as elements asked for");
 constexpr uint32_t kMasked = 0xFF80FF80u;
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
@@ -64,9 +67,18 @@ __device__ __forceinline__ float as_float(uint32_t w, int h) {
   return __uint_as_float(h ? w & 0xFFFF0000u : w << 16);
 }
 
+// Over the lanes of a wave, by DPP moves; lanes that a move does not reach give `old`.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int dpp(int x, int old) {
   return __builtin_amdgcn_update_dpp(old, x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp(uint64_t x) {
+  return (uint64_t)(uint32_t)dpp<CTRL, ROWS>((int)(x >> 32), 0) << 32 | (uint32_t)dpp<CTRL, ROWS>((int)(uint32_t)x, 0);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+  return __longlong_as_double((long long)dpp<CTRL, ROWS>((uint64_t)__double_as_longlong(x)));
 }
 __device__ __forceinline__ int wave_max(int x) {
   constexpr int kLow = -0x7FFFFFFF - 1;
@@ -78,15 +90,27 @@ __device__ __forceinline__ int wave_max(int x) {
   x = max(x, dpp<0x143, 0xC>(x, kLow));
   return __builtin_amdgcn_readlane(x, 63);
 }
+__device__ __forceinline__ uint64_t read_lane(uint64_t x, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
 __device__ __forceinline__ uint64_t wave_max(uint64_t x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x = max(x, (uint64_t)__shfl_xor((unsigned long long)x, d));
-  return x;
+  x = max(x, dpp<0x111, 0xF>(x));
+  x = max(x, dpp<0x112, 0xF>(x));
+  x = max(x, dpp<0x114, 0xF>(x));
+  x = max(x, dpp<0x118, 0xF>(x));
+  x = max(x, dpp<0x142, 0xA>(x));
+  x = max(x, dpp<0x143, 0xC>(x));
+  return read_lane(x, 63);
 }
 __device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
-  return x;
+  x += dpp<0x111, 0xF>(x);
+  x += dpp<0x112, 0xF>(x);
+  x += dpp<0x114, 0xF>(x);
+  x += dpp<0x118, 0xF>(x);
+  x += dpp<0x142, 0xA>(x);
+  x += dpp<0x143, 0xC>(x);
+  return __longlong_as_double((long long)read_lane((uint64_t)__double_as_longlong(x), 63));
 }
 
 // What a set of elements comes to: its first element, and of all others the sum
@@ -95,21 +119,50 @@ struct Sum {
   double rest, wx;
   uint64_t top;
 };
+// The same of a slice as it was added up: `equal` elements have the first one's
+// value, the others' sums are off by the rounding of m c (where c is not 0) and
+// count in powers of two.
+struct Raw {
+  float c, equal;
+  double rest, wx;
+  uint64_t top;
+};
 // (l - m) / T of a row, in binary64.
 __device__ __forceinline__ double scaled(float l, float m, float T) {
   if (l == m) return 0.0;
   return __builtin_isinf(m) ? -INFINITY : ((double)l - (double)m) / (double)T;
 }
-__device__ __forceinline__ Sum join(const Sum &a, const Sum &b, float T) {
-  if (!a.top || !b.top) return a.top ? a : b;
-  const Sum &hi = a.top > b.top ? a : b, &lo = a.top > b.top ? b : a;
-  const double x = scaled(value_of(ord_of(lo.top)), value_of(ord_of(hi.top)), T), f = exp(x);
-  Sum s = hi;
-  if (f > 0) {  // not so where x is -inf
-    s.rest += f * (1.0 + lo.rest);
-    s.wx += f * (lo.wx + (1.0 + lo.rest) * x);
+__device__ __forceinline__ Sum settled(const Raw &r) {
+  Sum s = {(double)r.equal - 1.0, 0, r.top};
+  if (r.c != 0.0f) {
+    const float m = value_of(ord_of(r.top));
+    const double off = (double)(m * r.c) - (double)m * (double)r.c;  // every power is too small by this
+    const double f = exp2(off);
+    s.rest += f * r.rest;
+    s.wx = f * (r.wx + off * r.rest) * 0.6931471805599453;
+  } else {
+    s.rest += r.rest;
+    s.wx = r.wx;
   }
   return s;
+}
+// The sums of all lanes' sets, by a whole wave.  (Greedy: the first element alone.)
+__device__ __forceinline__ Sum join(Sum s, float T) {
+  const uint64_t top = wave_max(s.top);
+  Sum all = {0, 0, top};
+  if (!top || !(T > 0.0f)) return all;
+  double rest = s.rest, wx = s.wx;
+  if (s.top != top) {
+    const double x = s.top ? scaled(value_of(ord_of(s.top)), value_of(ord_of(top)), T) : -INFINITY, f = exp(x);
+    rest = wx = 0;
+    if (f > 0) {  // not so where x is -inf
+      rest = f * (1.0 + s.rest);
+      wx = f * (s.wx + (1.0 + s.rest) * x);
+    }
+  }
+  all.rest = wave_sum(rest);
+  all.wx = wave_sum(wx);
+  return all;
 }
 
 // The next BF16 number above v (NaN above +inf, which nothing reaches).
@@ -139,8 +192,34 @@ __device__ __forceinline__ uint64_t token_key(const LogprobArgs &a, uint32_t row
   return 0;
 }
 
-// The row's results from its sum, its tokens' ranks and its best elements; by
-// the threads of a workgroup.
+// The sums of n slices or parts, by a whole wave.
+__device__ __forceinline__ Sum join_slices(const Raw *r, uint32_t n, float T) {
+  Sum s = {0, 0, 0};
+#pragma unroll 1
+  for (uint32_t i = 0; i < n; i += 64) {
+    Sum one = {0, 0, 0};
+    const uint32_t at = i + threadIdx.x % 64;
+    if (at < n && r[at].top) one = settled(r[at]);
+    if (i && threadIdx.x % 64 == 0) {
+      // the 64 before stand beside the first of these
+      const bool before = s.top > one.top;
+      const Sum hi = before ? s : one, lo = before ? one : s;
+      one = hi;
+      if (lo.top && T > 0.0f) {
+        const double x = scaled(value_of(ord_of(lo.top)), value_of(ord_of(hi.top)), T), f = exp(x);
+        if (f > 0) {
+          one.rest += f * (1.0 + lo.rest);
+          one.wx += f * (lo.wx + (1.0 + lo.rest) * x);
+        }
+      }
+    }
+    s = join(one, T);
+  }
+  return s;
+}
+
+// The row's results from its sum, its tokens' ranks and its best elements, by a
+// whole wave.
 __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const Sum &sum, float T,
                                        const uint32_t *ranks, const uint64_t *best) {
   const uint32_t tid = threadIdx.x;
@@ -163,10 +242,21 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
   }
 }
 
+// The n_top best of what is listed (one element once), in order; what lies past their end is left.
+__device__ __forceinline__ void best_of(const uint64_t *list, uint32_t n, uint32_t n_top, uint64_t *best) {
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = list[i];
+    uint32_t before = 0;
+    for (uint32_t j = 0; j < n; ++j) before += list[j] > key;
+    if (key && before < n_top) best[before] = key;
+  }
+}
+
 struct Shared {
   uint64_t list[kList];           // what reaches the bound
   uint64_t best[kMaxTop];         // the best so far, in order
   uint64_t token[kMaxTokens];
+  Raw slice[kMaxSlices];
   uint32_t rank[kMaxTokens];
   int32_t wave_top[kWaves], wave_bound[kWaves];
   double wave_rest[kWaves], wave_wx[kWaves];
@@ -179,20 +269,19 @@ __device__ __forceinline__ float bound_value(int32_t o) {
   return o > 0 ? value_of((uint32_t)o) : __uint_as_float(0xFF7F0000u);  // or the lowest finite number
 }
 
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
   __shared__ Shared sh;
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   const uint32_t n_slices = a.slices[0] + a.slices[1];
   const uint32_t k0 = (uint32_t)((uint64_t)n_slices * part / a.parts), k1 = (uint32_t)((uint64_t)n_slices * (part + 1) / a.parts);
   const float T = a.temperature ? a.temperature[row] : 1.0f;
-  const bool greedy = !(T > 0.0f);
+  const float c = T > 0.0f ? 1.4426950408889634f / T : 0.0f;
   if (tid < a.n_tokens) {
     sh.token[tid] = token_key(a, row, a.tokens[(uint64_t)row * a.n_tokens + tid]);
     sh.rank[tid] = 0;
   }
   if (tid < a.n_top) sh.best[tid] = 0;
-  Sum total = {0, 0, 0};  // thread 0's
 
 #pragma unroll 1
   for (uint32_t k = k0; k < k1; ++k) {
@@ -203,6 +292,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       const uint32_t end = s.cols / 8;
       v4u last = v4u{kMasked, kMasked, kMasked, kMasked};
       if (s.cols % 8 && tid == end % kThreads) {
+#pragma unroll 1
         for (uint32_t i = 0; i < s.cols % 8; ++i) {
           const uint32_t v = s.ptr[8 * end + i], low = 16 * (i % 2);
 #pragma unroll
@@ -217,18 +307,28 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
         if (at < end) w[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(s.ptr) + at);
       }
     }
-    // f(word, half, column) for each element that this thread holds
-    auto each = [&](auto &&f) {
+    // f(round) for each that the slice has
+    auto rounds = [&](auto &&f) {
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
-        if ((uint32_t)r * kThreads * 8 >= s.cols) continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t x = w[r][q];
-          f(x, 0, 8 * (r * kThreads + tid) + 2 * q);
-          f(x, 1, 8 * (r * kThreads + tid) + 2 * q + 1);
-        }
+        if ((uint32_t)r * kThreads * 8 < s.cols) f(r);
+        __builtin_amdgcn_sched_barrier(0);  // or what all rounds leave would be held at once
       }
+    };
+    // f(word, half, columns from this thread's first one on) for each element of a round
+    auto of_round = [&](int r, auto &&f) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = w[r][q];
+        f(x, 0, 8 * r * kThreads + 2 * q);
+        f(x, 1, 8 * r * kThreads + 2 * q + 1);
+      }
+    };
+    // This thread's first column, made anew: the columns of all elements, ready in registers, would not fit.
+    auto first_column = [&] {
+      uint32_t c = 8 * tid;
+      asm volatile("" : "+v"(c));
+      return c;
     };
     // f(pattern, column) for each element, read again: for what is rare
     auto again = [&](auto &&f) {
@@ -237,18 +337,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     };
 
     // 1. The largest, and a bound that n_top elements of a wave reach.
-    v2s two = {-0x8000, -0x8000};
+    v2s round_top[kRounds], two = {-0x8000, -0x8000};
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t x = w[r][q];
-        two = __builtin_elementwise_max(two, __builtin_bit_cast(v2s, x));
-      }
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t x0 = w[r][0], x1 = w[r][1], x2 = w[r][2], x3 = w[r][3];
+      round_top[r] = __builtin_elementwise_max(
+          __builtin_elementwise_max(__builtin_bit_cast(v2s, x0), __builtin_bit_cast(v2s, x1)),
+          __builtin_elementwise_max(__builtin_bit_cast(v2s, x2), __builtin_bit_cast(v2s, x3)));
+      two = __builtin_elementwise_max(two, round_top[r]);
+    }
     const int mine = max((int)two.x, (int)two.y);
     int top = wave_max(mine);
     int own = mine >= 0 ? 0x8000 + mine : 0;  // this lane's largest in the order; 0: not known
-    const bool plain = top > 0 && top <= 0x7F80 && (uint32_t)__popcll(__ballot(mine >= 0)) >= a.n_top;
+    const uint32_t known = (uint32_t)__popcll(__ballot(mine >= 0));
+    const bool plain = top > 0 && top <= 0x7F80 && known >= a.n_top;
     if (!plain) {
       own = 0;
       again([&](uint32_t v, uint32_t) { own = max(own, (int)ord(v)); });
@@ -275,41 +377,54 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       o = max(o, (uint32_t)sh.wave_top[i]);
       reach = max(reach, sh.wave_bound[i]);
     }
-    if (o == 0) continue;  // nothing here is in the order
+    o = __builtin_amdgcn_readfirstlane(o);
+    reach = __builtin_amdgcn_readfirstlane(reach);
+    if (o == 0) {  // nothing here is in the order
+      if (tid == 0) sh.slice[k - k0] = Raw{};
+      continue;
+    }
     const float m = value_of(o);
 
     // 2. What reaches the bound.
     if (a.n_top) {
       const float at_least = bound_value(reach);
-      each([&](uint32_t x, int h, uint32_t c) {
-        const bool in = as_float(x, h) >= at_least;
-        const uint64_t mask = __ballot(in);
-        if (!mask) return;
-        uint32_t base = 0;
-        if (lane == 0) base = atomicAdd(&sh.listed, (uint32_t)__popcll(mask));
-        base = __builtin_amdgcn_readfirstlane(base);
-        const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        if (in && at < kList) sh.list[at] = key_of(ord(half(x, h)), s.gid + c);
+      const int pattern = reach > 0x8000 && plain ? reach - 0x8000 : -0x8000;  // as a round's largest
+      rounds([&](int r) {
+        if (!__any(max((int)round_top[r].x, (int)round_top[r].y) >= pattern)) return;
+        of_round(r, [&](uint32_t x, int h, uint32_t col) {
+          const bool in = as_float(x, h) >= at_least;
+          const uint64_t mask = __ballot(in);
+          if (!mask) return;
+          uint32_t base = 0;
+          if (lane == 0) base = atomicAdd(&sh.listed, (uint32_t)__popcll(mask));
+          base = __builtin_amdgcn_readfirstlane(base);
+          const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+          if (in && at < kList) sh.list[at] = key_of(ord(half(x, h)), s.gid + first_column() + col);
+        });
       });
     }
 
     // 3. The elements before each token.
+#pragma unroll 1
     for (uint32_t i = 0; i < a.n_tokens; ++i) {
-      const uint64_t key = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(sh.token[i] >> 32)) << 32 |
-                           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)sh.token[i]);
+      const uint64_t key = read_lane(sh.token[i], 0);
       if (!key) continue;
       const uint32_t id = id_of(key);
       const float g = value_of(ord_of(key));
       uint32_t n = 0;
       if (id > s.gid && id < s.gid + s.cols) {
-        each([&](uint32_t x, int h, uint32_t c) {
-          const float l = as_float(x, h);
-          n += (uint32_t)__popcll(__ballot(l > g || (l == g && s.gid + c < id)));
+        rounds([&](int r) {
+          of_round(r, [&](uint32_t x, int h, uint32_t col) {
+            const float l = as_float(x, h);
+            n += (uint32_t)__popcll(__ballot(l > g || (l == g && (int)(8 * tid) < (int)(id - s.gid - col))));
+          });
         });
       } else {
         // equal ones come before it where their ids do
         const float from = id > s.gid ? g : above(g);
-        each([&](uint32_t x, int h, uint32_t) { n += (uint32_t)__popcll(__ballot(as_float(x, h) >= from)); });
+        rounds([&](int r) {
+          of_round(r, [&](uint32_t x, int h, uint32_t) { n += (uint32_t)__popcll(__ballot(as_float(x, h) >= from)); });
+        });
       }
       if (lane == 0 && n) atomicAdd(&sh.rank[i], n);
     }
@@ -317,38 +432,44 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     // 4. The weights.  Elements equal to the largest are taken out and counted.
     if (own == (int)o || !plain) {
       uint32_t n = 0, first = 0xFFFFFFFFu;
+      const short pattern = (short)(o - 0x8000);
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r)
+      for (int r = 0; r < kRounds; ++r) {
+        if (plain && round_top[r].x != pattern && round_top[r].y != pattern) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t x = w[r][q];
           const bool lo = as_float(x, 0) == m, hi = as_float(x, 1) == m;
           n += lo + hi;
-          first = min(first, lo || hi ? 8 * (r * kThreads + tid) + 2 * q + (lo ? 0 : 1) : 0xFFFFFFFFu);
+          if (lo || hi) first = min(first, first_column() + 8 * r * kThreads + 2 * q + (lo ? 0 : 1));
           x = lo ? (x & 0xFFFF0000u) | (kMasked & 0xFFFFu) : x;
           w[r][q] = hi ? (x & 0xFFFFu) | (kMasked & 0xFFFF0000u) : x;
         }
-      atomicAdd(&sh.equal, n);
-      atomicMin(&sh.first, first);
+      }
+      if (n) {
+        atomicAdd(&sh.equal, n);
+        atomicMin(&sh.first, first);
+      }
     }
     double rest = 0, wx = 0;
-    const float c = 1.4426950408889634f / T;
-    if (greedy || __builtin_isinf(m)) {
+    float used = 0;
+    if (!(T > 0.0f) || __builtin_isinf(m)) {
       // all weight is the largest elements'
-    } else if (__builtin_fabsf(m) * c <= 0x1p20f && c <= 0x1p64f) {
+    } else if (__builtin_fabsf(m) * c <= 0x1p20f && c <= 0x1p64f && c > 0) {
       const float mc = m * c;
+      used = c;
       float sum_w = 0, sum_wt = 0;
-      each([&](uint32_t x, int h, uint32_t) {
-        // what is masked or NaN, and what is 2^-200 or less, has no weight
-        const float t = fmaxf(fmaf(as_float(x, h), c, -mc), -200.0f);
-        const float e = __builtin_amdgcn_exp2f(t);
-        sum_w += e;
-        sum_wt = fmaf(e, t, sum_wt);
+      rounds([&](int r) {
+        of_round(r, [&](uint32_t x, int h, uint32_t) {
+          // what is masked or NaN, and what is 2^-200 or less, has no weight
+          const float t = fmaxf(fmaf(as_float(x, h), c, -mc), -200.0f);
+          const float e = __builtin_amdgcn_exp2f(t);
+          sum_w += e;
+          sum_wt = fmaf(e, t, sum_wt);
+        });
       });
-      const double off = (double)mc - (double)m * (double)c;  // t is too small by this
-      const double f = exp2(off);
-      rest = sum_w * f;
-      wx = f * ((double)sum_wt + off * sum_w) * 0.6931471805599453;
+      rest = sum_w;
+      wx = sum_wt;
     } else {
       again([&](uint32_t v, uint32_t) {
         if (!ord(v) || as_float(v, 0) == m) return;
@@ -361,28 +482,25 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     if (lane == 0) sh.wave_rest[wave] = rest, sh.wave_wx[wave] = wx;
     __syncthreads();
     if (tid == 0) {
-      Sum one = {(double)sh.equal - 1.0, 0, key_of(o, s.gid + sh.first)};
-      for (int i = 0; i < kWaves; ++i) one.rest += sh.wave_rest[i], one.wx += sh.wave_wx[i];
-      total = greedy ? (one.top > total.top ? one : total) : join(total, one, T);
+      Raw raw = {used, (float)sh.equal, 0, 0, key_of(o, s.gid + sh.first)};
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) raw.rest += sh.wave_rest[i], raw.wx += sh.wave_wx[i];
+      sh.slice[k - k0] = raw;
     }
     // The best of what is listed.
     if (a.n_top) {
       const uint32_t n = sh.listed;
       if (n <= kList) {
-        for (uint32_t i = tid; i < n; i += kThreads) {
-          const uint64_t key = sh.list[i];
-          uint32_t before = 0;
-          for (uint32_t j = 0; j < n; ++j) before += sh.list[j] > key;
-          if (key && before < a.n_top) sh.best[before] = key;
-        }
+        best_of(sh.list, n, a.n_top, sh.best);
       } else {
         // Very many equal elements, or few lanes with all of them: one after
         // the other, the largest below the one before.
         uint64_t below = ~0ull;
+#pragma unroll 1
         for (uint32_t i = 0; i < a.n_top; ++i) {
           uint64_t key = tid < a.n_top && sh.list[tid] < below ? sh.list[tid] : 0;
-          again([&](uint32_t v, uint32_t c) {
-            const uint64_t y = key_of(ord(v), s.gid + c);
+          again([&](uint32_t v, uint32_t col) {
+            const uint64_t y = key_of(ord(v), s.gid + col);
             if (y < below && y > key) key = y;
           });
           key = wave_max(key);
@@ -399,37 +517,55 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   __syncthreads();
   if (a.parts > 1) {
     const uint64_t at = (uint64_t)row * a.parts + part;
-    if (tid == 0) static_cast<Sum *>(a.sums)[at] = total;
+    // a part of several slices joins them itself
+    if (k1 - k0 == 1) {
+      if (tid == 0) static_cast<Raw *>(a.sums)[at] = sh.slice[0];
+    } else if (wave == 0) {
+      const Sum sum = join_slices(sh.slice, k1 - k0, T);
+      if (lane == 0) static_cast<Raw *>(a.sums)[at] = Raw{0, 1, sum.rest, sum.wx, sum.top};
+    }
     if (tid < a.n_tokens) a.ranks[at * a.n_tokens + tid] = sh.rank[tid];
     if (tid < a.n_top) a.keys[at * a.n_top + tid] = sh.best[tid];
     return;
   }
-  __shared__ Sum all;
-  if (tid == 0) all = total;
-  __syncthreads();
-  finish(a, row, all, T, sh.rank, sh.best);
+  if (wave == 0) finish(a, row, join_slices(sh.slice, k1 - k0, T), T, sh.rank, sh.best);
 }
 
-// One wave for each row.
-__global__ __launch_bounds__(64) void logprobs_fold_kernel(LogprobArgs a) {
+// One workgroup for each row, whose first wave joins the sums while the others look for the best.
+__global__ __launch_bounds__(kThreads) void logprobs_fold_kernel(LogprobArgs a) {
   __shared__ uint32_t rank[kMaxTokens];
-  __shared__ uint64_t best[kMaxTop];
-  const uint32_t row = blockIdx.x, lane = threadIdx.x;
+  __shared__ uint64_t head[kMaxParts], list[kList], best[kMaxTop];
+  __shared__ uint64_t least;
+  __shared__ uint32_t listed;
+  const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const float T = a.temperature ? a.temperature[row] : 1.0f;
   const uint64_t at = (uint64_t)row * a.parts;
-  Sum s = {0, 0, 0};
-  for (uint32_t p = lane; p < a.parts; p += 64) {
-    const Sum b = static_cast<const Sum *>(a.sums)[at + p];
-    s = T > 0.0f ? join(s, b, T) : b.top > s.top ? b : s;
+  const uint64_t *keys = a.keys + at * a.n_top;
+  if (a.n_top) {
+    // The parts' lists are in order.  Where there are as many parts as elements asked for, none that is below
+    // that many of their first ones is among the best.
+    if (tid < a.parts) head[tid] = keys[(uint64_t)tid * a.n_top];
+    if (tid < a.n_top) best[tid] = 0;
+    if (tid == 0) least = 1, listed = 0;
+    __syncthreads();
+    if (tid < a.parts && a.parts >= a.n_top) {
+      uint32_t before = 0;
+      for (uint32_t j = 0; j < a.parts; ++j) before += head[j] > head[tid] || (head[j] == head[tid] && j < tid);
+      if (before == a.n_top - 1 && head[tid]) least = head[tid];
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < a.parts * a.n_top; i += kThreads) {
+      const uint64_t key = keys[i];
+      if (key >= least) {
+        const uint32_t to = atomicAdd(&listed, 1u);
+        if (to < kList) list[to] = key;
+      }
+    }
+    __syncthreads();
+    best_of(list, listed, a.n_top, best);
+    __syncthreads();
   }
-#pragma unroll 1
-  for (int d = 1; d < 64; d *= 2) {
-    Sum b;
-    b.rest = __shfl_xor(s.rest, d);
-    b.wx = __shfl_xor(s.wx, d);
-    b.top = __shfl_xor((unsigned long long)s.top, d);
-    s = T > 0.0f ? join(s, b, T) : b.top > s.top ? b : s;
-  }
+  if (wave != 0) return;
   for (uint32_t i = 0; i < a.n_tokens; ++i) {
     uint32_t n = 0;
     for (uint32_t p = lane; p < a.parts; p += 64) n += a.ranks[(at + p) * a.n_tokens + i];
@@ -437,25 +573,8 @@ __global__ __launch_bounds__(64) void logprobs_fold_kernel(LogprobArgs a) {
     for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
     if (lane == 0) rank[i] = n;
   }
-  // The parts' lists are in order: each lane shows the first of its two.
-  uint32_t used[2] = {0, 0};
-  auto head = [&](uint32_t j) -> uint64_t {
-    const uint32_t p = lane + 64 * j;
-    return p < a.parts && used[j] < a.n_top ? a.keys[(at + p) * a.n_top + used[j]] : 0;
-  };
-  uint64_t h[2] = {a.n_top ? head(0) : 0, a.n_top ? head(1) : 0};
-  for (uint32_t i = 0; i < a.n_top; ++i) {
-    const uint64_t key = wave_max(max(h[0], h[1]));
-    if (lane == 0) best[i] = key;
-#pragma unroll
-    for (uint32_t j = 0; j < 2; ++j)
-      if (key && h[j] == key) {
-        ++used[j];
-        h[j] = head(j);
-      }
-  }
-  __syncthreads();
-  finish(a, row, s, T, rank, best);
+  const Sum sum = join_slices(static_cast<const Raw *>(a.sums) + at, a.parts, T);
+  finish(a, row, sum, T, rank, best);
 }
 
 struct Shape {
@@ -492,7 +611,7 @@ uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols
   const Shape s = shape_of(rows, ncols0, ncols1);
   if (s.parts == 1) return 0;
   const uint64_t n = (uint64_t)rows * s.parts;
-  return up16(n * sizeof(Sum)) + up16(n * n_top * 8) + up16(n * n_tokens * 4);
+  return up16(n * sizeof(Raw)) + up16(n * n_top * 8) + up16(n * n_tokens * 4);
 }
 
 hipError_t launch_logprobs(const LogprobArgs &in, void *workspace, hipStream_t stream) {
@@ -504,12 +623,12 @@ hipError_t launch_logprobs(const LogprobArgs &in, void *workspace, hipStream_t s
     const uint64_t n = (uint64_t)a.rows * s.parts;
     uint8_t *at = static_cast<uint8_t *>(workspace);
     a.sums = at;
-    a.keys = reinterpret_cast<uint64_t *>(at += up16(n * sizeof(Sum)));
+    a.keys = reinterpret_cast<uint64_t *>(at += up16(n * sizeof(Raw)));
     a.ranks = reinterpret_cast<uint32_t *>(at + up16(n * a.n_top * 8));
   }
   const hipError_t e = launch(logprobs_kernel, dim3(a.rows * s.parts), dim3(kThreads), 0, stream, a);
   if (e != hipSuccess || s.parts == 1) return e;
-  return launch(logprobs_fold_kernel, dim3(a.rows), dim3(64), 0, stream, a);
+  return launch(logprobs_fold_kernel, dim3(a.rows), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace xfer
