@@ -22,7 +22,7 @@
 //      and the hardware's power.  m c is rounded to binary32; what that moves
 //      all weights by is a factor that is put right afterwards.
 // Thread sums are binary32 (of up to 64 elements), everything above binary64.
-// The slices' sums are put together at the end, a slice to a lane.
+// The sums of a row's slices are kept relative to the largest so far.
 //
 // Where rows are few, each is cut into several workgroups' parts, which a
 // second launch folds: (largest, R, sum w x) scaled to the row's largest.
@@ -38,13 +38,14 @@ constexpr uint32_t kSliceCols = kThreads * 8 * kRounds;   // 16,384
 constexpr uint32_t kMinCols = 2048;                       // of a slice where rows are cut into parts
 constexpr uint32_t kWorkgroups = 1024;                    // that a call is cut up for
 constexpr uint32_t kMaxParts = 128;                       // of a row
-constexpr uint32_t kMaxSlices = 2 * (kArgmaxMaxShardCols / kSliceCols);
 constexpr uint32_t kList = 1024;                          // elements that reach the bound, at most
 static_assert(kList >= kMaxTop * kMaxTop, "the fold's, of as many parts as elements asked for");
 constexpr uint32_t kMasked = 0xFF80FF80u;
+constexpr unsigned short kFar = 0xF149;                   // -1e30
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef short v2s __attribute__((ext_vector_type(2)));
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
 
 // A place in the row's order: 0 for what is not in it (NaN, -inf), larger for
 // larger values, -0 as +0.
@@ -119,45 +120,25 @@ struct Sum {
   double rest, wx;
   uint64_t top;
 };
-// The same of a slice as it was added up: `equal` elements have the first one's
-// value, the others' sums are off by the rounding of m c (where c is not 0) and
-// count in powers of two.
-struct Raw {
-  float c, equal;
-  double rest, wx;
-  uint64_t top;
-};
 // (l - m) / T of a row, in binary64.
 __device__ __forceinline__ double scaled(float l, float m, float T) {
   if (l == m) return 0.0;
   return __builtin_isinf(m) ? -INFINITY : ((double)l - (double)m) / (double)T;
 }
-__device__ __forceinline__ Sum settled(const Raw &r) {
-  Sum s = {(double)r.equal - 1.0, 0, r.top};
-  if (r.c != 0.0f) {
-    const float m = value_of(ord_of(r.top));
-    const double off = (double)(m * r.c) - (double)m * (double)r.c;  // every power is too small by this
-    const double f = exp2(off);
-    s.rest += f * r.rest;
-    s.wx = f * (r.wx + off * r.rest) * 0.6931471805599453;
-  } else {
-    s.rest += r.rest;
-    s.wx = r.wx;
-  }
-  return s;
-}
-// The sums of all lanes' sets, by a whole wave.  (Greedy: the first element alone.)
-__device__ __forceinline__ Sum join(Sum s, float T) {
-  const uint64_t top = wave_max(s.top);
-  Sum all = {0, 0, top};
-  if (!top || !(T > 0.0f)) return all;
-  double rest = s.rest, wx = s.wx;
-  if (s.top != top) {
-    const double x = s.top ? scaled(value_of(ord_of(s.top)), value_of(ord_of(top)), T) : -INFINITY, f = exp(x);
-    rest = wx = 0;
+// The sum of all lanes' two sets, by a whole wave.  (Greedy: the first element alone.)
+__device__ __forceinline__ Sum join(const Sum &s0, const Sum &s1, float T) {
+  Sum all = {0, 0, wave_max(max(s0.top, s1.top))};
+  if (!all.top || !(T > 0.0f)) return all;
+  const float m = value_of(ord_of(all.top));
+  double rest = 0, wx = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const Sum s = i ? s1 : s0;
+    if (!s.top) continue;
+    const double x = scaled(value_of(ord_of(s.top)), m, T), f = exp(x), own = s.top == all.top ? 0.0 : 1.0;
     if (f > 0) {  // not so where x is -inf
-      rest = f * (1.0 + s.rest);
-      wx = f * (s.wx + (1.0 + s.rest) * x);
+      rest += f * (own + s.rest);
+      wx += f * (s.wx + (own + s.rest) * x);
     }
   }
   all.rest = wave_sum(rest);
@@ -190,32 +171,6 @@ __device__ __forceinline__ uint64_t token_key(const LogprobArgs &a, uint32_t row
       return key_of(ord(a.s[s].ptr[row * a.s[s].ld + c]), (uint32_t)id);
   }
   return 0;
-}
-
-// The sums of n slices or parts, by a whole wave.
-__device__ __forceinline__ Sum join_slices(const Raw *r, uint32_t n, float T) {
-  Sum s = {0, 0, 0};
-#pragma unroll 1
-  for (uint32_t i = 0; i < n; i += 64) {
-    Sum one = {0, 0, 0};
-    const uint32_t at = i + threadIdx.x % 64;
-    if (at < n && r[at].top) one = settled(r[at]);
-    if (i && threadIdx.x % 64 == 0) {
-      // the 64 before stand beside the first of these
-      const bool before = s.top > one.top;
-      const Sum hi = before ? s : one, lo = before ? one : s;
-      one = hi;
-      if (lo.top && T > 0.0f) {
-        const double x = scaled(value_of(ord_of(lo.top)), value_of(ord_of(hi.top)), T), f = exp(x);
-        if (f > 0) {
-          one.rest += f * (1.0 + lo.rest);
-          one.wx += f * (lo.wx + (1.0 + lo.rest) * x);
-        }
-      }
-    }
-    s = join(one, T);
-  }
-  return s;
 }
 
 // The row's results from its sum, its tokens' ranks and its best elements, by a
@@ -256,12 +211,12 @@ struct Shared {
   uint64_t list[kList];           // what reaches the bound
   uint64_t best[kMaxTop];         // the best so far, in order
   uint64_t token[kMaxTokens];
-  Raw slice[kMaxSlices];
   uint32_t rank[kMaxTokens];
   int32_t wave_top[kWaves], wave_bound[kWaves];
   double wave_rest[kWaves], wave_wx[kWaves];
   uint64_t wave_key[kWaves];
-  uint32_t listed, equal, first;  // elements listed; elements equal to the largest, and the first one's column
+  uint32_t listed;
+  uint32_t equal[2], first[2];  // elements equal to the largest so far, and the lowest id; of the one before it no longer
 };
 
 // What reaches `bound` and is in the row's order.
@@ -282,6 +237,11 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
     sh.rank[tid] = 0;
   }
   if (tid < a.n_top) sh.best[tid] = 0;
+  if (tid < 2) sh.equal[tid] = 0, sh.first[tid] = 0xFFFFFFFFu;
+  // The largest so far, and of all others this thread's sums relative to it.
+  uint32_t o = 0, which = 0;
+  float m = 0;
+  double rest = 0, wx = 0;
 
 #pragma unroll 1
   for (uint32_t k = k0; k < k1; ++k) {
@@ -324,11 +284,11 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
         f(x, 1, 8 * r * kThreads + 2 * q + 1);
       }
     };
-    // This thread's first column, made anew: the columns of all elements, ready in registers, would not fit.
-    auto first_column = [&] {
-      uint32_t c = 8 * tid;
-      asm volatile("" : "+v"(c));
-      return c;
+    // A number made anew for each use: what follows from it for every element, ready in registers for all passes, would
+    // not fit.
+    auto anew = [](uint32_t x) {
+      asm volatile("" : "+v"(x));
+      return x;
     };
     // f(pattern, column) for each element, read again: for what is rare
     auto again = [&](auto &&f) {
@@ -367,23 +327,32 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
       sh.wave_top[wave] = top + 0x8000;
       sh.wave_bound[wave] = bound;
     }
-    if (tid == 0) sh.listed = a.n_top, sh.equal = 0, sh.first = 0xFFFFFFFFu;
+    if (tid == 0) sh.listed = a.n_top;
     if (tid < a.n_top) sh.list[tid] = sh.best[tid];
     __syncthreads();
-    uint32_t o = 0;
+    uint32_t largest = o;
     int32_t reach = a.n_top ? (int32_t)ord_of(sh.best[a.n_top - 1]) : 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      o = max(o, (uint32_t)sh.wave_top[i]);
+      largest = max(largest, (uint32_t)sh.wave_top[i]);
       reach = max(reach, sh.wave_bound[i]);
     }
-    o = __builtin_amdgcn_readfirstlane(o);
+    largest = __builtin_amdgcn_readfirstlane(largest);
     reach = __builtin_amdgcn_readfirstlane(reach);
-    if (o == 0) {  // nothing here is in the order
-      if (tid == 0) sh.slice[k - k0] = Raw{};
-      continue;
+    if (largest == 0) continue;  // nothing so far is in the order
+    if (largest != o) {
+      const float before = m;
+      m = value_of(largest);
+      if (o) {
+        const double x = scaled(before, m, T), f = T > 0.0f ? exp(x) : 0.0;
+        const double n = tid == 0 ? sh.equal[which] : 0;
+        wx = f > 0 ? f * (wx + x * (rest + n)) : 0.0;  // not so where x is -inf
+        rest = f * (rest + n);
+        if (tid == 0) sh.equal[which] = 0, sh.first[which] = 0xFFFFFFFFu;
+        which ^= 1;
+      }
+      o = largest;
     }
-    const float m = value_of(o);
 
     // 2. What reaches the bound.
     if (a.n_top) {
@@ -399,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
           if (lane == 0) base = atomicAdd(&sh.listed, (uint32_t)__popcll(mask));
           base = __builtin_amdgcn_readfirstlane(base);
           const uint32_t at = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-          if (in && at < kList) sh.list[at] = key_of(ord(half(x, h)), s.gid + first_column() + col);
+          if (in && at < kList) sh.list[at] = key_of(ord(half(x, h)), s.gid + 8 * anew(tid) + col);
         });
       });
     }
@@ -415,16 +384,26 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
       if (id > s.gid && id < s.gid + s.cols) {
         rounds([&](int r) {
           of_round(r, [&](uint32_t x, int h, uint32_t col) {
-            const float l = as_float(x, h);
+            const float l = as_float(anew(x), h);
             n += (uint32_t)__popcll(__ballot(l > g || (l == g && (int)(8 * tid) < (int)(id - s.gid - col))));
           });
         });
       } else {
         // equal ones come before it where their ids do
         const float from = id > s.gid ? g : above(g);
-        rounds([&](int r) {
-          of_round(r, [&](uint32_t x, int h, uint32_t) { n += (uint32_t)__popcll(__ballot(as_float(x, h) >= from)); });
-        });
+        if (plain && from > 0) {
+          // as whole numbers, straight from where they lie
+          const int at_least = (int)(__float_as_uint(from) >> 16);
+          rounds([&](int r) {
+            of_round(r, [&](uint32_t x, int h, uint32_t) {
+              n += (uint32_t)__popcll(h ? __ballot((int)x >= at_least << 16) : __ballot((short)x >= (short)at_least));
+            });
+          });
+        } else {
+          rounds([&](int r) {
+            of_round(r, [&](uint32_t x, int h, uint32_t) { n += (uint32_t)__popcll(__ballot(as_float(anew(x), h) >= from)); });
+          });
+        }
       }
       if (lane == 0 && n) atomicAdd(&sh.rank[i], n);
     }
@@ -441,35 +420,42 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
           uint32_t x = w[r][q];
           const bool lo = as_float(x, 0) == m, hi = as_float(x, 1) == m;
           n += lo + hi;
-          if (lo || hi) first = min(first, first_column() + 8 * r * kThreads + 2 * q + (lo ? 0 : 1));
-          x = lo ? (x & 0xFFFF0000u) | (kMasked & 0xFFFFu) : x;
-          w[r][q] = hi ? (x & 0xFFFFu) | (kMasked & 0xFFFF0000u) : x;
+          if (lo || hi) first = min(first, 8 * anew(tid) + 8 * r * kThreads + 2 * q + (lo ? 0 : 1));
+          const bool lo_out = lo || __builtin_isnan(as_float(x, 0)), hi_out = hi || __builtin_isnan(as_float(x, 1));
+          x = lo_out ? (x & 0xFFFF0000u) | (kMasked & 0xFFFFu) : x;
+          w[r][q] = hi_out ? (x & 0xFFFFu) | (kMasked & 0xFFFF0000u) : x;
         }
       }
       if (n) {
-        atomicAdd(&sh.equal, n);
-        atomicMin(&sh.first, first);
+        atomicAdd(&sh.equal[which], n);
+        atomicMin(&sh.first[which], s.gid + first);
       }
     }
-    double rest = 0, wx = 0;
-    float used = 0;
     if (!(T > 0.0f) || __builtin_isinf(m)) {
       // all weight is the largest elements'
-    } else if (__builtin_fabsf(m) * c <= 0x1p20f && c <= 0x1p64f && c > 0) {
+    } else if (__builtin_fabsf(m) * c <= 0x1p20f && c <= 0x1p20f && c >= 0x1p-60f) {
       const float mc = m * c;
-      used = c;
       float sum_w = 0, sum_wt = 0;
       rounds([&](int r) {
+        // What is masked or a negative NaN becomes a large negative number, like what is below it: all have weight 0.
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x = w[r][q];
+          w[r][q] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(v2us, x), v2us{kFar, kFar}));
+        }
         of_round(r, [&](uint32_t x, int h, uint32_t) {
-          // what is masked or NaN, and what is 2^-200 or less, has no weight
-          const float t = fmaxf(fmaf(as_float(x, h), c, -mc), -200.0f);
+          const float t = fmaf(as_float(x, h), c, -mc);
           const float e = __builtin_amdgcn_exp2f(t);
           sum_w += e;
           sum_wt = fmaf(e, t, sum_wt);
         });
       });
-      rest = sum_w;
-      wx = sum_wt;
+      // Every power is too small by off, at most 2^-4: 2^off - 1 by its series, to 2^-45.
+      constexpr double kLn2 = 0.6931471805599453;
+      const double off = (double)mc - (double)m * (double)c, y = off * kLn2;
+      const double f = 1 + y * (1 + y / 2 * (1 + y / 3 * (1 + y / 4 * (1 + y / 5 * (1 + y / 6 * (1 + y / 7 * (1 + y / 8)))))));
+      rest += f * sum_w;
+      wx += f * kLn2 * (sum_wt + off * sum_w);
     } else {
       again([&](uint32_t v, uint32_t) {
         if (!ord(v) || as_float(v, 0) == m) return;
@@ -477,18 +463,9 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
         if (e > 0) rest += e, wx += e * t;
       });
     }
-    rest = wave_sum(rest);
-    wx = wave_sum(wx);
-    if (lane == 0) sh.wave_rest[wave] = rest, sh.wave_wx[wave] = wx;
-    __syncthreads();
-    if (tid == 0) {
-      Raw raw = {used, (float)sh.equal, 0, 0, key_of(o, s.gid + sh.first)};
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) raw.rest += sh.wave_rest[i], raw.wx += sh.wave_wx[i];
-      sh.slice[k - k0] = raw;
-    }
     // The best of what is listed.
     if (a.n_top) {
+      __syncthreads();
       const uint32_t n = sh.listed;
       if (n <= kList) {
         best_of(sh.list, n, a.n_top, sh.best);
@@ -514,21 +491,21 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
       }
     }
   }
+  rest = wave_sum(rest);
+  wx = wave_sum(wx);
+  if (lane == 0) sh.wave_rest[wave] = rest, sh.wave_wx[wave] = wx;
   __syncthreads();
+  Sum sum = {(double)sh.equal[which] - 1.0, 0, key_of(o, sh.first[which])};
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) sum.rest += sh.wave_rest[i], sum.wx += sh.wave_wx[i];
   if (a.parts > 1) {
     const uint64_t at = (uint64_t)row * a.parts + part;
-    // a part of several slices joins them itself
-    if (k1 - k0 == 1) {
-      if (tid == 0) static_cast<Raw *>(a.sums)[at] = sh.slice[0];
-    } else if (wave == 0) {
-      const Sum sum = join_slices(sh.slice, k1 - k0, T);
-      if (lane == 0) static_cast<Raw *>(a.sums)[at] = Raw{0, 1, sum.rest, sum.wx, sum.top};
-    }
+    if (tid == 0) static_cast<Sum *>(a.sums)[at] = sum;
     if (tid < a.n_tokens) a.ranks[at * a.n_tokens + tid] = sh.rank[tid];
     if (tid < a.n_top) a.keys[at * a.n_top + tid] = sh.best[tid];
     return;
   }
-  if (wave == 0) finish(a, row, join_slices(sh.slice, k1 - k0, T), T, sh.rank, sh.best);
+  if (wave == 0) finish(a, row, sum, T, sh.rank, sh.best);
 }
 
 // One workgroup for each row, whose first wave joins the sums while the others look for the best.
@@ -573,7 +550,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_fold_kernel(LogprobArgs a) 
     for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
     if (lane == 0) rank[i] = n;
   }
-  const Sum sum = join_slices(static_cast<const Raw *>(a.sums) + at, a.parts, T);
+  // Two parts to a lane.
+  const Sum *sums = static_cast<const Sum *>(a.sums) + at;
+  const Sum none = {0, 0, 0};
+  const Sum sum = join(lane < a.parts ? sums[lane] : none, lane + 64 < a.parts ? sums[lane + 64] : none, T);
   finish(a, row, sum, T, rank, best);
 }
 
@@ -611,7 +591,7 @@ uint64_t logprobs_workspace_bytes(uint32_t rows, uint32_t ncols0, uint32_t ncols
   const Shape s = shape_of(rows, ncols0, ncols1);
   if (s.parts == 1) return 0;
   const uint64_t n = (uint64_t)rows * s.parts;
-  return up16(n * sizeof(Raw)) + up16(n * n_top * 8) + up16(n * n_tokens * 4);
+  return up16(n * sizeof(Sum)) + up16(n * n_top * 8) + up16(n * n_tokens * 4);
 }
 
 hipError_t launch_logprobs(const LogprobArgs &in, void *workspace, hipStream_t stream) {
@@ -623,7 +603,7 @@ hipError_t launch_logprobs(const LogprobArgs &in, void *workspace, hipStream_t s
     const uint64_t n = (uint64_t)a.rows * s.parts;
     uint8_t *at = static_cast<uint8_t *>(workspace);
     a.sums = at;
-    a.keys = reinterpret_cast<uint64_t *>(at += up16(n * sizeof(Raw)));
+    a.keys = reinterpret_cast<uint64_t *>(at += up16(n * sizeof(Sum)));
     a.ranks = reinterpret_cast<uint32_t *>(at + up16(n * a.n_top * 8));
   }
   const hipError_t e = launch(logprobs_kernel, dim3(a.rows * s.parts), dim3(kThreads), 0, stream, a);
