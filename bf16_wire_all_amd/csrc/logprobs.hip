@@ -290,10 +290,10 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
       asm volatile("" : "+v"(x));
       return x;
     };
-    // f(pattern, column) for each element, read again: for what is rare
+    // f(pattern, column) for each element that this thread holds, read again: for what is rare
     auto again = [&](auto &&f) {
 #pragma unroll 1
-      for (uint32_t c = tid; c < s.cols; c += kThreads) f((uint32_t)s.ptr[c], c);
+      for (uint32_t c = 8 * tid; c < s.cols; c += c % 8 == 7 ? 8 * kThreads - 7 : 1) f((uint32_t)s.ptr[c], c);
     };
 
     // 1. The largest, and a bound that n_top elements of a wave reach.

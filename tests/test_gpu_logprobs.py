@@ -114,9 +114,9 @@ class Call:
         return (host[0][:r * self.nt * 8].view(decode.TOKEN_LOGPROB).reshape(r, self.nt),
                 host[1][:r * self.n_top * 8].view(decode.TOP_LOGPROB).reshape(r, self.n_top), host[2][:r * 4].view(np.float32))
 
-    def check(self):
+    def check(self, rows=None):
         tok, top, ent = self.results()
-        for r in range(self.rows):
+        for r in range(self.rows if rows is None else rows):
             T = 1.0 if self.T is None else float(np.float32(self.T[r]))
             want = reference(values_of(self.bits[r]), self.ids, T, self.tokens[r], self.n_top)
             assert list(tok[r]["rank"]) == want["rank"], f"row {r}"
@@ -213,6 +213,34 @@ def test_special_rows_at_special_temperatures(cols, n0, n_top):
             c.check()
         except AssertionError as e:
             raise AssertionError(f"T = {T}, rows {list(enumerate(rows))}: {e}") from None
+
+
+def test_special_rows_of_several_slices_to_a_workgroup():
+    """From 1,024 rows on a workgroup goes through a row's slices one after the other: larger ones later, and none."""
+    cols, n0 = 50000, 20000
+    rows = special_rows(cols)
+    falling = rows["rising"][::-1]
+    late = np.full(cols, 0xFF80, np.uint16)
+    late[-300:] = rows["plain"][:300]
+    early = np.full(cols, 0xFF80, np.uint16)
+    early[:300] = rows["plain"][:300]
+    steps = rows["plain"].copy()
+    for i, v in enumerate((-3.0, 20.0, 20.0, 200.0)):   # the largest of each slice, twice the same
+        steps[[100 + i * 10000 + j for j in (3, 777)]] = BF(v)
+    infinite = steps.copy()
+    infinite[-5:] = [0x7F80, BF(1.0), 0x7F80, 0x7FC0, 0xFF80]
+    made = list(rows.values()) + [falling, late, early, steps, infinite]
+    n = -(-1024 // len(made)) * len(made)
+    bits = np.stack(made)
+    tokens = np.tile(np.array([0, 103, 10103, cols - 1], np.int32), (n, 1))
+    for T in (1.0, 0.05, 0.0):
+        say("several slices", T)
+        c = Call(np.tile(bits, (n // len(made), 1)), n0, tokens, 8, temperature=[T] * n)
+        c.run()
+        got = [t.reshape(-1, len(made), *t.shape[1:]) for t in c.results()]
+        for t in got:
+            assert all(t[i].tobytes() == t[0].tobytes() for i in range(1, len(t)))
+        c.check(len(made))
 
 
 @pytest.mark.parametrize("cols,n0,rows", [(40000, 20000, 1100), (16384 * 3, 16384, 1030), (300000, 100, 1)])
