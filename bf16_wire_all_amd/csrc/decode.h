@@ -110,9 +110,11 @@ struct WireArgs {
   const int64_t *slots;
   uint8_t *records;  // written by quantize, read by restore
   uint64_t record_ld;
-  uint32_t tokens, lanes_log2;  // log2 of the lanes that share a head's row (set by the launch)
+  uint32_t tokens;
+  // set by the launch: log2 of the lanes that share a head's row, and what divides by a record's rows
+  uint32_t lanes_log2, magic, magic_shift;
 };
-uint64_t wire_workgroups(uint32_t tokens, uint32_t kv_heads, uint32_t head_dim);
+uint64_t wire_workgroups(uint32_t tokens, uint32_t kv_heads, uint32_t head_dim, int kind, int bits);
 hipError_t launch_wire(const WireArgs &a, int kind, int bits, bool restore, hipStream_t stream);
 
 // ---- sampling (sample.hip)

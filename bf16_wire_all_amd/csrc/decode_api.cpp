@@ -215,7 +215,8 @@ int wire_call(const xfer_kv_cache *cache, const int64_t *slots, uint32_t tokens,
   if (restore && (!slots_disjoint(cache) || !values_apart(cache))) return XFER_E_OVERLAP;
   if (tokens == 0) return XFER_OK;
   const uint64_t need = record_bytes(cache, bits);
-  if (need > 0x7FFFFFFFu || xfer::wire_workgroups(tokens, cache->kv_heads, cache->head_dim) > xfer::kMaxGridBlocks)
+  if (need > 0x7FFFFFFFu ||
+      xfer::wire_workgroups(tokens, cache->kv_heads, cache->head_dim, cache->kind, bits) > xfer::kMaxGridBlocks)
     return XFER_E_UNSUPPORTED;
   if (!slots || (uintptr_t)slots % 8 || !records || !aligned16(records) || record_ld % 16) return XFER_E_INVAL;
   if (tokens > 1 && (record_ld < need || record_ld > kMaxExtent || tokens - 1 > kMaxExtent / record_ld))

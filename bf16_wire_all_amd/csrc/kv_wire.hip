@@ -10,19 +10,28 @@
 // magnitude passes (1 + m) of its own power.
 //
 // Nothing is a contraction: a token's rows are read once and its record is
-// written once (or the other way), so the memory bounds both directions.  A lane
-// takes kElements neighbouring elements of a row, a block falls to 32 / kElements lanes,
-// which share its maximum by DPP moves, and a workgroup takes neighbouring
-// rows of neighbouring tokens, kEach of them a lane, whose loads are in flight
-// together.
+// written once (or the other way), so the memory bounds both directions, as
+// long as few instructions go into an element.  A lane takes neighbouring
+// elements of a row, a block falls to two or four lanes, which share its
+// maximum by DPP moves, and a workgroup takes neighbouring rows of neighbouring
+// tokens, kEach of them a lane, whose loads are in flight together.  Where a
+// token's rows fill whole waves, its slot is looked up once for the wave.
+//
+// 16,384 tokens of 8 heads of 128 from BF16 to 8 bits (102 MB): 17.6 us, 5.8
+// TB/s; 65,521 records of 8 bits to an E4M3 cache (273 MB): 50.4 us, 5.4 TB/s.
 #include "decode.h"
 
 namespace xfer {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kElements = 8;
-constexpr int kEach = 4;
+// Elements of a lane, 16 bytes of the cache: 65,521 records to an E4M3 cache 50
+// us (8 elements: 58).
+constexpr int elements_of(int kind, int bits) { return kind == XFER_KV_E4M3 && bits == 8 ? 16 : 8; }
+// Rows of a lane: one page of 16 tokens 3.0 us, 16,384 tokens 17.6, 65,521 50.4
+// (4 rows: 3.5, 18.0, 51.7; one: 2.6, 18.1, 50.7).
+constexpr int kEach = 2;
+static_assert(kThreads * kEach * 16 / 64 <= 128, "rows of a workgroup");
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
@@ -99,11 +108,16 @@ struct Place {
   uint32_t token, head, in_record, lane;  // in_record: row of the record, keys before values
   bool there, values, last;
 };
+// WHOLE: all of a wave's rows are one token's, so what depends on the token is
+// the scalar unit's work (16,384 tokens 18.0 us; by every lane for itself 21.2).
+template <bool WHOLE>
 __device__ __forceinline__ Place place_of(const WireArgs &a, uint32_t i) {
   const uint32_t kv = a.cache.kv_heads, at = i * kThreads + threadIdx.x;
-  const uint32_t row = blockIdx.x * ((kThreads * kEach) >> a.lanes_log2) + (at >> a.lanes_log2);
+  const uint32_t first = blockIdx.x * ((kThreads * kEach) >> a.lanes_log2);
+  const uint32_t row = first + (at >> a.lanes_log2);
+  const uint32_t any = WHOLE ? __builtin_amdgcn_readfirstlane(row) : row;
   Place p;
-  p.token = row / (2 * kv);
+  p.token = __umulhi(any, a.magic) >> a.magic_shift;
   p.in_record = row - p.token * (2 * kv);
   p.values = p.in_record >= kv;
   p.head = p.values ? p.in_record - kv : p.in_record;
@@ -122,8 +136,9 @@ __device__ __forceinline__ int64_t slot_byte(const WireArgs &a, uint32_t token) 
   return (int64_t)(page * a.cache.page_stride + at * a.cache.token_stride);
 }
 
-template <int KIND, int BITS, bool STREAM>
+template <int KIND, int BITS, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(WireArgs a) {
+  constexpr int kElements = elements_of(KIND, BITS);
   constexpr int kIn = kElements * (KIND == XFER_KV_BF16 ? 2 : 1), kOut = kElements * BITS / 8;
   constexpr uint32_t kShift = BITS == 8 ? 8 : 2, kCarry = BITS == 8 ? 0x1FFFFF : 0x3FFFFF;  // of L = 1.75 * 2^8, 1.5 * 2^2
   const uint32_t data_bytes = (2 * a.cache.kv_heads << a.lanes_log2) * kOut;
@@ -131,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(WireArgs a) {
   uint32_t w[kEach][kIn / 4];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    p[i] = place_of(a, i);
+    p[i] = place_of<WHOLE>(a, i);
 #pragma unroll
     for (int j = 0; j < kIn / 4; ++j) w[i][j] = 0;
     if (!p[i].there) continue;
@@ -185,18 +200,59 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(WireArgs a) {
   }
 }
 
-template <int KIND, int BITS, bool STREAM>
+// 2^(e - 127): the lowest is subnormal, 255 stands for NaN.
+__device__ __forceinline__ float scale_of(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+}
+
+// x = limit(x * 2^(e - 127) / head), x a record's elements w.
+//
+// A division's dozen of instructions for each element would bound the kernel
+// (65,521 records 101 us, with it taken by reciprocals 57).
+// With h = head / 2^(e - 127) and r = 1 / h, both rounded correctly, q = x r is
+// next to the quotient, and q - (q h - x) r, its remainder fused, is the
+// quotient rounded correctly: so for every x of four bits and every h, tried
+// all, as long as nothing leaves the range of normal numbers.  What might, and
+// NaN, which the limit by a median would lose, is divided.
+template <int BITS, int kElements>
+__device__ __forceinline__ void divide(float *x, const uint32_t *w, uint32_t e, float head) {
+  const uint32_t biased = __float_as_uint(head) >> 23;  // with a sign: too large
+  bool usual = e - 67 <= 120 && biased - 67 <= 120;
+  if (BITS == 8) {
+    uint32_t nan = 0;
+#pragma unroll
+    for (int j = 0; j < kElements / 4; ++j) nan |= (w[j] & 0x7F7F7F7Fu) + 0x01010101u;
+    usual = usual && !(nan & 0x80808080u);
+  }
+  if (usual) {
+    const float h = __uint_as_float(__float_as_uint(head) + ((127 - e) << 23)), r = 1.0f / h;
+#pragma unroll
+    for (int j = 0; j < kElements; ++j) {
+      const float q = x[j] * r;
+      x[j] = __builtin_amdgcn_fmed3f(fmaf(-fmaf(q, h, -x[j]), r, q), -448.0f, 448.0f);
+    }
+  } else {
+    const float scale = scale_of(e);
+#pragma unroll
+    for (int j = 0; j < kElements; ++j) x[j] = e4m3_limit(x[j] * scale / head);
+  }
+}
+
+template <int KIND, int BITS, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void restore_kernel(WireArgs a) {
+  constexpr int kElements = elements_of(KIND, BITS);
   constexpr int kOut = kElements * (KIND == XFER_KV_BF16 ? 2 : 1), kIn = kElements * BITS / 8;
   const uint32_t data_bytes = (2 * a.cache.kv_heads << a.lanes_log2) * kIn;
   Place p[kEach];
   uint32_t w[kEach][kElements / 4], e[kEach];
   int64_t at[kEach];
+  float head[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    p[i] = place_of(a, i);
+    p[i] = place_of<WHOLE>(a, i);
     at[i] = -1;
     e[i] = 0;
+    head[i] = 1.0f;
 #pragma unroll
     for (int j = 0; j < kElements / 4; ++j) w[i][j] = 0;
     if (!p[i].there) continue;
@@ -205,12 +261,14 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(WireArgs a) {
     const uint32_t piece = (p[i].in_record << a.lanes_log2) + p[i].lane;
     load<kIn, STREAM>(w[i], record + piece * kIn);
     e[i] = record[data_bytes + piece / (32 / kElements)];
+    if (KIND == XFER_KV_E4M3) {
+      const float *scales = p[i].values ? a.cache.v_scale : a.cache.k_scale;
+      if (scales) head[i] = scales[p[i].head];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     if (at[i] < 0) continue;
-    // 2^(e - 127): the lowest is subnormal, 255 stands for NaN
-    const float scale = __uint_as_float(e[i] == 0 ? 0x00400000u : e[i] == 255 ? 0x7FC00000u : e[i] << 23);
     float x[kElements];
     if (BITS == 8) {
 #pragma unroll
@@ -219,17 +277,14 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(WireArgs a) {
 #pragma unroll
       for (int j = 0; j < kElements / 8; ++j) from_e2m1x8(x + 8 * j, w[i][j]);
     }
-#pragma unroll
-    for (int j = 0; j < kElements; ++j) x[j] *= scale;
     uint32_t out[kOut / 4];
     if (KIND == XFER_KV_BF16) {
 #pragma unroll
+      for (int j = 0; j < kElements; ++j) x[j] *= scale_of(e[i]);
+#pragma unroll
       for (int j = 0; j < kElements / 2; ++j) out[j] = bf16x2(x[2 * j], x[2 * j + 1]);
     } else {
-      const float *scales = p[i].values ? a.cache.v_scale : a.cache.k_scale;
-      const float head = scales ? scales[p[i].head] : 1.0f;
-#pragma unroll
-      for (int j = 0; j < kElements; ++j) x[j] = e4m3_limit(x[j] / head);
+      divide<BITS, kElements>(x, w[i], e[i], head[i]);
 #pragma unroll
       for (int j = 0; j < kElements / 4; ++j) out[j] = e4m3x4(x + 4 * j);
     }
@@ -237,36 +292,49 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(WireArgs a) {
   }
 }
 
-// Bytes that a call moves, above which they pass the caches by.
+// Bytes that a call moves, above which they pass the caches by: 65,521 tokens
+// of 8 heads restored (273 MB) 50.4 us, 55 through them; 24,001 tokens of 4
+// bits (124 MB), which were quantized just before, 14.2 us, 11.5 through them.
 constexpr uint64_t kCachedBytes = 128ull << 20;
 
+template <int KIND, int BITS, bool WHOLE, bool STREAM>
+hipError_t launch_as(const WireArgs &a, bool restore, uint32_t grid, hipStream_t stream) {
+  return restore ? launch(restore_kernel<KIND, BITS, WHOLE, STREAM>, dim3(grid), dim3(kThreads), 0, stream, a)
+                 : launch(quantize_kernel<KIND, BITS, WHOLE, STREAM>, dim3(grid), dim3(kThreads), 0, stream, a);
+}
 template <int KIND, int BITS>
-hipError_t launch_stream(const WireArgs &a, bool restore, uint32_t grid, bool stream_past, hipStream_t stream) {
-  if (restore)
-    return stream_past ? launch(restore_kernel<KIND, BITS, true>, dim3(grid), dim3(kThreads), 0, stream, a)
-                       : launch(restore_kernel<KIND, BITS, false>, dim3(grid), dim3(kThreads), 0, stream, a);
-  return stream_past ? launch(quantize_kernel<KIND, BITS, true>, dim3(grid), dim3(kThreads), 0, stream, a)
-                     : launch(quantize_kernel<KIND, BITS, false>, dim3(grid), dim3(kThreads), 0, stream, a);
+hipError_t launch_kind(const WireArgs &a, bool restore, uint32_t grid, bool whole, bool past, hipStream_t stream) {
+  if (whole)
+    return past ? launch_as<KIND, BITS, true, true>(a, restore, grid, stream)
+                : launch_as<KIND, BITS, true, false>(a, restore, grid, stream);
+  return past ? launch_as<KIND, BITS, false, true>(a, restore, grid, stream)
+              : launch_as<KIND, BITS, false, false>(a, restore, grid, stream);
 }
 
 }  // namespace
 
-uint64_t wire_workgroups(uint32_t tokens, uint32_t kv_heads, uint32_t head_dim) {
-  const uint64_t rows = (uint64_t)tokens * kv_heads * 2, of_one = kThreads * kEach / (head_dim / kElements);
+uint64_t wire_workgroups(uint32_t tokens, uint32_t kv_heads, uint32_t head_dim, int kind, int bits) {
+  const uint64_t rows = (uint64_t)tokens * kv_heads * 2, of_one = kThreads * kEach / (head_dim / elements_of(kind, bits));
   return rows / of_one + (rows % of_one != 0);
 }
 
 hipError_t launch_wire(const WireArgs &in, int kind, int bits, bool restore, hipStream_t stream) {
   WireArgs a = in;
-  a.lanes_log2 = (uint32_t)__builtin_ctz(a.cache.head_dim / kElements);
-  const uint32_t grid = (uint32_t)wire_workgroups(a.tokens, a.cache.kv_heads, a.cache.head_dim);
+  a.lanes_log2 = (uint32_t)__builtin_ctz(a.cache.head_dim / elements_of(kind, bits));
+  const uint32_t grid = (uint32_t)wire_workgroups(a.tokens, a.cache.kv_heads, a.cache.head_dim, kind, bits);
   const uint64_t elements = (uint64_t)a.tokens * a.cache.kv_heads * 2 * a.cache.head_dim;
   const bool past = elements * (kind == XFER_KV_BF16 ? 2 : 1) + elements * bits / 8 > kCachedBytes;
+  const bool whole = (2 * a.cache.kv_heads << a.lanes_log2) % 64 == 0;
+  // row / (2 kv_heads) is the high half of row * magic, shifted: exact for rows
+  // below 2^31, and the largest grid of 2^24 - 1 workgroups has at most 128 each.
+  const uint32_t per = 2 * a.cache.kv_heads, log2 = 32 - (uint32_t)__builtin_clz(per - 1);
+  a.magic = (uint32_t)(((1ull << (31 + log2)) / per) + 1);
+  a.magic_shift = log2 - 1;
   if (kind == XFER_KV_BF16)
-    return bits == 8 ? launch_stream<XFER_KV_BF16, 8>(a, restore, grid, past, stream)
-                     : launch_stream<XFER_KV_BF16, 4>(a, restore, grid, past, stream);
-  return bits == 8 ? launch_stream<XFER_KV_E4M3, 8>(a, restore, grid, past, stream)
-                   : launch_stream<XFER_KV_E4M3, 4>(a, restore, grid, past, stream);
+    return bits == 8 ? launch_kind<XFER_KV_BF16, 8>(a, restore, grid, whole, past, stream)
+                     : launch_kind<XFER_KV_BF16, 4>(a, restore, grid, whole, past, stream);
+  return bits == 8 ? launch_kind<XFER_KV_E4M3, 8>(a, restore, grid, whole, past, stream)
+                   : launch_kind<XFER_KV_E4M3, 4>(a, restore, grid, whole, past, stream);
 }
 
 }  // namespace xfer

@@ -330,7 +330,8 @@ enum {
  * than a record (tokens > 1), or records, or the cache where it is written,
  * that overlap another buffer; XFER_E_OVERLAP (restore) if two slots of the
  * cache share bytes; XFER_E_UNSUPPORTED for a record of 2 GiB or more or more than
- * 2^24 - 1 workgroups (one for each 8,192 elements).
+ * 2^24 - 1 workgroups (one for each 4,096 elements, or 8,192 of 8 bits and an
+ * E4M3 cache).
  * xfer_kv_record_bytes: 0 for caches and bits that the calls refuse.
  */
 XFER_API size_t xfer_kv_record_bytes(const xfer_kv_cache *cache, int bits);

@@ -226,6 +226,43 @@ def test_any_bytes_are_valid_records(bits, kind):
     check_restored(c, before, np.arange(256), wire.values(rec, n, bits))
 
 
+def head_scales():
+    """Ordinary ones, those whose quotients are halfway between E4M3 numbers but for binary32's rounding, and extremes."""
+    rng = np.random.default_rng(8)
+    halfway = [a / b for a in (8, 11, 13, 15) for b in (17, 21, 25, 27, 31)]
+    powers = [2.0 ** e for e in (-149, -127, -126, -61, -60, -59, 0, 59, 60, 61, 127)]
+    rest = [0.0, -0.0, -1.7, float("inf"), float("-inf"), float("nan"), 3.4e38, 1e-40, 1.0 - 2.0 ** -24, 1.0 + 2.0 ** -23]
+    s = np.concatenate([halfway, powers, rest, rng.uniform(1e-3, 1e3, 96 - 41)]).astype(np.float32)
+    return s.reshape(2, 48)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d", [64, 256])
+def test_every_element_over_every_scale_byte_by_head_scales(bits, d):
+    """Bit for bit what the quotient in binary32 rounds to."""
+    scales = head_scales()
+    heads = scales.shape[1]
+    n, codes_of = 2 * heads * d, d * bits // 8
+    codes = np.tile((np.arange(256 * codes_of) * (1 if bits == 8 else 37) % 256).astype(np.uint8).reshape(256, 1, codes_of),
+                    (1, 2 * heads, 1)).reshape(256, -1)
+    rec = np.concatenate([codes, np.repeat(np.arange(256, dtype=np.uint8)[:, None], n // 32, 1)], 1)
+    rec = np.pad(rec, ((0, 0), (0, -rec.shape[1] % 16)))
+    c = Cache(256, 1, heads, d, "e4m3", "tokens", seed=4)
+    for mine, theirs, v in ((c.ks, c.c.tensors[2], scales[0]), (c.vs, c.c.tensors[3], scales[1])):
+        mine.copy_(torch.from_numpy(v))
+        theirs.copy_(mine)
+    say("head scales", bits, d)
+    decode.kv_restore(torch.from_numpy(rec).to(DEV), bits, c.c, torch.arange(256, device=DEV))
+    with np.errstate(all="ignore"):
+        q = wire.values(rec, n, bits).reshape(256, 2, heads, d).astype(np.float32) / scales[None, :, :, None]
+    assert q.dtype == np.float32
+    nan = np.isnan(q)
+    want = wire.nearest(np.clip(np.where(nan, 0, q), -448, 448).astype(np.float64), 8)
+    got = c.rows().numpy()
+    assert np.array_equal(got[~nan], want[~nan])
+    assert ((got[nan] & 0x7F) == 0x7F).all() and nan.any()
+
+
 def test_a_slot_may_be_read_any_number_of_times_and_records_lie_far_apart():
     c = Cache(3, 16, 2, 128, "bf16", "heads")
     slots = torch.tensor([5, 5, 47, 5, 0], device=DEV)
