@@ -4,35 +4,57 @@
 // A softmax over a row's tokens splits into sums over any parts of them, each
 // with a maximum of its own, so a row is its group's shared tokens and the
 // rest of its own, and three steps make it up:
-//   1. plan: one workgroup turns the groups and lengths into two lists of
-//      entries, a run of tokens with the query heads that see all of it: a row's
-//      own tokens with its heads, a group's shared tokens with the heads of
-//      all its rows.  Rows that do not see all of the shared tokens are kept
-//      out of them and read theirs alone, so no entry needs a mask;
-//   2. walk: the entries' units (128 tokens of a kv head and up to 16 or 32
-//      query heads) are one line that is cut into equal runs, as the attention
-//      of one token cuts its rows, and with the same walk;
-//   3. join: a workgroup for each (row, query head) scales the parts of the
-//      shared tokens and of the row's own to the largest maximum and adds
+//   1. plan: the groups and lengths become entries, a run of tokens with the
+//      query heads that see all of it: a row's own tokens with its heads, a
+//      group's shared tokens with the heads of all its rows.  Rows that do not
+//      see all of the shared tokens are kept out of them and read theirs
+//      alone, so no entry needs a mask.  Up to 255 rows and groups, every
+//      workgroup of the walk makes the plan itself (64 answers: 41.3 us; by a
+//      launch of its own 5.2 us and then 39.8); for more a workgroup of
+//      shared_plan_kernel does (5.5 us for 300);
+//   2. walk, two ways in one launch:
+//      - entries of up to 32 query heads for a kv head (or of one row): their
+//        units (32 tokens of a kv head and up to 16 or 32 query heads) are one
+//        line that is cut into equal runs, one for each wave, with the walk of
+//        the attention of one token.  The memory bounds it, or, where runs
+//        are short, its latency: 2.5 us for a unit;
+//      - groups of more: units of 64 tokens and 128 query heads through LDS,
+//        a run for each workgroup.  The matrix cores and the weights between
+//        the products bound it.
+//      The resident workgroups are shared out between the two so that both end
+//      together (in one launch after the other 64 answers took 85 us, so 58);
+//   3. join: one or four waves for each (row, query head) scale the parts of the
+//      shared tokens and of the row's own to the largest maximum and add
 //      them up, in a fixed order.
+//
+// 64 answers to a prompt of 8192 tokens (32 query heads on 8 of 128, 124 MB):
+// 41 us of walk and 8.8 of join; 24 rows over 131056 shared tokens in F32
+// (548 MB, 193 GFLOP with the weights in three parts): 180 + 12 us.
 #include "attn_tile.h"
+
+#include <type_traits>
 
 namespace xfer {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr uint32_t kUnit = kTile * kWaves;       // tokens of a unit
+constexpr uint32_t kUnit = kTile;                // tokens of a unit
+// Units of a wave's run, at least: 4 drafted positions each of 4 requests of up to 6000 tokens 23.6 us and 9.9 of join;
+// 4 units 28.7 + 7.5, 8 units 39.8 + 6.5.
+constexpr uint32_t kLeast = 2;
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kXcds = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, since the memory bounds the walk
 
 // Groups of more than kFewHeads query heads for a kv head go another way, kManyHeads of them and
-// kManyUnit tokens at a time, and at least kManyLeast such units to a workgroup.
+// kManyUnit tokens at a time (groups of 40 heads of 128: 74 us over 8 x 8000 tokens and 40 over 30000, 32 heads at a time 99
+// and 59; of 64 in E4M3 45, 32 at a time 40), and at least kManyLeast such units to a workgroup (of a group that has as
+// many; with 1 in 64 answers' 16 shared tokens 25 us, with 4 whatever there is 35).
 constexpr uint32_t kFewHeads = 32, kManyHeads = 128, kManyUnit = 64, kManyLeast = 4;
 
-constexpr uint32_t kZeros = 16;  // bytes that stand for tokens that are not there
+__device__ const v4u kZeros = {0, 0, 0, 0};  // stands for tokens that are not there
 
 // ------------------------------------------------------------------- plan
 
@@ -44,7 +66,7 @@ struct Extent {
 };
 __device__ __forceinline__ Extent operator+(const Extent &x, const Extent &y) { return {x.units + y.units, x.tiles + y.tiles}; }
 __device__ __forceinline__ Extent extent_of(const SharedArgs &a, const SharedEntry &e, uint32_t tile, uint32_t unit) {
-  const uint32_t tiles = (uint32_t)(((uint64_t)e.q_rows * a.group + tile - 1) / tile);
+  const uint32_t tiles = (e.q_rows * a.group + tile - 1) >> (31 - __builtin_clz(tile));  // a power of two
   return {(uint64_t)((e.n + unit - 1) / unit) * a.cache.kv_heads * tiles, tiles};
 }
 
@@ -68,46 +90,65 @@ __device__ __forceinline__ T wave_scan(T x, F &&op) {
   return op(x, dpp<0x143, 0xC>(x));
 }
 
-__global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a) {
-  constexpr uint32_t kPlanWaves = kPlanThreads / 64;
-  __shared__ uint32_t start[kMaxGroups + 1], prefix[kMaxGroups];
-  __shared__ uint32_t wave_top[kPlanWaves];
-  __shared__ Extent wave_sum[3][kPlanWaves];
+// Query heads of a tile in the list of few: 16 at a time, or 32 where there are more, so that their tokens are read once
+// (16 groups of 20 heads over 6000 tokens each 92 us, 16 at a time 128; 4 such groups of up to 6000, which leave workgroups
+// without work, 24 and 22.6).
+__device__ __forceinline__ uint32_t tile_of(uint32_t heads) { return heads > 16 ? 32 : 16; }
+
+template <int THREADS>
+struct PlanLds {
+  static constexpr uint32_t kGroups = THREADS == kPlanThreads ? kMaxGroups : THREADS;
+  uint32_t start[kGroups + 1], prefix[kGroups];
+  uint32_t len[THREADS == kPlanThreads ? 1 : THREADS];  // of the rows, where each thread has one at most
+  uint32_t wave_top[THREADS / 64], longest;
+  Extent wave_sum[2][THREADS / 64];
+};
+
+// The lists, by all threads of a workgroup: begin(units of rows and groups of few heads, of groups of many, most tokens of
+// one of those), then put(many, index, entry) by one thread for each entry.
+template <int THREADS, typename Begin, typename Put>
+__device__ __forceinline__ void plan(const SharedArgs &a, PlanLds<THREADS> &lds, Begin &&begin, Put &&put) {
+  constexpr uint32_t kPlanWaves = THREADS / 64;
+  constexpr bool kOne = THREADS != kPlanThreads;  // a thread has one row and one start at most
+  auto &start = lds.start;
+  auto &prefix = lds.prefix;
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  if (tid < kZeros / 4) reinterpret_cast<uint32_t *>(a.zeros)[tid] = 0;
-  // This thread's starts, groups and rows.  Loads that depend on nothing first.
-  const uint32_t n_starts = a.groups + 1, s_each = (n_starts + kPlanThreads - 1) / kPlanThreads;
+  // This thread's starts, groups and entries (rows, then groups).  Loads that depend on nothing first.
+  const uint32_t n_starts = a.groups + 1, s_each = kOne ? 1 : (n_starts + THREADS - 1) / THREADS;
   const uint32_t s0 = min(tid * s_each, n_starts), s1 = min(s0 + s_each, n_starts);
   const uint32_t g0 = min(s0, a.groups), g1 = min(s1, a.groups);
-  const uint32_t r_each = (a.rows + kPlanThreads - 1) / kPlanThreads;
-  const uint32_t r0 = min(tid * r_each, a.rows), r1 = min(r0 + r_each, a.rows);
-  const uint32_t first_len = r0 < r1 ? a.lens[r0] : 0, first_shared = g0 < g1 ? a.shared[g0] : 0;
+  const uint32_t n_entries = a.rows + a.groups, e_each = kOne ? 1 : (n_entries + THREADS - 1) / THREADS;
+  const uint32_t e0 = min(tid * e_each, n_entries), e1 = min(e0 + e_each, n_entries);
+  const uint32_t first_len = e0 < a.rows ? a.lens[e0] : 0, first_shared = g0 < g1 ? a.shared[g0] : 0;
   // The groups' first rows: a start below the one before counts as that one,
   // so that no row is in two groups, whatever the caller's numbers are.
   auto given = [&](uint32_t i) { return a.groups ? min(a.starts[i], a.rows) : a.rows; };
   auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
   uint32_t top = 0;
   for (uint32_t i = s0; i < s1; ++i) start[i] = top = max(top, given(i));
+  if (kOne) lds.len[tid] = first_len;
   const uint32_t through = wave_scan(top, larger);
-  if (lane == 63) wave_top[wave] = through;
+  if (lane == 63) lds.wave_top[wave] = through;
+  if (tid == 0) lds.longest = 0;
   __syncthreads();
   uint32_t before = __shfl_up(through, 1);  // by all lanes: one that sits out gives nothing
   if (lane == 0) before = 0;
-  for (uint32_t w = 0; w < wave; ++w) before = max(before, wave_top[w]);
+  for (uint32_t w = 0; w < wave; ++w) before = max(before, lds.wave_top[w]);
   for (uint32_t i = s0; i < s1; ++i) start[i] = max(start[i], before);
   __syncthreads();
   for (uint32_t g = g0; g < g1; ++g) {
     const uint32_t row = start[g], n = start[g + 1] - row;
     uint32_t p = n > 1 ? min(g == g0 ? first_shared : a.shared[g], a.max_len) : 0;
-    if (p) p = min(p, a.lens[row]);  // the first row's pages are read
+    if (p) p = min(p, kOne ? lds.len[row] : a.lens[row]);  // the first row's pages are read
     prefix[g] = p;
+    if (p && n * a.group > kFewHeads) atomicMax(&lds.longest, p);
   }
   __syncthreads();
   // A group's shared tokens, if its rows' heads are in the list of many or the other.
   auto of_group = [&](uint32_t g, bool many) {
     SharedEntry e{};
     const uint32_t rows = start[g + 1] - start[g];
-    if (!prefix[g] || ((uint64_t)rows * a.group > kFewHeads) != many) return e;
+    if (!prefix[g] || (rows * a.group > kFewHeads) != many) return e;
     e.n = prefix[g];
     e.row = e.q_row = start[g];
     e.q_rows = rows;
@@ -123,7 +164,7 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
       else
         hi = mid;
     }
-    const uint32_t len = min(i == r0 ? first_len : a.lens[i], a.max_len);
+    const uint32_t len = min(i == e0 ? first_len : a.lens[i], a.max_len);
     const uint32_t p = lo > 0 && lo <= a.groups ? prefix[lo - 1] : 0;
     e.first = p <= len ? p : 0;
     e.n = len - e.first;
@@ -132,57 +173,98 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
     e.group = e.first ? lo - 1 : kNoGroup;
     return e;
   };
-  // Where each entry's units and parts begin: rows, groups of few heads after them, and groups of many.
-  Extent mine[3] = {};
-  for (uint32_t i = r0; i < r1; ++i) mine[0] = mine[0] + extent_of(a, of_row(i), a.tile, kUnit);
-  for (uint32_t g = g0; g < g1; ++g) {
-    mine[1] = mine[1] + extent_of(a, of_group(g, false), a.tile, kUnit);
-    mine[2] = mine[2] + extent_of(a, of_group(g, true), kManyHeads, kManyUnit);
+  auto of = [&](uint32_t i) { return i < a.rows ? of_row(i) : of_group(i - a.rows, false); };
+  // Where each entry's units and parts begin, in either list.
+  auto few = [&](const SharedEntry &e) { return extent_of(a, e, tile_of(e.q_rows * a.group), kUnit); };
+  auto many = [&](const SharedEntry &e) { return extent_of(a, e, kManyHeads, kManyUnit); };
+  const SharedEntry first = e0 < e1 ? of(e0) : SharedEntry{};
+  Extent at[2] = {}, all[2] = {};
+  for (uint32_t i = e0; i < e1; ++i) {
+    at[0] = at[0] + few(i == e0 ? first : of(i));
+    if (i >= a.rows) at[1] = at[1] + many(of_group(i - a.rows, true));
   }
-  Extent at[3], all[3];
-  auto add = [](const Extent &x, const Extent &y) { return x + y; };
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    at[k] = wave_scan(mine[k], add);
-    if (lane == 63) wave_sum[k][wave] = at[k];
+  for (int k = 0; k < 2; ++k) {
+    const Extent mine = at[k];
+    at[k] = wave_scan(mine, [](const Extent &x, const Extent &y) { return x + y; });
+    if (lane == 63) lds.wave_sum[k][wave] = at[k];
+    at[k] = {at[k].units - mine.units, at[k].tiles - mine.tiles};
   }
   __syncthreads();
+  const uint32_t longest = lds.longest;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const Extent waves = wave_scan(lane < kPlanWaves ? wave_sum[k][lane] : Extent{}, add);  // up to each wave
-    auto of_wave = [&](uint32_t w) -> Extent {
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)waves.units, w),
-                     hi = __builtin_amdgcn_readlane((uint32_t)(waves.units >> 32), w);
-      return {(uint64_t)hi << 32 | lo, (uint32_t)__builtin_amdgcn_readlane(waves.tiles, w)};
-    };
-    all[k] = of_wave(kPlanWaves - 1);
-    const Extent before_wave = wave ? of_wave(wave - 1) : Extent{};
-    at[k] = {at[k].units - mine[k].units + before_wave.units, at[k].tiles - mine[k].tiles + before_wave.tiles};
-  }
-  at[1] = at[1] + all[0];
-  auto put = [&](SharedEntry &to, SharedEntry e, Extent &from, uint32_t part0, uint32_t tile, uint32_t unit) {
+  for (uint32_t w = 0; w < kPlanWaves; ++w)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (w == wave) at[k] = at[k] + all[k];
+      all[k] = all[k] + lds.wave_sum[k][w];
+    }
+  begin(all[0].units, all[1].units, longest);
+  auto place = [&](SharedEntry &e, Extent &from, uint32_t part0, const Extent &extent) {
     e.unit0 = from.units;
     e.part0 = part0 + from.tiles * a.cache.kv_heads;
-    to = e;
-    from = from + extent_of(a, e, tile, unit);
+    from = from + extent;
   };
-  for (uint32_t i = r0; i < r1; ++i) put(a.entries[i], of_row(i), at[0], 0, a.tile, kUnit);
-  for (uint32_t g = g0; g < g1; ++g) {
-    put(a.entries[a.rows + g], of_group(g, false), at[1], 0, a.tile, kUnit);
-    if (a.many) put(a.many[g], of_group(g, true), at[2], a.many_part0, kManyHeads, kManyUnit);
+  for (uint32_t i = e0; i < e1; ++i) {
+    SharedEntry e = i == e0 ? first : of(i);
+    place(e, at[0], 0, few(e));
+    put(false, i, e);
+    if (i < a.rows || !a.many) continue;
+    e = of_group(i - a.rows, true);
+    place(e, at[1], a.many_part0, many(e));
+    put(true, i - a.rows, e);
   }
-  if (tid == 0) {
-    a.entries[a.rows + a.groups].unit0 = all[0].units + all[1].units;
-    if (a.many) {
-      a.many[a.groups].unit0 = all[2].units;
-      // Both lists' workgroups are to end together, by what a unit of each costs.
-      const double few = (double)(all[0].units + all[1].units) * a.unit_cost, many = (double)all[2].units * a.many_unit_cost;
-      uint32_t n = few + many > 0 ? (uint32_t)(a.places_of_xcd * (many / (few + many)) + 0.5) : 0;
-      if (all[2].units) n = max(n, 1u);
-      if (few > 0) n = min(n, a.places_of_xcd - 1);
-      *a.many_places = n;
-    }
-  }
+}
+
+// Of an XCD's workgroups, those that take the list of many: both lists' are to end together, by what a unit of each costs.
+__device__ __forceinline__ uint32_t many_places(const SharedArgs &a, uint64_t few_units, uint64_t many_units) {
+  const float few = (float)few_units * (float)a.unit_cost, many = (float)many_units * (float)a.many_unit_cost;
+  uint32_t n = few + many > 0 ? (uint32_t)((float)a.places_of_xcd * (many / (few + many)) + 0.5f) : 0;
+  if (many_units) n = max(n, 1u);
+  if (few_units) n = min(n, a.places_of_xcd - 1);
+  return n;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a) {
+  __shared__ PlanLds<kPlanThreads> lds;
+  plan<kPlanThreads>(
+      a, lds,
+      [&](uint64_t few_units, uint64_t many_units, uint32_t longest) {
+        if (threadIdx.x != 0) return;
+        a.entries[a.rows + a.groups].unit0 = few_units;
+        if (!a.many) return;
+        a.many[a.groups].unit0 = many_units;
+        a.many[a.groups].n = longest;
+        *a.many_places = many_places(a, few_units, many_units);
+      },
+      [&](bool many, uint32_t i, const SharedEntry &e) { (many ? a.many : a.entries)[i] = e; });
+}
+
+// The list that a workgroup of the walk takes, in LDS: where each thread has one row and one start at most, every
+// workgroup makes it itself, which costs no more than to read it and saves a launch; the first one also
+// writes both lists for the join.
+struct LocalPlan {
+  SharedEntry list[kThreads + 1];
+};
+// choose(many_places): whether this workgroup takes the list of many.
+template <typename Choose>
+__device__ __forceinline__ bool plan_here(const SharedArgs &a, LocalPlan &to, PlanLds<kThreads> &lds, Choose &&choose) {
+  bool takes_many = false;
+  plan<kThreads>(
+      a, lds,
+      [&](uint64_t few_units, uint64_t many_units, uint32_t longest) {
+        takes_many = choose(a.many ? many_places(a, few_units, many_units) : 0);
+        if (threadIdx.x != 0) return;
+        SharedEntry &end = to.list[takes_many ? a.groups : a.rows + a.groups];
+        end.unit0 = takes_many ? many_units : few_units;
+        end.n = longest;
+      },
+      [&](bool many, uint32_t i, const SharedEntry &e) {
+        if (many == takes_many) to.list[i] = e;
+        if (blockIdx.x == 0) (many ? a.many : a.entries)[i] = e;
+      });
+  __syncthreads();
+  return takes_many;
 }
 
 // ------------------------------------------------------------------- walk
@@ -191,49 +273,63 @@ __global__ __launch_bounds__(kPlanThreads) void shared_plan_kernel(SharedArgs a)
 // its first part's slot (kWhole: one workgroup did it all), and how many parts.
 constexpr uint32_t kWhole = 0xFFFFFFFFu;
 
-template <int D, int TILES>
+// Queries that registers do not hold, of each wave.
+template <int D, int KIND, int TILES>
 struct WalkLds {
-  static constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
-  float o[kWaves][16][D + kPad];
-  float m[TILES][kWaves][16], l[TILES][kWaves][16];
+  static constexpr int kMost = TILES == 2 && Residence<D, KIND, 2>::kQInLds ? 2 : Residence<D, KIND, 1>::kQInLds ? 1 : 0;
+  v4u q[kMost ? kWaves : 1][kMost ? kMost * Layout<D, KIND>::kMfmaK * 64 : 1];
 };
 
-// The entry that unit `from` of a list falls to; by all threads.
+// Query heads of a slot for what a wave has of a tile's tokens.
+constexpr uint32_t slot_heads(int tiles) { return 16 * tiles; }
+
+// An entry that is the same for all lanes.
+__device__ __forceinline__ SharedEntry scalar(const SharedEntry &e) {
+  static_assert(sizeof(SharedEntry) % 4 == 0, "words");
+  uint32_t w[sizeof(SharedEntry) / 4];
+  __builtin_memcpy(w, &e, sizeof(e));
+#pragma unroll
+  for (uint32_t &x : w) x = __builtin_amdgcn_readfirstlane(x);
+  SharedEntry s;
+  __builtin_memcpy(&s, w, sizeof(s));
+  return s;
+}
+// The entry that unit `from` of a list falls to, by a wave: the last whose units begin there or before.
 __device__ __forceinline__ uint32_t entry_at(const SharedEntry *entries, uint32_t n, uint64_t from) {
-  __shared__ uint32_t start;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-    if (entries[i].unit0 <= from && from < entries[i + 1].unit0) start = i;
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(start);
+  uint32_t first = 0;
+#pragma unroll 1
+  for (uint32_t left = n; left > 1;) {
+    const uint32_t step = (left + 63) / 64, i = threadIdx.x % 64 * step;
+    const uint32_t before = (uint32_t)__popcll(__ballot(i < left && entries[first + i].unit0 <= from)) - 1;
+    first += before * step;
+    left = min(step, left - before * step);
+  }
+  return first;
 }
 
-// The run of workgroup wg of n_wg.
+// The runs of workgroup wg of n_wg, one of each wave.  TILES: 16 query heads at a time, or (2) 32 of the entries that
+// have more.
 template <int D, int KIND, int TILES>
-__device__ __forceinline__ void walk(const SharedArgs &a, uint32_t wg, uint32_t n_wg, WalkLds<D, TILES> &lds) {
+__device__ __forceinline__ void walk(const SharedArgs &a, const SharedEntry *entries, uint32_t wg, uint32_t n_wg,
+                                     WalkLds<D, KIND, TILES> &lds) {
   using L = Layout<D, KIND>;
-  using R = Residence<D, KIND, TILES>;
-  constexpr int MR = TILES;
-  constexpr uint32_t kHeads = 16 * TILES;
-  auto &lds_o = lds.o;
-  auto &lds_all_m = lds.m;
-  auto &lds_all_l = lds.l;
-  const uint32_t n_entries = a.rows + a.groups;
-  const uint64_t all = a.entries[n_entries].unit0, per = (all + n_wg - 1) / n_wg, from = wg * per;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
+  const uint32_t n_entries = a.rows + a.groups, n_runs = n_wg * kWaves, run = wg * kWaves + wave;
+  const uint64_t all = entries[n_entries].unit0, share = (all + n_runs - 1) / n_runs;
+  const uint64_t per = share < kLeast ? kLeast : share, from = run * per;
   if (from >= all) return;
   uint64_t left = min(per, all - from);
-  uint32_t index = entry_at(a.entries, n_entries, from);
-  SharedEntry e = a.entries[index];
+  uint32_t index = entry_at(entries, n_entries, from);
+  SharedEntry e = scalar(entries[index]);
   uint64_t at = from - e.unit0;
-
-  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 16,
-                 g = lane / 16;
-  // The queries, in the lanes' order, where the exchange lies later.
-  v4u *const lds_q = reinterpret_cast<v4u *>(&lds_o[0][0][0]);
-  static_assert(!R::kQInLds || MR * L::kMfmaK * 64 * 16 <= (int)sizeof(lds_o), "they fit");
+  v4u *const lds_q = WalkLds<D, KIND, TILES>::kMost ? lds.q[wave] : lds.q[0];
   bool first_segment = true;
 
-#pragma unroll 1
-  while (left) {
+  // What is left of an entry, MR times 16 heads at a time.
+  auto entry = [&](auto tiles) {
+    constexpr int MR = decltype(tiles)::value;
+    using R = Residence<D, KIND, MR>;
+    constexpr uint32_t kHeads = 16 * MR;
     const uint32_t heads = e.q_rows * a.group, m_groups = (heads + kHeads - 1) / kHeads;
     const uint32_t units = (e.n + kUnit - 1) / kUnit, inner_n = m_groups * a.cache.kv_heads;
     uint32_t inner = __builtin_amdgcn_readfirstlane((uint32_t)(at / units));
@@ -246,96 +342,70 @@ __device__ __forceinline__ void walk(const SharedArgs &a, uint32_t wg, uint32_t 
       const Visible vis{e.n, 0, e.first};
       // Q: query head h0 + 16 * r + n of the entry, the dims that this lane's K loads hold.
       v4u q[R::kQInLds ? 1 : MR][L::kMfmaK];
-      auto load_q = [&](int r, int k) {
+#pragma unroll
+      for (int r = 0; r < MR; ++r) {
         const uint32_t h = h0 + 16 * r + n;
-        const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
-        if (h >= heads) return v4u{0, 0, 0, 0};
-        return *reinterpret_cast<const v4u *>(a.q + (e.q_row + h / a.group) * a.q_ld +
-                                              (uint64_t)(kvh * a.group + h % a.group) * D + d);
-      };
-      if constexpr (R::kQInLds) {
-        for (int k = wave; k < MR * L::kMfmaK; k += kWaves) lds_q[k * 64 + lane] = load_q(k / L::kMfmaK, k % L::kMfmaK);
-        __syncthreads();
-      } else {
+        const uint16_t *from_q = a.q + (e.q_row + h / a.group) * a.q_ld + (uint64_t)(kvh * a.group + h % a.group) * D;
 #pragma unroll
-        for (int r = 0; r < MR; ++r)
-#pragma unroll
-          for (int k = 0; k < L::kMfmaK; ++k) q[r][k] = load_q(r, k);
+        for (int k = 0; k < L::kMfmaK; ++k) {
+          const uint32_t d = KIND == XFER_KV_BF16 ? k * 32 + g * 8 : (k / 2) * 64 + g * 16 + (k % 2) * 8;
+          const v4u x = h < heads ? *reinterpret_cast<const v4u *>(from_q + d) : v4u{0, 0, 0, 0};
+          if constexpr (R::kQInLds)
+            lds_q[(r * L::kMfmaK + k) * 64 + lane] = x;  // which this lane reads again
+          else
+            q[r][k] = x;
+        }
       }
       float scale2 = a.scale * 1.4426950408889634f;
       if (KIND == XFER_KV_E4M3 && a.cache.k_scale) scale2 *= a.cache.k_scale[kvh];
       const uint32_t *table = a.page_table + e.row * a.table_ld;
       v4f o[MR][L::kMfmaV];
       float mx[MR], sum[MR];
-      attn_walk<D, KIND, MR, kParts, kUnit, false>(a.cache, kvh, table, vis, v0 + wave * kTile, v1, scale2, n, g, lane, q,
-                                                   lds_q, o, mx, sum);
+      attn_walk<D, KIND, MR, kParts, kUnit, false>(a.cache, kvh, table, vis, v0, v1, scale2, n, g, lane, q, lds_q, o, mx, sum);
 
-      // The waves' results, joined in LDS.
       const bool whole = take == units;
-      const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
-      if (unit == 0 && tid == 0)
+      const uint32_t slot = 2 * run + (first_segment ? 0 : 1);
+      if (unit == 0 && lane == 0)
         a.parts[e.part0 + inner] = whole ? SharedParts{kWhole, 1} : SharedParts{slot, 1 + (uint32_t)((units - take + per - 1) / per)};
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
         sum[r] += __shfl_xor(sum[r], 16);
         sum[r] += __shfl_xor(sum[r], 32);
+        const uint32_t h = h0 + 16 * r + n;
+        if (h >= heads) continue;
+        // a whole one's place is its row's and head's, in the half for shared or own tokens
+        const uint64_t mine = (uint64_t)(e.q_row + h / a.group) * a.q_heads + kvh * a.group + h % a.group;
+        const uint64_t to = whole ? a.whole0 + (index < a.rows ? 0 : (uint64_t)a.rows * a.q_heads) + mine
+                                  : (uint64_t)slot * slot_heads(TILES) + 16 * r + n;
         if (g == 0) {
-          lds_all_m[r][wave][n] = mx[r];
-          lds_all_l[r][wave][n] = sum[r];
+          a.part_ml[2 * to] = mx[r];
+          a.part_ml[2 * to + 1] = sum[r];
         }
-      }
-      __syncthreads();
 #pragma unroll
-      for (int r = 0; r < MR; ++r) {
-        auto &lds_m = lds_all_m[r];
-        auto &lds_l = lds_all_l[r];
-        if (r) __syncthreads();
-        {
-          float top = -INFINITY;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][n]);
-          const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - top);
-#pragma unroll
-          for (int j = 0; j < L::kMfmaV; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lds_o[wave][n][dim_of<D, KIND>(j, 4 * g + i)] = o[r][j][i] * f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (uint32_t i = tid; i < 4 * D; i += kThreads) {
-          const uint32_t hq = i / (D / 4), d = i % (D / 4) * 4, h = h0 + 16 * r + hq;
-          if (h >= heads) continue;
-          float top = -INFINITY, total = 0;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][hq]);
-          v4f v = {0, 0, 0, 0};
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
-            const float mw = lds_m[w][hq];
-            total += mw == -INFINITY ? lds_l[w][hq] : lds_l[w][hq] * __builtin_amdgcn_exp2f(mw - top);
-            v += *reinterpret_cast<const v4f *>(&lds_o[w][hq][d]);
+          for (int j = 0; j < L::kMfmaV; j += 4) {
+            const uint32_t d = dim_of<D, KIND>(j, 4 * g + i);
+            v4f v = {o[r][j][i], o[r][j + 1][i], o[r][j + 2][i], o[r][j + 3][i]};
+            if constexpr (KIND == XFER_KV_BF16) {
+              if (isnan(v.x + v.y + v.z + v.w) && !isnan(sum[r])) v = with_infinities<KIND>(a.cache, kvh, table, vis, v0, v1, v, d);
+            }
+            *reinterpret_cast<v4f *>(a.part_o + to * D + d) = v;
           }
-          if constexpr (KIND == XFER_KV_BF16) {
-            if (isnan(v.x + v.y + v.z + v.w)) v = with_infinities<KIND>(a.cache, kvh, table, vis, v0, v1, v, d);
-          }
-          // a whole one's place is its row's and head's, in the half for shared or own tokens
-          const uint64_t mine = (uint64_t)(e.q_row + h / a.group) * a.q_heads + kvh * a.group + h % a.group;
-          const uint64_t to = whole ? a.whole0 + (index < a.rows ? 0 : (uint64_t)a.rows * a.q_heads) + mine
-                                    : (uint64_t)slot * kHeads + 16 * r + hq;
-          *reinterpret_cast<v4f *>(a.part_o + to * D + d) = v;
-          if (d == 0) {
-            a.part_ml[2 * to] = top;
-            a.part_ml[2 * to + 1] = total;
-          }
-        }
       }
       left -= take;
       first_segment = false;
-      if (left) __syncthreads();  // LDS is written again
     }
+  };
+#pragma unroll 1
+  while (left) {
+    if (TILES == 2 && e.q_rows * a.group > 16)
+      entry(std::integral_constant<int, TILES>{});
+    else
+      entry(std::integral_constant<int, 1>{});
     at = 0;
     if (left) {
-      do e = a.entries[++index];
+      do e = scalar(entries[++index]);
       while (e.n == 0);  // there is one with tokens as long as units are left
     }
   }
@@ -377,17 +447,19 @@ __device__ __forceinline__ v2u column4(const uint8_t *p) {
 // The run of workgroup wg of n_wg; lds0 and lds1 are two variables, not one of two: then the compiler knows that what
 // is on its way to one does not change the other.
 template <int D, int KIND, int PARTS>
-__device__ __forceinline__ void walk_many(const SharedArgs &a, uint32_t wg, uint32_t n_wg, uint8_t *lds0, uint8_t *lds1) {
+__device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry *entries, uint32_t wg, uint32_t n_wg,
+                                          uint8_t *lds0, uint8_t *lds1) {
   using M = Many<D, KIND>;
   constexpr int kDims = D / 32;   // blocks of dims
   constexpr int kSteps = D / 16;  // of a score
   __shared__ __align__(8) uint16_t lds_gone[2][kWaves];  // a bit for each token of 16 that is not there
-  const uint64_t all = a.many[a.groups].unit0, share = (all + n_wg - 1) / n_wg;
-  const uint64_t per = share < kManyLeast ? kManyLeast : share, from = wg * per;
+  const uint64_t all = entries[a.groups].unit0, share = (all + n_wg - 1) / n_wg;
+  const uint64_t least = min(kManyLeast, (entries[a.groups].n + kManyUnit - 1) / kManyUnit);
+  const uint64_t per = share < least ? least : share, from = wg * per;
   if (from >= all) return;
   uint64_t left = min(per, all - from);
-  uint32_t index = entry_at(a.many, a.groups, from);
-  SharedEntry e = a.many[index];
+  uint32_t index = entry_at(entries, a.groups, from);
+  SharedEntry e = scalar(entries[index]);
   uint64_t at = from - e.unit0;
 
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, n = lane % 32,
@@ -443,7 +515,8 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, uint32_t wg, uint
           const uint64_t off = p.page[i] * a.cache.page_stride + (token & slot_mask) * a.cache.token_stride +
                                (place ^ (local & 7)) * 8 * M::kBytes;
           // one that is not there is all zeros: no weight times it is NaN
-          const uint8_t *key = there ? kbase + off : a.zeros, *value = there ? vbase + off : a.zeros;
+          const uint8_t *zeros = reinterpret_cast<const uint8_t *>(&kZeros);
+          const uint8_t *key = there ? kbase + off : zeros, *value = there ? vbase + off : zeros;
           if constexpr (KIND == XFER_KV_BF16) {
             typedef const __attribute__((address_space(1))) void *Global;
             typedef __attribute__((address_space(3))) void *Lds;
@@ -623,34 +696,50 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, uint32_t wg, uint
     }
     at = 0;
     if (left) {
-      do e = a.many[++index];
+      do e = scalar(entries[++index]);
       while (e.n == 0);  // there is one with tokens as long as units are left
     }
   }
 }
 
 // Neighbouring runs on one XCD: its L2 then serves the tokens that the heads of an entry have in common.
-template <int D, int KIND, int TILES>
+// LOCAL: the workgroups make the plan themselves.
+template <int D, int KIND, int TILES, bool LOCAL>
 __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void shared_walk_kernel(SharedArgs a) {
-  __shared__ WalkLds<D, TILES> lds;
-  walk<D, KIND, TILES>(a, blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds, gridDim.x, lds);
+  __shared__ WalkLds<D, KIND, TILES> lds;
+  __shared__ LocalPlan local;
+  __shared__ PlanLds<kThreads> plan;
+  if (LOCAL) plan_here(a, local, plan, [](uint32_t) { return false; });
+  const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  if (LOCAL)
+    walk<D, KIND, TILES>(a, local.list, wg, gridDim.x, lds);
+  else
+    walk<D, KIND, TILES>(a, a.entries, wg, gridDim.x, lds);
 }
 
 // Both lists at once, so that one's loads and the other's products share the compute units: of the workgroups
 // that are resident, as many take the list of many heads as the plan found, spread evenly over the others.
-template <int D, int KIND, int TILES, int PARTS>
+template <int D, int KIND, int PARTS, bool LOCAL>
 __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_both_kernel(SharedArgs a) {
   constexpr uint32_t kTile = 2 * Many<D, KIND>::kTileBytes;
-  __shared__ __align__(16) uint8_t lds0[kTile < sizeof(WalkLds<D, TILES>) ? sizeof(WalkLds<D, TILES>) : kTile];
+  __shared__ __align__(16) uint8_t lds0[kTile];
+  static_assert(sizeof(WalkLds<D, KIND, 2>) <= kTile, "it fits");
   __shared__ __align__(16) uint8_t lds1[kTile];
+  __shared__ LocalPlan local;
+  static_assert(sizeof(PlanLds<kThreads>) <= sizeof(lds0), "it fits");
   const uint32_t xcd = blockIdx.x % kXcds, place = blockIdx.x / kXcds, places = gridDim.x / kXcds;
-  const uint32_t many = *a.many_places;  // of an XCD's places
-  const uint32_t before = place * many / places;
-  if ((place + 1) * many / places > before)
-    walk_many<D, KIND, PARTS>(a, xcd * many + before, kXcds * many, lds0, lds1);
+  uint32_t many, before;  // of an XCD's places, and of those before this one
+  auto choose = [&](uint32_t n) {
+    many = n;
+    before = place * many / places;
+    return (place + 1) * many / places > before;
+  };
+  const bool takes_many = LOCAL ? plan_here(a, local, reinterpret_cast<PlanLds<kThreads> &>(lds0), choose) : choose(*a.many_places);
+  if (takes_many)
+    walk_many<D, KIND, PARTS>(a, LOCAL ? local.list : a.many, xcd * many + before, kXcds * many, lds0, lds1);
   else
-    walk<D, KIND, TILES>(a, xcd * (places - many) + place - before, kXcds * (places - many),
-                         *reinterpret_cast<WalkLds<D, TILES> *>(lds0));
+    walk<D, KIND, 2>(a, LOCAL ? local.list : a.entries, xcd * (places - many) + place - before, kXcds * (places - many),
+                     *reinterpret_cast<WalkLds<D, KIND, 2> *>(lds0));
 }
 
 // ------------------------------------------------------------------- join
@@ -674,10 +763,12 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
     uint32_t n;                 // parts
     uint64_t at0, at1, stride;  // places: part 0's; part p's at1 + p * stride
   };
-  auto source = [&](const SharedEntry &e, bool prefix, uint32_t tile, uint64_t cut0) {
+  auto source = [&](const SharedEntry &e, bool prefix, bool many) {
     Source s{};
     if (!e.n) return s;
-    const uint32_t heads = e.q_rows * a.group, m_groups = (heads + tile - 1) / tile;
+    const uint32_t heads = e.q_rows * a.group, tile = many ? kManyHeads : tile_of(heads), m_groups = (heads + tile - 1) / tile;
+    const uint32_t slot = many ? kManyHeads : a.slot_heads;
+    const uint64_t cut0 = many ? a.many_place0 : 0;
     const uint32_t i = (row - e.q_row) * a.group + h;
     const SharedParts p = a.parts[e.part0 + kvh * m_groups + i / tile];
     s.n = p.n;
@@ -685,18 +776,18 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
       s.at0 = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
     } else {
       // Part p > 0 is the first thing that the workgroup p further on did.
-      s.at0 = cut0 + (uint64_t)p.slot * tile + i % tile;
-      s.at1 = cut0 + (uint64_t)(p.slot / 2 * 2) * tile + i % tile;
-      s.stride = 2 * tile;
+      s.at0 = cut0 + (uint64_t)p.slot * slot + i % tile;
+      s.at1 = cut0 + (uint64_t)(p.slot / 2 * 2) * slot + i % tile;
+      s.stride = 2 * slot;
     }
     return s;
   };
   Source pre{};
   if (own.group != kNoGroup) {
     const SharedEntry e = a.entries[a.rows + own.group];
-    pre = e.n ? source(e, true, a.tile, 0) : source(a.many[own.group], true, kManyHeads, a.many_place0);
+    pre = e.n ? source(e, true, false) : source(a.many[own.group], true, true);
   }
-  const Source mine = source(own, false, a.tile, 0);
+  const Source mine = source(own, false, false);
   const uint32_t n = pre.n + mine.n;
   auto place = [&](uint32_t p) -> uint64_t {
     const Source &s = p < pre.n ? pre : mine;
@@ -772,25 +863,26 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
 
 // ----------------------------------------------------------------- launches
 
-template <int D, int KIND>
-hipError_t launch_kind(const SharedArgs &a, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
-  const dim3 block(kThreads);
+template <int D, int KIND, bool LOCAL>
+hipError_t launch_walk(const SharedArgs &a, uint32_t workgroups, hipStream_t stream) {
+  const dim3 grid(workgroups), block(kThreads);
   if (!a.many)
-    return a.tile == 16 ? launch(shared_walk_kernel<D, KIND, 1>, dim3(workgroups), block, 0, stream, a)
-                        : launch(shared_walk_kernel<D, KIND, 2>, dim3(workgroups), block, 0, stream, a);
-  const dim3 grid(many_workgroups);
-  if (a.out_mode == XFER_OUT_F32)
-    return a.tile == 16 ? launch(shared_both_kernel<D, KIND, 1, 3>, grid, block, 0, stream, a)
-                        : launch(shared_both_kernel<D, KIND, 2, 3>, grid, block, 0, stream, a);
-  return a.tile == 16 ? launch(shared_both_kernel<D, KIND, 1, 2>, grid, block, 0, stream, a)
-                      : launch(shared_both_kernel<D, KIND, 2, 2>, grid, block, 0, stream, a);
+    return a.slot_heads == 16 ? launch(shared_walk_kernel<D, KIND, 1, LOCAL>, grid, block, 0, stream, a)
+                              : launch(shared_walk_kernel<D, KIND, 2, LOCAL>, grid, block, 0, stream, a);
+  return a.out_mode == XFER_OUT_F32 ? launch(shared_both_kernel<D, KIND, 3, LOCAL>, grid, block, 0, stream, a)
+                                    : launch(shared_both_kernel<D, KIND, 2, LOCAL>, grid, block, 0, stream, a);
+}
+template <int D, bool LOCAL>
+hipError_t launch_kind(const SharedArgs &a, int kind, uint32_t workgroups, hipStream_t stream) {
+  return kind == XFER_KV_BF16 ? launch_walk<D, XFER_KV_BF16, LOCAL>(a, workgroups, stream)
+                              : launch_walk<D, XFER_KV_E4M3, LOCAL>(a, workgroups, stream);
 }
 template <int D>
-hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, uint32_t many_workgroups, hipStream_t stream) {
-  hipError_t e = launch(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, hipStream_t stream) {
+  const bool local = a.rows <= kThreads && a.rows + a.groups < kThreads;
+  hipError_t e = local ? hipSuccess : launch(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
   if (e != hipSuccess) return e;
-  e = kind == XFER_KV_BF16 ? launch_kind<D, XFER_KV_BF16>(a, workgroups, many_workgroups, stream)
-                           : launch_kind<D, XFER_KV_E4M3>(a, workgroups, many_workgroups, stream);
+  e = local ? launch_kind<D, true>(a, kind, workgroups, stream) : launch_kind<D, false>(a, kind, workgroups, stream);
   if (e != hipSuccess) return e;
   const uint32_t items = a.rows * a.q_heads;
   if (items >= kJoinHeads)
@@ -799,35 +891,35 @@ hipError_t launch_dim(const SharedArgs &a, int kind, uint32_t workgroups, uint32
 }
 
 struct Shape {
-  uint32_t tile, workgroups, many_workgroups;
+  uint32_t slot_heads, workgroups;
+  bool many;
   uint64_t parts, many_part0;             // (entry, kv head, tile)s at most, and where those of many heads begin
   uint64_t places, many_place0, whole0;   // query heads of all parts, and where those of many heads and whole ones begin
 };
 template <int D, int KIND>
-uint32_t per_simd(uint32_t tile) {
-  return tile == 16 ? Residence<D, KIND, 1>::kPerSimd : Residence<D, KIND, 2>::kPerSimd;
+uint32_t per_simd(int tiles) {
+  return tiles == 1 ? Residence<D, KIND, 1>::kPerSimd : Residence<D, KIND, 2>::kPerSimd;
 }
 template <int KIND>
-uint32_t per_simd(uint32_t head_dim, uint32_t tile) {
-  return head_dim == 64 ? per_simd<64, KIND>(tile) : head_dim == 128 ? per_simd<128, KIND>(tile) : per_simd<256, KIND>(tile);
+uint32_t per_simd(uint32_t head_dim, int tiles) {
+  return head_dim == 64 ? per_simd<64, KIND>(tiles) : head_dim == 128 ? per_simd<128, KIND>(tiles) : per_simd<256, KIND>(tiles);
 }
 Shape shape_of(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim, int kind) {
   Shape s{};
-  // 32 heads at a time where a row or the average group has more than 16
-  s.tile = group > 16 ? 32 : 16;
-  s.workgroups = kComputeUnits * (kind == XFER_KV_BF16 ? per_simd<XFER_KV_BF16>(head_dim, s.tile)
-                                                       : per_simd<XFER_KV_E4M3>(head_dim, s.tile));
-  const uint64_t row_tiles = (group + s.tile - 1) / s.tile;
-  s.many_part0 = kv_heads * (rows * row_tiles + (uint64_t)rows * group / s.tile + groups);
+  const int tiles = (groups ? (uint64_t)rows * group : group) > 16 ? 2 : 1;  // that an entry of few heads may have
+  s.many = groups && (uint64_t)rows * group > kFewHeads;                     // some group may be that large
+  s.slot_heads = slot_heads(tiles);
+  s.workgroups = kComputeUnits * (s.many ? (head_dim == 256 ? 1 : head_dim == 128 ? 2 : 3)
+                                         : kind == XFER_KV_BF16 ? per_simd<XFER_KV_BF16>(head_dim, tiles)
+                                                                : per_simd<XFER_KV_E4M3>(head_dim, tiles));
+  const uint64_t row_tiles = (group + 15) / 16;
+  s.many_part0 = kv_heads * (rows * row_tiles + (uint64_t)rows * group / 16 + groups);
   s.parts = s.many_part0;
-  s.many_place0 = 2ull * s.workgroups * s.tile;
+  s.many_place0 = 2ull * s.workgroups * kWaves * s.slot_heads;
   s.whole0 = s.many_place0;
-  if (groups && (uint64_t)rows * group > kFewHeads) {  // some group may be that large
-    s.workgroups = s.many_workgroups = kComputeUnits * (head_dim == 256 ? 1 : head_dim == 128 ? 2 : 3);
-    s.many_place0 = 2ull * s.workgroups * s.tile;
-    s.whole0 = s.many_place0;
+  if (s.many) {
     s.parts += kv_heads * ((uint64_t)rows * group / kManyHeads + groups);
-    s.whole0 += 2ull * s.many_workgroups * kManyHeads;
+    s.whole0 += 2ull * s.workgroups * kManyHeads;
   }
   s.places = s.whole0 + 2ull * rows * kv_heads * group;
   return s;
@@ -845,31 +937,31 @@ bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
                                 int kind) {
   const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
-  return 2 * kZeros + up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
+  return 16 + up16(((uint64_t)rows + 2ull * groups + 2) * sizeof(SharedEntry)) + up16(s.parts * sizeof(SharedParts)) + up16(s.places * 8) +
          s.places * head_dim * 4;
 }
 
 hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStream_t stream) {
   SharedArgs a = in;
   const Shape s = shape_of(a.rows, a.groups, a.cache.kv_heads, a.group, a.cache.head_dim, kind);
-  a.tile = s.tile;
+  a.slot_heads = s.slot_heads;
   a.whole0 = s.whole0;
   uint8_t *at = static_cast<uint8_t *>(workspace);
-  a.zeros = at;
-  a.many_places = reinterpret_cast<uint32_t *>(at + kZeros);
-  a.places_of_xcd = s.many_workgroups / kXcds;
+  a.many_places = reinterpret_cast<uint32_t *>(at);
+  a.places_of_xcd = s.workgroups / kXcds;
   a.unit_cost = kUnit * 2 * a.cache.head_dim * (kind == XFER_KV_BF16 ? 2 : 1) / 64;
   a.many_unit_cost = a.cache.head_dim * (a.out_mode == XFER_OUT_F32 ? 4 : 3) * 2;
-  a.entries = reinterpret_cast<SharedEntry *>(at += 2 * kZeros);
+
+  a.entries = reinterpret_cast<SharedEntry *>(at += 16);
   a.parts = reinterpret_cast<SharedParts *>(at += up16(((uint64_t)a.rows + 2ull * a.groups + 2) * sizeof(SharedEntry)));
-  if (s.many_workgroups) a.many = a.entries + a.rows + a.groups + 1;
+  if (s.many) a.many = a.entries + a.rows + a.groups + 1;
   a.many_part0 = (uint32_t)s.many_part0;
   a.many_place0 = s.many_place0;
   a.part_ml = reinterpret_cast<float *>(at += up16(s.parts * sizeof(SharedParts)));
   a.part_o = reinterpret_cast<float *>(at + up16(s.places * 8));
-  if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s.workgroups, s.many_workgroups, stream);
-  if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s.workgroups, s.many_workgroups, stream);
-  return launch_dim<256>(a, kind, s.workgroups, s.many_workgroups, stream);
+  if (a.cache.head_dim == 64) return launch_dim<64>(a, kind, s.workgroups, stream);
+  if (a.cache.head_dim == 128) return launch_dim<128>(a, kind, s.workgroups, stream);
+  return launch_dim<256>(a, kind, s.workgroups, stream);
 }
 
 }  // namespace xfer

@@ -88,8 +88,7 @@ struct SharedArgs {
   void *out;
   int out_mode;
   // set by the launch
-  uint32_t tile;  // query heads that a workgroup takes at a time
-  uint8_t *zeros;
+  uint32_t slot_heads;  // query heads of a slot for parts of few
   uint32_t *many_places;  // workgroups of each XCD that take groups of many query heads
   uint32_t places_of_xcd, unit_cost, many_unit_cost;
   SharedEntry *entries;  // of rows, then of groups of few query heads

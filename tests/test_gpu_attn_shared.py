@@ -243,6 +243,31 @@ def test_any_numbers_stay_within_the_buffers():
         w.run(rows=range(0, n, 3))
 
 
+def few_and_many(group, rows):
+    """Groups of up to 16, 17 to 32 and more query heads, one that is shorter than a tile, and rows alone up to `rows`."""
+    groups = [(200, [200 + i for i in range(n)]) for n in (2, -(-17 // group), -(-33 // group), -(-150 // group)) if n > 1]
+    groups += [(7, [9, 8]), (1500, [1501, 1999, 1500])]
+    n = sum(len(lens) for _, lens in groups)
+    return groups + [[i % 70] for i in range(rows - n)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_every_way_through(d, kind, out):
+    """Few rows and more than a workgroup plans for itself; no group, groups of few and of many query heads; heads of a row past 16."""
+    for group, rows, alone in ((4, 2, False), (5, 4, False), (2, 260, True), (20, 257, True), (3, 254, False), (3, 255, False),
+                               (9, 100, False), (20, 300, False), (1, 600, False)):
+        say("ways", d, kind, out, group, rows, alone)
+        if alone:
+            w = World([[1 + 37 * i % 150] for i in range(rows)], 2 * group, 2, d, 16, kind, "tokens", out, starts=[0], shared=[])
+        elif rows <= 4:
+            w = World([(300, [301] * rows)], 2 * group, 2, d, 16, kind, "tokens", out)
+        else:
+            w = World(few_and_many(group, rows), 2 * group, 2, d, 16, kind, "tokens", out)
+        w.run(rows=sorted({*range(0, w.n, 1 + w.n // 12), w.n - 1}))
+
+
 def test_very_many_groups():
     say("4096 groups")
     groups = [(20, [21, 20])] * 700 + [(0, [3])] * 3000 + [(5, [6, 7])] * 396
