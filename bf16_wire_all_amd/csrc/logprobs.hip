@@ -39,7 +39,7 @@ constexpr uint32_t kMinCols = 2048;                       // of a slice where ro
 constexpr uint32_t kWorkgroups = 1024;                    // that a call is cut up for
 constexpr uint32_t kMaxParts = 128;                       // of a row
 constexpr uint32_t kList = 1024;                          // elements that reach the bound, at most
-static_assert(kList >= kMaxTop * kMaxTop, "the fold's, of as many parts as elements asked for");
+static_assert(kMaxParts % 8 == 0 && kList % 8 == 0 && kList >= kMaxTop * kMaxTop, "the fold's, of as many parts as elements asked for");
 constexpr uint32_t kMasked = 0xFF80FF80u;
 constexpr unsigned short kFar = 0xF149;                   // -1e30
 
@@ -197,12 +197,20 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, uint32_t row, const
   }
 }
 
-// The n_top best of what is listed (one element once), in order; what lies past their end is left.
-__device__ __forceinline__ void best_of(const uint64_t *list, uint32_t n, uint32_t n_top, uint64_t *best) {
+// The n_top best of what is listed (one element once), in order; what lies past their end is left.  By all threads; the
+// list's places up to the next multiple of kBlock are written.
+constexpr uint32_t kBlock = 8;  // keys that are on their way together
+__device__ __forceinline__ void best_of(uint64_t *list, uint32_t n, uint32_t n_top, uint64_t *best) {
+  const uint32_t up = (n + kBlock - 1) / kBlock * kBlock;
+  if (n + threadIdx.x < up) list[n + threadIdx.x] = 0;
+  __syncthreads();
   for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t key = list[i];
     uint32_t before = 0;
-    for (uint32_t j = 0; j < n; ++j) before += list[j] > key;
+#pragma unroll 1
+    for (uint32_t j = 0; j < up; j += kBlock)
+#pragma unroll
+      for (uint32_t k = 0; k < kBlock; ++k) before += list[j + k] > key;
     if (key && before < n_top) best[before] = key;
   }
 }
@@ -232,10 +240,8 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
   const uint32_t k0 = (uint32_t)((uint64_t)n_slices * part / a.parts), k1 = (uint32_t)((uint64_t)n_slices * (part + 1) / a.parts);
   const float T = a.temperature ? a.temperature[row] : 1.0f;
   const float c = T > 0.0f ? 1.4426950408889634f / T : 0.0f;
-  if (tid < a.n_tokens) {
-    sh.token[tid] = token_key(a, row, a.tokens[(uint64_t)row * a.n_tokens + tid]);
-    sh.rank[tid] = 0;
-  }
+  const int32_t token = tid < a.n_tokens ? a.tokens[(uint64_t)row * a.n_tokens + tid] : -1;
+  if (tid < a.n_tokens) sh.rank[tid] = 0;
   if (tid < a.n_top) sh.best[tid] = 0;
   if (tid < 2) sh.equal[tid] = 0, sh.first[tid] = 0xFFFFFFFFu;
   // The largest so far, and of all others this thread's sums relative to it.
@@ -267,6 +273,7 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
         if (at < end) w[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(s.ptr) + at);
       }
     }
+    if (k == k0 && tid < a.n_tokens) sh.token[tid] = token_key(a, row, token);  // on its way with the first slice
     // f(round) for each that the slice has
     auto rounds = [&](auto &&f) {
 #pragma unroll
@@ -313,7 +320,9 @@ __global__ __launch_bounds__(kThreads, 4) void logprobs_kernel(LogprobArgs a) {
     const bool plain = top > 0 && top <= 0x7F80 && known >= a.n_top;
     if (!plain) {
       own = 0;
-      again([&](uint32_t v, uint32_t) { own = max(own, (int)ord(v)); });
+      rounds([&](int r) {
+        of_round(r, [&](uint32_t x, int h, uint32_t) { own = max(own, (int)ord(half(anew(x), h))); });
+      });
       top = wave_max(own) - 0x8000;
     }
     int bound = 0;
@@ -518,16 +527,30 @@ __global__ __launch_bounds__(kThreads) void logprobs_fold_kernel(LogprobArgs a) 
   const float T = a.temperature ? a.temperature[row] : 1.0f;
   const uint64_t at = (uint64_t)row * a.parts;
   const uint64_t *keys = a.keys + at * a.n_top;
+  // Two parts to a lane.  All loads that depend on nothing first.
+  const Sum *sums = static_cast<const Sum *>(a.sums) + at;
+  const Sum none = {0, 0, 0};
+  const Sum s0 = lane < a.parts ? sums[lane] : none, s1 = lane + 64 < a.parts ? sums[lane + 64] : none;
+  for (uint32_t i = wave; i < a.n_tokens; i += kWaves) {
+    uint32_t n = lane < a.parts ? a.ranks[(at + lane) * a.n_tokens + i] : 0;
+    n += lane + 64 < a.parts ? a.ranks[(at + lane + 64) * a.n_tokens + i] : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+    if (lane == 0) rank[i] = n;
+  }
   if (a.n_top) {
     // The parts' lists are in order.  Where there are as many parts as elements asked for, none that is below
     // that many of their first ones is among the best.
-    if (tid < a.parts) head[tid] = keys[(uint64_t)tid * a.n_top];
+    if (tid < kMaxParts) head[tid] = tid < a.parts ? keys[(uint64_t)tid * a.n_top] : 0;
     if (tid < a.n_top) best[tid] = 0;
     if (tid == 0) least = 1, listed = 0;
     __syncthreads();
     if (tid < a.parts && a.parts >= a.n_top) {
       uint32_t before = 0;
-      for (uint32_t j = 0; j < a.parts; ++j) before += head[j] > head[tid] || (head[j] == head[tid] && j < tid);
+#pragma unroll 1
+      for (uint32_t j = 0; j < a.parts; j += kBlock)
+#pragma unroll
+        for (uint32_t k = 0; k < kBlock; ++k) before += head[j + k] > head[tid] || (head[j + k] == head[tid] && j + k < tid);
       if (before == a.n_top - 1 && head[tid]) least = head[tid];
     }
     __syncthreads();
@@ -540,21 +563,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_fold_kernel(LogprobArgs a) 
     }
     __syncthreads();
     best_of(list, listed, a.n_top, best);
-    __syncthreads();
   }
-  if (wave != 0) return;
-  for (uint32_t i = 0; i < a.n_tokens; ++i) {
-    uint32_t n = 0;
-    for (uint32_t p = lane; p < a.parts; p += 64) n += a.ranks[(at + p) * a.n_tokens + i];
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-    if (lane == 0) rank[i] = n;
-  }
-  // Two parts to a lane.
-  const Sum *sums = static_cast<const Sum *>(a.sums) + at;
-  const Sum none = {0, 0, 0};
-  const Sum sum = join(lane < a.parts ? sums[lane] : none, lane + 64 < a.parts ? sums[lane + 64] : none, T);
-  finish(a, row, sum, T, rank, best);
+  __syncthreads();
+  if (wave == 0) finish(a, row, join(s0, s1, T), T, rank, best);
 }
 
 struct Shape {
