@@ -432,6 +432,7 @@ struct Many {
   static constexpr uint32_t kTileBytes = kManyUnit * D * 2;        // of keys, and of values
 };
 
+typedef float v2f __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
@@ -758,36 +759,35 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
   const uint32_t item = WAVES == 1 ? blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : blockIdx.x;
   if (item >= a.rows * a.q_heads) return;  // by waves that share nothing
   const uint32_t row = item / a.q_heads, head = item % a.q_heads, kvh = head / a.group, h = head % a.group;
+  // The row's own entry and its group's in either list, then what each came to: loads that wait for no more than they must.
   const SharedEntry own = a.entries[row];
+  const bool shares = own.group != kNoGroup;
+  const uint32_t of_group = shares ? own.group : 0;
+  const SharedEntry few = a.entries[a.rows + of_group], many = a.many ? a.many[of_group] : few;
+  const bool is_many = shares && few.n == 0;
+  const SharedEntry &whose = is_many ? many : few;
+  auto tile_for = [&](const SharedEntry &e, bool m) { return m ? kManyHeads : tile_of(e.q_rows * a.group); };
+  auto index = [&](const SharedEntry &e) { return (row - e.q_row) * a.group + h; };  // this head's among the entry's
+  auto part_of = [&](const SharedEntry &e, uint32_t tile) {
+    return e.part0 + kvh * ((e.q_rows * a.group + tile - 1) / tile) + index(e) / tile;
+  };
+  const uint32_t own_tile = tile_for(own, false), pre_tile = tile_for(whose, is_many);
+  const uint32_t own_part = own.n ? part_of(own, own_tile) : 0, pre_part = shares ? part_of(whose, pre_tile) : own_part;
+  const SharedParts own_parts = a.parts[own_part], pre_parts = a.parts[pre_part];
   struct Source {
     uint32_t n;                 // parts
     uint64_t at0, at1, stride;  // places: part 0's; part p's at1 + p * stride
   };
-  auto source = [&](const SharedEntry &e, bool prefix, bool many) {
-    Source s{};
-    if (!e.n) return s;
-    const uint32_t heads = e.q_rows * a.group, tile = many ? kManyHeads : tile_of(heads), m_groups = (heads + tile - 1) / tile;
-    const uint32_t slot = many ? kManyHeads : a.slot_heads;
-    const uint64_t cut0 = many ? a.many_place0 : 0;
-    const uint32_t i = (row - e.q_row) * a.group + h;
-    const SharedParts p = a.parts[e.part0 + kvh * m_groups + i / tile];
-    s.n = p.n;
-    if (p.slot == kWhole) {
-      s.at0 = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
-    } else {
-      // Part p > 0 is the first thing that the workgroup p further on did.
-      s.at0 = cut0 + (uint64_t)p.slot * slot + i % tile;
-      s.at1 = cut0 + (uint64_t)(p.slot / 2 * 2) * slot + i % tile;
-      s.stride = 2 * slot;
-    }
-    return s;
+  auto source = [&](const SharedParts &p, bool prefix, bool m, uint32_t in_tile) {
+    const uint32_t slot = m ? kManyHeads : a.slot_heads;
+    const uint64_t cut0 = (m ? a.many_place0 : 0) + in_tile;
+    const uint64_t whole = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
+    // Part p > 0 is the first thing that the run p further on did.
+    return Source{p.n, p.slot == kWhole ? whole : cut0 + (uint64_t)p.slot * slot, cut0 + (uint64_t)(p.slot / 2 * 2) * slot, 2 * slot};
   };
-  Source pre{};
-  if (own.group != kNoGroup) {
-    const SharedEntry e = a.entries[a.rows + own.group];
-    pre = e.n ? source(e, true, false) : source(a.many[own.group], true, true);
-  }
-  const Source mine = source(own, false, false);
+  Source pre{}, mine{};
+  if (shares) pre = source(pre_parts, true, is_many, index(whose) % pre_tile);
+  if (own.n) mine = source(own_parts, false, false, index(own) % own_tile);
   const uint32_t n = pre.n + mine.n;
   auto place = [&](uint32_t p) -> uint64_t {
     const Source &s = p < pre.n ? pre : mine;
@@ -795,13 +795,15 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
     return k ? s.at1 + k * s.stride : s.at0;
   };
 
-  // Lane l of wave w has part p0 + l * WAVES + w of every 64 * WAVES.
-  float top = -INFINITY;
-#pragma unroll 1
-  for (uint32_t p0 = 0; p0 < n; p0 += 64 * WAVES) {
+  // Lane l of wave w has part p0 + l * WAVES + w of every 64 * WAVES.  Its maximum and sum of weights; the first's are kept.
+  auto max_sum = [&](uint32_t p0) {
     const uint32_t p = p0 + lane * WAVES + wave;
-    top = fmaxf(top, p < n ? a.part_ml[2 * place(p)] : -INFINITY);
-  }
+    return p < n ? *reinterpret_cast<const v2f *>(a.part_ml + 2 * place(p)) : v2f{-INFINITY, 0};
+  };
+  const v2f first = max_sum(0);
+  float top = first.x;
+#pragma unroll 1
+  for (uint32_t p0 = 64 * WAVES; p0 < n; p0 += 64 * WAVES) top = fmaxf(top, max_sum(p0).x);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
   if constexpr (WAVES > 1) {
@@ -818,8 +820,8 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
     const uint32_t p = p0 + lane * WAVES + wave;
     float f = 0;
     if (p < n) {
-      const uint64_t at = place(p);
-      const float m = a.part_ml[2 * at], l = a.part_ml[2 * at + 1];
+      const v2f ml = p0 ? max_sum(p0) : first;
+      const float m = ml.x, l = ml.y;
       f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
       total += m == -INFINITY ? l : l * f;
       if (f == 0.0f) f = __uint_as_float(1);  // a part's infinity stays one, however small its weights
