@@ -26,6 +26,13 @@
 //
 // Where rows are few, each is cut into several workgroups' parts, which a
 // second launch folds: (largest, R, sum w x) scaled to the row's largest.
+//
+// 2048 rows of 151,936 with one token's rank each (622 MB): 155-168
+// us, 4 TB/s.  The vector unit bounds it, at some 12 instructions for each
+// element, half of them the weights': with the sums of slices kept apart and
+// joined at the end it took 182 us, with ranks compared as floats and each
+// weight clamped by itself 313.  More waves on a SIMD spill (226 us and more).
+// 16 rows of 129,280: 10.5 + 5.8 us, chains of dependent steps.
 #include "decode.h"
 
 namespace xfer {
@@ -35,8 +42,11 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRounds = 8;                                // vectors of 8 elements that a thread holds
 constexpr uint32_t kSliceCols = kThreads * 8 * kRounds;   // 16,384
-constexpr uint32_t kMinCols = 2048;                       // of a slice where rows are cut into parts
-constexpr uint32_t kWorkgroups = 1024;                    // that a call is cut up for
+// How rows are cut into parts: for so many workgroups (1024: 500 rows of 32,000 29.3 us for 25.2, 512: 16 rows of 129,280
+// 15.1 for 10.5), of so many columns at least (2048: 100 rows of 32,000 20.6 us for 12.4, 16 rows 11.9 + 6.7 for 10.5 + 5.8,
+// one row 8.5 + 6.8 for 9.3 + 5.9; 8192: one row with 20 alternatives 14.0 + 13.4 for 12.5 + 6.8).
+constexpr uint32_t kWorkgroups = 1536;
+constexpr uint32_t kMinCols = 4096;
 constexpr uint32_t kMaxParts = 128;                       // of a row
 constexpr uint32_t kList = 1024;                          // elements that reach the bound, at most
 static_assert(kMaxParts % 8 == 0 && kList % 8 == 0 && kList >= kMaxTop * kMaxTop, "the fold's, of as many parts as elements asked for");

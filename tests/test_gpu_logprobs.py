@@ -216,7 +216,7 @@ def test_special_rows_at_special_temperatures(cols, n0, n_top):
 
 
 def test_special_rows_of_several_slices_to_a_workgroup():
-    """From 1,024 rows on a workgroup goes through a row's slices one after the other: larger ones later, and none."""
+    """From 1,536 rows on a workgroup goes through a row's slices one after the other: larger ones later, and none."""
     cols, n0 = 50000, 20000
     rows = special_rows(cols)
     falling = rows["rising"][::-1]
@@ -230,7 +230,7 @@ def test_special_rows_of_several_slices_to_a_workgroup():
     infinite = steps.copy()
     infinite[-5:] = [0x7F80, BF(1.0), 0x7F80, 0x7FC0, 0xFF80]
     made = list(rows.values()) + [falling, late, early, steps, infinite]
-    n = -(-1024 // len(made)) * len(made)
+    n = -(-1536 // len(made)) * len(made)
     bits = np.stack(made)
     tokens = np.tile(np.array([0, 103, 10103, cols - 1], np.int32), (n, 1))
     for T in (1.0, 0.05, 0.0):
