@@ -29,7 +29,7 @@
 //
 // 64 answers to a prompt of 8192 tokens (32 query heads on 8 of 128, 124 MB):
 // 41 us of walk and 8.8 of join; 24 rows over 131056 shared tokens in F32
-// (548 MB, 193 GFLOP with the weights in three parts): 180 + 12 us.
+// (548 MB, 129 GFLOP with the weights in three parts): 160-190 + 12 us.
 #include "attn_tile.h"
 
 #include <type_traits>
@@ -745,7 +745,7 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_bo
 
 // ------------------------------------------------------------------- join
 
-// kJoinWaves (or one) for each (row, query head): its parts of the shared tokens, then of its own, each scaled to
+// kWaves (or one) for each (row, query head): its parts of the shared tokens, then of its own, each scaled to
 // the largest maximum, in a fixed order.  One wave where there are many heads to join, since each has few parts then
 // (6336 heads of 64: 6 us with a wave each, 18 with four); four where few heads are cut into many parts.
 constexpr uint32_t kJoinHeads = 4096;  // from which on a wave takes a whole one
