@@ -243,6 +243,43 @@ def test_any_numbers_stay_within_the_buffers():
         w.run(rows=range(0, n, 3))
 
 
+def test_any_numbers_of_many_rows_stay_within_the_buffers():
+    """More rows than a workgroup plans for itself: starts, prefixes and lengths without sense read and write nothing else."""
+    w = World([(40, [50, 60])] * 100 + [(300, [310] * 60)] + [[30]] * 40, 8, 2, 64, 16, "bf16", "tokens")
+    raw, out = w.buffer()
+    g = torch.Generator().manual_seed(6)
+    for i in range(8):
+        w.starts.copy_(torch.randint(-2 ** 31, 2 ** 31, w.starts.shape, generator=g, dtype=torch.int64).int() if i % 2 else
+                       torch.randint(0, 400, w.starts.shape, generator=g).int())
+        w.shared.copy_(torch.randint(-2 ** 31, 2 ** 31, w.shared.shape, generator=g, dtype=torch.int64).int() if i % 3 else
+                       torch.randint(0, 320, w.shared.shape, generator=g).int())
+        w.lens.copy_(torch.randint(0, 2 ** 31, w.lens.shape, generator=g, dtype=torch.int64).int() if i == 7 else
+                     torch.randint(0, 320, w.lens.shape, generator=g).int())
+        say("any numbers of many rows", i)
+        w.call(out)
+        torch.cuda.synchronize()
+        assert (raw.cpu()[:, -16:] == 0x5A).all() and (w.ws[w.need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("rows", [40, 300])
+def test_two_graphs_that_share_a_workspace(rows):
+    worlds = [World([(500 + 90 * s, [600 + i % 50 for i in range(rows)])], 8, 2, 128, 16, seed=s, max_len=660) for s in (1, 2)]
+    worlds[1].ws = worlds[0].ws
+    outs, graphs, want = [w.buffer()[1] for w in worlds], [], []
+    for w, o in zip(worlds, outs):
+        w.call(o)
+        torch.cuda.synchronize()
+        want.append(o.clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            w.call(o)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].fill_(3)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want[i])
+
+
 def few_and_many(group, rows):
     """Groups of up to 16, 17 to 32 and more query heads, one that is shorter than a tile, and rows alone up to `rows`."""
     groups = [(200, [200 + i for i in range(n)]) for n in (2, -(-17 // group), -(-33 // group), -(-150 // group)) if n > 1]

@@ -316,6 +316,36 @@ def test_another_stream_and_a_captured_graph(rows):
         assert want == [a.tobytes() for a in c.results()]
 
 
+def test_two_calls_at_once_and_two_graphs_that_share_a_workspace():
+    calls = [Call(logits(9, 30000, 60 + i), 11000, some_tokens(9, 30000, 3, i), 7, temperature=[1.1] * 9) for i in range(2)]
+    want = []
+    for c in calls:
+        c.run()
+        want.append([a.tobytes() for a in c.results()])
+        c.check()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for c in calls:
+        for o in c.out:
+            o.fill_(0x5A)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, stream in zip(calls, streams):
+            c.run(stream=stream)
+    for c, w in zip(calls, want):
+        assert [a.tobytes() for a in c.results()] == w
+    calls[1].ws = calls[0].ws
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    for graph, c in zip(graphs, calls):
+        with torch.cuda.graph(graph):
+            c.run()
+    for i in (1, 0, 0, 1, 0):
+        for o in calls[i].out:
+            o.fill_(0x5A)
+        torch.cuda.synchronize()
+        graphs[i].replay()
+        assert [a.tobytes() for a in calls[i].results()] == want[i]
+
+
 def test_the_binding_refuses_what_it_cannot_read():
     c = Call(logits(3, 200, 1), 100, some_tokens(3, 200, 2, 1), 4)
     r = c.rows
