@@ -16,7 +16,7 @@
 //      - entries of up to 32 query heads for a kv head (or of one row): their
 //        units (32 tokens of a kv head and up to 16 or 32 query heads) are one
 //        line that is cut into equal runs, one for each wave, with the walk of
-//        the attention of one token.  The memory bounds it, or, where runs
+//        the attention of one token; four runs of one kind are joined in LDS.  The memory bounds it, or, where runs
 //        are short, its latency: 2.5 us for a unit;
 //      - groups of more: units of 64 tokens and 128 query heads through LDS,
 //        a run for each workgroup.  The matrix cores and the weights between
@@ -41,7 +41,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kUnit = kTile;                // tokens of a unit
 // Units of a wave's run, at least: 4 drafted positions each of 4 requests of up to 6000 tokens 23.6 us and 9.9 of join;
-// 4 units 28.7 + 7.5, 8 units 39.8 + 6.5.
+// 4 units 28.7 + 7.5, 8 units 39.8 + 6.5 (measured where each run left a part).
 constexpr uint32_t kLeast = 2;
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kXcds = 8;
@@ -269,15 +269,19 @@ __device__ __forceinline__ bool plan_here(const SharedArgs &a, LocalPlan &to, Pl
 
 // ------------------------------------------------------------------- walk
 
-// What a (entry, kv head, tile of heads) that fell to several workgroups leaves:
-// its first part's slot (kWhole: one workgroup did it all), and how many parts.
+// What a (entry, kv head, tile of heads) that fell to several runs leaves:
+// its first part's slot (kWhole: one run did it all), and how many parts.
 constexpr uint32_t kWhole = 0xFFFFFFFFu;
 
-// Queries that registers do not hold, of each wave.
-template <int D, int KIND, int TILES>
-struct WalkLds {
+template <int D, int KIND, int TILES, bool JOIN>
+union WalkLds {
+  static constexpr int kPad = 4;  // floats between rows of the exchange, so that 16 rows' stores fall on all banks
   static constexpr int kMost = TILES == 2 && Residence<D, KIND, 2>::kQInLds ? 2 : Residence<D, KIND, 1>::kQInLds ? 1 : 0;
-  v4u q[kMost ? kWaves : 1][kMost ? kMost * Layout<D, KIND>::kMfmaK * 64 : 1];
+  v4u q[kMost ? kWaves : 1][kMost ? kMost * Layout<D, KIND>::kMfmaK * 64 : 1];  // queries that registers do not hold, of each wave
+  struct {
+    float o[JOIN ? kWaves : 1][16][D + kPad];
+    float m[kWaves][16], l[kWaves][16];
+  } exchange;
 };
 
 // Query heads of a slot for what a wave has of a tile's tokens.
@@ -307,22 +311,41 @@ __device__ __forceinline__ uint32_t entry_at(const SharedEntry *entries, uint32_
   return first;
 }
 
+// x / y, most often of 32 bits.
+__device__ __forceinline__ uint32_t quotient(uint64_t x, uint64_t y) {
+  return (x | y) >> 32 ? (uint32_t)(x / y) : (uint32_t)x / (uint32_t)y;
+}
+
 // The runs of workgroup wg of n_wg, one of each wave.  TILES: 16 query heads at a time, or (2) 32 of the entries that
-// have more.
-template <int D, int KIND, int TILES>
+// have more.  JOIN: a workgroup whose four runs are of one (entry, kv head, tile of heads) leaves one part (two answers
+// to 16,000 tokens 17.2 us and 7.2 of join, otherwise 17.4 and 15.4; drafted positions 23.2 + 6.3 and 23.7 + 9.6).
+template <int D, int KIND, int TILES, bool JOIN>
 __device__ __forceinline__ void walk(const SharedArgs &a, const SharedEntry *entries, uint32_t wg, uint32_t n_wg,
-                                     WalkLds<D, KIND, TILES> &lds) {
+                                     WalkLds<D, KIND, TILES, JOIN> &lds) {
   using L = Layout<D, KIND>;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, n = lane % 16, g = lane / 16;
   const uint32_t n_entries = a.rows + a.groups, n_runs = n_wg * kWaves, run = wg * kWaves + wave;
   const uint64_t all = entries[n_entries].unit0, share = (all + n_runs - 1) / n_runs;
-  const uint64_t per = share < kLeast ? kLeast : share, from = run * per;
+  const uint64_t per = share < kLeast ? kLeast : share, per_wg = kWaves * per, from_wg = wg * per_wg;
+  uint64_t from = JOIN ? from_wg : run * per;
   if (from >= all) return;
-  uint64_t left = min(per, all - from);
   uint32_t index = entry_at(entries, n_entries, from);
   SharedEntry e = scalar(entries[index]);
   uint64_t at = from - e.unit0;
-  v4u *const lds_q = WalkLds<D, KIND, TILES>::kMost ? lds.q[wave] : lds.q[0];
+  const uint32_t wg_units = (e.n + kUnit - 1) / kUnit;
+  const bool together = JOIN && from_wg + (kWaves - 1) * per < all && min(per_wg, all - from_wg) <= wg_units &&
+                        at - (uint64_t)quotient(at, wg_units) * wg_units + min(per_wg, all - from_wg) <= wg_units;
+  if (JOIN && wave) {
+    from += wave * per;
+    if (from >= all) return;  // by no wave of such a workgroup
+    if (!together) {
+      index = entry_at(entries, n_entries, from);
+      e = scalar(entries[index]);
+    }
+    at = from - e.unit0;
+  }
+  uint64_t left = min(per, all - from);
+  v4u *const lds_q = WalkLds<D, KIND, TILES, JOIN>::kMost ? lds.q[wave] : lds.q[0];
   bool first_segment = true;
 
   // What is left of an entry, MR times 16 heads at a time.
@@ -363,35 +386,91 @@ __device__ __forceinline__ void walk(const SharedArgs &a, const SharedEntry *ent
       float mx[MR], sum[MR];
       attn_walk<D, KIND, MR, kParts, kUnit, false>(a.cache, kvh, table, vis, v0, v1, scale2, n, g, lane, q, lds_q, o, mx, sum);
 
+      // made anew, or the places of all results would be ready, and held, while the tokens are walked through
+      uint32_t en = n, eg = g;
+      if (JOIN) asm volatile("" : "+v"(en), "+v"(eg));
       const bool whole = take == units;
       const uint32_t slot = 2 * run + (first_segment ? 0 : 1);
-      if (unit == 0 && lane == 0)
-        a.parts[e.part0 + inner] = whole ? SharedParts{kWhole, 1} : SharedParts{slot, 1 + (uint32_t)((units - take + per - 1) / per)};
+      if (unit == 0 && lane == 0) {
+        SharedParts parts{whole ? kWhole : slot, 1 + (uint32_t)((units - take + per - 1) / per), 0};
+        // The workgroups that leave one part, of those that begin here, and the runs before them; counted from this one on.
+        const uint64_t begin = e.unit0 + (uint64_t)inner * units, span = begin + units - from_wg;
+        const uint32_t first = begin > from_wg;
+        uint32_t last = span < per_wg ? 0 : quotient(span, per_wg);
+        if (begin + units == all && last * per_wg + (kWaves - 1) * per < span) ++last;
+        if (JOIN && last > first) {
+          parts.wgs = last - first;
+          parts.lead = (wg + first) * kWaves - run;
+          parts.n -= min(parts.n - parts.lead, parts.wgs * kWaves) - parts.wgs;
+        }
+        a.parts[e.part0 + inner] = parts;
+      }
+      auto put = [&](uint64_t to, uint32_t d, v4f v, float total, uint32_t t0, uint32_t t1) {
+        if constexpr (KIND == XFER_KV_BF16) {
+          if (isnan(v.x + v.y + v.z + v.w) && !isnan(total)) v = with_infinities<KIND>(a.cache, kvh, table, vis, t0, t1, v, d);
+        }
+        *reinterpret_cast<v4f *>(a.part_o + to * D + d) = v;
+      };
 #pragma unroll
       for (int r = 0; r < MR; ++r) {
         sum[r] += __shfl_xor(sum[r], 16);
         sum[r] += __shfl_xor(sum[r], 32);
-        const uint32_t h = h0 + 16 * r + n;
+        const uint32_t h = h0 + 16 * r + en;
+        if (together) {
+          auto &x = lds.exchange;
+          __syncthreads();
+          if (eg == 0) {
+            x.m[wave][en] = mx[r];
+            x.l[wave][en] = sum[r];
+          }
+          __syncthreads();
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top = fmaxf(top, x.m[w][en]);
+          const float f = mx[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[r] - top);
+#pragma unroll
+          for (int j = 0; j < L::kMfmaV; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.o[wave][en][dim_of<D, KIND>(j, 4 * eg + i)] = o[r][j][i] * f;
+          __syncthreads();
+#pragma unroll
+          for (uint32_t i = threadIdx.x; i < 4 * D; i += kThreads) {
+            const uint32_t hq = i / (D / 4), d = i % (D / 4) * 4;
+            if (h0 + 16 * r + hq >= heads) continue;
+            float best = -INFINITY, total = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) best = fmaxf(best, x.m[w][hq]);
+            v4f v = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+              const float mw = x.m[w][hq];
+              total += mw == -INFINITY ? x.l[w][hq] : x.l[w][hq] * __builtin_amdgcn_exp2f(mw - best);
+              v += *reinterpret_cast<const v4f *>(&x.o[w][hq][d]);
+            }
+            const uint64_t to = (uint64_t)(2 * wg * kWaves) * slot_heads(TILES) + 16 * r + hq;
+            const uint32_t t0 = v0 - (uint32_t)(wave * per) * kUnit;
+            put(to, d, v, total, t0, min(t0 + (uint32_t)per_wg * kUnit, e.n));
+            if (d == 0) {
+              a.part_ml[2 * to] = best;
+              a.part_ml[2 * to + 1] = total;
+            }
+          }
+          continue;
+        }
         if (h >= heads) continue;
         // a whole one's place is its row's and head's, in the half for shared or own tokens
         const uint64_t mine = (uint64_t)(e.q_row + h / a.group) * a.q_heads + kvh * a.group + h % a.group;
         const uint64_t to = whole ? a.whole0 + (index < a.rows ? 0 : (uint64_t)a.rows * a.q_heads) + mine
-                                  : (uint64_t)slot * slot_heads(TILES) + 16 * r + n;
-        if (g == 0) {
+                                  : (uint64_t)slot * slot_heads(TILES) + 16 * r + en;
+        if (eg == 0) {
           a.part_ml[2 * to] = mx[r];
           a.part_ml[2 * to + 1] = sum[r];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < L::kMfmaV; j += 4) {
-            const uint32_t d = dim_of<D, KIND>(j, 4 * g + i);
-            v4f v = {o[r][j][i], o[r][j + 1][i], o[r][j + 2][i], o[r][j + 3][i]};
-            if constexpr (KIND == XFER_KV_BF16) {
-              if (isnan(v.x + v.y + v.z + v.w) && !isnan(sum[r])) v = with_infinities<KIND>(a.cache, kvh, table, vis, v0, v1, v, d);
-            }
-            *reinterpret_cast<v4f *>(a.part_o + to * D + d) = v;
-          }
+          for (int j = 0; j < L::kMfmaV; j += 4)
+            put(to, dim_of<D, KIND>(j, 4 * eg + i), v4f{o[r][j][i], o[r][j + 1][i], o[r][j + 2][i], o[r][j + 3][i]}, sum[r], v0, v1);
       }
       left -= take;
       first_segment = false;
@@ -669,7 +748,7 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
       const bool whole = take == units;
       const uint32_t slot = 2 * wg + (first_segment ? 0 : 1);
       if (unit == 0 && tid == 0)
-        a.parts[e.part0 + inner] = whole ? SharedParts{kWhole, 1} : SharedParts{slot, 1 + (uint32_t)((units - take + per - 1) / per)};
+        a.parts[e.part0 + inner] = SharedParts{whole ? kWhole : slot, 1 + (uint32_t)((units - take + per - 1) / per), 0};
       sum += __shfl_xor(sum, 32);
       if (h < heads) {
         const uint64_t to = whole ? a.whole0 + ((uint64_t)a.rows + e.q_row + h / a.group) * a.q_heads + head
@@ -707,15 +786,15 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
 // LOCAL: the workgroups make the plan themselves.
 template <int D, int KIND, int TILES, bool LOCAL>
 __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) void shared_walk_kernel(SharedArgs a) {
-  __shared__ WalkLds<D, KIND, TILES> lds;
+  __shared__ WalkLds<D, KIND, TILES, true> lds;
   __shared__ LocalPlan local;
-  __shared__ PlanLds<kThreads> plan;
-  if (LOCAL) plan_here(a, local, plan, [](uint32_t) { return false; });
+  static_assert(sizeof(PlanLds<kThreads>) <= sizeof(lds), "it fits");
+  if (LOCAL) plan_here(a, local, reinterpret_cast<PlanLds<kThreads> &>(lds), [](uint32_t) { return false; });
   const uint32_t wg = blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
   if (LOCAL)
-    walk<D, KIND, TILES>(a, local.list, wg, gridDim.x, lds);
+    walk<D, KIND, TILES, true>(a, local.list, wg, gridDim.x, lds);
   else
-    walk<D, KIND, TILES>(a, a.entries, wg, gridDim.x, lds);
+    walk<D, KIND, TILES, true>(a, a.entries, wg, gridDim.x, lds);
 }
 
 // Both lists at once, so that one's loads and the other's products share the compute units: of the workgroups
@@ -723,8 +802,7 @@ __global__ __launch_bounds__(kThreads, (Residence<D, KIND, TILES>::kPerSimd)) vo
 template <int D, int KIND, int PARTS, bool LOCAL>
 __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_both_kernel(SharedArgs a) {
   constexpr uint32_t kTile = 2 * Many<D, KIND>::kTileBytes;
-  __shared__ __align__(16) uint8_t lds0[kTile];
-  static_assert(sizeof(WalkLds<D, KIND, 2>) <= kTile, "it fits");
+  __shared__ __align__(16) uint8_t lds0[kTile < sizeof(WalkLds<D, KIND, 2, (D > 64)>) ? sizeof(WalkLds<D, KIND, 2, (D > 64)>) : kTile];
   __shared__ __align__(16) uint8_t lds1[kTile];
   __shared__ LocalPlan local;
   static_assert(sizeof(PlanLds<kThreads>) <= sizeof(lds0), "it fits");
@@ -738,9 +816,9 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_bo
   const bool takes_many = LOCAL ? plan_here(a, local, reinterpret_cast<PlanLds<kThreads> &>(lds0), choose) : choose(*a.many_places);
   if (takes_many)
     walk_many<D, KIND, PARTS>(a, LOCAL ? local.list : a.many, xcd * many + before, kXcds * many, lds0, lds1);
-  else
-    walk<D, KIND, 2>(a, LOCAL ? local.list : a.entries, xcd * (places - many) + place - before, kXcds * (places - many),
-                     *reinterpret_cast<WalkLds<D, KIND, 2> *>(lds0));
+  else  // with heads of 64 the walk of many would spill more: three system prompts 42.0 + 8.3 us, so 37.8 + 7.9
+    walk<D, KIND, 2, (D > 64)>(a, LOCAL ? local.list : a.entries, xcd * (places - many) + place - before, kXcds * (places - many),
+                     *reinterpret_cast<WalkLds<D, KIND, 2, (D > 64)> *>(lds0));
 }
 
 // ------------------------------------------------------------------- join
@@ -775,15 +853,15 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
   const uint32_t own_part = own.n ? part_of(own, own_tile) : 0, pre_part = shares ? part_of(whose, pre_tile) : own_part;
   const SharedParts own_parts = a.parts[own_part], pre_parts = a.parts[pre_part];
   struct Source {
-    uint32_t n;                 // parts
-    uint64_t at0, at1, stride;  // places: part 0's; part p's at1 + p * stride
+    uint32_t n, lead, wgs;      // parts; those of workgroups as a whole, after the first `lead`
+    uint64_t at0, at1, stride;  // places: run 0's; run p's at1 + p * stride
   };
   auto source = [&](const SharedParts &p, bool prefix, bool m, uint32_t in_tile) {
     const uint32_t slot = m ? kManyHeads : a.slot_heads;
     const uint64_t cut0 = (m ? a.many_place0 : 0) + in_tile;
     const uint64_t whole = a.whole0 + (prefix ? (uint64_t)a.rows * a.q_heads : 0) + (uint64_t)row * a.q_heads + head;
-    // Part p > 0 is the first thing that the run p further on did.
-    return Source{p.n, p.slot == kWhole ? whole : cut0 + (uint64_t)p.slot * slot, cut0 + (uint64_t)(p.slot / 2 * 2) * slot, 2 * slot};
+    // Run p > 0 began with this.
+    return Source{p.n, p.lead, p.wgs, p.slot == kWhole ? whole : cut0 + (uint64_t)p.slot * slot, cut0 + (uint64_t)(p.slot / 2 * 2) * slot, 2 * slot};
   };
   Source pre{}, mine{};
   if (shares) pre = source(pre_parts, true, is_many, index(whose) % pre_tile);
@@ -791,7 +869,8 @@ __global__ __launch_bounds__(kThreads) void shared_join_kernel(SharedArgs a) {
   const uint32_t n = pre.n + mine.n;
   auto place = [&](uint32_t p) -> uint64_t {
     const Source &s = p < pre.n ? pre : mine;
-    const uint32_t k = p < pre.n ? p : p - pre.n;
+    uint32_t k = p < pre.n ? p : p - pre.n;
+    k += (kWaves - 1) * min(k - min(k, s.lead), s.wgs);  // a workgroup's one part is its first run's
     return k ? s.at1 + k * s.stride : s.at0;
   };
 

@@ -72,7 +72,8 @@ struct SharedEntry {
 };
 static_assert(sizeof(SharedEntry) % 8 == 0, "entries lie one after the other");
 struct SharedParts {
-  uint32_t slot, n;
+  uint32_t slot, n;    // its first run's, and how many parts: one of each run,
+  uint32_t wgs, lead;  // but of `wgs` workgroups after the first `lead` runs
 };
 struct SharedArgs {
   CacheView cache;
