@@ -327,23 +327,23 @@ __device__ __forceinline__ void walk(const SharedArgs &a, const SharedEntry *ent
   const uint32_t n_entries = a.rows + a.groups, n_runs = n_wg * kWaves, run = wg * kWaves + wave;
   const uint64_t all = entries[n_entries].unit0, share = (all + n_runs - 1) / n_runs;
   const uint64_t per = share < kLeast ? kLeast : share, per_wg = kWaves * per, from_wg = wg * per_wg;
-  uint64_t from = JOIN ? from_wg : run * per;
-  if (from >= all) return;
-  uint32_t index = entry_at(entries, n_entries, from);
-  SharedEntry e = scalar(entries[index]);
-  uint64_t at = from - e.unit0;
-  const uint32_t wg_units = (e.n + kUnit - 1) / kUnit;
-  const bool together = JOIN && from_wg + (kWaves - 1) * per < all && min(per_wg, all - from_wg) <= wg_units &&
-                        at - (uint64_t)quotient(at, wg_units) * wg_units + min(per_wg, all - from_wg) <= wg_units;
-  if (JOIN && wave) {
-    from += wave * per;
-    if (from >= all) return;  // by no wave of such a workgroup
-    if (!together) {
-      index = entry_at(entries, n_entries, from);
-      e = scalar(entries[index]);
-    }
-    at = from - e.unit0;
+  const uint64_t from = run * per;
+  uint32_t index = 0;
+  SharedEntry e;
+  bool together = false;
+  if (JOIN && from_wg + (kWaves - 1) * per < all) {
+    index = entry_at(entries, n_entries, from_wg);
+    e = scalar(entries[index]);
+    const uint64_t at = from_wg - e.unit0, takes = min(per_wg, all - from_wg);
+    const uint32_t units = (e.n + kUnit - 1) / kUnit;
+    together = takes <= units && at - (uint64_t)quotient(at, units) * units + takes <= units;
   }
+  if (from >= all) return;  // by no wave of those that are joined
+  if (!together) {
+    index = entry_at(entries, n_entries, from);
+    e = scalar(entries[index]);
+  }
+  uint64_t at = from - e.unit0;
   uint64_t left = min(per, all - from);
   v4u *const lds_q = WalkLds<D, KIND, TILES, JOIN>::kMost ? lds.q[wave] : lds.q[0];
   bool first_segment = true;
