@@ -18,8 +18,9 @@ KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALVES, ROPE_PAIRS = 0, 1
 
 EXPORTED = ["xfer_qkv_rope_store", "xfer_attn_workspace_bytes", "xfer_attn_paged",
-            "xfer_attn_shared_workspace_bytes", "xfer_attn_shared", "xfer_kv_record_bytes", "xfer_kv_quantize", "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge",
-            "xfer_logprobs_workspace_bytes", "xfer_logprobs_merge"]
+            "xfer_attn_shared_workspace_bytes", "xfer_attn_shared", "xfer_kv_record_bytes", "xfer_kv_quantize",
+            "xfer_kv_restore", "xfer_sample_workspace_bytes", "xfer_sample_merge", "xfer_logprobs_workspace_bytes",
+            "xfer_logprobs_merge"]
 
 SAMPLE_PARAMS = np.dtype([("temperature", "<f4"), ("top_k", "<u4"), ("top_p", "<f4"), ("min_p", "<f4")])
 SAMPLED = np.dtype([("prob", "<f4"), ("idx", "<i4")])
@@ -162,6 +163,7 @@ class KVCache:
                 raise ValueError("one scale for each head")
         self.device, self.kv_heads, self.head_dim, self.page_tokens, self.n_pages = k.get_device(), h, d, p, n
         self.tensors = (k, v, k_scale, v_scale)
+        self.record_bytes = {}  # of a token, by bits: asked once
         # the stride of a dimension of one element is never walked: any multiple of 16 will do
         stride = [s[i] * e if k.shape[i] > 1 else 0 for i in range(3)]
         self.c = KVCacheC(k.data_ptr(), v.data_ptr(), _flat(k_scale, _F32, self.device, "k_scale") or None,
@@ -225,10 +227,15 @@ def attn_workspace_bytes(cache: KVCache, rows: int, q_heads: int, max_len: int, 
     return int(lib().xfer_attn_workspace_bytes(ctypes.byref(cache.c), ctypes.byref(batch), q_heads))
 
 
-def _attn_call(cache: KVCache, q, page_table, lens, max_len: int, out, workspace, window: int, sinks: int):
-    """What both attention calls make of their arguments: (batch, q, q_ld, q_heads, out, out_ld, out_mode, workspace,
-    its bytes)."""
+def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
+               sinks: int = 0, stream=None) -> None:
+    """q: [rows, q_heads, head_dim] (BF16 or its patterns); page_table: int32 or
+    uint32 [rows, at least ceil(max_len / page_tokens)], dense within a row;
+    lens: int32 or uint32 [rows] (a negative one is a large length, cut to
+    max_len); out: like q, BF16 (or its patterns) or F32; workspace: a CUDA
+    tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
     dev, d = cache.device, cache.head_dim
+    stream = _stream_on(dev, stream)
     qp, rows, q_heads, q_ld = _rows(q, None, d, _BF16, dev, "q")
     f32 = out.dtype in _F32
     op, o_rows, _, o_ld = _rows(out, q_heads, d, _F32 if f32 else _BF16, dev, "out")
@@ -244,21 +251,8 @@ def _attn_call(cache: KVCache, q, page_table, lens, max_len: int, out, workspace
         ws_bytes, ws = workspace.numel() * workspace.element_size(), _flat(workspace, None, dev, "workspace")
     batch = PagedBatchC(page_table.data_ptr(), _flat(lens, _INT32, dev, "lens"), ts[0] if rows > 1 else width, rows,
                         max_len, window, sinks)
-    return batch, qp, q_ld, q_heads, op, o_ld, OUT_F32 if f32 else OUT_BF16, ws, ws_bytes
-
-
-def attn_paged(cache: KVCache, q, page_table, lens, max_len: int, scale: float, out, workspace=None, window: int = 0,
-               sinks: int = 0, stream=None) -> None:
-    """q: [rows, q_heads, head_dim] (BF16 or its patterns); page_table: int32 or
-    uint32 [rows, at least ceil(max_len / page_tokens)], dense within a row;
-    lens: int32 or uint32 [rows] (a negative one is a large length, cut to
-    max_len); out: like q, BF16 (or its patterns) or F32; workspace: a CUDA
-    tensor of at least attn_workspace_bytes() bytes (None if that is 0)."""
-    stream = _stream_on(cache.device, stream)
-    batch, qp, q_ld, q_heads, op, o_ld, mode, ws, ws_bytes = _attn_call(cache, q, page_table, lens, max_len, out, workspace,
-                                                                        window, sinks)
     status = lib().xfer_attn_paged(ctypes.byref(cache.c), ctypes.byref(batch), qp, q_ld, q_heads, scale, op, o_ld,
-                                   mode, ws, ws_bytes, stream)
+                                   OUT_F32 if f32 else OUT_BF16, ws, ws_bytes, stream)
     if status != OK:
         _check(status, "xfer_attn_paged")
 
@@ -285,15 +279,29 @@ def attn_shared(cache: KVCache, q, page_table, lens, max_len: int, starts, share
     shared: int32 or uint32 [groups], how many tokens a group's rows have in
     common (a negative one is a large number, cut to what there is);
     workspace: at least attn_shared_workspace_bytes() bytes."""
-    stream = _stream_on(cache.device, stream)
-    batch, qp, q_ld, q_heads, op, o_ld, mode, ws, ws_bytes = _attn_call(cache, q, page_table, lens, max_len, out, workspace,
-                                                                        0, 0)
+    dev, d = cache.device, cache.head_dim
+    stream = _stream_on(dev, stream)
+    qp, rows, q_heads, q_ld = _rows(q, None, d, _BF16, dev, "q")
+    f32 = out.dtype in _F32
+    op, o_rows, _, o_ld = _rows(out, q_heads, d, _F32 if f32 else _BF16, dev, "out")
+    if o_rows != rows or lens.numel() != rows or page_table.dim() != 2 or page_table.shape[0] != rows:
+        raise ValueError("q, page_table, lens and out must have the same rows")
+    width, ts = page_table.shape[1], page_table.stride()
+    if page_table.get_device() != dev or page_table.dtype not in _INT32 or (width > 1 and ts[1] != 1):
+        raise ValueError(f"page_table: expected {_names(_INT32)} on cuda:{dev}, dense within a row")
+    if width * cache.page_tokens < max_len:
+        raise ValueError("page_table is too narrow for max_len")
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws_bytes, ws = workspace.numel() * workspace.element_size(), _flat(workspace, None, dev, "workspace")
+    batch = PagedBatchC(page_table.data_ptr(), _flat(lens, _INT32, dev, "lens"), ts[0] if rows > 1 else width, rows,
+                        max_len, 0, 0)
     groups = shared.numel()
     if starts.numel() != groups + 1:
         raise ValueError("starts must have one number more than shared")
-    g = PrefixGroupsC(_flat(starts, _INT32, cache.device, "starts"), _flat(shared, _INT32, cache.device, "shared"), groups, 0)
+    g = PrefixGroupsC(_flat(starts, _INT32, dev, "starts"), _flat(shared, _INT32, dev, "shared"), groups, 0)
     status = lib().xfer_attn_shared(ctypes.byref(cache.c), ctypes.byref(batch), ctypes.byref(g), qp, q_ld, q_heads, scale,
-                                    op, o_ld, mode, ws, ws_bytes, stream)
+                                    op, o_ld, OUT_F32 if f32 else OUT_BF16, ws, ws_bytes, stream)
     if status != OK:
         _check(status, "xfer_attn_shared")
 
@@ -321,7 +329,10 @@ def _records(records, slots, cache: KVCache, bits: int):
     s0, s1 = records.stride()
     if records.get_device() != cache.device or records.dtype not in _BYTES or (width > 1 and s1 != 1):
         raise ValueError(f"records: expected {_names(_BYTES)} on cuda:{cache.device}, dense within a row")
-    if tokens != slots.numel() or width < kv_record_bytes(cache, bits):
+    need = cache.record_bytes.get(bits)
+    if need is None:
+        need = cache.record_bytes[bits] = kv_record_bytes(cache, bits)
+    if tokens != slots.numel() or width < need:
         raise ValueError("records must have a row of at least kv_record_bytes() for each slot")
     return records.data_ptr(), s0 if tokens > 1 else 0, tokens
 
