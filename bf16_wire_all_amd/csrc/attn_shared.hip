@@ -682,6 +682,14 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
           }
         };
         read_values(0);
+        // Scores above the running maximum; where one passes it by kRaise, the maximum moves and they with it.
+        float base = mx == -INFINITY ? 0.0f : mx, top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[0][i] = fmaf(s[0][i], scale2, -base);
+          s[1][i] = fmaf(s[1][i], scale2, -base);
+        }
+        // Tokens that are not there, after the product: -inf times a scale of 0 is NaN.
         if ((out.x | out.y) != 0) {
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
@@ -689,14 +697,8 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
             for (int i = 0; i < 16; ++i)
               if (out[blk] >> (8 * (i / 4) + 4 * hf + i % 4) & 1) s[blk][i] = -INFINITY;
         }
-        // Scores above the running maximum; where one passes it by kRaise, the maximum moves and they with it.
-        float base = mx == -INFINITY ? 0.0f : mx, top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[0][i] = fmaf(s[0][i], scale2, -base);
-          s[1][i] = fmaf(s[1][i], scale2, -base);
-          top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
-        }
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
         if (__any(top + base > mx + kRaise)) {
           top = fmaxf(top, __shfl_xor(top, 32)) + base;
           const float raised = fmaxf(mx, top);
