@@ -212,12 +212,15 @@ __device__ __forceinline__ float scale_of(uint32_t e) {
 // With h = head / 2^(e - 127) and r = 1 / h, both rounded correctly, q = x r is
 // next to the quotient, and q - (q h - x) r, its remainder fused, is the
 // quotient rounded correctly: so for every x of four bits and every h, tried
-// all, as long as nothing leaves the range of normal numbers.  What might, and
-// NaN, which the limit by a median would lose, is divided.
+// all, as long as x r is finite (below 2^-126 it may be off, and is 0 in E4M3
+// all the same).  h is at least 2^-119, for e up to 186 and a head's scale from
+// 2^-60 on, so 448 r is 1.75 * 2^127 at most; one power less and it would be
+// infinite.  What lies outside, and NaN, which the limit by a median would lose,
+// is divided.
 template <int BITS, int kElements>
 __device__ __forceinline__ void divide(float *x, const uint32_t *w, uint32_t e, float head) {
   const uint32_t biased = __float_as_uint(head) >> 23;  // with a sign: too large
-  bool usual = e - 67 <= 120 && biased - 67 <= 120;
+  bool usual = e - 67 <= 119 && biased - 67 <= 120;
   if (BITS == 8) {
     uint32_t nan = 0;
 #pragma unroll
