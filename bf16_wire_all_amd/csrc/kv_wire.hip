@@ -144,13 +144,16 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(WireArgs a) {
   const uint32_t data_bytes = (2 * a.cache.kv_heads << a.lanes_log2) * kOut;
   Place p[kEach];
   uint32_t w[kEach][kIn / 4];
+  bool missing[kEach];  // its zeros are no head's: the sign, infinity or NaN of a scale is not theirs
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     p[i] = place_of<WHOLE>(a, i);
+    missing[i] = true;
 #pragma unroll
     for (int j = 0; j < kIn / 4; ++j) w[i][j] = 0;
     if (!p[i].there) continue;
     const int64_t at = slot_byte(a, p[i].token);
+    missing[i] = at < 0;
     if (at >= 0)
       load<kIn, STREAM>(w[i], (p[i].values ? a.cache.v : a.cache.k) + at + p[i].head * a.cache.head_stride + p[i].lane * kIn);
   }
@@ -165,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(WireArgs a) {
       }
     } else {
       const float *scales = p[i].values ? a.cache.v_scale : a.cache.k_scale;
-      const float scale = scales && p[i].there ? scales[p[i].head] : 1.0f;
+      const float scale = scales && !missing[i] ? scales[p[i].head] : 1.0f;
 #pragma unroll
       for (int j = 0; j < kElements / 4; ++j) from_e4m3x4(x + 4 * j, w[i][j]);
 #pragma unroll
