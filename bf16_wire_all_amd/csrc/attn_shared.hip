@@ -53,6 +53,10 @@ constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, si
 // and 59; of 64 in E4M3 45, 32 at a time 40), and at least kManyLeast such units to a workgroup (of a group that has as
 // many; with 1 in 64 answers' 16 shared tokens 25 us, with 4 whatever there is 35).
 constexpr uint32_t kFewHeads = 32, kManyHeads = 128, kManyUnit = 64, kManyLeast = 4;
+// Scores in powers of two up to which the maximum's own rounding, 2^-18, moves no weight by more than that.  Beside larger
+// ones all are rounded as it is: 64 answers 42.0 us so, 41.5 with fused products alone, which made alike scores of 2^9 weigh
+// differently from tile to tile and those of 2^31 infinite.
+constexpr float kRounded = 128.0f;
 
 __device__ const v4u kZeros = {0, 0, 0, 0};  // stands for tokens that are not there
 
@@ -635,6 +639,9 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
       // a negative scale's sign goes to the queries, so that the largest product is the largest score
       const uint32_t flip = scale2 < 0 ? 0x80008000u : 0;
       scale2 = __builtin_fabsf(scale2);
+      // a scale of 0 is taken before tokens that are not there get -inf, and then any other will do
+      const bool flat = scale2 == 0.0f;
+      if (flat) scale2 = 1.0f;
       v4u q[kSteps];
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
@@ -682,14 +689,10 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
           }
         };
         read_values(0);
-        // Scores above the running maximum; where one passes it by kRaise, the maximum moves and they with it.
-        float base = mx == -INFINITY ? 0.0f : mx, top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[0][i] = fmaf(s[0][i], scale2, -base);
-          s[1][i] = fmaf(s[1][i], scale2, -base);
+        if (flat) {
+          s[0] *= 0.0f;
+          s[1] *= 0.0f;
         }
-        // Tokens that are not there, after the product: -inf times a scale of 0 is NaN.
         if ((out.x | out.y) != 0) {
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
@@ -697,19 +700,33 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
             for (int i = 0; i < 16; ++i)
               if (out[blk] >> (8 * (i / 4) + 4 * hf + i % 4) & 1) s[blk][i] = -INFINITY;
         }
+        // The largest product is the largest score; where it passes the running maximum by kRaise, that moves.
+        float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
-        if (__any(top + base > mx + kRaise)) {
-          top = fmaxf(top, __shfl_xor(top, 32)) + base;
+        top *= scale2;
+        if (__any(top > mx + kRaise)) {
+          top = fmaxf(top, __shfl_xor(top, 32));
           const float raised = fmaxf(mx, top);
           const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx - raised);
-          const float by = base - (raised == -INFINITY ? 0.0f : raised);
           mx = raised;
           sum *= f;
 #pragma unroll
           for (int d = 0; d < kDims; ++d) o[d] *= f;
-          s[0] += by;
-          s[1] += by;
+        }
+        // Scores above it.  The fused product is not rounded as the maximum was, so the largest is above or below it by that
+        // rounding; where it would be much, scores are rounded first.
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float by = scale2;
+        if (__any(__builtin_fabsf(base) > kRounded)) {
+          s[0] *= scale2;
+          s[1] *= scale2;
+          by = 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[0][i] = fmaf(s[0][i], by, -base);
+          s[1][i] = fmaf(s[1][i], by, -base);
         }
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
