@@ -11,7 +11,7 @@
 //      alone, so no entry needs a mask.  Up to 255 rows and groups, every
 //      workgroup of the walk makes the plan itself (64 answers: 41.3 us; by a
 //      launch of its own 5.2 us and then 39.8); for more a workgroup of
-//      shared_plan_kernel does (5.5 us for 300);
+//      shared_plan_kernel does (6.4 us for 300);
 //   2. walk, two ways in one launch:
 //      - entries of up to 32 query heads for a kv head (or of one row): their
 //        units (32 tokens of a kv head and up to 16 or 32 query heads) are one
@@ -28,8 +28,9 @@
 //      them up, in a fixed order.
 //
 // 64 answers to a prompt of 8192 tokens (32 query heads on 8 of 128, 124 MB):
-// 41 us of walk and 8.8 of join; 24 rows over 131056 shared tokens in F32
-// (548 MB, 129 GFLOP with the weights in three parts): 160-190 + 12 us.
+// 42-45 us of walk and 9.4 of join, on two sets of inputs in turn or on three;
+// 24 rows over 131056 shared tokens in F32 (548 MB, 129 GFLOP with the weights in
+// three parts): 164-195 + 12 us.
 #include "attn_tile.h"
 
 #include <type_traits>
@@ -46,7 +47,9 @@ constexpr uint32_t kLeast = 2;
 constexpr uint32_t kComputeUnits = 256;
 constexpr uint32_t kXcds = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kParts = 3;  // BF16 numbers of a weight: exact, and no slower, since the memory bounds the walk
+// BF16 numbers of a weight in the walk of few heads: exact.  With two, 2^-17, drafted positions take 22.0 us for 23.2, and 64
+// answers and 300 rows as long as now.
+constexpr int kParts = 3;
 
 // Groups of more than kFewHeads query heads for a kv head go another way, kManyHeads of them and
 // kManyUnit tokens at a time (groups of 40 heads of 128: 74 us over 8 x 8000 tokens and 40 over 30000, 32 heads at a time 99
@@ -835,7 +838,8 @@ __global__ __launch_bounds__(kThreads, (Many<D, KIND>::kPerSimd)) void shared_bo
   const bool takes_many = LOCAL ? plan_here(a, local, reinterpret_cast<PlanLds<kThreads> &>(lds0), choose) : choose(*a.many_places);
   if (takes_many)
     walk_many<D, KIND, PARTS>(a, LOCAL ? local.list : a.many, xcd * many + before, kXcds * many, lds0, lds1);
-  else  // with heads of 64 the walk of many would spill more: three system prompts 42.0 + 8.3 us, so 37.8 + 7.9
+  else  // in this kernel heads of 64 leave each run's part: joined, the walk of many would spill more, and three system prompts
+        // take 42.0 + 8.3 us for 37.8 + 7.9
     walk<D, KIND, 2, (D > 64)>(a, LOCAL ? local.list : a.entries, xcd * (places - many) + place - before, kXcds * (places - many),
                      *reinterpret_cast<WalkLds<D, KIND, 2, (D > 64)> *>(lds0));
 }
@@ -1033,7 +1037,8 @@ bool shared_launches(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t
          shape_of(rows, groups, kv_heads, group, head_dim, kind).parts <= UINT32_MAX;
 }
 
-// Layout: the entries, the parts of each (entry, kv head, tile), (max, sum) of each part, the weighted sums.
+// Layout: the entries, the parts of each (entry, kv head, tile), (max, sum) of each part, the weighted sums.  For every run
+// of a full grid, whatever max_len is: a caller's workspace then serves all lengths.
 uint64_t shared_workspace_bytes(uint32_t rows, uint32_t groups, uint32_t kv_heads, uint32_t group, uint32_t head_dim,
                                 int kind) {
   const Shape s = shape_of(rows, groups, kv_heads, group, head_dim, kind);
@@ -1049,6 +1054,9 @@ hipError_t launch_shared(const SharedArgs &in, int kind, void *workspace, hipStr
   uint8_t *at = static_cast<uint8_t *>(workspace);
   a.many_places = reinterpret_cast<uint32_t *>(at);
   a.places_of_xcd = s.workgroups / kXcds;
+  // What a unit of either list costs, one to the other: bytes of keys and values, or products with keys and each part of the
+  // weights.  64 answers 44.8 us, three system prompts 39.3, 300 rows in 20 groups 64; with the second 0.6 times that 53.4, 42
+  // and 85, 1.6 times 51.0, 44.5 and 52: no one ratio serves all.
   a.unit_cost = kUnit * 2 * a.cache.head_dim * (kind == XFER_KV_BF16 ? 2 : 1) / 64;
   a.many_unit_cost = a.cache.head_dim * (a.out_mode == XFER_OUT_F32 ? 4 : 3) * 2;
 

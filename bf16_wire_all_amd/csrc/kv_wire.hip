@@ -17,19 +17,25 @@
 // tokens, kEach of them a lane, whose loads are in flight together.  Where a
 // token's rows fill whole waves, its slot is looked up once for the wave.
 //
-// 16,384 tokens of 8 heads of 128 from BF16 to 8 bits (102 MB): 17.6 us, 5.8
-// TB/s; 65,521 records of 8 bits to an E4M3 cache (273 MB): 50.4 us, 5.4 TB/s.
+// Kernel times on three sets of inputs in turn (two would stay in the last cache
+// in part): 16,384 tokens of 8 heads of 128 from BF16 to 8 bits (102 MB) 21 us,
+// 4.9 TB/s; 65,521 tokens of E4M3 to 8 bits (273 MB) 50 us, 5.4 TB/s; as many
+// records of 8 bits to an E4M3 cache 51 us, 5.3 TB/s, to a BF16 one (408 MB)
+// 75 us, 5.4 TB/s; 24,001 tokens of 8 heads of 64 from E4M3 to 4 bits (38 MB) 12
+// us, and from there to BF16 (63 MB) 11.6 us.
 #include "decode.h"
 
 namespace xfer {
 namespace {
 
 constexpr int kThreads = 256;
-// Elements of a lane, 16 bytes of the cache: 65,521 records to an E4M3 cache 50
-// us (8 elements: 58).
+// Elements of a lane, 16 bytes of the cache: 65,521 records to an E4M3 cache 51
+// us, and as many tokens from one 50 (8 elements: 65 and 60).  A lane of E4M3 to
+// or from 4 bits has 8.
 constexpr int elements_of(int kind, int bits) { return kind == XFER_KV_E4M3 && bits == 8 ? 16 : 8; }
-// Rows of a lane: one page of 16 tokens 3.0 us, 16,384 tokens 17.6, 65,521 50.4
-// (4 rows: 3.5, 18.0, 51.7; one: 2.6, 18.1, 50.7).
+// Rows of a lane: one page of 16 tokens 3.0 us, 16,384 tokens 21.6, 24,001 to 4
+// bits 13.7, 65,521 restored 51.7 (4 rows: 3.4, 21.3, 13.7, 53.6; one: 2.6, 22.5,
+// 15.1, 50.1).
 constexpr int kEach = 2;
 static_assert(kThreads * kEach * 16 / 64 <= 128, "rows of a workgroup");
 
@@ -109,7 +115,7 @@ struct Place {
   bool there, values, last;
 };
 // WHOLE: all of a wave's rows are one token's, so what depends on the token is
-// the scalar unit's work (16,384 tokens 18.0 us; by every lane for itself 21.2).
+// the scalar unit's work (16,384 tokens 21.6 us; by every lane for itself 24.6).
 template <bool WHOLE>
 __device__ __forceinline__ Place place_of(const WireArgs &a, uint32_t i) {
   const uint32_t kv = a.cache.kv_heads, at = i * kThreads + threadIdx.x;
