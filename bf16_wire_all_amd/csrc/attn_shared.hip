@@ -642,8 +642,9 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
       // a negative scale's sign goes to the queries, so that the largest product is the largest score
       const uint32_t flip = scale2 < 0 ? 0x80008000u : 0;
       scale2 = __builtin_fabsf(scale2);
-      // a scale of 0 is taken before tokens that are not there get -inf, and then any other will do
-      const bool flat = scale2 == 0.0f;
+      // a scale of 0 or NaN is taken before tokens that are not there get -inf, and then any other will do
+      const bool flat = !(scale2 > 0.0f);
+      const float flat_by = scale2;
       if (flat) scale2 = 1.0f;
       v4u q[kSteps];
 #pragma unroll
@@ -693,8 +694,8 @@ __device__ __forceinline__ void walk_many(const SharedArgs &a, const SharedEntry
         };
         read_values(0);
         if (flat) {
-          s[0] *= 0.0f;
-          s[1] *= 0.0f;
+          s[0] *= flat_by;
+          s[1] *= flat_by;
         }
         if ((out.x | out.y) != 0) {
 #pragma unroll

@@ -57,3 +57,22 @@ def test_a_head_s_scale_of_zero_and_below(rows, value):
     w.cache.tensors[2][1] = value
     say("k_scale", rows, value)
     w.run(rows=[0, 1, rows - 1, rows])
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_holes_alone_give_zeros_whatever_a_head_s_scale_is(rows, value):
+    """A head whose scale is no number has NaN in every row that sees a token, and zeros in the others."""
+    w = World([(64, [64] * rows), (96, [97] * rows), [16], [33]], 8, 2, 128, 16, "e4m3", "heads", "f32",
+              holes=[(0, p) for p in range(4)] + [(2 * rows, 0)])
+    w.ks[1] = value
+    w.cache.tensors[2][1] = value
+    raw, out = w.buffer()
+    say("holes alone", rows, value)
+    w.call(out)
+    got = out.cpu().double().numpy()
+    assert (got[:rows] == 0).all() and (got[2 * rows] == 0).all()
+    assert np.isnan(got[rows:2 * rows, 4:]).all() and np.isnan(got[2 * rows + 1, 4:]).all()
+    for r in (rows, 2 * rows - 1, 2 * rows + 1):
+        want, tol = w.want(r)
+        assert (np.abs(got[r] - want) <= tol)[:4].all()
