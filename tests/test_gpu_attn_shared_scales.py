@@ -74,5 +74,6 @@ def test_holes_alone_give_zeros_whatever_a_head_s_scale_is(rows, value):
     assert (got[:rows] == 0).all() and (got[2 * rows] == 0).all()
     assert np.isnan(got[rows:2 * rows, 4:]).all() and np.isnan(got[2 * rows + 1, 4:]).all()
     for r in (rows, 2 * rows - 1, 2 * rows + 1):
-        want, tol = w.want(r)
-        assert (np.abs(got[r] - want) <= tol)[:4].all()
+        with np.errstate(invalid="ignore"):
+            want, tol = w.want(r)
+            assert (np.abs(got[r] - want) <= tol)[:4].all()
